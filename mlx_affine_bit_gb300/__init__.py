@@ -1,7 +1,9 @@
-"""Python binding of libtfqmm, the MLX-affine quantized row product for GB300.
+"""Python binding of libtfqmm, the MLX-affine quantized row product for GB300, and
+of the 8-bit cache, attention and sampling around it.
 
 Argument marshalling only: every step of the product runs in the library's
-CUDA kernels (``csrc/``).  The names and arguments follow ``include/tfqmm.h``.
+CUDA kernels (``csrc/``).  The names and arguments follow ``include/tfqmm.h`` and
+``include/tfdecode.h``.
 Tensors may be passed as torch tensors (their ``data_ptr()`` is used) or as
 raw integer addresses; ``stream`` is a ``torch.cuda.Stream``, a raw
 ``cudaStream_t`` integer, or None for torch's current stream.
@@ -28,9 +30,11 @@ STATUS = {
 }
 SYMBOLS = ("tf_qmm", "tf_qmm_ex", "tf_qmm_prompt", "tf_qmm_gather", "tf_qmm_noalloc", "tf_noalloc_status", "tf_qmm_stack", "tf_widen",
            "tf_widen_host", "tf_common_width", "tf_qmm_bytes", "tf_device_status", "tf_set_launch_mode",
-           "tf_inject_stall", "tf_last_error_string", "tf_version")
+           "tf_inject_stall", "tf_last_error_string", "tf_version",
+           "tf_kv_append", "tf_kv_read", "tf_kv_attend", "tf_sample")
 TF_LAUNCH_PDL, TF_LAUNCH_EARLY_WEIGHTS, TF_LAUNCH_EARLY_X = 1, 2, 4
 TF_OUT_BF16, TF_EPI_RELU2 = 1, 2
+TF_IN_F32, TF_KV_CAUSAL, TF_IN_BF16 = 4, 8, 16
 
 
 class TfError(RuntimeError):
@@ -47,6 +51,17 @@ class TfRun(ctypes.Structure):
 class TfMember(ctypes.Structure):
     _fields_ = [("run", ctypes.c_int), ("src_col", ctypes.c_int), ("n_cols", ctypes.c_int),
                 ("dst_col", ctypes.c_int)]
+
+
+class TfKv(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "open_k", "open_v", "open_max")] + \
+               [(n, ctypes.c_int) for n in ("n_blocks", "n_slots", "kv_heads", "block", "dim", "f32")]
+
+
+class TfKvBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_seqs", "rows", "max_rows", "max_len")] + \
+               [(n, ctypes.c_void_p) for n in ("row_start", "kv_len", "table")] + \
+               [("table_stride", ctypes.c_int64), ("slots", ctypes.c_void_p)]
 
 
 _lib = None
@@ -124,11 +139,16 @@ def _load(path):
     L.tf_noalloc_status.argtypes = []
     L.tf_set_launch_mode.argtypes = [i32]
     L.tf_inject_stall.argtypes = []
+    kv, batch = ctypes.POINTER(TfKv), ctypes.POINTER(TfKvBatch)
+    L.tf_kv_append.argtypes = [kv, batch, P, i64, P, i64, P]
+    L.tf_kv_read.argtypes = [kv, batch, P, i64, P, i64, i32, P]
+    L.tf_kv_attend.argtypes = [kv, batch, P, i64, i32, P, i64, ctypes.c_float, i32, i32, P]
+    L.tf_sample.argtypes = [P, i32, i32, i64, P, P, P, P, P, P, P, i32, P]
     L.tf_last_error_string.restype = ctypes.c_char_p
     L.tf_version.restype = ctypes.c_char_p
     for name in ("tf_qmm", "tf_qmm_ex", "tf_qmm_prompt", "tf_qmm_gather", "tf_qmm_noalloc", "tf_qmm_stack", "tf_widen",
                  "tf_widen_host", "tf_common_width", "tf_qmm_bytes", "tf_device_status", "tf_noalloc_status",
-                 "tf_set_launch_mode", "tf_inject_stall"):
+                 "tf_set_launch_mode", "tf_inject_stall", "tf_kv_append", "tf_kv_read", "tf_kv_attend", "tf_sample"):
         getattr(L, name).restype = i32
     return L
 
@@ -255,6 +275,30 @@ def tf_inject_stall() -> None:
     _check(lib().tf_inject_stall())
 
 
+def tf_kv_append(kv: TfKv, batch: TfKvBatch, k, k_stride, v, v_stride, stream=None) -> None:
+    """Quantize new tokens' keys and values into the cache (see include/tfdecode.h)."""
+    _check(lib().tf_kv_append(kv, batch, _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream)))
+
+
+def tf_kv_read(kv: TfKv, batch: TfKvBatch, k_out, k_stride, v_out, v_stride, flags=0, stream=None) -> None:
+    """Read the batch's tokens back as fp32 (bf16 with TF_OUT_BF16) rows; either output may be None."""
+    _check(lib().tf_kv_read(kv, batch, _ptr(k_out), k_stride, _ptr(v_out), v_stride, flags, _stream(stream)))
+
+
+def tf_kv_attend(kv: TfKv, batch: TfKvBatch, q, q_stride, heads, out, out_stride, scale, window=0, flags=TF_KV_CAUSAL,
+                 stream=None) -> None:
+    """Attention of the batch's rows over the cache; out is bf16 (see include/tfdecode.h)."""
+    _check(lib().tf_kv_attend(kv, batch, _ptr(q), q_stride, heads, _ptr(out), out_stride, scale, window, flags,
+                              _stream(stream)))
+
+
+def tf_sample(logits, rows, vocab, stride, u, temperature, top_k, top_p, min_p, tokens, probs=None, flags=0,
+              stream=None) -> None:
+    """One token per row of logits from the random numbers u (see include/tfdecode.h)."""
+    _check(lib().tf_sample(_ptr(logits), rows, vocab, stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                           _ptr(min_p), _ptr(tokens), _ptr(probs), flags, _stream(stream)))
+
+
 def tf_version() -> str:
     return lib().tf_version().decode()
 
@@ -273,3 +317,158 @@ def qmm(x, W, scales, biases, bits, group, y=None, y_stride=None, stream=None):
     tf_qmm(x, rows, K, W, scales, biases, N, bits, group, y,
            y_stride if y_stride is not None else y.stride(0), stream)
     return y
+
+
+def _tensor(t, name, dtypes, shape=None, contiguous=True):
+    """Refuse a tensor that a call could not take: TypeError for its type, ValueError for the rest."""
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _rows(t, name, dtypes, rows, width):
+    """The row stride of a [rows][width] matrix whose rows are contiguous."""
+    _tensor(t, name, dtypes, (rows, width), contiguous=False)
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.stride(0) if rows > 1 else max(width, t.stride(0))
+
+
+class KvBatch:
+    """The rows of one call on a KvCache (tf_kv_batch), on torch tensors.
+
+    kv_len [seqs] int32 (the new tokens included), table [seqs][pages] int32,
+    max_len a bound of kv_len; row_start [seqs + 1] int32 with rows and
+    max_rows, or max_rows (1) rows for each sequence; slots [seqs] int32, or
+    None for 0, 1, ...  The tensors are kept, and read by the device at each call."""
+
+    def __init__(self, kv_len, table, max_len, row_start=None, rows=None, max_rows=1, slots=None):
+        import torch
+        i32 = (torch.int32,)
+        n = kv_len.shape[0]
+        _tensor(kv_len, "kv_len", i32, (n,))
+        _tensor(table, "table", i32, (n, table.shape[-1]), contiguous=False)
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table must have contiguous rows")
+        if row_start is not None:
+            _tensor(row_start, "row_start", i32, (n + 1,))
+            if rows is None:
+                raise ValueError("row_start needs rows")
+        if slots is not None:
+            _tensor(slots, "slots", i32, (n,))
+        if max_len > table.shape[1] * 128:
+            raise ValueError("max_len exceeds the table")
+        self.rows = n * max_rows if row_start is None else rows
+        self._keep = (kv_len, table, row_start, slots)
+        self._pages = table.shape[1]
+        self.c = TfKvBatch(n, self.rows, max_rows, max_len, _ptr(row_start), _ptr(kv_len), _ptr(table),
+                           table.stride(0) if n > 1 else table.shape[1], _ptr(slots))
+
+
+class KvCache:
+    """An 8-bit paged key/value cache (tf_kv) on torch tensors.
+
+    k, v [n_blocks][kv_heads][block][dim] int8 and k_scale, v_scale
+    [n_blocks][kv_heads] fp32; for append also open_k, open_v
+    [n_slots][kv_heads][2 * block][dim] (bf16 or fp32, the type of the appended
+    rows) and open_max [n_slots][2][kv_heads][2 * block] fp32."""
+
+    def __init__(self, k, v, k_scale, v_scale, open_k=None, open_v=None, open_max=None):
+        import torch
+        if k.dim() != 4:
+            raise ValueError("k must be [n_blocks][kv_heads][block][dim]")
+        n_blocks, heads, block, dim = k.shape
+        _tensor(k, "k", (torch.int8,))
+        _tensor(v, "v", (torch.int8,), k.shape)
+        _tensor(k_scale, "k_scale", (torch.float32,), (n_blocks, heads))
+        _tensor(v_scale, "v_scale", (torch.float32,), (n_blocks, heads))
+        n_slots = 0
+        self.dtype = torch.bfloat16
+        if open_k is not None:
+            n_slots, self.dtype = open_k.shape[0], open_k.dtype
+            _tensor(open_k, "open_k", (torch.bfloat16, torch.float32), (n_slots, heads, 2 * block, dim))
+            _tensor(open_v, "open_v", (self.dtype,), open_k.shape)
+            _tensor(open_max, "open_max", (torch.float32,), (n_slots, 2, heads, 2 * block))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.open_k, self.open_v, self.open_max = open_k, open_v, open_max
+        self.kv_heads, self.block, self.dim = heads, block, dim
+        self.c = TfKv(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(open_k), _ptr(open_v), _ptr(open_max),
+                      n_blocks, n_slots, heads, block, dim, int(self.dtype == torch.float32))
+
+    @classmethod
+    def empty(cls, n_blocks, kv_heads, dim, block=64, n_slots=1, dtype=None, device="cuda"):
+        """A new cache of n_blocks pages for n_slots sequences that grow at a time."""
+        import torch
+        dtype = dtype or torch.bfloat16
+        code = dict(dtype=torch.int8, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        shape, ring = (n_blocks, kv_heads, block, dim), (n_slots, kv_heads, 2 * block, dim)
+        return cls(torch.zeros(shape, **code), torch.zeros(shape, **code), torch.zeros(shape[:2], **f32),
+                   torch.zeros(shape[:2], **f32), torch.zeros(ring, dtype=dtype, device=device),
+                   torch.zeros(ring, dtype=dtype, device=device),
+                   torch.zeros((n_slots, 2, kv_heads, 2 * block), **f32))
+
+    def _batch(self, batch):
+        if batch.c.max_len > batch._pages * self.block:
+            raise ValueError("max_len exceeds the table's pages")
+        return batch.c
+
+    def append(self, k, v, batch, stream=None) -> None:
+        """Quantize rows k, v [rows][kv_heads * dim] (row stride free) in as the batch's last tokens."""
+        width = self.kv_heads * self.dim
+        ks = _rows(k, "k", (self.dtype,), batch.rows, width)
+        vs = _rows(v, "v", (self.dtype,), batch.rows, width)
+        tf_kv_append(self.c, self._batch(batch), k, ks, v, vs, stream)
+
+    def read(self, batch, dtype=None, k_out=None, v_out=None, stream=None):
+        """The batch's tokens as k, v rows [rows][kv_heads * dim] of dtype (the appended rows' type by default)."""
+        import torch
+        dtype = dtype or self.dtype
+        width = self.kv_heads * self.dim
+        out = [torch.empty((batch.rows, width), dtype=dtype, device=self.k.device) if t is None else t
+               for t in (k_out, v_out)]
+        strides = [_rows(t, "output", (torch.bfloat16, torch.float32), batch.rows, width) for t in out]
+        if out[0].dtype != out[1].dtype:
+            raise TypeError("k_out and v_out must have one type")
+        tf_kv_read(self.c, self._batch(batch), out[0], strides[0], out[1], strides[1],
+                   TF_OUT_BF16 if out[0].dtype == torch.bfloat16 else 0, stream)
+        return out[0], out[1]
+
+    def attend(self, q, batch, out=None, scale=None, causal=True, window=0, stream=None):
+        """Attention of q [rows][heads * dim] (bf16 or fp32) over the cache; out is bf16, scale 1/sqrt(dim) by default."""
+        import torch
+        rows, width = q.shape
+        qs = _rows(q, "q", (torch.bfloat16, torch.float32), batch.rows, width)
+        if out is None:
+            out = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device)
+        os_ = _rows(out, "out", (torch.bfloat16,), rows, width)
+        if width % self.dim:
+            raise ValueError("q's rows must hold heads * dim values")
+        tf_kv_attend(self.c, self._batch(batch), q, qs, width // self.dim, out, os_,
+                     self.dim ** -0.5 if scale is None else scale, window,
+                     (TF_KV_CAUSAL if causal else 0) | (TF_IN_F32 if q.dtype == torch.float32 else 0), stream)
+        return out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+    """tf_sample on torch tensors: logits [rows][vocab] fp32 or bf16 (row stride free), u [rows] fp32 random
+    numbers, per-row temperature, top_p, min_p (fp32) and top_k (int32) or None.  Returns (tokens, probs)."""
+    import torch
+    rows, vocab = logits.shape
+    stride = _rows(logits, "logits", (torch.float32, torch.bfloat16), rows, vocab)
+    f32, i32 = (torch.float32,), (torch.int32,)
+    for t, name, types in ((u, "u", f32), (temperature, "temperature", f32), (top_k, "top_k", i32), (top_p, "top_p", f32),
+                           (min_p, "min_p", f32), (tokens, "tokens", i32), (probs, "probs", f32)):
+        if t is not None:
+            _tensor(t, name, types, (rows,))
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    tf_sample(logits, rows, vocab, stride, u, temperature, top_k, top_p, min_p, tokens, probs,
+              TF_IN_BF16 if logits.dtype == torch.bfloat16 else 0, stream)
+    return tokens, probs

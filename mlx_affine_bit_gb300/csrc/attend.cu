@@ -1,0 +1,139 @@
+// attend.cu -- tf_kv_attend: attention over the 8-bit paged cache (tfdecode.h).
+// Host side: checks, the split of long sequences, the per-(device, stream)
+// workspace for the parts' sums; the kernels are in attend_rows.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "attend_rows.cuh"
+#include "kv.h"
+
+using namespace tfq;
+
+namespace {
+
+// Parts of split sequences (floats) and their arrival counters (zero between launches).
+struct Ws {
+    float *part = nullptr;
+    size_t floats = 0;
+    int *count = nullptr;
+    size_t counters = 0;
+};
+std::mutex g_mu;
+std::map<std::pair<int, cudaStream_t>, Ws> g_ws;
+
+int workspace(cudaStream_t st, size_t floats, size_t counters, Ws *out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    std::lock_guard<std::mutex> lk(g_mu);
+    Ws &w = g_ws[{dev, st}];
+    if (w.floats < floats || w.counters < counters) {
+        if (w.part || w.count) {
+            // Earlier launches on this stream may still use it.
+            e = cudaStreamSynchronize(st);
+            if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
+        }
+        if (w.floats < floats) {
+            cudaFree(w.part);
+            w.part = nullptr;
+            w.floats = 0;
+            e = cudaMalloc(&w.part, floats * sizeof(float));
+            if (e != cudaSuccess) return cuda_error(e, "cudaMalloc(attention parts)");
+            w.floats = floats;
+        }
+        if (w.counters < counters) {
+            cudaFree(w.count);
+            w.count = nullptr;
+            w.counters = 0;
+            e = cudaMalloc(&w.count, counters * sizeof(int));
+            if (e != cudaSuccess) return cuda_error(e, "cudaMalloc(attention counters)");
+            e = cudaMemsetAsync(w.count, 0, counters * sizeof(int), st);
+            if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync(attention counters)");
+            w.counters = counters;
+        }
+    }
+    *out = w;
+    return TF_OK;
+}
+
+template <int D, int NT>
+cudaError_t launch_rows(const attend::Params &P, unsigned grid, cudaStream_t st) {
+    attend::rows_kernel<D, NT><<<grid, attend::THREADS, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace
+
+extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const void *q, int64_t q_stride, int heads,
+                            void *out, int64_t out_stride, float scale, int window, int flags, void *stream) {
+    fail_message(TF_OK, "");
+    if (flags & ~(TF_IN_F32 | TF_KV_CAUSAL))
+        return fail_message(TF_EINVAL_FLAGS, "tf_kv_attend takes TF_IN_F32 and TF_KV_CAUSAL only");
+    int rc = check_kv(kv);
+    if (!rc) rc = check_batch(kv, batch);
+    if (rc) return rc;
+    if (heads < 1 || heads % kv->kv_heads != 0)
+        return fail_message(TF_EINVAL_SIZE, "heads must be a multiple of kv_heads");
+    if (heads / kv->kv_heads > 1024) return fail_message(TF_EINVAL_SIZE, "more than 1024 query heads a key/value head");
+    if (window < 0 || (window > 0 && !(flags & TF_KV_CAUSAL)))
+        return fail_message(TF_EINVAL_SIZE, "window must be 0, or positive with TF_KV_CAUSAL");
+    if (!q || !out || !aligned(q, flags & TF_IN_F32 ? 4 : 2) || !aligned(out, 2))
+        return fail_message(TF_EINVAL_PTR, "NULL q or out, or not aligned to their type");
+    const long long width = (long long)heads * kv->dim;
+    if (q_stride < width || out_stride < width)
+        return fail_message(TF_EINVAL_STRIDE, "q_stride or out_stride below heads * dim");
+    int nsm = 0, *status = nullptr;
+    rc = device_info(&nsm, &status);
+    if (rc) return rc;
+
+    attend::Params P{};
+    P.kv = *kv;
+    P.b = *batch;
+    P.q = q;
+    P.q_stride = q_stride;
+    P.out = static_cast<uint16_t *>(out);
+    P.out_stride = out_stride;
+    P.status = status;
+    P.group = heads / kv->kv_heads;
+    P.scale = scale;
+    P.window = window;
+    P.causal = (flags & TF_KV_CAUSAL) != 0;
+    P.q_f32 = (flags & TF_IN_F32) != 0;
+    const long long max_group_rows = (long long)batch->max_rows * P.group;
+    if (max_group_rows > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "too many rows of one sequence");
+    const int nt = max_group_rows <= 8 ? 1 : 2;
+    const long long tiles = (max_group_rows + 8 * nt - 1) / (8 * nt);
+    const long long items = (long long)batch->n_seqs * kv->kv_heads * tiles;
+    // The tokens that a tile of rows may see, and their split: pieces of at
+    // least 128 tokens, enough of them for four CTAs an SM.
+    long long span = batch->max_len;
+    if (window > 0) span = std::min(span, (long long)window + batch->max_rows + attend::STEP);
+    long long want = std::max(1LL, (4LL * nsm + items - 1) / items);
+    long long piece = std::max(128LL, (span + want - 1) / want);
+    piece = std::min<long long>((piece + attend::STEP - 1) / attend::STEP * attend::STEP, attend::MAX_PIECE);
+    P.piece = (int)piece;
+    P.nsplit = (int)((span + piece - 1) / piece) + (window > 0 ? 1 : 0);
+    P.tiles = (int)tiles;
+    const long long grid = items * P.nsplit;
+    if (tiles > 0x7FFFFFFF || grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (P.nsplit > 1) {
+        Ws w;
+        rc = workspace(st, (size_t)grid * 8 * nt * (kv->dim + 3), (size_t)items, &w);
+        if (rc) return rc;
+        P.part = w.part;
+        P.count = w.count;
+    }
+    cudaError_t e = cudaErrorInvalidValue;
+    const unsigned g = (unsigned)grid;
+    if (kv->dim == 64) e = nt == 1 ? launch_rows<64, 1>(P, g, st) : launch_rows<64, 2>(P, g, st);
+    if (kv->dim == 128) e = nt == 1 ? launch_rows<128, 1>(P, g, st) : launch_rows<128, 2>(P, g, st);
+    if (kv->dim == 256) e = nt == 1 ? launch_rows<256, 1>(P, g, st) : launch_rows<256, 2>(P, g, st);
+    return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_attend launch");
+}

@@ -1,0 +1,355 @@
+// kv.cu -- tf_kv_append and tf_kv_read: the 8-bit paged cache of tfdecode.h,
+// quantized as it is written, and read back.
+//
+// A page (block tokens x dim of one head) has scale = amax * (1 / 127) and codes
+// rint(x / scale).  Both kernels stream: append reads each new row once, holds a
+// page's new values in registers between the maximum and the rounding, and
+// writes codes; read turns 16 codes a thread into a row's values.  Memory
+// bound on prompts, latency bound on single tokens.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <string>
+
+#include "kv.h"
+
+using namespace tfq;
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// ----------------------------------------------------------------- append --
+
+struct AppendParams {
+    tf_kv kv;
+    tf_kv_batch b;
+    const void *src[2];
+    long long stride[2];
+    int nb;                 // pages that a sequence's new tokens may touch
+    int *status;
+};
+
+// Magnitude of a finite value; 0 for an infinity or NaN (see the header).
+__device__ __forceinline__ float finite_mag(float x) {
+    const float a = fabsf(x);
+    return a <= FLT_MAX ? a : 0.f;
+}
+
+__device__ __forceinline__ uint32_t code_of(float x, float scale) {
+    // 0 / 0 and NaN convert to 0; an infinity saturates and is clamped.
+    int c = __float2int_rn(__fdiv_rn(x, scale));
+    c = max(-127, min(127, c));
+    return (uint32_t)(c & 255);
+}
+
+__device__ __forceinline__ void load8(float (&x)[8], const float *p, bool vec) {
+    if (vec) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+    }
+}
+__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16 *p, bool vec) {
+    const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+    if (vec) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((uint32_t)h[i] << 16);
+    }
+}
+// The originals go back as they came (16-byte aligned destination).
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= code_of(x[i], scale) << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+constexpr int VPT = 4;      // 8-value vectors a thread: block * dim / 32 threads cover a page
+
+// One CTA a (sequence, page, head, keys or values).  Its new tokens are read
+// into registers once; if they change the scale of a page that was already
+// begun, the page's earlier tokens are quantized again from the open ring.
+// The last two pages' originals go into the ring.  Its halves alternate with the
+// pages: a long call may put a last page where the begun page's earlier tokens
+// still are, and then the begun page's CTA writes that page's originals, after
+// it has read its own.
+template <typename T>
+__global__ void __launch_bounds__(1024) kv_append_kernel(const AppendParams P) {
+    const tf_kv &kv = P.kv;
+    const int H = kv.kv_heads, B = kv.block, D = kv.dim;
+    unsigned id = blockIdx.x;
+    const int side = id & 1;
+    id >>= 1;
+    const int h = id % H;
+    id /= H;
+    const int j = id % P.nb, s = id / P.nb;
+
+    const SeqRows q = seq_rows(P.b, s);
+    const int slot = P.b.slots ? P.b.slots[s] : s;
+    const int first = q.end - q.n;
+    const int pg = first / B + j;                   // page of the sequence
+    if (q.n == 0) return;
+    if (!q.ok || first < 0 || slot < 0 || slot >= kv.n_slots) {
+        if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
+        return;
+    }
+    const int base = pg * B;                        // the page's first token
+    if (base >= q.end) return;
+    const int page = P.b.table[s * P.b.table_stride + pg];
+    if (page < 0 || page >= kv.n_blocks) {
+        if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
+        return;
+    }
+    const int lo = max(first, base) - base, hi = min(q.end, base + B) - base;   // new tokens of the page
+    const int pg0 = first / B, last = (q.end - 1) / B;
+    const bool begun = first % B != 0;
+    // The last two pages; one whose half of the ring the begun page occupies is left to that page's CTA.
+    const bool keep = pg >= last - 1 && !(begun && pg > pg0 && ((pg - pg0) & 1) == 0);
+    const T *src = static_cast<const T *>(P.src[side]);
+    const bool vec = ((reinterpret_cast<uintptr_t>(src) | (P.stride[side] * sizeof(T))) & 15) == 0;
+    int8_t *codes = (side ? kv.v : kv.k) + ((long long)page * H + h) * B * D;
+    float *scales = (side ? kv.v_scale : kv.k_scale) + (long long)page * H + h;
+    T *ring = static_cast<T *>(side ? kv.open_v : kv.open_k) + (((long long)slot * H + h) * 2 * B + base % (2 * B)) * D;
+    float *ring_max = kv.open_max + (((long long)slot * 2 + side) * H + h) * 2 * B + base % (2 * B);
+
+    const int vd = D / 8;                           // vectors a token: 8, 16 or 32 lanes of one warp
+    const int nt = blockDim.x, tid = threadIdx.x;
+    float x[VPT][8];
+    float amax = 0.f;
+    const float old_scale = lo > 0 ? *scales : 0.f;
+    for (int t = tid; t < lo; t += nt) amax = fmaxf(amax, ring_max[t]);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * nt, t = v / vd, d = (v - t * vd) * 8;
+        const bool mine = t >= lo && t < hi;
+        float m = 0.f;
+        if (mine) {
+            load8(x[i], src + (long long)(q.row0 + base + t - first) * P.stride[side] + h * D + d, vec);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(x[i][e]));
+        }
+        for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if (mine && keep) {
+            store8(ring + t * D + d, x[i]);
+            if (d == 0) ring_max[t] = m;
+        }
+        amax = fmaxf(amax, m);
+    }
+    __shared__ float part[32];
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if ((tid & 31) == 0) part[tid >> 5] = amax;
+    __syncthreads();
+    amax = part[0];
+    for (int w = 1; w < nt / 32; ++w) amax = fmaxf(amax, part[w]);
+    const float scale = __fmul_rn(amax, 1.f / 127.f);
+    // (A long call, which takes these originals out of the ring, does so in any case.)
+    const int other = (last - pg) & 1 ? last - 1 : last;      // the last page in this half of the ring
+    const bool leaves = pg == pg0 && begun && other > pg;
+    const bool again = lo > 0 && (scale != old_scale || leaves);
+    if (tid == 0) *scales = scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * nt, t = v / vd, d = (v - t * vd) * 8;
+        if (t < lo && again) load8(x[i], ring + t * D + d, true);
+        if (t < hi && (t >= lo || again)) *reinterpret_cast<uint2 *>(codes + t * D + d) = codes8(x[i], scale);
+    }
+    if (leaves) {
+        __syncthreads();
+        const int first_t = other * B, n = min(q.end - first_t, B);
+        for (int i = 0; i < VPT; ++i) {
+            const int v = tid + i * nt, t = v / vd, d = (v - t * vd) * 8;
+            float y[8], m = 0.f;
+            if (t < n) {
+                load8(y, src + (long long)(q.row0 + first_t + t - first) * P.stride[side] + h * D + d, vec);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(y[e]));
+                store8(ring + t * D + d, y);
+            }
+            for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            if (t < n && d == 0) ring_max[t] = m;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- read --
+
+struct ReadParams {
+    tf_kv kv;
+    tf_kv_batch b;
+    void *out[2];
+    long long stride[2];
+    int tiles;              // tiles of READ_TOKENS tokens that a sequence may have
+    int *status;
+};
+constexpr int READ_TOKENS = 16;
+
+// One CTA a (sequence, 16 of its rows, keys or values): a thread turns 16 codes
+// into 16 values of a row.
+template <typename T>
+__global__ void kv_read_kernel(const ReadParams P) {
+    const tf_kv &kv = P.kv;
+    const int H = kv.kv_heads, B = kv.block, D = kv.dim;
+    unsigned id = blockIdx.x;
+    const int side = id & 1;
+    id >>= 1;
+    const int tile = id % P.tiles, s = id / P.tiles;
+    if (!P.out[side]) return;
+    const SeqRows q = seq_rows(P.b, s);
+    if (!q.ok || q.end < q.n) {
+        if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
+        return;
+    }
+    const int t0 = tile * READ_TOKENS;
+    const int nt = min(READ_TOKENS, q.n - t0);
+    const int vd = D / 16, per = H * vd;            // 16-code vectors a head, a row
+    T *out = static_cast<T *>(P.out[side]);
+    const bool vec = ((reinterpret_cast<uintptr_t>(out) | (P.stride[side] * sizeof(T))) & 15) == 0;
+    for (int v = threadIdx.x; v < nt * per; v += blockDim.x) {
+        const int t = v / per, c = v - t * per, h = c / vd, d = (c - h * vd) * 16;
+        const int pos = q.end - q.n + t0 + t;
+        const int page = P.b.table[s * P.b.table_stride + pos / B];
+        if (page < 0 || page >= kv.n_blocks) {
+            atomicOr(P.status, STATUS_BOUNDS);
+            continue;
+        }
+        const long long ph = (long long)page * H + h;
+        const uint4 w = *reinterpret_cast<const uint4 *>((side ? kv.v : kv.k) + (ph * B + pos % B) * D + d);
+        const float scale = (side ? kv.v_scale : kv.k_scale)[ph];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        float y[2][8];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i >> 3][i & 7] = scale * (float)(int8_t)(u[i >> 2] >> (8 * (i & 3)));
+        T *dst = out + (long long)(q.row0 + t0 + t) * P.stride[side] + h * D + d;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[k][i] = __bfloat162float(__float2bfloat16_rn(y[k][i]));
+            }
+            if (vec) {
+                store8(dst + 8 * k, y[k]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[8 * k + i] = (T)y[k][i];
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int tfq::check_kv(const tf_kv *kv) {
+    if (!kv) return fail_message(TF_EINVAL_PTR, "NULL cache");
+    if (!kv->k || !kv->v || !kv->k_scale || !kv->v_scale) return fail_message(TF_EINVAL_PTR, "NULL cache pointer");
+    if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4))
+        return fail_message(TF_EINVAL_PTR, "k and v must be 16-byte aligned, scales 4-byte aligned");
+    if (kv->block != 16 && kv->block != 32 && kv->block != 64 && kv->block != 128)
+        return fail_message(TF_EINVAL_SIZE, "block must be 16, 32, 64 or 128");
+    if (kv->dim != 64 && kv->dim != 128 && kv->dim != 256)
+        return fail_message(TF_EINVAL_SIZE, "dim must be 64, 128 or 256");
+    if (kv->kv_heads < 1 || kv->kv_heads > 1024) return fail_message(TF_EINVAL_SIZE, "kv_heads must be in [1, 1024]");
+    if (kv->n_blocks < 1) return fail_message(TF_EINVAL_SIZE, "n_blocks must be at least 1");
+    return TF_OK;
+}
+
+int tfq::check_batch(const tf_kv *kv, const tf_kv_batch *b) {
+    if (!b) return fail_message(TF_EINVAL_PTR, "NULL batch");
+    if (!b->kv_len || !b->table) return fail_message(TF_EINVAL_PTR, "NULL kv_len or table");
+    if (!aligned(b->kv_len, 4) || !aligned(b->table, 4) || !aligned(b->row_start, 4) || !aligned(b->slots, 4))
+        return fail_message(TF_EINVAL_PTR, "kv_len, table, row_start and slots must be 4-byte aligned");
+    if (b->n_seqs < 1 || b->n_seqs > 65536) return fail_message(TF_EINVAL_SIZE, "n_seqs must be in [1, 65536]");
+    if (b->rows < 1 || b->max_rows < 1 || b->max_rows > b->rows)
+        return fail_message(TF_EINVAL_ROWS, "rows must be at least 1, and max_rows in [1, rows]");
+    if (!b->row_start && (long long)b->n_seqs * b->max_rows != b->rows)
+        return fail_message(TF_EINVAL_ROWS, "without row_start, rows must be n_seqs * max_rows");
+    if (b->max_len < 1 || b->max_len > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "max_len must be in [1, 2^30]");
+    if (b->table_stride < (b->max_len + kv->block - 1) / kv->block)
+        return fail_message(TF_EINVAL_STRIDE, "table_stride holds fewer pages than max_len needs");
+    return TF_OK;
+}
+
+extern "C" int tf_kv_append(const tf_kv *kv, const tf_kv_batch *batch, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, void *stream) {
+    fail_message(TF_OK, "");
+    int rc = check_kv(kv);
+    if (!rc) rc = check_batch(kv, batch);
+    if (rc) return rc;
+    if (kv->f32 != 0 && kv->f32 != 1) return fail_message(TF_EINVAL_FLAGS, "f32 must be 0 or 1");
+    if (!kv->open_k || !kv->open_v || !kv->open_max || !aligned(kv->open_k, 16) || !aligned(kv->open_v, 16) ||
+        !aligned(kv->open_max, 4))
+        return fail_message(TF_EINVAL_PTR, "open_k and open_v must be 16-byte aligned, open_max 4-byte aligned");
+    if (kv->n_slots < 1) return fail_message(TF_EINVAL_SIZE, "n_slots must be at least 1");
+    if (!batch->slots && batch->n_seqs > kv->n_slots)
+        return fail_message(TF_EINVAL_SIZE, "without slots, n_seqs must not exceed n_slots");
+    const int es = kv->f32 ? 4 : 2;
+    if (!k || !v || !aligned(k, es) || !aligned(v, es))
+        return fail_message(TF_EINVAL_PTR, "NULL k or v, or not aligned to their type");
+    const int width = kv->kv_heads * kv->dim;
+    if (k_stride < width || v_stride < width)
+        return fail_message(TF_EINVAL_STRIDE, "k_stride or v_stride below kv_heads * dim");
+    int nsm = 0, *status = nullptr;
+    rc = device_info(&nsm, &status);
+    if (rc) return rc;
+    AppendParams P{*kv, *batch, {k, v}, {k_stride, v_stride}, (batch->max_rows + kv->block - 2) / kv->block + 1, status};
+    const long long grid = 2LL * kv->kv_heads * P.nb * batch->n_seqs;
+    if (grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many pages in one call");
+    const int threads = kv->block * kv->dim / (8 * VPT);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (kv->f32)
+        kv_append_kernel<float><<<(unsigned)grid, threads, 0, st>>>(P);
+    else
+        kv_append_kernel<__nv_bfloat16><<<(unsigned)grid, threads, 0, st>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_append launch");
+}
+
+extern "C" int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k_stride, void *v_out,
+                          int64_t v_stride, int flags, void *stream) {
+    fail_message(TF_OK, "");
+    if (flags & ~TF_OUT_BF16) return fail_message(TF_EINVAL_FLAGS, "tf_kv_read takes TF_OUT_BF16 only");
+    int rc = check_kv(kv);
+    if (!rc) rc = check_batch(kv, batch);
+    if (rc) return rc;
+    const int es = flags & TF_OUT_BF16 ? 2 : 4;
+    if ((!k_out && !v_out) || !aligned(k_out, es) || !aligned(v_out, es))
+        return fail_message(TF_EINVAL_PTR, "no output, or an output not aligned to its type");
+    const int width = kv->kv_heads * kv->dim;
+    if ((k_out && k_stride < width) || (v_out && v_stride < width))
+        return fail_message(TF_EINVAL_STRIDE, "k_stride or v_stride below kv_heads * dim");
+    int nsm = 0, *status = nullptr;
+    rc = device_info(&nsm, &status);
+    if (rc) return rc;
+    ReadParams P{*kv, *batch, {k_out, v_out}, {k_stride, v_stride}, (batch->max_rows + READ_TOKENS - 1) / READ_TOKENS, status};
+    const long long grid = 2LL * P.tiles * batch->n_seqs;
+    if (grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (flags & TF_OUT_BF16)
+        kv_read_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(P);
+    else
+        kv_read_kernel<float><<<(unsigned)grid, 256, 0, st>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_read launch");
+}
