@@ -61,7 +61,7 @@ typedef struct tf_kv_batch {
     int n_seqs;
     int rows;                 /* rows of the row matrices (no row index reaches it) */
     int max_rows;             /* at least every sequence's number of rows */
-    int max_len;              /* at least every kv_len; at most table_stride * block */
+    int max_len;              /* at least every kv_len; at most table_stride * block, and 2^20 */
     const int32_t *row_start; /* [n_seqs + 1], or NULL: max_rows rows each (rows = n_seqs * max_rows) */
     const int32_t *kv_len;    /* [n_seqs] */
     const int32_t *table;     /* [n_seqs][table_stride]: page of each `block` tokens */

@@ -686,6 +686,21 @@ int tfq::tensor_map_2d(CUtensorMap *m, const void *base, int elem_bytes, long lo
     return encode_2d(m, base, t, elem_bytes, cols, rows, box_cols, box_rows);
 }
 
+int tfq::tensor_map_rows128(CUtensorMap *m, const void *base, long long rows, int box_rows) {
+    const int rc = get_encoder();
+    if (rc) return rc;
+    cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode.load(std::memory_order_acquire)(
+        m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(TF_ECUDA, "cuTensorMapEncodeTiled(rows) failed (" + std::to_string((int)r) + ")");
+    return TF_OK;
+}
+
 int tfq::tensor_map_3d(CUtensorMap *m, const void *base, int elem_bytes, long long d0, long long d1, long long d2,
                        long long s1, long long s2, int b0, int b1, int b2) {
     const int rc = get_encoder();

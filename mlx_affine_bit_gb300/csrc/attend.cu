@@ -62,7 +62,19 @@ int workspace(cudaStream_t st, size_t floats, size_t counters, Ws *out) {
 
 template <int D, int NT>
 cudaError_t launch_rows(const attend::Params &P, unsigned grid, cudaStream_t st) {
-    attend::rows_kernel<D, NT><<<grid, attend::THREADS, 0, st>>>(P);
+    auto k = attend::rows_kernel<D, NT>;
+    constexpr int smem = attend::smem_bytes(D, NT);
+    static unsigned attr_set = 0;   // one bit per device: shared-memory limit raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned bit = 1u << (dev & 31);
+    if (!(__atomic_load_n(&attr_set, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
+    }
+    k<<<grid, attend::THREADS, smem, st>>>(P);
     return cudaGetLastError();
 }
 
@@ -92,7 +104,13 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     rc = device_info(&nsm, &status);
     if (rc) return rc;
 
+    const long long pool_rows = (long long)kv->n_blocks * kv->kv_heads * kv->block * kv->dim / 128;
+    if (pool_rows > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "a pool of more than 2^38 bytes");
     attend::Params P{};
+    const int box_rows = std::min(kv->block, 32) * kv->dim / 128;
+    rc = tensor_map_rows128(&P.tm_k, kv->k, pool_rows, box_rows);
+    if (!rc) rc = tensor_map_rows128(&P.tm_v, kv->v, pool_rows, box_rows);
+    if (rc) return rc;
     P.kv = *kv;
     P.b = *batch;
     P.q = q;
@@ -103,6 +121,7 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     P.group = heads / kv->kv_heads;
     P.scale = scale;
     P.window = window;
+    P.block_log2 = __builtin_ctz(kv->block);
     P.causal = (flags & TF_KV_CAUSAL) != 0;
     P.q_f32 = (flags & TF_IN_F32) != 0;
     const long long max_group_rows = (long long)batch->max_rows * P.group;
@@ -114,11 +133,16 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     // least 128 tokens, enough of them for four CTAs an SM.
     long long span = batch->max_len;
     if (window > 0) span = std::min(span, (long long)window + batch->max_rows + attend::STEP);
-    long long want = std::max(1LL, (4LL * nsm + items - 1) / items);
-    long long piece = std::max(128LL, (span + want - 1) / want);
+#ifndef WAVES
+#define WAVES 4
+#define MINP 128LL
+#endif
+    long long want = std::max(1LL, ((long long)WAVES * nsm + items - 1) / items);
+    want = std::min<long long>(want, attend::MAX_PIECES);
+    long long piece = std::max(MINP, (span + want - 1) / want);
     piece = std::min<long long>((piece + attend::STEP - 1) / attend::STEP * attend::STEP, attend::MAX_PIECE);
     P.piece = (int)piece;
-    P.nsplit = (int)((span + piece - 1) / piece) + (window > 0 ? 1 : 0);
+    P.nsplit = (int)((span + piece - 1) / piece);
     P.tiles = (int)tiles;
     const long long grid = items * P.nsplit;
     if (tiles > 0x7FFFFFFF || grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");

@@ -4,6 +4,7 @@
 // For the rows r of one (sequence, key/value head) -- G query heads a token --
 // and the tokens j they see:
 //     s_rj = (q_r . c_j) * (scale log2(e) ks_page / f_r)      q_r: fp16, times the power of two f_r
+//     (q_r . c_j = sum_d q_rd (c_jd + 128) - 128 sum_d q_rd: bytes are fp16 subnormals as they stand)
 //     p_rj = 2^(s_rj - m_r),  l_r = sum_j p_rj,  out_r = sum_j p_rj vs_page c'_j / l_r
 // with the running maximum m_r of a warp's tokens.  Codes are exact in fp16.  What
 // enters the second product is w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16, with
@@ -12,13 +13,18 @@
 // and comes to nothing below 2^-40.
 //
 // Bound by reading the cache.  A CTA takes up to 8 * NT rows and one piece of the
-// tokens; a warp takes 16 tokens at a time straight from global memory into the
-// fragments of mma.sync m16n8k16: a lane's 16 bytes of a key are four k steps of
-// a B fragment (the rows of q are loaded in the same order), and 16 bytes of the
-// values of four tokens are eight A fragments of the transposed values, whose
-// token pairs are put together by the byte permutes that widen the codes anyway.
-// The maxima, sums and outputs of the warps are joined in shared memory, those of
-// the pieces by the last CTA to arrive, in piece order.
+// tokens, a warp 16 tokens at a time, in the fragments of mma.sync m16n8k16: a
+// lane's 16 bytes of a key are four k steps of a B fragment (the rows of q are
+// loaded in the same order), and 16 bytes of the values of four tokens are eight
+// A fragments of the transposed values, whose token pairs are put together by the
+// byte permutes that widen the codes anyway.  Each warp has a ring of its own in
+// shared memory, which its first lane fills by TMA a pair of tiles at a time, and
+// no barrier with the other warps.  The pool is seen as rows of 128 bytes (two
+// tokens of 64, half a token of 256) that the copies swizzle (16-byte chunk c of
+// row r at c ^ (r & 7)); with the order of a tile's tokens chosen for it (order()
+// below) the fragments' reads meet no bank conflicts.  The maxima, sums and outputs
+// of the warps are joined in shared memory, those of the pieces by the last CTA to
+// arrive, in piece order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,17 +32,20 @@
 #include <stdint.h>
 
 #include "kv.h"
+#include "qmm_kernel.cuh"
 
 namespace tfq {
 namespace attend {
 
 constexpr int WARPS = 4, THREADS = WARPS * 32;
-constexpr int STEP = 16 * WARPS;         // tokens a CTA takes at a time
+constexpr int STEP = 32 * WARPS;         // tokens a CTA takes at a time, two tiles of 16 a warp
 constexpr int MAX_PIECE = 4096;          // tokens of one piece
 constexpr int MAX_PAGES = MAX_PIECE / 16 + 1;
+constexpr int MAX_PIECES = 256;          // pieces of one sequence, at most (max_len is at most their product)
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
 
 struct Params {
+    CUtensorMap tm_k, tm_v;  // the pools as rows of 128 bytes; a box is a pair of tiles, or one of 16-token pages
     tf_kv kv;
     tf_kv_batch b;
     const void *q;
@@ -47,6 +56,7 @@ struct Params {
     int *status;
     float scale;
     int group, window, causal, q_f32;
+    int block_log2;         // of kv.block
     int tiles, piece, nsplit;
 };
 
@@ -61,6 +71,9 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t w, uint32_t sel) {
     const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// The same as fp16 subnormals, (128 + c) 2^-24: the keys' offset comes off in the accumulators' start.
+__device__ __forceinline__ uint32_t lo2_tiny(uint32_t w) { return prmt(w, 0u, 0x4140u); }
+__device__ __forceinline__ uint32_t hi2_tiny(uint32_t w) { return prmt(w, 0u, 0x4342u); }
 __device__ __forceinline__ uint32_t lo2(uint32_t w) { return half2_of(w, 0x4140u); }
 __device__ __forceinline__ uint32_t hi2(uint32_t w) { return half2_of(w, 0x4342u); }
 
@@ -94,6 +107,34 @@ __device__ __forceinline__ float out_factor(const RowSum &a) {
     return a.l == 0.f ? 0.f : exp2f(a.n - a.m - W_EXP) / a.l;
 }
 
+#ifndef NSTAGES
+#define NSTAGES 2
+#endif
+// Pairs of tiles in a warp's ring and CTAs an SM, by the registers that outputs and q take.
+TFQ_HD constexpr int stages(int d) { return NSTAGES; }
+TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? 6 : 5) : d == 128 ? (nt == 1 ? 4 : 3) : 2; }
+TFQ_HD constexpr int tile_bytes(int d) { return 32 * d; }          // 16 tokens of keys and of values
+TFQ_HD constexpr int out_pitch(int d) { return d + 4; }            // floats between joined rows
+// Shared memory: the rings; after the tokens are done, every warp's outputs, then the parts' factors.
+TFQ_HD constexpr int smem_bytes(int d, int nt) {
+    const int ring = WARPS * stages(d) * 2 * tile_bytes(d), outs = WARPS * 8 * nt * out_pitch(d) * 4;
+    const int join = (MAX_PIECES + 1) * 8 * nt * 4, most = outs > join ? outs : join;
+    return ring > most ? ring : most;
+}
+
+// Token of a tile (in eights) that column n of the scores stands for.  A quarter
+// of a warp reads 16 bytes a lane of the keys of tokens order(2 a), order(2 a + 1),
+// and of the values of the four tokens order(2 a) (or the four order(2 a + 1)).
+template <int D>
+__device__ __forceinline__ int order(int n) {
+    const int a = n >> 1;
+    if (D == 64) return (a + (a & 2)) ^ (n & 1 ? 3 : 0);
+    if (D == 128) return n ^ (n & 1 ? 4 : 0);
+    return n & 1 ? (a ^ 2) + 4 : a;
+}
+// Offset of a byte of a tile under the copies' swizzle.
+__device__ __forceinline__ int swizzled(int byte) { return byte ^ ((byte >> 3) & 0x70); }
+
 // The rows and tokens of one CTA.
 struct Work {
     int s, h, tile, split;       // sequence, key/value head, tile of rows, piece
@@ -110,19 +151,24 @@ __device__ __forceinline__ float row_factor(float amax) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
+__global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid_constant__ Params P) {
     constexpr int R = 8 * NT;                    // rows of a tile
     constexpr int KV = D / 64;                   // 16-byte vectors of a key a lane (a quad covers 64 bytes)
     constexpr int MT = D / 16;                   // m tiles of the transposed values
-    __shared__ __align__(16) __half sq[R][D];
-    __shared__ float s_row[R];
+    constexpr int VB = D >= 128 ? 16 : 8;        // bytes that a lane takes of a token's values at once
+    constexpr int NV = D / (8 * VB);             // ... and how often
+    constexpr int NST = stages(D);
+    extern __shared__ __align__(1024) uint8_t ring[];
+    __shared__ uint64_t bars[WARPS][NST];
+    __shared__ int s_abort;
+    __shared__ __align__(16) __half sq[R][D + 8];
+    __shared__ float2 s_row[R];
     __shared__ RowSum s_sum[WARPS][R];
     __shared__ float s_ks[MAX_PAGES], s_vs[MAX_PAGES];
     __shared__ int s_page[MAX_PAGES];
-    __shared__ __align__(16) float so[R][D + 4];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane >> 2, lc = lane & 3;
-    const int H = P.kv.kv_heads, B = P.kv.block, G = P.group;
+    const int H = P.kv.kv_heads, G = P.group, BL = P.block_log2, BM = P.kv.block - 1;
 
     Work w;
     unsigned id = blockIdx.x;
@@ -154,7 +200,7 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
         w.to = min(w.end, w.end - w.n + i1 + 1);
         if (P.window) w.from = max(0, w.end - w.n + i0 - P.window + 1);
     }
-    const int base = w.from / 16 * 16;
+    const int base = w.from & ~31;
     w.pieces = w.to > w.from ? (w.to - base + P.piece - 1) / P.piece : 0;
     uint16_t *out = P.out + (long long)w.row0 * P.out_stride;
     auto out_at = [&](int r) {                  // first value of the tile's row r
@@ -169,8 +215,14 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
     if (w.split >= w.pieces) return;
     const int t0 = base + w.split * P.piece, t1 = min(t0 + P.piece, w.to);   // tokens of the piece
 
-    // Pages and scales of the piece (of the values' the logarithm).
-    const int pg0 = t0 / B, npages = (t1 - 1) / B - pg0 + 1;
+    if (tid == 0) {
+        for (int i = 0; i < WARPS * NST; ++i) mbar_init(&bars[0][i], 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // Pages of the piece.
+    const int pg0 = t0 >> BL, npages = ((t1 - 1) >> BL) - pg0 + 1;
     for (int i = tid; i < npages; i += THREADS) {
         int page = P.b.table[w.s * P.b.table_stride + pg0 + i];
         if (page < 0 || page >= P.kv.n_blocks) {
@@ -178,46 +230,90 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
             page = -1;
         }
         s_page[i] = page;
-        const long long ph = (long long)page * H + w.h;
-        s_ks[i] = page < 0 ? 0.f : P.kv.k_scale[ph];
-        s_vs[i] = page < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
     }
-    // The rows of q in fp16, times a power of two each.
-    for (int r = warp; r < R; r += WARPS) {
-        float x[D / 32], m = 0.f;
-        const int gr = w.r0 + r, i = gr / G;
-        const long long at = (long long)(w.row0 + i) * P.q_stride + ((long long)w.h * G + gr - i * G) * D;
+    // (The rows of q are on their way meanwhile.)
+    float qx[R / WARPS][D / 32];
+#pragma unroll
+    for (int k = 0; k < R / WARPS; ++k) {
+        const int r = warp + k * WARPS, gr = w.r0 + r, i = gr / G;
+        const long long at = (long long)(w.row0 + i) * P.q_stride + ((long long)w.h * G + gr - i * G) * D + lane;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
-            x[e] = 0.f;
+            qx[k][e] = 0.f;
             if (r < w.rows)
-                x[e] = P.q_f32 ? static_cast<const float *>(P.q)[at + e * 32 + lane]
-                               : __uint_as_float((uint32_t) static_cast<const uint16_t *>(P.q)[at + e * 32 + lane] << 16);
-            m = fmaxf(m, fabsf(x[e]));
+                qx[k][e] = P.q_f32 ? static_cast<const float *>(P.q)[at + e * 32]
+                                   : __uint_as_float((uint32_t) static_cast<const uint16_t *>(P.q)[at + e * 32] << 16);
         }
+    }
+    __syncthreads();
+    // A warp's ring: stages of a pair of tiles' keys, then their values.
+    constexpr int STAGE = 2 * tile_bytes(D);
+    uint8_t *mine = ring + warp * NST * STAGE;
+    uint64_t *bar = bars[warp];
+    volatile int *abort = &s_abort;
+    const bool single = BL == 4;                 // pages of one tile
+    auto fetch = [&](int t, int stage) {         // (the warp's first lane)
+        if (t >= t1) return;
+        const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < t1 ? s_page[(t >> BL) + 1 - pg0] : -1;
+        mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : 2) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
+        uint8_t *dst = mine + stage * STAGE;
+        auto copy = [&](int page, int at, uint8_t *to) {
+            const int row = (int)((((((long long)page * H + w.h) << BL) + (at & BM)) * D) >> 7);
+            tma_2d(to, &P.tm_k, 0, row, &bar[stage]);
+            tma_2d(to + STAGE / 2, &P.tm_v, 0, row, &bar[stage]);
+        };
+        if (p0 >= 0) copy(p0, t, dst);
+        if (p1 >= 0) copy(p1, t + 16, dst + 16 * D);
+    };
+    int ft = t0 + 32 * warp;                     // next pair to fetch
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i, ft += STEP)
+        if (lane == 0) fetch(ft, i);
+
+    // Scales of the pages (of the values' the logarithm), and the rows of q in fp16, times a power of two each.
+    for (int i = tid; i < npages; i += THREADS) {
+        const long long ph = (long long)s_page[i] * H + w.h;
+        s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
+        s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
+    }
+#pragma unroll
+    for (int k = 0; k < R / WARPS; ++k) {
+        const int r = warp + k * WARPS;
+        float m = 0.f, sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) m = fmaxf(m, fabsf(qx[k][e]));
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         const float f = row_factor(m);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) sq[r][e * 32 + lane] = __float2half_rn(x[e] * f);
-        if (lane == 0) s_row[r] = P.scale * 1.44269504088896340736f / f;
+        for (int e = 0; e < D / 32; ++e) {
+            const __half h = __float2half_rn(qx[k][e] * f);
+            sq[r][e * 32 + lane] = h;
+            sum += __half2float(h);
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) s_row[r] = make_float2(P.scale * 1.44269504088896340736f / f * 16777216.f, sum * (-128.f / 16777216.f));
     }
     __syncthreads();
 
-    // A fragments of q: k step (v, i) holds d = 64 v + 16 lc + 4 i + {0, 1 | 2, 3}.
-    uint2 qa[NT][KV][4];
+    // A fragments of q: k step (v, i) holds d = 64 v + 16 lc + 4 i + {0, 1 | 2, 3}.  (dim 256: read again for every tile.)
+    constexpr bool Q_REGS = D < 256;
+    uint2 qa[NT][Q_REGS ? KV : 1][4];
+    auto q_at = [&](int u, int v, int i) { return *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]); };
+    if constexpr (Q_REGS) {
 #pragma unroll
-    for (int u = 0; u < NT; ++u)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int v = 0; v < KV; ++v)
+            for (int v = 0; v < KV; ++v)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                qa[u][v][i] = *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]);
-    float rowf[NT];
+                for (int i = 0; i < 4; ++i) qa[u][v][i] = q_at(u, v, i);
+    }
+    float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24
     int see_from[NT], see_to[NT];                // tokens that rows lr (+ 8) see
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
         const int r = min(lr + 8 * u, w.rows - 1);   // (rows past the tile's end are computed, never stored)
-        rowf[u] = s_row[r];
+        rowf[u] = s_row[r].x;
+        off[u] = s_row[r].y;
         const int pos = w.end - w.n + (w.r0 + r) / G;
         see_to[u] = P.causal ? min(w.end, pos + 1) : w.end;
         see_from[u] = P.window ? pos - P.window + 1 : 0;
@@ -239,53 +335,82 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[p][u][e] = 0.f;
     }
-    for (int t = t0 + 16 * warp; t < t1; t += STEP) {
-        const int pi = t / B - pg0, page = s_page[pi];
-        if (page < 0) continue;
-        const long long at = (((long long)page * H + w.h) * B + t % B) * D;
-        const int8_t *kp = P.kv.k + at, *vp = P.kv.v + at;
-        // Scores of 16 tokens: two n tiles of 8.
-        float sc[2][4];
+    // Offsets of this lane's reads in a stage: keys of token order(lr) (+ 8, + 16, + 24), values of four tokens of a tile.
+    int k_at[KV][2], v_at[NV][4];
+    const int tok[2] = {order<D>(2 * lc), order<D>(2 * lc + 1)};
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+    for (int v = 0; v < KV; ++v)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nb][e] = 0.f;
+        for (int nb = 0; nb < 2; ++nb) k_at[v][nb] = swizzled((order<D>(lr) + 8 * nb) * D + 64 * v + 16 * lc);
 #pragma unroll
-            for (int v = 0; v < KV; ++v) {
-                const uint4 kk = *reinterpret_cast<const uint4 *>(kp + (8 * nb + lr) * D + 64 * v + 16 * lc);
-                const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x = kw[i] ^ 0x80808080u;
-                    mma_f16(sc[nb], qa[0][v][i].x, NT > 1 ? qa[NT - 1][v][i].x : 0u, qa[0][v][i].y,
-                            NT > 1 ? qa[NT - 1][v][i].y : 0u, lo2(x), hi2(x));
-                }
+        for (int k = 0; k < 4; ++k) v_at[v][k] = swizzled((tok[k & 1] + 8 * (k >> 1)) * D + v * 8 * VB + VB * lr) + STAGE / 2;
+    uint32_t it = 0;                             // pairs taken
+    for (int t = t0 + 32 * warp; t < t1; t += STEP, ++it) {
+        if (lane == 0) fetch(ft, (it + NST - 1) % NST);
+        ft += STEP;
+        mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
+        const uint8_t *tiles = mine + (it % NST) * STAGE;
+        // Tiles t and t + 16: their pages (a tile of no page is not seen).
+        const int pi[2] = {(t >> BL) - pg0, min(((t + 16) >> BL) - pg0, npages - 1)};
+        const bool on[2] = {s_page[pi[0]] >= 0, s_page[pi[1]] >= 0 && !(single && t + 16 >= t1)};
+        // Scores of 32 tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
+        float sc[4][4];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
+#pragma unroll
+        for (int v = 0; v < KV; ++v) {
+            uint32_t kw[4][4];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
+                kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
+                kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
+                uint2 qa1 = make_uint2(0u, 0u);
+                if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
             }
         }
-        // Rows lr and lr + 8: tokens t + 8 nb + 2 lc + {0, 1} in sc[nb][2 u + {0, 1}].
-        const bool full = t >= all_from && t + 16 <= all_to;
-        const float ks = s_ks[pi], vs = s_vs[pi];
-        uint32_t pb[NT][2];
+        // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
+        const bool full = t >= all_from && t + 32 <= all_to && on[0] && on[1];
+        const float ks[2] = {s_ks[pi[0]], s_ks[pi[1]]}, vs[2] = {s_vs[pi[0]], s_vs[pi[1]]};
+        uint32_t pb[NT][4];
         bool grew = false;
         float mt[NT], nt[NT];
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const float f = rowf[u] * ks;
-            float top = -INFINITY;
+            float top[2];
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
+            for (int h = 0; h < 2; ++h) {
+                const float f = rowf[u] * ks[h];
+                top[h] = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float &x = sc[nb][2 * u + e];
-                    x *= f;
-                    const int j = t + 8 * nb + 2 * lc + e;
-                    if (!full && !(j >= see_from[u] && j < see_to[u])) x = -INFINITY;
-                    top = fmaxf(top, x);
-                }
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            mt[u] = fmaxf(m[u], top);
-            nt[u] = fmaxf(n[u], top + vs);
+                for (int nb = 2 * h; nb < 2 * h + 2; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = sc[nb][2 * u + e];
+                        x *= f;
+                        const int j = t + 8 * nb + tok[e];
+                        if (!full && !(on[h] && j >= see_from[u] && j < see_to[u])) x = -INFINITY;
+                        top[h] = fmaxf(top[h], x);
+                    }
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const float a = __shfl_xor_sync(~0u, top[0], o), b = __shfl_xor_sync(~0u, top[1], o);
+                top[0] = fmaxf(top[0], a);
+                top[1] = fmaxf(top[1], b);
+            }
+            mt[u] = fmaxf(m[u], fmaxf(top[0], top[1]));
+            nt[u] = fmaxf(n[u], fmaxf(top[0] + vs[0], top[1] + vs[1]));
             grew |= mt[u] > m[u] || nt[u] > n[u];
         }
         if (__any_sync(~0u, grew)) {
@@ -309,55 +434,79 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             const float mm = m[u] == -INFINITY ? 0.f : m[u];
-            const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs - n[u] + W_EXP, 115.f));
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-                const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
-                l[u] += p0 + p1;
-                pb[u][nb] = pack_half(p0 * f, p1 * f);
-            }
-        }
-        // Transposed values: tokens 2 lc, 2 lc + 1 (+ 8) of d = 16 lr + .. (D = 64: 8 lr + ..).
-        constexpr int VB = D >= 128 ? 16 : 8;        // bytes a lane takes of a token at once
+            for (int h = 0; h < 2; ++h) {
+                const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs[h] - n[u] + W_EXP, 115.f));
 #pragma unroll
-        for (int v = 0; v < D / (8 * VB); ++v) {
-            uint32_t a[4][VB / 4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int8_t *src = vp + (2 * lc + (k & 1) + 8 * (k >> 1)) * D + v * 8 * VB + VB * lr;
-                if constexpr (VB == 16) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                    a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                    a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                    a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < VB / 4; ++i) {
-                // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
-                const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
-                const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
-                const int p = v * VB / 2 + 2 * i;
-                const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
-                const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
-#pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    mma_f16(o[p][u], f0, f1, f2, f3, pb[u][0], pb[u][1]);
-                    mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][0], pb[u][1]);
+                for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
+                    const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
+                    l[u] += p0 + p1;
+                    pb[u][nb] = pack_half(p0 * f, p1 * f);
                 }
             }
         }
+        // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 16 lr + .. (dim 64: 8 lr + ..).
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!on[h]) continue;                // (its codes were not fetched)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                uint32_t a[4][VB / 4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
+                    if constexpr (VB == 16) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                        a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                        a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                        a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < VB / 4; ++i) {
+                    // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
+                    const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
+                    const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
+                    const int p = v * VB / 2 + 2 * i;
+                    const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
+                    const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
+                        mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();                            // (every lane has read the stage that is filled next)
+    }
+    if (*abort && lane == 0) {
+        // A wait ran out: no copy may be in flight when the ring is used again.
+        for (uint32_t j = it > NST ? it - NST : 0; j < it; ++j) mbar_wait(&bar[j % NST], (j / NST) & 1, abort, P.status, false);
     }
 
-    // Join the warps: row sums, then the outputs in warp order.
+    // Join the warps: row sums, and the outputs (in the rings' place) in warp order.
+    auto out_of = [&](int wi, int r) { return reinterpret_cast<float *>(ring) + (wi * R + r) * out_pitch(D); };
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
         l[u] += __shfl_xor_sync(~0u, l[u], 1);
         l[u] += __shfl_xor_sync(~0u, l[u], 2);
         if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], n[u], l[u]};
     }
+    __syncthreads();                             // (every ring has been read)
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float *dst = out_of(warp, 2 * lc + e + 8 * u);
+#pragma unroll
+            for (int p = 0; p < MT; ++p) {
+                const int d = p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2));
+                *reinterpret_cast<float2 *>(dst + d) = make_float2(o[p][u][e], o[p][u][2 + e]);
+            }
+        }
     __syncthreads();
     auto joined = [&](int r) {
         RowSum a = s_sum[0][r];
@@ -366,43 +515,37 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
         for (int k = 0; k < WARPS; ++k) a.l += s_sum[k][r].l * l_factor(s_sum[k][r], a.m);
         return a;
     };
-    constexpr int VB = D >= 128 ? 16 : 8;
-    for (int wi = 0; wi < WARPS; ++wi) {
-        if (warp == wi) {
-#pragma unroll
-            for (int u = 0; u < NT; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 2 * lc + e + 8 * u;
-                    const float a = o_factor(s_sum[wi][r], joined(r).n);
-#pragma unroll
-                    for (int p = 0; p < MT; ++p) {
-                        const int d = p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2));
-                        float *dst = &so[r][d];
-                        if (wi == 0) {
-                            dst[0] = o[p][u][e] * a;
-                            dst[1] = o[p][u][2 + e] * a;
-                        } else {
-                            dst[0] += o[p][u][e] * a;
-                            dst[1] += o[p][u][2 + e] * a;
-                        }
-                    }
-                }
+    auto joined4 = [&](int r, int d, const RowSum &a) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < WARPS; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(out_of(k, r) + d);
+            const float f = o_factor(s_sum[k][r], a.n);
+            y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
         }
-        __syncthreads();
-    }
-    auto store = [&](int r, int d, float x) {
-        out_at(r)[d] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        return y;
+    };
+    // Four values of an output row (aligned to 2 bytes only).
+    auto store4 = [&](int r, int d, float4 x, float f) {
+        uint16_t *dst = out_at(r) + d;
+        dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x.x * f));
+        dst[1] = __bfloat16_as_ushort(__float2bfloat16_rn(x.y * f));
+        dst[2] = __bfloat16_as_ushort(__float2bfloat16_rn(x.z * f));
+        dst[3] = __bfloat16_as_ushort(__float2bfloat16_rn(x.w * f));
     };
     if (w.pieces == 1) {
-        for (int v = tid; v < w.rows * D; v += THREADS) store(v / D, v % D, so[v / D][v % D] * out_factor(joined(v / D)));
+        for (int v = 4 * tid; v < w.rows * D; v += 4 * THREADS)
+        {
+            const RowSum a = joined(v / D);
+            store4(v / D, v % D, joined4(v / D, v % D, a), out_factor(a));
+        }
         return;
     }
     // A part: its outputs and row sums.
     const long long first = (long long)item * P.nsplit;
     RowSum *sums = reinterpret_cast<RowSum *>(P.part + (long long)gridDim.x * R * D) + first * R;
     float *part = P.part + first * R * D;
-    for (int v = tid; v < w.rows * D; v += THREADS) part[w.split * R * D + v] = so[v / D][v % D];
+    for (int v = 4 * tid; v < w.rows * D; v += 4 * THREADS)
+        *reinterpret_cast<float4 *>(part + w.split * R * D + v) = joined4(v / D, v % D, joined(v / D));
     if (tid < w.rows) sums[w.split * R + tid] = joined(tid);
     __threadfence();
     __syncthreads();
@@ -411,25 +554,47 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params P) {
     if (!s_last) return;
     __threadfence();
     if (tid == 0) P.count[item] = 0;
-    auto sum_of = [&](int k, int r) {
-        const float *x = &sums[k * R + r].m;
-        return RowSum{__ldcg(x), __ldcg(x + 1), __ldcg(x + 2)};
-    };
-    for (int v = tid; v < w.rows * D; v += THREADS) {
+    // The parts' factors, a warp a row; then the outputs in piece order.
+    float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (this CTA's outputs have been read: a barrier lies between)
+    for (int r = warp; r < w.rows; r += WARPS) {
+        RowSum x[MAX_PIECES / 32], a{-INFINITY, -INFINITY, 0.f};
+#pragma unroll
+        for (int i = 0; i < MAX_PIECES / 32; ++i) {
+            const int k = 32 * i + lane;
+            x[i] = RowSum{-INFINITY, -INFINITY, 0.f};
+            if (k < w.pieces) {
+                const float *src = &sums[k * R + r].m;
+                x[i] = RowSum{__ldcg(src), __ldcg(src + 1), __ldcg(src + 2)};
+            }
+            a.m = fmaxf(a.m, x[i].m);
+            a.n = fmaxf(a.n, x[i].n);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            a.m = fmaxf(a.m, __shfl_xor_sync(~0u, a.m, o));
+            a.n = fmaxf(a.n, __shfl_xor_sync(~0u, a.n, o));
+        }
+#pragma unroll
+        for (int i = 0; i < MAX_PIECES / 32; ++i) {
+            a.l += x[i].l * l_factor(x[i], a.m);
+            if (32 * i + lane < w.pieces) s_fac[32 * i + lane][r] = o_factor(x[i], a.n);
+        }
+        for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
+        if (lane == 0) s_fac[MAX_PIECES][r] = out_factor(a);
+    }
+    __syncthreads();
+    for (int v = 4 * tid; v < w.rows * D; v += 4 * THREADS) {
         const int r = v / D;
-        RowSum a{-INFINITY, -INFINITY, 0.f};
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int k = 0; k < w.pieces; ++k) {
-            const RowSum x = sum_of(k, r);
-            a.m = fmaxf(a.m, x.m);
-            a.n = fmaxf(a.n, x.n);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + (long long)k * R * D + v));
+            const float f = s_fac[k][r];
+            acc.x = fmaf(x.x, f, acc.x);
+            acc.y = fmaf(x.y, f, acc.y);
+            acc.z = fmaf(x.z, f, acc.z);
+            acc.w = fmaf(x.w, f, acc.w);
         }
-        float acc = 0.f;
-        for (int k = 0; k < w.pieces; ++k) {
-            const RowSum x = sum_of(k, r);
-            a.l += x.l * l_factor(x, a.m);
-            acc += __ldcg(part + (long long)k * R * D + v) * o_factor(x, a.n);
-        }
-        store(r, v % D, acc * out_factor(a));
+        store4(r, v % D, acc, s_fac[MAX_PIECES][r]);
     }
 }
 

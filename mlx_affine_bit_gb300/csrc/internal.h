@@ -45,6 +45,9 @@ int tensor_map_2d(CUtensorMap *m, const void *base, int elem_bytes, long long co
                   int box_cols, int box_rows);
 int tensor_map_3d(CUtensorMap *m, const void *base, int elem_bytes, long long d0, long long d1, long long d2,
                   long long s1, long long s2, int b0, int b1, int b2);
+// Rows of 128 bytes one after another, copied box_rows at a time with the 128-byte
+// swizzle (16-byte chunk c of a box's row r at c ^ (r & 7)).
+int tensor_map_rows128(CUtensorMap *m, const void *base, long long rows, int box_rows);
 
 // SM count and device status word of the current device (allocated on first use).
 int device_info(int *nsm, int **status);

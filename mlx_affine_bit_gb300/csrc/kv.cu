@@ -285,7 +285,7 @@ int tfq::check_batch(const tf_kv *kv, const tf_kv_batch *b) {
         return fail_message(TF_EINVAL_ROWS, "rows must be at least 1, and max_rows in [1, rows]");
     if (!b->row_start && (long long)b->n_seqs * b->max_rows != b->rows)
         return fail_message(TF_EINVAL_ROWS, "without row_start, rows must be n_seqs * max_rows");
-    if (b->max_len < 1 || b->max_len > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "max_len must be in [1, 2^30]");
+    if (b->max_len < 1 || b->max_len > (1 << 20)) return fail_message(TF_EINVAL_SIZE, "max_len must be in [1, 2^20]");
     if (b->table_stride < (b->max_len + kv->block - 1) / kv->block)
         return fail_message(TF_EINVAL_STRIDE, "table_stride holds fewer pages than max_len needs");
     return TF_OK;
