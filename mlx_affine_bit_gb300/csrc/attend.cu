@@ -60,22 +60,43 @@ int workspace(cudaStream_t st, size_t floats, size_t counters, Ws *out) {
     return TF_OK;
 }
 
+// CTAs of a rows kernel that an SM holds at once (looked up once a device, with its shared-memory limit raised).
 template <int D, int NT>
-cudaError_t launch_rows(const attend::Params &P, unsigned grid, cudaStream_t st) {
-    auto k = attend::rows_kernel<D, NT>;
-    constexpr int smem = attend::smem_bytes(D, NT);
-    static unsigned attr_set = 0;   // one bit per device: shared-memory limit raised
+cudaError_t resident(int *out) {
+    static int n[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const unsigned bit = 1u << (dev & 31);
-    if (!(__atomic_load_n(&attr_set, __ATOMIC_ACQUIRE) & bit)) {
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int v = __atomic_load_n(&n[dev], __ATOMIC_ACQUIRE);
+    if (!v) {
+        auto k = attend::rows_kernel<D, NT>;
+        constexpr int smem = attend::smem_bytes(D, NT);
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, k, attend::THREADS, smem);
         if (e != cudaSuccess) return e;
-        __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
+        if (v < 1) return cudaErrorLaunchOutOfResources;
+        __atomic_store_n(&n[dev], v, __ATOMIC_RELEASE);
     }
-    k<<<grid, attend::THREADS, smem, st>>>(P);
-    return cudaGetLastError();
+    *out = v;
+    return cudaSuccess;
+}
+
+// The launch: as many CTAs as are resident at once, or one a step where there are fewer.
+template <int D, int NT>
+int launch_rows(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
+    int per_sm = 0;
+    cudaError_t e = resident<D, NT>(&per_sm);
+    if (e != cudaSuccess) return cuda_error(e, "kv_attend set-up");
+    const long long grid = std::min(steps, (long long)nsm * per_sm);
+    Ws w;
+    const int rc = workspace(st, (size_t)grid * 2 * 8 * NT * (D + 3), (size_t)grid, &w);
+    if (rc) return rc;
+    P.part = w.part;
+    P.count = w.count;
+    attend::rows_kernel<D, NT><<<(unsigned)grid, attend::THREADS, attend::smem_bytes(D, NT), st>>>(P);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_attend launch");
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -107,7 +128,7 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     const long long pool_rows = (long long)kv->n_blocks * kv->kv_heads * kv->block * kv->dim / 128;
     if (pool_rows > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "a pool of more than 2^38 bytes");
     attend::Params P{};
-    const int box_rows = std::min(kv->block, 32) * kv->dim / 128;
+    const int box_rows = std::min(kv->block, 16 * attend::tiles_of(kv->dim)) * kv->dim / 128;
     rc = tensor_map_rows128(&P.tm_k, kv->k, pool_rows, box_rows);
     if (!rc) rc = tensor_map_rows128(&P.tm_v, kv->v, pool_rows, box_rows);
     if (rc) return rc;
@@ -128,36 +149,15 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     if (max_group_rows > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "too many rows of one sequence");
     const int nt = max_group_rows <= 8 ? 1 : 2;
     const long long tiles = (max_group_rows + 8 * nt - 1) / (8 * nt);
-    const long long items = (long long)batch->n_seqs * kv->kv_heads * tiles;
-    // The tokens that a tile of rows may see, and their split: pieces of at
-    // least 128 tokens, enough of them for four CTAs an SM.
     long long span = batch->max_len;
-    if (window > 0) span = std::min(span, (long long)window + batch->max_rows + attend::STEP);
-#ifndef WAVES
-#define WAVES 4
-#define MINP 128LL
-#endif
-    long long want = std::max(1LL, ((long long)WAVES * nsm + items - 1) / items);
-    want = std::min<long long>(want, attend::MAX_PIECES);
-    long long piece = std::max(MINP, (span + want - 1) / want);
-    piece = std::min<long long>((piece + attend::STEP - 1) / attend::STEP * attend::STEP, attend::MAX_PIECE);
-    P.piece = (int)piece;
-    P.nsplit = (int)((span + piece - 1) / piece);
-    P.tiles = (int)tiles;
-    const long long grid = items * P.nsplit;
-    if (tiles > 0x7FFFFFFF || grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");
+    if (window > 0) span = std::min(span, (long long)window + batch->max_rows + 32);
+    const int step = attend::step_of(kv->dim);
+    const long long most = std::max(1LL, (1LL << 40) / (batch->n_seqs * (long long)kv->kv_heads));
+    const long long steps = batch->n_seqs * (long long)kv->kv_heads * std::min(most, tiles * ((span + step - 1) / step));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (P.nsplit > 1) {
-        Ws w;
-        rc = workspace(st, (size_t)grid * 8 * nt * (kv->dim + 3), (size_t)items, &w);
-        if (rc) return rc;
-        P.part = w.part;
-        P.count = w.count;
+    switch (kv->dim) {
+        case 64: return nt == 1 ? launch_rows<64, 1>(P, steps, nsm, st) : launch_rows<64, 2>(P, steps, nsm, st);
+        case 128: return nt == 1 ? launch_rows<128, 1>(P, steps, nsm, st) : launch_rows<128, 2>(P, steps, nsm, st);
+        default: return nt == 1 ? launch_rows<256, 1>(P, steps, nsm, st) : launch_rows<256, 2>(P, steps, nsm, st);
     }
-    cudaError_t e = cudaErrorInvalidValue;
-    const unsigned g = (unsigned)grid;
-    if (kv->dim == 64) e = nt == 1 ? launch_rows<64, 1>(P, g, st) : launch_rows<64, 2>(P, g, st);
-    if (kv->dim == 128) e = nt == 1 ? launch_rows<128, 1>(P, g, st) : launch_rows<128, 2>(P, g, st);
-    if (kv->dim == 256) e = nt == 1 ? launch_rows<256, 1>(P, g, st) : launch_rows<256, 2>(P, g, st);
-    return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_attend launch");
 }

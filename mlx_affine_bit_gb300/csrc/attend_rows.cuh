@@ -4,7 +4,9 @@
 // For the rows r of one (sequence, key/value head) -- G query heads a token --
 // and the tokens j they see:
 //     s_rj = (q_r . c_j) * (scale log2(e) ks_page / f_r)      q_r: fp16, times the power of two f_r
-//     (q_r . c_j = sum_d q_rd (c_jd + 128) - 128 sum_d q_rd: bytes are fp16 subnormals as they stand)
+// (the first product runs over bytes as they stand, fp16 subnormals (c + 128) 2^-24,
+// from a start of -128 2^-24 sum(q_r); the second needs the codes themselves: what
+// 128 sum(p) would round away is the small share of tokens that are far from the maximum)
 //     p_rj = 2^(s_rj - m_r),  l_r = sum_j p_rj,  out_r = sum_j p_rj vs_page c'_j / l_r
 // with the running maximum m_r of a warp's tokens.  Codes are exact in fp16.  What
 // enters the second product is w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16, with
@@ -12,8 +14,12 @@
 // contribution, however far apart the scales are, it keeps 11 bits down to 2^-29
 // and comes to nothing below 2^-40.
 //
-// Bound by reading the cache.  A CTA takes up to 8 * NT rows and one piece of the
-// tokens, a warp 16 tokens at a time, in the fragments of mma.sync m16n8k16: a
+// Bound by reading the cache.  The work -- for every sequence, head and tile of
+// up to 8 * NT rows the tokens in steps of 128 -- is one line of steps that the
+// CTAs, as many as are resident at once, cut into equal shares, whatever the
+// lengths.  A CTA takes its share item by item; an item (one tile's tokens) that
+// several CTAs share is joined by the last of them to arrive, in their order.
+// A warp takes 32 tokens at a time, in the fragments of mma.sync m16n8k16: a
 // lane's 16 bytes of a key are four k steps of a B fragment (the rows of q are
 // loaded in the same order), and 16 bytes of the values of four tokens are eight
 // A fragments of the transposed values, whose token pairs are put together by the
@@ -23,8 +29,7 @@
 // tokens of 64, half a token of 256) that the copies swizzle (16-byte chunk c of
 // row r at c ^ (r & 7)); with the order of a tile's tokens chosen for it (order()
 // below) the fragments' reads meet no bank conflicts.  The maxima, sums and outputs
-// of the warps are joined in shared memory, those of the pieces by the last CTA to
-// arrive, in piece order.
+// of the warps are joined in shared memory.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,10 +43,15 @@ namespace tfq {
 namespace attend {
 
 constexpr int WARPS = 4, THREADS = WARPS * 32;
-constexpr int STEP = 32 * WARPS;         // tokens a CTA takes at a time, two tiles of 16 a warp
-constexpr int MAX_PIECE = 4096;          // tokens of one piece
-constexpr int MAX_PAGES = MAX_PIECE / 16 + 1;
-constexpr int MAX_PIECES = 256;          // pieces of one sequence, at most (max_len is at most their product)
+// Tiles of 16 tokens that a warp takes at a time (dim 256: one, or its ring would leave one CTA an SM), and a CTA's tokens.
+#ifndef T128
+#define T128 2
+#endif
+TFQ_HD constexpr int tiles_of(int d) { return d == 256 ? 1 : d == 128 ? T128 : 2; }
+TFQ_HD constexpr int step_of(int d) { return 16 * tiles_of(d) * WARPS; }
+constexpr int CHUNK_TOKENS = 4096;       // tokens whose pages and scales a CTA keeps at a time
+constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
+constexpr int PART_BATCH = 64;           // parts whose factors are in shared memory at a time
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
 
 struct Params {
@@ -51,13 +61,12 @@ struct Params {
     const void *q;
     uint16_t *out;
     long long q_stride, out_stride;
-    float *part;            // [grid][8 NT][dim] sums, then [grid][8 NT][3] maxima m and n, sums of p
-    int *count;             // [items] arrivals, zero between launches
+    float *part;            // [2 grid][8 NT][dim] outputs, then [2 grid][8 NT][3] row sums (see RowSum)
+    int *count;             // [grid] arrivals at the item that a CTA began to share, zero between launches
     int *status;
     float scale;
     int group, window, causal, q_f32;
     int block_log2;         // of kv.block
-    int tiles, piece, nsplit;
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -65,15 +74,16 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
 }
-// Two biased codes (c + 128) in bytes 0, 1 (or 2, 3) of w as fp16: 1024 + 128 + c, minus 1152 (exact).
+// Two biased codes (c + 128) in bytes 0, 1 (or 2, 3) of w as fp16 subnormals, (c + 128) 2^-24.
+__device__ __forceinline__ uint32_t lo2_tiny(uint32_t w) { return prmt(w, 0u, 0x4140u); }
+__device__ __forceinline__ uint32_t hi2_tiny(uint32_t w) { return prmt(w, 0u, 0x4342u); }
+constexpr float TINY = 1.f / 16777216.f;         // 2^-24
+// The codes themselves: 1024 + 128 + c, minus 1152 (exact).
 __device__ __forceinline__ uint32_t half2_of(uint32_t w, uint32_t sel) {
     const uint32_t u = prmt(w, 0x64646464u, sel);
     const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// The same as fp16 subnormals, (128 + c) 2^-24: the keys' offset comes off in the accumulators' start.
-__device__ __forceinline__ uint32_t lo2_tiny(uint32_t w) { return prmt(w, 0u, 0x4140u); }
-__device__ __forceinline__ uint32_t hi2_tiny(uint32_t w) { return prmt(w, 0u, 0x4342u); }
 __device__ __forceinline__ uint32_t lo2(uint32_t w) { return half2_of(w, 0x4140u); }
 __device__ __forceinline__ uint32_t hi2(uint32_t w) { return half2_of(w, 0x4342u); }
 
@@ -107,18 +117,42 @@ __device__ __forceinline__ float out_factor(const RowSum &a) {
     return a.l == 0.f ? 0.f : exp2f(a.n - a.m - W_EXP) / a.l;
 }
 
-#ifndef NSTAGES
-#define NSTAGES 2
+#ifndef ST64
+#define ST64 2
 #endif
-// Pairs of tiles in a warp's ring and CTAs an SM, by the registers that outputs and q take.
-TFQ_HD constexpr int stages(int d) { return NSTAGES; }
-TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? 6 : 5) : d == 128 ? (nt == 1 ? 4 : 3) : 2; }
+#ifndef ST128
+#define ST128 2
+#endif
+#ifndef ST256
+#define ST256 3
+#endif
+#ifndef C64
+#define C64 5
+#endif
+#ifndef C64B
+#define C64B 4
+#endif
+#ifndef C128
+#define C128 3
+#endif
+#ifndef C128B
+#define C128B 3
+#endif
+#ifndef C256
+#define C256 2
+#endif
+#ifndef C256B
+#define C256B 2
+#endif
+// Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q take.
+TFQ_HD constexpr int stages(int d) { return d == 64 ? ST64 : d == 128 ? ST128 : ST256; }
+TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? C64 : C64B) : d == 128 ? (nt == 1 ? C128 : C128B) : (nt == 1 ? C256 : C256B); }
 TFQ_HD constexpr int tile_bytes(int d) { return 32 * d; }          // 16 tokens of keys and of values
 TFQ_HD constexpr int out_pitch(int d) { return d + 4; }            // floats between joined rows
 // Shared memory: the rings; after the tokens are done, every warp's outputs, then the parts' factors.
 TFQ_HD constexpr int smem_bytes(int d, int nt) {
-    const int ring = WARPS * stages(d) * 2 * tile_bytes(d), outs = WARPS * 8 * nt * out_pitch(d) * 4;
-    const int join = (MAX_PIECES + 1) * 8 * nt * 4, most = outs > join ? outs : join;
+    const int ring = WARPS * stages(d) * tiles_of(d) * tile_bytes(d), outs = WARPS * 8 * nt * out_pitch(d) * 4;
+    const int join = PART_BATCH * 8 * nt * 4, most = outs > join ? outs : join;
     return ring > most ? ring : most;
 }
 
@@ -135,13 +169,26 @@ __device__ __forceinline__ int order(int n) {
 // Offset of a byte of a tile under the copies' swizzle.
 __device__ __forceinline__ int swizzled(int byte) { return byte ^ ((byte >> 3) & 0x70); }
 
-// The rows and tokens of one CTA.
-struct Work {
-    int s, h, tile, split;       // sequence, key/value head, tile of rows, piece
-    int row0, n, end;            // the sequence's rows and tokens
-    int r0, rows;                // group rows r0 .. r0 + rows - 1 (row r: token r / G, head r % G)
-    int from, to, pieces;        // tokens that any of them sees, and the pieces that holds
+// Steps of one sequence: for every head and tile of its rows the tokens from
+// `base` on, in steps of STEP.
+struct SeqWork {
+    SeqRows q;
+    int base, steps, tiles;
 };
+template <int D, int R>
+__device__ __forceinline__ SeqWork seq_work(const Params &P, int s) {
+    SeqWork w;
+    w.q = seq_rows(P.b, s);
+    if (!w.q.ok) {
+        // Rows that lie within the matrices get zeros (no token is seen).
+        w.q.end = 0;
+        if (w.q.row0 < 0 || w.q.n < 0 || w.q.n > P.b.max_rows || w.q.row0 + w.q.n > P.b.rows) w.q.n = 0;
+    }
+    w.tiles = (w.q.n * P.group + R - 1) / R;
+    w.base = P.window ? max(0, w.q.end - w.q.n - P.window + 1) & ~31 : 0;
+    w.steps = max(1, (w.q.end - w.base + step_of(D) - 1) / step_of(D));
+    return w;
+}
 
 // Row factor f of a magnitude: the power of two that brings it into [1, 4).
 __device__ __forceinline__ float row_factor(float amax) {
@@ -157,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     constexpr int MT = D / 16;                   // m tiles of the transposed values
     constexpr int VB = D >= 128 ? 16 : 8;        // bytes that a lane takes of a token's values at once
     constexpr int NV = D / (8 * VB);             // ... and how often
-    constexpr int NST = stages(D);
+    constexpr int NST = stages(D), TILES = tiles_of(D), TP = 16 * TILES, STEP = step_of(D);
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ uint64_t bars[WARPS][NST];
     __shared__ int s_abort;
@@ -166,175 +213,64 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     __shared__ RowSum s_sum[WARPS][R];
     __shared__ float s_ks[MAX_PAGES], s_vs[MAX_PAGES];
     __shared__ int s_page[MAX_PAGES];
+    __shared__ long long s_warp[WARPS], s_first;
+    __shared__ int s_seq;
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane >> 2, lc = lane & 3;
     const int H = P.kv.kv_heads, G = P.group, BL = P.block_log2, BM = P.kv.block - 1;
 
-    Work w;
-    unsigned id = blockIdx.x;
-    w.split = id % P.nsplit;
-    id /= P.nsplit;
-    const unsigned item = id;
-    w.tile = id % P.tiles;
-    id /= P.tiles;
-    w.h = id % H;
-    w.s = id / H;
-    const SeqRows q = seq_rows(P.b, w.s);
-    w.row0 = q.row0;
-    w.n = q.n;
-    w.end = q.end;
-    if (!q.ok) {
-        if (tid == 0) atomicOr(P.status, STATUS_BOUNDS);
-        // Rows that lie within the matrices get zeros.
-        if (w.row0 < 0 || w.n < 0 || w.n > P.b.max_rows || w.row0 + w.n > P.b.rows) return;
-        w.end = 0;
+    // This CTA's share: steps [u0, u1) of the line, whose first sequence is s_seq, at s_first of the line.
+    const int per = (P.b.n_seqs + THREADS - 1) / THREADS;
+    const int s0 = tid * per, s1 = min(P.b.n_seqs, s0 + per);
+    long long mine_sum = 0;
+    for (int s = s0; s < s1; ++s) {
+        const SeqWork w = seq_work<D, R>(P, s);
+        if (!w.q.ok && blockIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
+        mine_sum += (long long)H * w.tiles * w.steps;
     }
-    w.r0 = w.tile * R;
-    w.rows = min(R, w.n * G - w.r0);
-    if (w.rows <= 0) return;
-    // Tokens that the tile's rows may see.
-    const int i0 = w.r0 / G, i1 = (w.r0 + w.rows - 1) / G;       // first and last of its tokens
-    w.from = 0;
-    w.to = w.end;
-    if (P.causal) {
-        w.to = min(w.end, w.end - w.n + i1 + 1);
-        if (P.window) w.from = max(0, w.end - w.n + i0 - P.window + 1);
+    long long incl = mine_sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += x;
     }
-    const int base = w.from & ~31;
-    w.pieces = w.to > w.from ? (w.to - base + P.piece - 1) / P.piece : 0;
-    uint16_t *out = P.out + (long long)w.row0 * P.out_stride;
-    auto out_at = [&](int r) {                  // first value of the tile's row r
-        const int gr = w.r0 + r, i = gr / G;
-        return out + (long long)i * P.out_stride + ((long long)w.h * G + gr - i * G) * D;
-    };
-    if (w.pieces == 0) {
-        if (w.split == 0)
-            for (int v = tid; v < w.rows * D; v += THREADS) out_at(v / D)[v % D] = 0;
-        return;
-    }
-    if (w.split >= w.pieces) return;
-    const int t0 = base + w.split * P.piece, t1 = min(t0 + P.piece, w.to);   // tokens of the piece
-
+    if (lane == 31) s_warp[warp] = incl;
     if (tid == 0) {
         for (int i = 0; i < WARPS * NST; ++i) mbar_init(&bars[0][i], 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    // Pages of the piece.
-    const int pg0 = t0 >> BL, npages = ((t1 - 1) >> BL) - pg0 + 1;
-    for (int i = tid; i < npages; i += THREADS) {
-        int page = P.b.table[w.s * P.b.table_stride + pg0 + i];
-        if (page < 0 || page >= P.kv.n_blocks) {
-            atomicOr(P.status, STATUS_BOUNDS);
-            page = -1;
-        }
-        s_page[i] = page;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < WARPS; ++i) {
+        if (i < warp) incl += s_warp[i];
+        total += s_warp[i];
     }
-    // (The rows of q are on their way meanwhile.)
-    float qx[R / WARPS][D / 32];
-#pragma unroll
-    for (int k = 0; k < R / WARPS; ++k) {
-        const int r = warp + k * WARPS, gr = w.r0 + r, i = gr / G;
-        const long long at = (long long)(w.row0 + i) * P.q_stride + ((long long)w.h * G + gr - i * G) * D + lane;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            qx[k][e] = 0.f;
-            if (r < w.rows)
-                qx[k][e] = P.q_f32 ? static_cast<const float *>(P.q)[at + e * 32]
-                                   : __uint_as_float((uint32_t) static_cast<const uint16_t *>(P.q)[at + e * 32] << 16);
+    const int C = (int)min((long long)gridDim.x, total);       // CTAs that get a share
+    if ((int)blockIdx.x >= C) return;
+    const long long u0 = total * blockIdx.x / C, u1 = total * (blockIdx.x + 1) / C;
+    auto cta_of = [&](long long u) { return (int)(((u + 1) * C - 1) / total); };
+    if (incl - mine_sum <= u0 && u0 < incl) {
+        long long at = incl - mine_sum;
+        int s = s0;
+        for (;; ++s) {
+            const SeqWork w = seq_work<D, R>(P, s);
+            const long long n = (long long)H * w.tiles * w.steps;
+            if (u0 < at + n) break;
+            at += n;
         }
+        s_seq = s;
+        s_first = at;
     }
     __syncthreads();
+
     // A warp's ring: stages of a pair of tiles' keys, then their values.
-    constexpr int STAGE = 2 * tile_bytes(D);
+    constexpr int STAGE = TILES * tile_bytes(D);
     uint8_t *mine = ring + warp * NST * STAGE;
     uint64_t *bar = bars[warp];
     volatile int *abort = &s_abort;
-    const bool single = BL == 4;                 // pages of one tile
-    auto fetch = [&](int t, int stage) {         // (the warp's first lane)
-        if (t >= t1) return;
-        const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < t1 ? s_page[(t >> BL) + 1 - pg0] : -1;
-        mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : 2) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
-        uint8_t *dst = mine + stage * STAGE;
-        auto copy = [&](int page, int at, uint8_t *to) {
-            const int row = (int)((((((long long)page * H + w.h) << BL) + (at & BM)) * D) >> 7);
-            tma_2d(to, &P.tm_k, 0, row, &bar[stage]);
-            tma_2d(to + STAGE / 2, &P.tm_v, 0, row, &bar[stage]);
-        };
-        if (p0 >= 0) copy(p0, t, dst);
-        if (p1 >= 0) copy(p1, t + 16, dst + 16 * D);
-    };
-    int ft = t0 + 32 * warp;                     // next pair to fetch
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i, ft += STEP)
-        if (lane == 0) fetch(ft, i);
-
-    // Scales of the pages (of the values' the logarithm), and the rows of q in fp16, times a power of two each.
-    for (int i = tid; i < npages; i += THREADS) {
-        const long long ph = (long long)s_page[i] * H + w.h;
-        s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
-        s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
-    }
-#pragma unroll
-    for (int k = 0; k < R / WARPS; ++k) {
-        const int r = warp + k * WARPS;
-        float m = 0.f, sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) m = fmaxf(m, fabsf(qx[k][e]));
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        const float f = row_factor(m);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            const __half h = __float2half_rn(qx[k][e] * f);
-            sq[r][e * 32 + lane] = h;
-            sum += __half2float(h);
-        }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if (lane == 0) s_row[r] = make_float2(P.scale * 1.44269504088896340736f / f * 16777216.f, sum * (-128.f / 16777216.f));
-    }
-    __syncthreads();
-
-    // A fragments of q: k step (v, i) holds d = 64 v + 16 lc + 4 i + {0, 1 | 2, 3}.  (dim 256: read again for every tile.)
-    constexpr bool Q_REGS = D < 256;
-    uint2 qa[NT][Q_REGS ? KV : 1][4];
-    auto q_at = [&](int u, int v, int i) { return *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]); };
-    if constexpr (Q_REGS) {
-#pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int v = 0; v < KV; ++v)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qa[u][v][i] = q_at(u, v, i);
-    }
-    float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24
-    int see_from[NT], see_to[NT];                // tokens that rows lr (+ 8) see
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-        const int r = min(lr + 8 * u, w.rows - 1);   // (rows past the tile's end are computed, never stored)
-        rowf[u] = s_row[r].x;
-        off[u] = s_row[r].y;
-        const int pos = w.end - w.n + (w.r0 + r) / G;
-        see_to[u] = P.causal ? min(w.end, pos + 1) : w.end;
-        see_from[u] = P.window ? pos - P.window + 1 : 0;
-    }
-    int all_from = 0, all_to = w.end;            // tokens that every row of the tile sees
-    if (P.causal) {
-        all_to = min(w.end, w.end - w.n + i0 + 1);
-        if (P.window) all_from = w.end - w.n + i1 - P.window + 1;
-    }
-
-    float o[MT][NT][4];
-    float m[NT], n[NT], l[NT];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-        m[u] = n[u] = -INFINITY;
-        l[u] = 0.f;
-#pragma unroll
-        for (int p = 0; p < MT; ++p)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[p][u][e] = 0.f;
-    }
+    const bool single = TILES == 2 && BL == 4;   // pages of one tile only: a stage's tiles come from two
+    uint32_t fit = 0, it = 0;                    // pairs fetched and taken, over all items
     // Offsets of this lane's reads in a stage: keys of token order(lr) (+ 8, + 16, + 24), values of four tokens of a tile.
     int k_at[KV][2], v_at[NV][4];
     const int tok[2] = {order<D>(2 * lc), order<D>(2 * lc + 1)};
@@ -346,255 +282,431 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int k = 0; k < 4; ++k) v_at[v][k] = swizzled((tok[k & 1] + 8 * (k >> 1)) * D + v * 8 * VB + VB * lr) + STAGE / 2;
-    uint32_t it = 0;                             // pairs taken
-    for (int t = t0 + 32 * warp; t < t1; t += STEP, ++it) {
-        if (lane == 0) fetch(ft, (it + NST - 1) % NST);
-        ft += STEP;
-        mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
-        const uint8_t *tiles = mine + (it % NST) * STAGE;
-        // Tiles t and t + 16: their pages (a tile of no page is not seen).
-        const int pi[2] = {(t >> BL) - pg0, min(((t + 16) >> BL) - pg0, npages - 1)};
-        const bool on[2] = {s_page[pi[0]] >= 0, s_page[pi[1]] >= 0 && !(single && t + 16 >= t1)};
-        // Scores of 32 tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
-        float sc[4][4];
+
+    int seq = s_seq;
+    long long seq_at = s_first;                  // the sequence's first step on the line
+    SeqWork sw = seq_work<D, R>(P, seq);
+    for (long long line = u0; line < u1;) {
+        while (line >= seq_at + (long long)H * sw.tiles * sw.steps) {
+            seq_at += (long long)H * sw.tiles * sw.steps;
+            sw = seq_work<D, R>(P, ++seq);
+        }
+        // The item: a head and a tile of the sequence's rows; this CTA's steps of it.
+        const int index = (int)((line - seq_at) / sw.steps), h = index / sw.tiles, tile = index - h * sw.tiles;
+        const long long item_at = seq_at + (long long)index * sw.steps;
+        const int step0 = (int)(line - item_at), step1 = (int)min((long long)sw.steps, u1 - item_at);
+        const int r0 = tile * R, rows = min(R, sw.q.n * G - r0);
+        const int end = sw.q.end, first = end - sw.q.n;              // (position of the sequence's first row)
+        const int i0 = r0 / G, i1 = (r0 + rows - 1) / G;             // first and last of the tile's tokens
+        const int to = P.causal ? min(end, first + i1 + 1) : end;    // tokens that any of the rows sees
+        const int t_begin = sw.base + step0 * STEP, t_end = min(sw.base + step1 * STEP, to);
+        uint16_t *out = P.out + (long long)sw.q.row0 * P.out_stride;
+        auto out_at = [&](int r) {               // first value of the tile's row r
+            const int gr = r0 + r, i = gr / G;
+            return out + (long long)i * P.out_stride + ((long long)h * G + gr - i * G) * D;
+        };
+
+        // The rows of q in fp16, times a power of two each.
+        float qx[R / WARPS][D / 32];
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
+        for (int k = 0; k < R / WARPS; ++k) {
+            const int r = warp + k * WARPS, gr = r0 + r, i = gr / G;
+            const long long at = (long long)(sw.q.row0 + i) * P.q_stride + ((long long)h * G + gr - i * G) * D + lane;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
-#pragma unroll
-        for (int v = 0; v < KV; ++v) {
-            uint32_t kw[4][4];
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
-                kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
-                kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
-                uint2 qa1 = make_uint2(0u, 0u);
-                if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
-#pragma unroll
-                for (int nb = 0; nb < 4; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
+            for (int e = 0; e < D / 32; ++e) {
+                qx[k][e] = 0.f;
+                if (r < rows)
+                    qx[k][e] = P.q_f32 ? static_cast<const float *>(P.q)[at + e * 32]
+                                       : __uint_as_float((uint32_t) static_cast<const uint16_t *>(P.q)[at + e * 32] << 16);
             }
         }
-        // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
-        const bool full = t >= all_from && t + 32 <= all_to && on[0] && on[1];
-        const float ks[2] = {s_ks[pi[0]], s_ks[pi[1]]}, vs[2] = {s_vs[pi[0]], s_vs[pi[1]]};
-        uint32_t pb[NT][4];
-        bool grew = false;
-        float mt[NT], nt[NT];
+#pragma unroll
+        for (int k = 0; k < R / WARPS; ++k) {
+            const int r = warp + k * WARPS;
+            float m = 0.f, sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) m = fmaxf(m, fabsf(qx[k][e]));
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            const float f = row_factor(m);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                const __half x = __float2half_rn(qx[k][e] * f);
+                sq[r][e * 32 + lane] = x;
+                sum += __half2float(x);
+            }
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            if (lane == 0) s_row[r] = make_float2(P.scale * 1.44269504088896340736f / f * (1.f / TINY), sum * (-128.f * TINY));
+        }
+        __syncthreads();
+
+        // A fragments of q: k step (v, i) holds d = 64 v + 16 lc + 4 i + {0, 1 | 2, 3}.  (dim 256: read again for every tile.)
+        constexpr bool Q_REGS = D < 256;
+        uint2 qa[NT][Q_REGS ? KV : 1][4];
+        auto q_at = [&](int u, int v, int i) { return *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]); };
+        if constexpr (Q_REGS) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int v = 0; v < KV; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qa[u][v][i] = q_at(u, v, i);
+        }
+        float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24
+        int see_from[NT], see_to[NT];                // tokens that rows lr (+ 8) see
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            float top[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float f = rowf[u] * ks[h];
-                top[h] = -INFINITY;
-#pragma unroll
-                for (int nb = 2 * h; nb < 2 * h + 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &x = sc[nb][2 * u + e];
-                        x *= f;
-                        const int j = t + 8 * nb + tok[e];
-                        if (!full && !(on[h] && j >= see_from[u] && j < see_to[u])) x = -INFINITY;
-                        top[h] = fmaxf(top[h], x);
-                    }
-            }
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                const float a = __shfl_xor_sync(~0u, top[0], o), b = __shfl_xor_sync(~0u, top[1], o);
-                top[0] = fmaxf(top[0], a);
-                top[1] = fmaxf(top[1], b);
-            }
-            mt[u] = fmaxf(m[u], fmaxf(top[0], top[1]));
-            nt[u] = fmaxf(n[u], fmaxf(top[0] + vs[0], top[1] + vs[1]));
-            grew |= mt[u] > m[u] || nt[u] > n[u];
+            const int r = min(lr + 8 * u, rows - 1);   // (rows past the tile's end are computed, never stored)
+            rowf[u] = s_row[r].x;
+            off[u] = s_row[r].y;
+            const int pos = first + (r0 + r) / G;
+            see_to[u] = P.causal ? min(end, pos + 1) : end;
+            see_from[u] = P.window ? pos - P.window + 1 : 0;
         }
-        if (__any_sync(~0u, grew)) {
+        int all_from = 0, all_to = end;            // tokens that every row of the tile sees
+        if (P.causal) {
+            all_to = min(end, first + i0 + 1);
+            if (P.window) all_from = first + i1 - P.window + 1;
+        }
+
+        float o[MT][NT][4];
+        float m[NT], n[NT], l[NT];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            m[u] = n[u] = -INFINITY;
+            l[u] = 0.f;
+#pragma unroll
+            for (int p = 0; p < MT; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[p][u][e] = 0.f;
+        }
+        const int from = P.window ? max(0, first + i0 - P.window + 1) & ~31 : 0;
+        for (int c0 = max(t_begin, from); c0 < t_end; c0 += CHUNK_TOKENS) {
+        const int c1 = min(c0 + CHUNK_TOKENS, t_end);
+        // Pages of the chunk and their scales (of the values' the logarithm).
+        const int pg0 = c0 >> BL, npages = ((c1 - 1) >> BL) - pg0 + 1;
+        for (int i = tid; i < npages; i += THREADS) {
+            int page = P.b.table[seq * P.b.table_stride + pg0 + i];
+            if (page < 0 || page >= P.kv.n_blocks) {
+                atomicOr(P.status, STATUS_BOUNDS);
+                page = -1;
+            }
+            s_page[i] = page;
+        }
+        __syncthreads();
+        auto fetch = [&](int t) {                // (the warp's first lane)
+            if (t >= c1) return;
+            const int stage = fit++ % NST;
+            const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < c1 ? s_page[(t >> BL) + 1 - pg0] : -1;
+            mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : TILES) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
+            uint8_t *dst = mine + stage * STAGE;
+            auto copy = [&](int page, int at, uint8_t *to) {
+                const int row = (int)((((((long long)page * H + h) << BL) + (at & BM)) * D) >> 7);
+                tma_2d(to, &P.tm_k, 0, row, &bar[stage]);
+                tma_2d(to + STAGE / 2, &P.tm_v, 0, row, &bar[stage]);
+            };
+            if (p0 >= 0) copy(p0, t, dst);
+            if (p1 >= 0) copy(p1, t + 16, dst + 16 * D);
+        };
+        int ft = c0 + TP * warp;                 // next stage to fetch
+#pragma unroll
+        for (int i = 0; i < NST - 1; ++i, ft += STEP)
+            if (lane == 0) fetch(ft);
+        for (int i = tid; i < npages; i += THREADS) {
+            const long long ph = (long long)s_page[i] * H + h;
+            s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
+            s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
+        }
+        __syncthreads();
+        for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
+            if (lane == 0) fetch(ft);
+            ft += STEP;
+            mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
+            const uint8_t *tiles = mine + (it % NST) * STAGE;
+            // Tiles t and t + 16: their pages (a tile of no page is not seen).
+            int pi[TILES];
+            bool on[TILES];
+#pragma unroll
+            for (int h = 0; h < TILES; ++h) {
+                pi[h] = min(((t + 16 * h) >> BL) - pg0, npages - 1);
+                on[h] = s_page[pi[h]] >= 0 && !(h == 1 && single && t + 16 >= c1);
+            }
+            // Scores of the tiles' tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
+            float sc[2 * TILES][4];
+#pragma unroll
+            for (int nb = 0; nb < 2 * TILES; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                uint32_t kw[2 * TILES][4];
+#pragma unroll
+                for (int nb = 0; nb < 2 * TILES; ++nb) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
+                    kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
+                    kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
+                    uint2 qa1 = make_uint2(0u, 0u);
+                    if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
+#pragma unroll
+                    for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
+                }
+            }
+            // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
+            const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
+            float ks[TILES], vs[TILES];
+#pragma unroll
+            for (int h = 0; h < TILES; ++h) ks[h] = s_ks[pi[h]], vs[h] = s_vs[pi[h]];
+            uint32_t pb[NT][2 * TILES];
+            bool grew = false;
+            float mt[NT], nt[NT];
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int h = 0; h < TILES; ++h) {
+                    const float f = rowf[u] * ks[h];
+#pragma unroll
+                    for (int nb = 2 * h; nb < 2 * h + 2; ++nb) sc[nb][2 * u] *= f, sc[nb][2 * u + 1] *= f;
+                }
+            if (!full) {
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+#pragma unroll
+                    for (int nb = 0; nb < 2 * TILES; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = t + 8 * nb + tok[e];
+                            if (!(on[nb >> 1] && j >= see_from[u] && j < see_to[u])) sc[nb][2 * u + e] = -INFINITY;
+                        }
+            }
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
-                if (m[u] != -INFINITY) l[u] *= exp2_fast(m[u] - mt[u]);
-                const float a = n[u] == -INFINITY ? 0.f : exp2_fast(n[u] - nt[u]);
-                m[u] = mt[u];
-                n[u] = nt[u];
-                // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
-                const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
+                float top[TILES];
 #pragma unroll
-                for (int p = 0; p < MT; ++p) {
-                    o[p][u][0] *= a0;
-                    o[p][u][1] *= a1;
-                    o[p][u][2] *= a0;
-                    o[p][u][3] *= a1;
+                for (int h = 0; h < TILES; ++h)
+                    top[h] = fmaxf(fmaxf(sc[2 * h][2 * u], sc[2 * h][2 * u + 1]), fmaxf(sc[2 * h + 1][2 * u], sc[2 * h + 1][2 * u + 1]));
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], o));
+                mt[u] = m[u];
+                nt[u] = n[u];
+#pragma unroll
+                for (int h = 0; h < TILES; ++h) {
+                    mt[u] = fmaxf(mt[u], top[h]);
+                    nt[u] = fmaxf(nt[u], top[h] + vs[h]);
+                }
+                grew |= mt[u] > m[u] || nt[u] > n[u];
+            }
+            if (__any_sync(~0u, grew)) {
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    if (m[u] != -INFINITY) l[u] *= exp2_fast(m[u] - mt[u]);
+                    const float a = n[u] == -INFINITY ? 0.f : exp2_fast(n[u] - nt[u]);
+                    m[u] = mt[u];
+                    n[u] = nt[u];
+                    // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
+                    const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
+#pragma unroll
+                    for (int p = 0; p < MT; ++p) {
+                        o[p][u][0] *= a0;
+                        o[p][u][1] *= a1;
+                        o[p][u][2] *= a0;
+                        o[p][u][3] *= a1;
+                    }
                 }
             }
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float mm = m[u] == -INFINITY ? 0.f : m[u];
+#pragma unroll
+                for (int h = 0; h < TILES; ++h) {
+                    const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs[h] - n[u] + W_EXP, 115.f));
+#pragma unroll
+                    for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
+                        const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
+                        l[u] += p0 + p1;
+                        pb[u][nb] = pack_half(p0 * f, p1 * f);
+                    }
+                }
+            }
+            // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 16 lr + .. (dim 64: 8 lr + ..).
+#pragma unroll
+            for (int h = 0; h < TILES; ++h) {
+                if (!on[h]) continue;                // (its codes were not fetched)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    uint32_t a[4][VB / 4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
+                        if constexpr (VB == 16) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                            a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                            a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                            a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < VB / 4; ++i) {
+                        // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
+                        const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
+                        const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
+                        const int p = v * VB / 2 + 2 * i;
+                        const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
+                        const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
+#pragma unroll
+                        for (int u = 0; u < NT; ++u) {
+                            mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
+                            mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();                        // (every lane has read the stage that is filled next)
         }
+        __syncthreads();                         // (and every warp this chunk's pages)
+        }
+
+        // Join the warps: row sums, and the outputs (in the rings' place) in warp order.
+        auto out_of = [&](int wi, int r) { return reinterpret_cast<float *>(ring) + (wi * R + r) * out_pitch(D); };
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const float mm = m[u] == -INFINITY ? 0.f : m[u];
+            l[u] += __shfl_xor_sync(~0u, l[u], 1);
+            l[u] += __shfl_xor_sync(~0u, l[u], 2);
+            if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], n[u], l[u]};
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs[h] - n[u] + W_EXP, 115.f));
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-                for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
-                    const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
-                    l[u] += p0 + p1;
-                    pb[u][nb] = pack_half(p0 * f, p1 * f);
+            for (int e = 0; e < 2; ++e) {
+                float *dst = out_of(warp, 2 * lc + e + 8 * u);
+#pragma unroll
+                for (int p = 0; p < MT; ++p) {
+                    const int d = p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2));
+                    *reinterpret_cast<float2 *>(dst + d) = make_float2(o[p][u][e], o[p][u][2 + e]);
+                }
+            }
+        __syncthreads();
+        auto joined = [&](int r) {
+            RowSum a = s_sum[0][r];
+            for (int k = 1; k < WARPS; ++k) a.m = fmaxf(a.m, s_sum[k][r].m), a.n = fmaxf(a.n, s_sum[k][r].n);
+            a.l = 0.f;
+            for (int k = 0; k < WARPS; ++k) a.l += s_sum[k][r].l * l_factor(s_sum[k][r], a.m);
+            return a;
+        };
+        auto joined4 = [&](int r, int d, const RowSum &a) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < WARPS; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(out_of(k, r) + d);
+                const float f = o_factor(s_sum[k][r], a.n);
+                y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
+            }
+            return y;
+        };
+        // Four values of an output row (aligned to 2 bytes only).
+        auto store4 = [&](int r, int d, float4 x, float f) {
+            uint16_t *dst = out_at(r) + d;
+            dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x.x * f));
+            dst[1] = __bfloat16_as_ushort(__float2bfloat16_rn(x.y * f));
+            dst[2] = __bfloat16_as_ushort(__float2bfloat16_rn(x.z * f));
+            dst[3] = __bfloat16_as_ushort(__float2bfloat16_rn(x.w * f));
+        };
+        // The CTAs that share the item, in order.
+        const int c_first = cta_of(item_at), parts = cta_of(item_at + sw.steps - 1) - c_first + 1;
+        if (parts == 1) {
+            for (int v = 4 * tid; v < rows * D; v += 4 * THREADS) {
+                const RowSum a = joined(v / D);
+                store4(v / D, v % D, joined4(v / D, v % D, a), out_factor(a));
+            }
+        } else {
+            // A CTA's first item's part is in its slot 0, that of a later one (its last) in slot 1.
+            RowSum *sums = reinterpret_cast<RowSum *>(P.part + 2LL * gridDim.x * R * D);
+            auto slot = [&](int k) {
+                const int c = c_first + k;
+                return 2 * c + (k == 0 && item_at > total * c / C ? 1 : 0);
+            };
+            const int mine_at = slot((int)blockIdx.x - c_first);
+            for (int v = 4 * tid; v < rows * D; v += 4 * THREADS)
+                *reinterpret_cast<float4 *>(P.part + (long long)mine_at * R * D + v) = joined4(v / D, v % D, joined(v / D));
+            if (tid < rows) sums[mine_at * R + tid] = joined(tid);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(P.count + c_first, 1) == parts - 1;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                if (tid == 0) P.count[c_first] = 0;
+                auto sum_of = [&](int k, int r) {
+                    const float *x = &sums[slot(k) * R + r].m;
+                    return RowSum{__ldcg(x), __ldcg(x + 1), __ldcg(x + 2)};
+                };
+                // The row sums of all parts, a warp a row (in s_sum[0]); then the outputs, some parts' factors at a time.
+                for (int r = warp; r < rows; r += WARPS) {
+                    RowSum a{-INFINITY, -INFINITY, 0.f};
+                    for (int k = lane; k < parts; k += 32) {
+                        const RowSum x = sum_of(k, r);
+                        a.m = fmaxf(a.m, x.m);
+                        a.n = fmaxf(a.n, x.n);
+                    }
+                    for (int o = 16; o > 0; o >>= 1) {
+                        a.m = fmaxf(a.m, __shfl_xor_sync(~0u, a.m, o));
+                        a.n = fmaxf(a.n, __shfl_xor_sync(~0u, a.n, o));
+                    }
+                    for (int k = lane; k < parts; k += 32) {
+                        const RowSum x = sum_of(k, r);
+                        a.l += x.l * l_factor(x, a.m);
+                    }
+                    for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
+                    if (lane == 0) s_sum[0][r] = a;
+                }
+                __syncthreads();
+                float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (the outputs in the ring have been read)
+                constexpr int ACC = R * D / 4 / THREADS;
+                float4 acc[ACC];
+#pragma unroll
+                for (int i = 0; i < ACC; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k0 = 0; k0 < parts; k0 += PART_BATCH) {
+                    const int kn = min(PART_BATCH, parts - k0);
+                    for (int i = tid; i < kn * R; i += THREADS)
+                        if (i % R < rows) s_fac[i / R][i % R] = o_factor(sum_of(k0 + i / R, i % R), s_sum[0][i % R].n);
+                    __syncthreads();
+#pragma unroll
+                    for (int i = 0; i < ACC; ++i) {
+                        const int v = 4 * (tid + i * THREADS);
+                        if (v < rows * D) {
+#pragma unroll 8
+                            for (int k = 0; k < kn; ++k) {
+                                const float4 x = __ldcg(reinterpret_cast<const float4 *>(P.part + (long long)slot(k0 + k) * R * D + v));
+                                const float f = s_fac[k][v / D];
+                                acc[i].x = fmaf(x.x, f, acc[i].x);
+                                acc[i].y = fmaf(x.y, f, acc[i].y);
+                                acc[i].z = fmaf(x.z, f, acc[i].z);
+                                acc[i].w = fmaf(x.w, f, acc[i].w);
+                            }
+                        }
+                    }
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int i = 0; i < ACC; ++i) {
+                    const int v = 4 * (tid + i * THREADS);
+                    if (v < rows * D) store4(v / D, v % D, acc[i], out_factor(s_sum[0][v / D]));
                 }
             }
         }
-        // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 16 lr + .. (dim 64: 8 lr + ..).
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!on[h]) continue;                // (its codes were not fetched)
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                uint32_t a[4][VB / 4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
-                    if constexpr (VB == 16) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                        a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                        a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                        a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < VB / 4; ++i) {
-                    // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
-                    const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
-                    const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
-                    const int p = v * VB / 2 + 2 * i;
-                    const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
-                    const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) {
-                        mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
-                        mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
-                    }
-                }
-            }
-        }
-        __syncwarp();                            // (every lane has read the stage that is filled next)
+        // The ring goes back from plain stores to copies.
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        line = item_at + step1;
     }
     if (*abort && lane == 0) {
-        // A wait ran out: no copy may be in flight when the ring is used again.
+        // A wait ran out: no copy may be in flight when the CTA ends.
         for (uint32_t j = it > NST ? it - NST : 0; j < it; ++j) mbar_wait(&bar[j % NST], (j / NST) & 1, abort, P.status, false);
-    }
-
-    // Join the warps: row sums, and the outputs (in the rings' place) in warp order.
-    auto out_of = [&](int wi, int r) { return reinterpret_cast<float *>(ring) + (wi * R + r) * out_pitch(D); };
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-        l[u] += __shfl_xor_sync(~0u, l[u], 1);
-        l[u] += __shfl_xor_sync(~0u, l[u], 2);
-        if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], n[u], l[u]};
-    }
-    __syncthreads();                             // (every ring has been read)
-#pragma unroll
-    for (int u = 0; u < NT; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float *dst = out_of(warp, 2 * lc + e + 8 * u);
-#pragma unroll
-            for (int p = 0; p < MT; ++p) {
-                const int d = p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2));
-                *reinterpret_cast<float2 *>(dst + d) = make_float2(o[p][u][e], o[p][u][2 + e]);
-            }
-        }
-    __syncthreads();
-    auto joined = [&](int r) {
-        RowSum a = s_sum[0][r];
-        for (int k = 1; k < WARPS; ++k) a.m = fmaxf(a.m, s_sum[k][r].m), a.n = fmaxf(a.n, s_sum[k][r].n);
-        a.l = 0.f;
-        for (int k = 0; k < WARPS; ++k) a.l += s_sum[k][r].l * l_factor(s_sum[k][r], a.m);
-        return a;
-    };
-    auto joined4 = [&](int r, int d, const RowSum &a) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < WARPS; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(out_of(k, r) + d);
-            const float f = o_factor(s_sum[k][r], a.n);
-            y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
-        }
-        return y;
-    };
-    // Four values of an output row (aligned to 2 bytes only).
-    auto store4 = [&](int r, int d, float4 x, float f) {
-        uint16_t *dst = out_at(r) + d;
-        dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x.x * f));
-        dst[1] = __bfloat16_as_ushort(__float2bfloat16_rn(x.y * f));
-        dst[2] = __bfloat16_as_ushort(__float2bfloat16_rn(x.z * f));
-        dst[3] = __bfloat16_as_ushort(__float2bfloat16_rn(x.w * f));
-    };
-    if (w.pieces == 1) {
-        for (int v = 4 * tid; v < w.rows * D; v += 4 * THREADS)
-        {
-            const RowSum a = joined(v / D);
-            store4(v / D, v % D, joined4(v / D, v % D, a), out_factor(a));
-        }
-        return;
-    }
-    // A part: its outputs and row sums.
-    const long long first = (long long)item * P.nsplit;
-    RowSum *sums = reinterpret_cast<RowSum *>(P.part + (long long)gridDim.x * R * D) + first * R;
-    float *part = P.part + first * R * D;
-    for (int v = 4 * tid; v < w.rows * D; v += 4 * THREADS)
-        *reinterpret_cast<float4 *>(part + w.split * R * D + v) = joined4(v / D, v % D, joined(v / D));
-    if (tid < w.rows) sums[w.split * R + tid] = joined(tid);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(P.count + item, 1) == w.pieces - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    if (tid == 0) P.count[item] = 0;
-    // The parts' factors, a warp a row; then the outputs in piece order.
-    float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (this CTA's outputs have been read: a barrier lies between)
-    for (int r = warp; r < w.rows; r += WARPS) {
-        RowSum x[MAX_PIECES / 32], a{-INFINITY, -INFINITY, 0.f};
-#pragma unroll
-        for (int i = 0; i < MAX_PIECES / 32; ++i) {
-            const int k = 32 * i + lane;
-            x[i] = RowSum{-INFINITY, -INFINITY, 0.f};
-            if (k < w.pieces) {
-                const float *src = &sums[k * R + r].m;
-                x[i] = RowSum{__ldcg(src), __ldcg(src + 1), __ldcg(src + 2)};
-            }
-            a.m = fmaxf(a.m, x[i].m);
-            a.n = fmaxf(a.n, x[i].n);
-        }
-        for (int o = 16; o > 0; o >>= 1) {
-            a.m = fmaxf(a.m, __shfl_xor_sync(~0u, a.m, o));
-            a.n = fmaxf(a.n, __shfl_xor_sync(~0u, a.n, o));
-        }
-#pragma unroll
-        for (int i = 0; i < MAX_PIECES / 32; ++i) {
-            a.l += x[i].l * l_factor(x[i], a.m);
-            if (32 * i + lane < w.pieces) s_fac[32 * i + lane][r] = o_factor(x[i], a.n);
-        }
-        for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
-        if (lane == 0) s_fac[MAX_PIECES][r] = out_factor(a);
-    }
-    __syncthreads();
-    for (int v = 4 * tid; v < w.rows * D; v += 4 * THREADS) {
-        const int r = v / D;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < w.pieces; ++k) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + (long long)k * R * D + v));
-            const float f = s_fac[k][r];
-            acc.x = fmaf(x.x, f, acc.x);
-            acc.y = fmaf(x.y, f, acc.y);
-            acc.z = fmaf(x.z, f, acc.z);
-            acc.w = fmaf(x.w, f, acc.w);
-        }
-        store4(r, v % D, acc, s_fac[MAX_PIECES][r]);
     }
 }
 
