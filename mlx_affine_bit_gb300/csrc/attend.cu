@@ -88,9 +88,9 @@ int launch_rows(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
     int per_sm = 0;
     cudaError_t e = resident<D, NT>(&per_sm);
     if (e != cudaSuccess) return cuda_error(e, "kv_attend set-up");
-    const long long grid = std::min(steps, (long long)nsm * per_sm);
+    const long long grid = std::min({steps, (long long)nsm * per_sm, (long long)attend::MAX_PARTS});
     Ws w;
-    const int rc = workspace(st, (size_t)grid * 2 * 8 * NT * (D + 3), (size_t)grid, &w);
+    const int rc = workspace(st, (size_t)grid * 2 * 8 * NT * (D + 4), (size_t)grid, &w);
     if (rc) return rc;
     P.part = w.part;
     P.count = w.count;

@@ -51,7 +51,7 @@ TFQ_HD constexpr int tiles_of(int d) { return d == 256 ? 1 : d == 128 ? T128 : 2
 TFQ_HD constexpr int step_of(int d) { return 16 * tiles_of(d) * WARPS; }
 constexpr int CHUNK_TOKENS = 4096;       // tokens whose pages and scales a CTA keeps at a time
 constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
-constexpr int PART_BATCH = 64;           // parts whose factors are in shared memory at a time
+constexpr int MAX_PARTS = 768;           // CTAs of a launch, at most
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
 
 struct Params {
@@ -61,7 +61,7 @@ struct Params {
     const void *q;
     uint16_t *out;
     long long q_stride, out_stride;
-    float *part;            // [2 grid][8 NT][dim] outputs, then [2 grid][8 NT][3] row sums (see RowSum)
+    float *part;            // [2 grid][8 NT][dim] outputs, then [2 grid][8 NT][4] row sums (see RowSum)
     int *count;             // [grid] arrivals at the item that a CTA began to share, zero between launches
     int *status;
     float scale;
@@ -105,8 +105,8 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 }
 
 // What has been summed of a row: maxima m of s and n of s + log2(vs), sum l of p.
-struct RowSum {
-    float m, n, l;
+struct __align__(16) RowSum {
+    float m, n, l, unused;
 };
 // Factors of a part's l and outputs in a join of maxima m and n: 0 for a part that
 // saw no token (l = 0) or only values of scale 0; NaN scores (l NaN) stay NaN.
@@ -152,7 +152,7 @@ TFQ_HD constexpr int out_pitch(int d) { return d + 4; }            // floats bet
 // Shared memory: the rings; after the tokens are done, every warp's outputs, then the parts' factors.
 TFQ_HD constexpr int smem_bytes(int d, int nt) {
     const int ring = WARPS * stages(d) * tiles_of(d) * tile_bytes(d), outs = WARPS * 8 * nt * out_pitch(d) * 4;
-    const int join = PART_BATCH * 8 * nt * 4, most = outs > join ? outs : join;
+    const int join = MAX_PARTS * 8 * nt * 4, most = outs > join ? outs : join;
     return ring > most ? ring : most;
 }
 
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             return out + (long long)i * P.out_stride + ((long long)h * G + gr - i * G) * D;
         };
 
-        // The rows of q in fp16, times a power of two each.
+        // The rows of q, in fp16 times a power of two each.
         float qx[R / WARPS][D / 32];
 #pragma unroll
         for (int k = 0; k < R / WARPS; ++k) {
@@ -320,6 +320,46 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                                        : __uint_as_float((uint32_t) static_cast<const uint16_t *>(P.q)[at + e * 32] << 16);
             }
         }
+        // Tokens [c0, c1): their pages, the first stages under way, and their scales (of the values' the logarithm).
+        const int from = P.window ? max(0, first + i0 - P.window + 1) & ~31 : 0;
+        int c0 = max(t_begin, from), c1 = c0, pg0 = 0, npages = 0, ft = 0;
+        auto fetch = [&](int t) {                // (the warp's first lane)
+            if (t >= c1) return;
+            const int stage = fit++ % NST;
+            const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < c1 ? s_page[(t >> BL) + 1 - pg0] : -1;
+            mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : TILES) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
+            uint8_t *dst = mine + stage * STAGE;
+            auto copy = [&](int page, int at, uint8_t *to) {
+                const int row = (int)((((((long long)page * H + h) << BL) + (at & BM)) * D) >> 7);
+                tma_2d(to, &P.tm_k, 0, row, &bar[stage]);
+                tma_2d(to + STAGE / 2, &P.tm_v, 0, row, &bar[stage]);
+            };
+            if (p0 >= 0) copy(p0, t, dst);
+            if (p1 >= 0) copy(p1, t + 16, dst + 16 * D);
+        };
+        auto open_chunk = [&]() {
+            c1 = min(c0 + CHUNK_TOKENS, t_end);
+            pg0 = c0 >> BL;
+            npages = ((c1 - 1) >> BL) - pg0 + 1;
+            for (int i = tid; i < npages; i += THREADS) {
+                int page = P.b.table[seq * P.b.table_stride + pg0 + i];
+                if (page < 0 || page >= P.kv.n_blocks) {
+                    atomicOr(P.status, STATUS_BOUNDS);
+                    page = -1;
+                }
+                s_page[i] = page;
+            }
+            __syncthreads();
+            ft = c0 + TP * warp;
+            for (int i = 0; i < NST - 1; ++i, ft += STEP)
+                if (lane == 0) fetch(ft);
+            for (int i = tid; i < npages; i += THREADS) {
+                const long long ph = (long long)s_page[i] * H + h;
+                s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
+                s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
+            }
+        };
+        if (c0 < t_end) open_chunk();            // (the loads of q are on their way meanwhile)
 #pragma unroll
         for (int k = 0; k < R / WARPS; ++k) {
             const int r = warp + k * WARPS;
@@ -379,44 +419,11 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[p][u][e] = 0.f;
         }
-        const int from = P.window ? max(0, first + i0 - P.window + 1) & ~31 : 0;
-        for (int c0 = max(t_begin, from); c0 < t_end; c0 += CHUNK_TOKENS) {
-        const int c1 = min(c0 + CHUNK_TOKENS, t_end);
-        // Pages of the chunk and their scales (of the values' the logarithm).
-        const int pg0 = c0 >> BL, npages = ((c1 - 1) >> BL) - pg0 + 1;
-        for (int i = tid; i < npages; i += THREADS) {
-            int page = P.b.table[seq * P.b.table_stride + pg0 + i];
-            if (page < 0 || page >= P.kv.n_blocks) {
-                atomicOr(P.status, STATUS_BOUNDS);
-                page = -1;
-            }
-            s_page[i] = page;
+        for (bool opened = true; c0 < t_end; c0 = c1, opened = false) {
+        if (!opened) {
+            open_chunk();
+            __syncthreads();
         }
-        __syncthreads();
-        auto fetch = [&](int t) {                // (the warp's first lane)
-            if (t >= c1) return;
-            const int stage = fit++ % NST;
-            const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < c1 ? s_page[(t >> BL) + 1 - pg0] : -1;
-            mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : TILES) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
-            uint8_t *dst = mine + stage * STAGE;
-            auto copy = [&](int page, int at, uint8_t *to) {
-                const int row = (int)((((((long long)page * H + h) << BL) + (at & BM)) * D) >> 7);
-                tma_2d(to, &P.tm_k, 0, row, &bar[stage]);
-                tma_2d(to + STAGE / 2, &P.tm_v, 0, row, &bar[stage]);
-            };
-            if (p0 >= 0) copy(p0, t, dst);
-            if (p1 >= 0) copy(p1, t + 16, dst + 16 * D);
-        };
-        int ft = c0 + TP * warp;                 // next stage to fetch
-#pragma unroll
-        for (int i = 0; i < NST - 1; ++i, ft += STEP)
-            if (lane == 0) fetch(ft);
-        for (int i = tid; i < npages; i += THREADS) {
-            const long long ph = (long long)s_page[i] * H + h;
-            s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
-            s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
-        }
-        __syncthreads();
         for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
             if (lane == 0) fetch(ft);
             ft += STEP;
@@ -578,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         for (int u = 0; u < NT; ++u) {
             l[u] += __shfl_xor_sync(~0u, l[u], 1);
             l[u] += __shfl_xor_sync(~0u, l[u], 2);
-            if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], n[u], l[u]};
+            if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], n[u], l[u], 0.f};
         }
 #pragma unroll
         for (int u = 0; u < NT; ++u)
@@ -625,15 +632,16 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             }
         } else {
             // A CTA's first item's part is in its slot 0, that of a later one (its last) in slot 1.
-            RowSum *sums = reinterpret_cast<RowSum *>(P.part + 2LL * gridDim.x * R * D);
-            auto slot = [&](int k) {
-                const int c = c_first + k;
-                return 2 * c + (k == 0 && item_at > total * c / C ? 1 : 0);
-            };
-            const int mine_at = slot((int)blockIdx.x - c_first);
+            const int slot0 = 2 * c_first + (item_at > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
+            auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (c_first + k); };
+            float4 *sums = reinterpret_cast<float4 *>(P.part + 2LL * gridDim.x * R * D);
+            float *part = P.part + (long long)slot(k_mine) * R * D;
             for (int v = 4 * tid; v < rows * D; v += 4 * THREADS)
-                *reinterpret_cast<float4 *>(P.part + (long long)mine_at * R * D + v) = joined4(v / D, v % D, joined(v / D));
-            if (tid < rows) sums[mine_at * R + tid] = joined(tid);
+                *reinterpret_cast<float4 *>(part + v) = joined4(v / D, v % D, joined(v / D));
+            if (tid < rows) {
+                const RowSum a = joined(tid);
+                sums[slot(k_mine) * R + tid] = make_float4(a.m, a.n, a.l, 0.f);
+            }
             __threadfence();
             __syncthreads();
             if (tid == 0) s_last = atomicAdd(P.count + c_first, 1) == parts - 1;
@@ -641,15 +649,17 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             if (s_last) {
                 __threadfence();
                 if (tid == 0) P.count[c_first] = 0;
-                auto sum_of = [&](int k, int r) {
-                    const float *x = &sums[slot(k) * R + r].m;
-                    return RowSum{__ldcg(x), __ldcg(x + 1), __ldcg(x + 2)};
-                };
-                // The row sums of all parts, a warp a row (in s_sum[0]); then the outputs, some parts' factors at a time.
+                // The row sums of all parts (in s_sum[0]) and the parts' factors, a warp a row.
+                float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (the outputs in the ring have been read)
                 for (int r = warp; r < rows; r += WARPS) {
-                    RowSum a{-INFINITY, -INFINITY, 0.f};
-                    for (int k = lane; k < parts; k += 32) {
-                        const RowSum x = sum_of(k, r);
+                    auto sum_of = [&](int k) {
+                        const float4 x = __ldcg(sums + slot(k) * R + r);
+                        return RowSum{x.x, x.y, x.z, 0.f};
+                    };
+                    const RowSum own = sum_of(min(lane, parts - 1));
+                    RowSum a = own;
+                    for (int k = lane + 32; k < parts; k += 32) {
+                        const RowSum x = sum_of(k);
                         a.m = fmaxf(a.m, x.m);
                         a.n = fmaxf(a.n, x.n);
                     }
@@ -657,45 +667,33 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                         a.m = fmaxf(a.m, __shfl_xor_sync(~0u, a.m, o));
                         a.n = fmaxf(a.n, __shfl_xor_sync(~0u, a.n, o));
                     }
+                    a.l = 0.f;
                     for (int k = lane; k < parts; k += 32) {
-                        const RowSum x = sum_of(k, r);
+                        const RowSum x = k < 32 ? own : sum_of(k);
                         a.l += x.l * l_factor(x, a.m);
+                        s_fac[k][r] = o_factor(x, a.n);
                     }
                     for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
                     if (lane == 0) s_sum[0][r] = a;
                 }
                 __syncthreads();
-                float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (the outputs in the ring have been read)
-                constexpr int ACC = R * D / 4 / THREADS;
-                float4 acc[ACC];
+                // The outputs, in the parts' order, eight loads at a time.
+                for (int v = 4 * tid; v < rows * D; v += 4 * THREADS) {
+                    const int r = v / D;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k0 = 0; k0 < parts; k0 += 8) {
+                        float4 x[8];
 #pragma unroll
-                for (int i = 0; i < ACC; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k0 = 0; k0 < parts; k0 += PART_BATCH) {
-                    const int kn = min(PART_BATCH, parts - k0);
-                    for (int i = tid; i < kn * R; i += THREADS)
-                        if (i % R < rows) s_fac[i / R][i % R] = o_factor(sum_of(k0 + i / R, i % R), s_sum[0][i % R].n);
-                    __syncthreads();
+                        for (int k = 0; k < 8; ++k)
+                            x[k] = __ldcg(reinterpret_cast<const float4 *>(P.part + (long long)slot(min(k0 + k, parts - 1)) * R * D + v));
 #pragma unroll
-                    for (int i = 0; i < ACC; ++i) {
-                        const int v = 4 * (tid + i * THREADS);
-                        if (v < rows * D) {
-#pragma unroll 8
-                            for (int k = 0; k < kn; ++k) {
-                                const float4 x = __ldcg(reinterpret_cast<const float4 *>(P.part + (long long)slot(k0 + k) * R * D + v));
-                                const float f = s_fac[k][v / D];
-                                acc[i].x = fmaf(x.x, f, acc[i].x);
-                                acc[i].y = fmaf(x.y, f, acc[i].y);
-                                acc[i].z = fmaf(x.z, f, acc[i].z);
-                                acc[i].w = fmaf(x.w, f, acc[i].w);
-                            }
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = k0 + k < parts ? s_fac[min(k0 + k, parts - 1)][r] : 0.f;
+                            y.x = fmaf(x[k].x, f, y.x), y.y = fmaf(x[k].y, f, y.y);
+                            y.z = fmaf(x[k].z, f, y.z), y.w = fmaf(x[k].w, f, y.w);
                         }
                     }
-                    __syncthreads();
-                }
-#pragma unroll
-                for (int i = 0; i < ACC; ++i) {
-                    const int v = 4 * (tid + i * THREADS);
-                    if (v < rows * D) store4(v / D, v % D, acc[i], out_factor(s_sum[0][v / D]));
+                    store4(r, v % D, y, out_factor(s_sum[0][r]));
                 }
             }
         }
