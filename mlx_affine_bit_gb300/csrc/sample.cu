@@ -2,15 +2,18 @@
 //
 // A token's weight is the whole number w = round(exp((x - max) / T) * 2^31), so
 // sums of weights are exact whatever their order.  top-k, top-p and min-p all
-// keep a prefix of the ranking by (logit, then index): the cut of such a prefix
-// is found by counting tokens and weights in bins, of z = (x - max) / T first
-// and then of the bits of x within the bin that holds the cut, until the bin is
-// one token or one value; equal values are cut by index.  The token is then the
+// keep a prefix of the ranking by (logit, then index), and the token is the
 // first, in index order, at which the running sum exceeds u times the whole.
 //
-// One cluster of CTAs a row: each keeps its slice of the row in shared memory (a
-// row's logits leave global memory once), counts its own bins, and the CTAs add
-// up and search a share of the bins each over distributed shared memory.
+// One cluster of CTAs a row, a slice of the row each, in shared memory where it
+// fits (the logits then leave global memory once).  The cut of a prefix is found
+// by counting tokens (and adding up weights) in bins: of z = (x - max) / T first,
+// each CTA its own slice, added up and searched a share of the bins a CTA over
+// distributed shared memory.  The tokens down to the bin that holds the cut are
+// mostly few: they move, in index order, to the first CTA, which cuts them by
+// bins of the bits of x and draws, alone.  Where they are many the cluster goes on
+// together in the same way on its slices.  Reading the logits bounds many rows,
+// the chain of cluster barriers (about ten) a few.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,13 +29,20 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int BINS = 1024;                       // bins of one counting step (at most THREADS)
-constexpr int MAX_CLUSTER = 8;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int BINS = 512;                        // bins of one counting step (at most THREADS)
+#ifndef MAXC
+#define MAXC 16
+#endif
+constexpr int MAX_CLUSTER = MAXC;
 constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit: 2^31
-// exp(z) * 2^31 rounds to 0 below z = -22.2: BINS / 23 bins a unit of z cover the rest.
+// exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest.
 constexpr float BINS_PER_Z = BINS / 23.f;
-constexpr int MAX_SLICE_BYTES = 200 * 1024;      // of a row in one CTA's shared memory
+constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone
+#ifndef SLICE_KB
+#define SLICE_KB 80
+#endif
+constexpr int MAX_SLICE_BYTES = SLICE_KB * 1024; // of a row in one CTA's shared memory (two CTAs an SM)
 
 struct Params {
     const void *logits;
@@ -50,14 +60,41 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// The scaled distribution of a row.
+struct Scale {
+    float top, inv;              // largest logit, 1 / temperature
+    __device__ __forceinline__ float z(float v) const { return v == top ? 0.f : __fmul_rn(__fsub_rn(v, top), inv); }
+    __device__ __forceinline__ unsigned weight(float v) const {
+        return v == -INFINITY ? 0u : __float2uint_rn(__fmul_rn(expf(z(v)), WEIGHT_ONE));
+    }
+    // Bin of z; BINS for what has no weight (-inf, and z below ln 2^-32 = -22.18 and a little).
+    __device__ __forceinline__ int bin(float v) const {
+        const float x = z(v);
+        return v == -INFINITY || x < -22.25f ? BINS : (int)(x * -BINS_PER_Z);
+    }
+};
+
+// Tokens and weights of a bin, and of all bins before it.
+struct Bin {
+    unsigned n, n_before;
+    u64 w, w_before;
+};
 // The bin that holds a cut, and what lies above it.
 struct Found {
     int bin;                     // -1: the whole distribution lies above
     unsigned count, above;       // tokens in the bin, tokens above it
     u64 mass, mass_above;        // weights in the bin, above it
 };
-
-// A prefix of the ranking: bins of z above z_bin whole, in it the keys >= key,
+// A target: the want-th token, or the first at which the running weight reaches goal.
+struct Target {
+    bool by_mass;
+    unsigned want;
+    u64 goal;
+    __device__ __forceinline__ bool in(unsigned n, unsigned bin_n, u64 w, u64 bin_w) const {
+        return by_mass ? w < goal && w + bin_w >= goal : n < want && n + bin_n >= want;
+    }
+};
+// A prefix of the ranking: bins of z above z_bin whole, in it the keys above key,
 // of the key itself the tokens up to index `last`.
 struct Cut {
     int z_bin;
@@ -71,274 +108,165 @@ struct Shared {
     u64 warp_sum[WARPS];
     float max;                   // of this CTA's slice
     int at;                      // its index
-    unsigned n_part;             // this CTA's share of the bins: tokens, weights
+    unsigned n_part;             // this CTA's share of the bins (or of the tokens): tokens, weights
     u64 part;
     Found found[2];              // of alternate searches: a CTA may be one search ahead of another's readers
     int tie_last;
-    unsigned n1[BINS], n2[BINS];
-    u64 w1[BINS], w2[BINS];
+    unsigned n[BINS], lo[BINS], hi[BINS];       // tokens, and weights in 16-bit halves (a slice holds at most 2^16 tokens)
+    float list_x[MAX_LIST];      // first CTA: the tokens that it finishes, in index order
+    int list_i[MAX_LIST];
 };
 
-template <bool BF16, bool RESIDENT>
-struct Row {
-    const void *p;               // this CTA's slice in global memory
-    const float *s;              // and in shared memory (RESIDENT)
-    __device__ __forceinline__ static float clean(float x) { return x != x ? -INFINITY : x + 0.f; }   // NaN, -0
-    __device__ __forceinline__ float global(int i) const {
-        return clean(BF16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16)
-                          : static_cast<const float *>(p)[i]);
+// The CTAs that work together: the row's cluster, or one CTA.
+template <bool CLUSTER>
+struct Group {
+    cg::cluster_group g;
+    int size, rank;
+    __device__ __forceinline__ void sync() const {
+        if (CLUSTER)
+            g.sync();
+        else
+            __syncthreads();
     }
-    __device__ __forceinline__ float operator[](int i) const { return RESIDENT ? s[i] : global(i); }
+    __device__ __forceinline__ Shared *of(Shared &S, int r) const { return CLUSTER ? g.map_shared_rank(&S, r) : &S; }
 };
 
-template <bool BF16, bool RESIDENT>
-__global__ void __launch_bounds__(THREADS) sample_kernel(const Params P) {
-    extern __shared__ __align__(16) float values[];
-    __shared__ Shared S;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
-    const int row = blockIdx.x / C;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int first = c * P.slice, len = max(0, min(P.slice, P.vocab - first));
-    const long long at0 = (long long)row * P.stride + first;
-    const Row<BF16, RESIDENT> x{BF16 ? (const void *)(static_cast<const uint16_t *>(P.logits) + at0)
-                                     : (const void *)(static_cast<const float *>(P.logits) + at0),
-                                values};
-    // A warp's part of the slice: indexes [i0, i1), lane by lane.
-    const int per = ((P.slice + WARPS - 1) / WARPS + 31) / 32 * 32;
-    const int i0 = min(len, warp * per), i1 = min(len, i0 + per);
-    auto each = [&](auto f) {
-        for (int i = i0 + lane; i < i1; i += 32) f(x[i], i);
-    };
-
-    // The slice, and the first of its largest logits.
-    float top = -INFINITY;
-    int top_at = 0x7FFFFFFF;
-    for (int i = i0 + lane; i < i1; i += 32) {
-        const float v = x.global(i);
-        if (RESIDENT) values[i] = v;
-        if (v > top) top = v, top_at = first + i;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        const float v = __shfl_xor_sync(~0u, top, o);
-        const int i = __shfl_xor_sync(~0u, top_at, o);
-        if (v > top || (v == top && i < top_at)) top = v, top_at = i;
-    }
-    if (lane == 0) S.warp_max[warp] = top, S.warp_at[warp] = top_at;
+// Counts every token f(slot) -> bin >= 0 (and its weight) in the bins, adds the
+// group's bins up, and gives thread t of rank r bin r * BINS / size + t with what
+// lies before it.  The sums of all bins are left in the ranks' n_part and part.
+template <bool CLUSTER, class Each>
+__device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, int search, Each each) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, share = BINS / G.size;
     __syncthreads();
-    if (warp == 0) {
-        top = S.warp_max[lane];
-        top_at = S.warp_at[lane];
-        for (int o = 16; o > 0; o >>= 1) {
-            const float v = __shfl_xor_sync(~0u, top, o);
-            const int i = __shfl_xor_sync(~0u, top_at, o);
-            if (v > top || (v == top && i < top_at)) top = v, top_at = i;
+    for (int b = tid; b < BINS; b += THREADS) S.n[b] = S.lo[b] = S.hi[b] = 0;
+    __syncthreads();
+    each([&](int b, unsigned w) {
+        atomicAdd(&S.n[b], 1u);
+        if (w) {
+            atomicAdd(&S.lo[b], w & 0xFFFFu);
+            if (w >> 16) atomicAdd(&S.hi[b], w >> 16);
         }
-        if (lane == 0) S.max = top, S.at = top_at;
+    });
+    G.sync();
+    Bin b{0, 0, 0, 0};
+    if (tid < share)
+        for (int r = 0; r < G.size; ++r) {
+            const Shared *o = G.of(S, r);
+            const int at = G.rank * share + tid;
+            b.n += o->n[at];
+            b.w += o->lo[at] + ((u64)o->hi[at] << 16);
+        }
+    unsigned ni = b.n;
+    u64 wi = b.w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned a = __shfl_up_sync(~0u, ni, o);
+        const u64 d = __shfl_up_sync(~0u, wi, o);
+        if (lane >= o) ni += a, wi += d;
     }
-    for (int b = tid; b < BINS; b += THREADS) S.n1[b] = 0, S.w1[b] = 0;
-    cluster.sync();
-    top = -INFINITY;
-    for (int k = 0; k < C; ++k) {
-        const Shared *o = cluster.map_shared_rank(&S, k);
-        if (o->max > top) top = o->max, top_at = o->at;
+    if (lane == 31) S.warp_at[warp] = (int)ni, S.warp_sum[warp] = wi;
+    __syncthreads();
+    for (int q = 0; q < warp; ++q) ni += (unsigned)S.warp_at[q], wi += S.warp_sum[q];
+    if (tid == share - 1) S.n_part = ni, S.part = wi;
+    if (tid == 0) S.found[search & 1].bin = -1;
+    G.sync();
+    for (int r = 0; r < G.rank; ++r) {
+        const Shared *o = G.of(S, r);
+        ni += o->n_part, wi += o->part;
     }
-    float T = P.temperature ? P.temperature[row] : 1.f;
-    if (top == -INFINITY || !(T > 0.f)) {
-        if (c == 0 && tid == 0) {
-            P.tokens[row] = top == -INFINITY ? -1 : top_at;
-            if (P.probs) P.probs[row] = top == -INFINITY ? 0.f : 1.f;
-        }
-        cluster.sync();          // the others may still read this CTA's maximum
-        return;
+    b.n_before = ni - b.n;
+    b.w_before = wi - b.w;
+    return b;
+}
+// The bin that the target falls into, with `above` and `mass_above` before all bins, known to every rank.
+template <bool CLUSTER>
+__device__ __forceinline__ Found find_bin(Shared &S, const Group<CLUSTER> &G, int &search, const Bin &b, unsigned above,
+                                          u64 mass_above, const Target &t) {
+    const int share = BINS / G.size;
+    if ((int)threadIdx.x < share && t.in(above + b.n_before, b.n, mass_above + b.w_before, b.w)) {
+        const Found f{G.rank * share + (int)threadIdx.x, b.n, above + b.n_before, b.w, mass_above + b.w_before};
+        for (int r = 0; r < G.size; ++r) G.of(S, r)->found[search & 1] = f;
     }
-    T = fminf(T, FLT_MAX);
-    const float inv = __fdiv_rn(1.f, T);
-    auto z_of = [&](float v) { return v == top ? 0.f : __fmul_rn(__fsub_rn(v, top), inv); };
-    auto weight = [&](float v) {
-        return v == -INFINITY ? 0u : __float2uint_rn(__fmul_rn(expf(z_of(v)), WEIGHT_ONE));
-    };
-    auto z_bin = [&](float v) { return min(BINS - 1, (int)(z_of(v) * -BINS_PER_Z)); };
+    G.sync();
+    return S.found[search++ & 1];
+}
 
-    const float p = P.top_p ? P.top_p[row] : 1.f;
-    const int k = P.top_k ? P.top_k[row] : 0;
-    const float mp = P.min_p ? fminf(P.min_p[row], 1.f) : 0.f;
-    const double least = (double)mp * 2147483648.0;
-
-    // Bins of this CTA's share: thread i < BINS / C holds bin c * BINS / C + i.
-    const int share = BINS / C;
-    int searches = 0;
-    // Adds up the cluster's bins; the exclusive prefix over all bins, and the bin's own.
-    struct Bin {
-        unsigned n, n_before;
-        u64 w, w_before;
-    };
-    auto gather = [&](unsigned (Shared::*n)[BINS], u64 (Shared::*w)[BINS]) {
-        cluster.sync();
-        Bin b{0, 0, 0, 0};
-        if (tid < share)
-            for (int r = 0; r < C; ++r) {
-                Shared *o = cluster.map_shared_rank(&S, r);
-                b.n += (o->*n)[c * share + tid];
-                b.w += (o->*w)[c * share + tid];
-            }
-        unsigned ni = b.n;
-        u64 wi = b.w;
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned a = __shfl_up_sync(~0u, ni, o);
-            const u64 d = __shfl_up_sync(~0u, wi, o);
-            if (lane >= o) ni += a, wi += d;
-        }
-        if (lane == 31) S.warp_at[warp] = (int)ni, S.warp_sum[warp] = wi;
-        __syncthreads();
-        for (int q = 0; q < warp; ++q) ni += (unsigned)S.warp_at[q], wi += S.warp_sum[q];
-        if (tid == share - 1) S.n_part = ni, S.part = wi;
-        if (tid == 0) S.found[searches & 1].bin = -1;
-        cluster.sync();
-        for (int r = 0; r < c; ++r) {
-            const Shared *o = cluster.map_shared_rank(&S, r);
-            ni += o->n_part, wi += o->part;
-        }
-        b.n_before = ni - b.n;
-        b.w_before = wi - b.w;
-        return b;
-    };
-    // The bin that the target falls into (by tokens: the want-th; by weight: the
-    // first whose running sum reaches goal), known to every CTA.
-    auto search = [&](const Bin &b, unsigned above, u64 mass_above, bool by_mass, unsigned want, double goal) {
-        bool hit = false;
-        if (tid < share) {
-            if (by_mass)
-                hit = (double)(mass_above + b.w_before) < goal && (double)(mass_above + b.w_before + b.w) >= goal;
-            else
-                hit = above + b.n_before < want && above + b.n_before + b.n >= want;
-        }
-        if (hit) {
-            const Found f{c * share + tid, b.n, above + b.n_before, b.w, mass_above + b.w_before};
-            for (int r = 0; r < C; ++r) cluster.map_shared_rank(&S, r)->found[searches & 1] = f;
-        }
-        cluster.sync();
-        return S.found[searches++ & 1];
-    };
-    // Index of the tie-th (from 1) of the tokens equal to `key`.
-    auto tie_index = [&](uint32_t key, unsigned tie) {
-        unsigned mine = 0;
-        each([&](float v, int) { mine += key_of(v) == key; });
-        mine = __reduce_add_sync(~0u, mine);
-        if (lane == 0) S.warp_at[warp] = (int)mine;
-        __syncthreads();
-        unsigned before = 0, all = 0;
-        for (int q = 0; q < WARPS; ++q) {
-            if (q == warp) before = all;
-            all += (unsigned)S.warp_at[q];
-        }
-        if (tid == 0) S.n_part = all;
-        cluster.sync();
-        for (int r = 0; r < c; ++r) before += cluster.map_shared_rank(&S, r)->n_part;
-        if (before < tie && before + mine >= tie) {
-            for (int i = i0; i < i1; i += 32) {
-                const bool is = i + lane < i1 && key_of(x[i + lane]) == key;
-                const unsigned mask = __ballot_sync(~0u, is);
-                if (before + __popc(mask) >= tie) {
-                    if (is && before + __popc(mask & ((2u << lane) - 1)) == tie)
-                        for (int r = 0; r < C; ++r) cluster.map_shared_rank(&S, r)->tie_last = first + i + lane;
-                    break;
-                }
-                before += __popc(mask);
-            }
-        }
-        cluster.sync();
-        return S.tie_last;
-    };
-
-    Cut cut{BINS, 0, 0x7FFFFFFF};
-    const bool by_k = k > 0 && k < P.vocab, by_p = p < 1.f;
-    if (by_k || by_p) {
-        each([&](float v, int) {
-            const unsigned w = weight(v);
-            if (w) {
-                const int b = z_bin(v);
-                atomicAdd(&S.n1[b], 1u);
-                atomicAdd(&S.w1[b], (u64)w);
-            }
+// Cuts the group's tokens, in bins of z down to `f.bin`, at the target, which lies in that bin; returns the weight kept.
+// each(g) calls g(logit, index) for this thread's tokens; in_order(g) does so warp by warp in index order,
+// 32 tokens at a time (index -1 past the end).
+template <bool CLUSTER, class Each, class InOrder>
+__device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &search, const Scale &sc, float T, Found f,
+                                      const Target &t, Cut &cut, Each each, InOrder in_order) {
+    // Keys that the bin can hold, a little more at both ends.
+    cut.z_bin = f.bin;
+    cut.last = 0x7FFFFFFF;
+    const double lo = (f.bin + 1) * (1 + 1e-5) / BINS_PER_Z * (double)T, hi = f.bin * (1 - 1e-5) / BINS_PER_Z * (double)T;
+    uint32_t k_lo = f.bin == BINS - 1 ? 0u : key_of(__double2float_rd((double)sc.top - lo) + 0.f);
+    uint32_t k_hi = key_of(__double2float_ru((double)sc.top - hi) + 0.f);
+    while (f.count > 1 && k_lo < k_hi && (t.by_mass || f.above + f.count != t.want)) {
+        int shift = 0;
+        while (((k_hi - k_lo) >> shift) >= (uint32_t)BINS) ++shift;
+        const Bin b = count_bins(S, G, search, [&](auto add) {
+            each([&](float v, int) {
+                const uint32_t key = key_of(v);
+                if (key >= k_lo && key <= k_hi && sc.bin(v) == cut.z_bin) add((int)((k_hi - key) >> shift), sc.weight(v));
+            });
         });
-        const Bin b1 = gather(&Shared::n1, &Shared::w1);
-        u64 whole = 0;           // weight of the tokens kept so far
-        for (int r = 0; r < C; ++r) whole += cluster.map_shared_rank(&S, r)->part;
-        for (int pass = 0; pass < 2; ++pass) {
-            const bool by_mass = pass == 1;
-            if (!(by_mass ? by_p : by_k)) continue;
-            // A goal of at least half a weight keeps the first token.
-            const double goal = by_mass ? fmax((double)p * (double)whole, 0.5) : 0.0;
-            Found f = search(b1, 0, 0, by_mass, (unsigned)k, goal);
-            if (f.bin < 0) continue;
-            // Keys that bin can hold, a little more at both ends.
-            cut.z_bin = f.bin;
-            cut.last = 0x7FFFFFFF;
-            const double lo = (f.bin + 1) * (1 + 1e-5) / BINS_PER_Z * (double)T, hi = f.bin * (1 - 1e-5) / BINS_PER_Z * (double)T;
-            uint32_t k_lo = f.bin == BINS - 1 ? 0u : key_of(__double2float_rd((double)top - lo) + 0.f);
-            uint32_t k_hi = key_of(__double2float_ru((double)top - hi) + 0.f);
-            while (f.count > 1 && k_lo < k_hi && !(!by_mass && f.above + f.count == (unsigned)k)) {
-                int shift = 0;
-                while (((k_hi - k_lo) >> shift) >= (uint32_t)BINS) ++shift;
-                __syncthreads();
-                for (int b = tid; b < BINS; b += THREADS) S.n2[b] = 0, S.w2[b] = 0;
-                __syncthreads();
-                each([&](float v, int) {
-                    const uint32_t key = key_of(v);
-                    if (key >= k_lo && key <= k_hi && v != -INFINITY && z_bin(v) == f.bin) {
-                        const unsigned w = weight(v);
-                        if (w) {
-                            const uint32_t b = (k_hi - key) >> shift;
-                            atomicAdd(&S.n2[b], 1u);
-                            atomicAdd(&S.w2[b], (u64)w);
-                        }
-                    }
-                });
-                const Bin b2 = gather(&Shared::n2, &Shared::w2);
-                const int zb = f.bin;
-                const Found g = search(b2, f.above, f.mass_above, by_mass, (unsigned)k, goal);
-                if (g.bin < 0) break;
-                f = g;
-                const uint32_t hi2 = k_hi - ((uint32_t)f.bin << shift);
-                const u64 room = (u64)(hi2 - k_lo) + 1, span = (u64)1 << shift;
-                k_lo = room > span ? hi2 - (uint32_t)(span - 1) : k_lo;
-                k_hi = hi2;
-                f.bin = zb;
-            }
-            cut.key = k_lo;
-            whole = f.mass_above + f.mass;
-            if (k_lo == k_hi && f.count > 1) {
-                // Equal tokens: those that the target needs, by index.
-                const u64 w = f.mass / f.count;
-                unsigned need;
-                if (by_mass) {
-                    need = 1;
-                    const double est = (goal - (double)f.mass_above) / (double)w;
-                    if (est > 2.0) need = (unsigned)fmin(est, (double)f.count) - 1;
-                    while (need < f.count && (double)(f.mass_above + w * need) < goal) ++need;
-                    while (need > 1 && (double)(f.mass_above + w * (need - 1)) >= goal) --need;
-                } else {
-                    need = (unsigned)k - f.above;
-                }
-                if (need < f.count) {
-                    cut.last = tie_index(k_lo, need);
-                    whole = f.mass_above + w * need;
-                }
-            }
-        }
+        const Found g = find_bin(S, G, search, b, f.above, f.mass_above, t);
+        if (g.bin < 0) break;
+        f = g;
+        const uint32_t hi2 = k_hi - ((uint32_t)f.bin << shift);
+        const u64 room = (u64)(hi2 - k_lo) + 1, span = (u64)1 << shift;
+        k_lo = room > span ? hi2 - (uint32_t)(span - 1) : k_lo;
+        k_hi = hi2;
     }
+    cut.key = k_lo;
+    if (k_lo != k_hi || f.count < 2) return f.mass_above + f.mass;
+    // Equal tokens: those that the target needs, by index.
+    const u64 w = f.mass / f.count;              // (a bin that a weight is reached in has some)
+    const unsigned need = t.by_mass ? (unsigned)((t.goal - f.mass_above + w - 1) / w) : t.want - f.above;
+    if (need >= f.count) return f.mass_above + f.mass;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned mine = 0;
+    each([&](float v, int) { mine += key_of(v) == k_lo; });
+    mine = __reduce_add_sync(~0u, mine);
+    if (lane == 0) S.warp_at[warp] = (int)mine;
+    __syncthreads();
+    unsigned before = 0, all = 0;
+    for (int q = 0; q < WARPS; ++q) {
+        if (q == warp) before = all;
+        all += (unsigned)S.warp_at[q];
+    }
+    if (threadIdx.x == 0) S.n_part = all;
+    G.sync();
+    for (int r = 0; r < G.rank; ++r) before += G.of(S, r)->n_part;
+    if (before < need && before + mine >= need)
+        in_order([&](float v, int i) {
+            const bool is = i >= 0 && key_of(v) == k_lo;
+            const unsigned mask = __ballot_sync(~0u, is);
+            if (is && before + __popc(mask & ((2u << lane) - 1)) == need)
+                for (int r = 0; r < G.size; ++r) G.of(S, r)->tie_last = i;
+            before += __popc(mask);
+            return before >= need;
+        });
+    G.sync();
+    cut.last = S.tie_last;
+    return f.mass_above + w * need;
+}
+
+// Draws among the group's tokens above the cut and of weight `least` at least.
+template <bool CLUSTER, class Each, class InOrder>
+__device__ __forceinline__ void draw(Shared &S, const Group<CLUSTER> &G, const Scale &sc, const Cut &cut, unsigned least, float u,
+                                     int *token, float *prob, Each each, InOrder in_order) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto kept = [&](float v, int i) {
-        const unsigned w = weight(v);
-        if (w == 0 || (double)w < least) return 0u;
-        const int b = z_bin(v);
+        const int b = sc.bin(v);
         if (b > cut.z_bin) return 0u;
+        const unsigned w = sc.weight(v);
+        if (w < least) return 0u;
         if (b < cut.z_bin) return w;
         const uint32_t key = key_of(v);
-        return key > cut.key || (key == cut.key && first + i <= cut.last) ? w : 0u;
+        return key > cut.key || (key == cut.key && i <= cut.last) ? w : 0u;
     };
-
-    // Kept weights by warp, by CTA, of the row; then the token.
     u64 mine = 0;
     each([&](float v, int i) { mine += kept(v, i); });
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
@@ -350,43 +278,289 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const Params P) {
         if (q == warp) before = all;
         all += S.warp_sum[q];
     }
-    if (tid == 0) S.part = all;
-    cluster.sync();
+    if (threadIdx.x == 0) S.part = all;
+    G.sync();
     u64 total = 0;
-    for (int r = 0; r < C; ++r) {
-        const u64 o = cluster.map_shared_rank(&S, r)->part;
-        if (r < c) before += o;
+    for (int r = 0; r < G.size; ++r) {
+        const u64 o = G.of(S, r)->part;
+        if (r < G.rank) before += o;
         total += o;
     }
-    const double goal = fmax(0.0, fmin((double)P.u[row] * (double)total, (double)total - 0.5));
-    if ((double)before <= goal && (double)(before + mine) > goal) {
-        for (int i = i0; i < i1; i += 32) {
-            const unsigned w = i + lane < i1 ? kept(x[i + lane], i + lane) : 0u;
+    // The running sum exceeds u * total where it exceeds its whole part (u from 1 on: the last token).
+    const u64 goal = (u64)fmax(0.0, fmin((double)u * (double)total, (double)total - 0.5));
+    if (before <= goal && before + mine > goal)
+        in_order([&](float v, int i) {
+            const unsigned w = i >= 0 ? kept(v, i) : 0u;
             u64 run = w;
             for (int o = 1; o < 32; o <<= 1) {
                 const u64 a = __shfl_up_sync(~0u, run, o);
                 if (lane >= o) run += a;
             }
             run += before;
-            const unsigned mask = __ballot_sync(~0u, (double)run > goal);
-            if (mask) {
-                if (lane == __ffs(mask) - 1) {
-                    P.tokens[row] = first + i + lane;
-                    if (P.probs) P.probs[row] = (float)((double)w / (double)total);
-                }
-                break;
+            const unsigned mask = __ballot_sync(~0u, run > goal);
+            if (mask && lane == __ffs(mask) - 1) {
+                *token = i;
+                if (prob) *prob = (float)((double)w / (double)total);
             }
             before = __shfl_sync(~0u, run, 31);
+            return mask != 0;
+        });
+}
+
+template <bool BF16, bool RESIDENT>
+__global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
+    extern __shared__ __align__(16) uint8_t slice[];
+    __shared__ Shared S;
+    const Group<true> G{cg::this_cluster(), (int)cg::this_cluster().num_blocks(), (int)cg::this_cluster().block_rank()};
+    const int row = blockIdx.x / G.size;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int first = G.rank * P.slice, len = max(0, min(P.slice, P.vocab - first));
+    const long long at0 = (long long)row * P.stride + first;
+    const uint16_t *g16 = static_cast<const uint16_t *>(P.logits) + (BF16 ? at0 : 0);
+    const float *g32 = static_cast<const float *>(P.logits) + (BF16 ? 0 : at0);
+    auto value = [](float x) { return x != x ? -INFINITY : x + 0.f; };                  // NaN is -inf, -0 is 0
+    auto of16 = [&](uint32_t h) { return value(__uint_as_float(h << 16)); };
+    auto at = [&](int i) {
+        if (BF16) return of16(RESIDENT ? reinterpret_cast<const uint16_t *>(slice)[i] : g16[i]);
+        return value(RESIDENT ? reinterpret_cast<const float *>(slice)[i] : g32[i]);
+    };
+    // A warp's part of the slice: indexes [i0, i1), lane by lane.
+    const int per = ((P.slice + WARPS - 1) / WARPS + 31) / 32 * 32;
+    const int i0 = min(len, warp * per), i1 = min(len, i0 + per);
+    auto each = [&](auto f) {
+#pragma unroll 4
+        for (int i = i0 + lane; i < i1; i += 32) f(at(i), first + i);
+    };
+    auto in_order = [&](auto f) {
+        for (int i = i0; i < i1; i += 32) {
+            const bool is = i + lane < i1;
+            if (f(is ? at(i + lane) : -INFINITY, is ? first + i + lane : -1)) break;
+        }
+    };
+
+    // The slice, and its largest logit.
+    float top = -INFINITY;
+    if (RESIDENT) {
+        // 16 bytes at a time from the first aligned token on.
+        constexpr int VEC = BF16 ? 8 : 4;
+        const int es = BF16 ? 2 : 4;
+        const uintptr_t base = BF16 ? reinterpret_cast<uintptr_t>(g16) : reinterpret_cast<uintptr_t>(g32);
+        const int head = min(len, (int)(((16 - base % 16) % 16) / es)), vecs = (len - head) / VEC;
+        auto one = [&](int i) {
+            if (BF16) {
+                const uint16_t h = g16[i];
+                reinterpret_cast<uint16_t *>(slice)[i] = h;
+                top = fmaxf(top, of16(h));
+            } else {
+                const float x = g32[i];
+                reinterpret_cast<float *>(slice)[i] = x;
+                top = fmaxf(top, value(x));
+            }
+        };
+        if (tid < head) one(tid);
+        for (int i = head + vecs * VEC + tid; i < len; i += THREADS) one(i);
+        // (A row whose first token is not aligned goes to shared memory word by word.)
+#pragma unroll 4
+        for (int v = tid; v < vecs; v += THREADS) {
+            const int i = head + v * VEC;
+            if (BF16) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(g16 + i);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                if (head == 0) *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(slice) + i) = x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (head) {
+                        reinterpret_cast<uint16_t *>(slice)[i + 2 * e] = (uint16_t)w[e];
+                        reinterpret_cast<uint16_t *>(slice)[i + 2 * e + 1] = (uint16_t)(w[e] >> 16);
+                    }
+                    top = fmaxf(top, fmaxf(of16(w[e] & 0xFFFFu), of16(w[e] >> 16)));
+                }
+            } else {
+                const float4 x = *reinterpret_cast<const float4 *>(g32 + i);
+                float *dst = reinterpret_cast<float *>(slice) + i;
+                if (head == 0)
+                    *reinterpret_cast<float4 *>(dst) = x;
+                else
+                    dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
+                top = fmaxf(top, fmaxf(fmaxf(value(x.x), value(x.y)), fmaxf(value(x.z), value(x.w))));
+            }
+        }
+    } else {
+        each([&](float v, int) { top = fmaxf(top, v); });
+    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) S.warp_max[warp] = top;
+    __syncthreads();
+    if (tid == 0) {
+        for (int q = 0; q < WARPS; ++q) top = fmaxf(top, S.warp_max[q]);
+        S.max = top;
+    }
+    G.sync();
+    top = -INFINITY;
+    for (int r = 0; r < G.size; ++r) top = fmaxf(top, G.of(S, r)->max);
+    const float T = fminf(P.temperature ? P.temperature[row] : 1.f, FLT_MAX);
+    if (top == -INFINITY) {
+        if (G.rank == 0 && tid == 0) {
+            P.tokens[row] = -1;
+            if (P.probs) P.probs[row] = 0.f;
+        }
+        G.sync();                // (the others may still read this CTA's maximum)
+        return;
+    }
+    const bool greedy = !(T > 0.f);
+    const Scale sc{top, greedy ? 1.f : __fdiv_rn(1.f, T)};
+    const float p = P.top_p ? P.top_p[row] : 1.f;
+    const int k = greedy ? 1 : P.top_k ? P.top_k[row] : 0;       // (the first of the largest: the one token that top-k 1 keeps)
+    // The least whole weight of at least min_p times the largest.
+    const float mp = P.min_p && !greedy ? P.min_p[row] : 0.f;
+    const unsigned least = mp > 0.f ? (unsigned)fmax(1.0, ceil((double)fminf(mp, 1.f) * 2147483648.0)) : 1u;
+    const bool by_k = k > 0 && k < P.vocab, by_p = p < 1.f && !greedy;
+    const float u = P.u[row], Tk = greedy ? 1.f : T;
+    float *prob = P.probs ? P.probs + row : nullptr;
+    // The goal of top-p over a weight: the least whole number that reaches it, at least 1 (the first token).
+    auto goal_of = [&](u64 whole) { return (u64)fmax(1.0, ceil((double)p * (double)whole)); };
+
+    Cut cut{BINS - 1, 0, 0x7FFFFFFF};
+    int search = 0;
+    if (by_k || by_p) {
+        const bool mass = by_p && !by_k;         // (top-p after top-k is cut among the tokens that top-k leaves)
+        const Bin b = count_bins(S, G, search, [&](auto add) {
+            each([&](float v, int) {
+                const int zb = sc.bin(v);
+                if (zb < BINS) add(zb, mass ? sc.weight(v) : 0u);
+            });
+        });
+        unsigned tokens = 0;
+        u64 whole = 0;
+        for (int r = 0; r < G.size; ++r) tokens += G.of(S, r)->n_part, whole += G.of(S, r)->part;
+        Found f = find_bin(S, G, search, b, 0, 0, Target{mass, (unsigned)k, mass ? goal_of(whole) : 0});
+        // Tokens in bins down to the cut's: the set that it cuts.
+        const int z_bin = f.bin < 0 ? BINS - 1 : f.bin;
+        const unsigned set = f.bin < 0 ? tokens : f.above + f.count;
+        if (set <= MAX_LIST) {
+            // They move to the first CTA, in index order.
+            unsigned mine = 0;
+            each([&](float v, int) { mine += sc.bin(v) <= z_bin; });
+            mine = __reduce_add_sync(~0u, mine);
+            if (lane == 0) S.warp_at[warp] = (int)mine;
+            __syncthreads();
+            unsigned before = 0, all = 0;
+            for (int q = 0; q < WARPS; ++q) {
+                if (q == warp) before = all;
+                all += (unsigned)S.warp_at[q];
+            }
+            if (tid == 0) S.n_part = all;
+            G.sync();
+            unsigned n = 0;
+            for (int r = 0; r < G.size; ++r) {
+                const unsigned o = G.of(S, r)->n_part;
+                if (r < G.rank) before += o;
+                n += o;
+            }
+            Shared *to = G.of(S, 0);
+            if (mine)
+                in_order([&](float v, int i) {
+                    const bool is = i >= 0 && sc.bin(v) <= z_bin;
+                    const unsigned mask = __ballot_sync(~0u, is), slot = before + __popc(mask & ((1u << lane) - 1));
+                    if (is && slot < MAX_LIST) to->list_x[slot] = v, to->list_i[slot] = i;
+                    before += __popc(mask);
+                    return false;
+                });
+            G.sync();
+            if (G.rank != 0) return;
+            // From here on the first CTA alone.
+            n = min(n, (unsigned)MAX_LIST);
+            const Group<false> one{G.g, 1, 0};
+            const int per_warp = ((int)n + THREADS - 1) / THREADS * 32, l0 = min((int)n, warp * per_warp), l1 = min((int)n, l0 + per_warp);
+            auto each_listed = [&](auto fn) {
+                for (int i = l0 + lane; i < l1; i += 32) fn(S.list_x[i], S.list_i[i]);
+            };
+            auto listed_in_order = [&](auto fn) {
+                for (int i = l0; i < l1; i += 32) {
+                    const bool is = i + lane < l1;
+                    if (fn(is ? S.list_x[i + lane] : -INFINITY, is ? S.list_i[i + lane] : -1)) break;
+                }
+            };
+            auto whole_listed = [&]() {          // weight of the list's tokens
+                u64 w = 0;
+                each_listed([&](float v, int) { w += sc.weight(v); });
+                for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
+                __syncthreads();
+                if (lane == 0) S.warp_sum[warp] = w;
+                __syncthreads();
+                w = 0;
+                for (int q = 0; q < WARPS; ++q) w += S.warp_sum[q];
+                return w;
+            };
+            if (!mass) whole = f.bin >= 0 ? refine(S, one, search, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each_listed, listed_in_order)
+                                          : whole_listed();
+            if (!mass && f.bin >= 0 && by_p) {
+                // (counted without weights: the weight that top-k keeps)
+                u64 w = 0;
+                each_listed([&](float v, int i) {
+                    const int zb = sc.bin(v);
+                    const uint32_t key = key_of(v);
+                    if (zb < cut.z_bin || (zb == cut.z_bin && (key > cut.key || (key == cut.key && i <= cut.last)))) w += sc.weight(v);
+                });
+                for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
+                __syncthreads();
+                if (lane == 0) S.warp_sum[warp] = w;
+                __syncthreads();
+                whole = 0;
+                for (int q = 0; q < WARPS; ++q) whole += S.warp_sum[q];
+            }
+            if (by_p) {
+                const Target t{true, 0, goal_of(whole)};
+                if (!mass) {
+                    const Bin lb = count_bins(S, one, search, [&](auto add) {
+                        each_listed([&](float v, int) { add(sc.bin(v), sc.weight(v)); });
+                    });
+                    f = find_bin(S, one, search, lb, 0, 0, t);
+                }
+                if (f.bin >= 0) refine(S, one, search, sc, Tk, f, t, cut, each_listed, listed_in_order);
+            }
+            draw(S, one, sc, cut, least, u, P.tokens + row, prob, each_listed, listed_in_order);
+            return;
+        }
+        // Too many tokens for one CTA: the cluster goes on, with weights.
+        const Bin wb = mass ? b : count_bins(S, G, search, [&](auto add) {
+            each([&](float v, int) {
+                const int zb = sc.bin(v);
+                if (zb < BINS) add(zb, sc.weight(v));
+            });
+        });
+        if (!mass) {
+            whole = 0;
+            for (int r = 0; r < G.size; ++r) whole += G.of(S, r)->part;
+            f = find_bin(S, G, search, wb, 0, 0, Target{false, (unsigned)k, 0});
+            if (f.bin >= 0) whole = refine(S, G, search, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each, in_order);
+            if (by_p) {
+                const Target t{true, 0, goal_of(whole)};
+                f = find_bin(S, G, search, wb, 0, 0, t);
+                if (f.bin >= 0) refine(S, G, search, sc, Tk, f, t, cut, each, in_order);
+            }
+        } else if (f.bin >= 0) {
+            refine(S, G, search, sc, Tk, f, Target{true, 0, goal_of(whole)}, cut, each, in_order);
         }
     }
-    cluster.sync();              // the others may still read this CTA's sum
+    draw(S, G, sc, cut, least, u, P.tokens + row, prob, each, in_order);
+    G.sync();                    // (the others may still read this CTA's sum)
 }
 
 template <bool BF16, bool RESIDENT>
 cudaError_t launch(const Params &P, int cluster, int smem, cudaStream_t st) {
     auto k = sample_kernel<BF16, RESIDENT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SLICE_BYTES);
+    static unsigned attr_set = 0;   // one bit per device: limits raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned bit = 1u << (dev & 31);
+    if (!(__atomic_load_n(&attr_set, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SLICE_BYTES);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(P.rows * cluster));
     cfg.blockDim = dim3(THREADS);
@@ -423,14 +597,14 @@ extern "C" int tf_sample(const void *logits, int rows, int vocab, int64_t stride
     if (rc) return rc;
     // CTAs a row: as few as hold it in shared memory, more while SMs are idle and slices long.
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && ((long long)vocab * 4 > (long long)cluster * MAX_SLICE_BYTES ||
-                                     ((long long)rows * cluster * 2 <= nsm && vocab / cluster > 4096)))
+    while (cluster < MAX_CLUSTER && ((long long)vocab * es > (long long)cluster * MAX_SLICE_BYTES ||
+                                     ((long long)rows * cluster <= nsm && vocab / cluster > 8192)))
         cluster *= 2;
     const int slice = ((vocab + cluster - 1) / cluster + 7) / 8 * 8;
-    const bool resident = (long long)slice * 4 <= MAX_SLICE_BYTES;
+    const bool resident = (long long)slice * es <= MAX_SLICE_BYTES;
     const Params P{logits, stride, rows, vocab, slice, u, temperature, top_p, min_p, top_k, tokens, probs};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int smem = resident ? slice * 4 : 0;
+    const int smem = resident ? slice * es : 0;
     cudaError_t e;
     if (flags & TF_IN_BF16)
         e = resident ? launch<true, true>(P, cluster, smem, st) : launch<true, false>(P, cluster, smem, st);
