@@ -38,6 +38,7 @@ constexpr int MAX_CLUSTER = MAXC;
 constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit: 2^31
 // exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest.
 constexpr float BINS_PER_Z = BINS / 23.f;
+static_assert(BINS == THREADS, "a thread a bin");
 constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone
 #ifndef SLICE_KB
 #define SLICE_KB 80
@@ -110,9 +111,13 @@ struct Shared {
     int at;                      // its index
     unsigned n_part;             // this CTA's share of the bins (or of the tokens): tokens, weights
     u64 part;
+    u64 goal;                    // 64-bit products are one thread's work: the SM has few units for them
+    unsigned least;
     Found found[2];              // of alternate searches: a CTA may be one search ahead of another's readers
     int tie_last;
     unsigned n[BINS], lo[BINS], hi[BINS];       // tokens, and weights in 16-bit halves (a slice holds at most 2^16 tokens)
+    unsigned all_n[THREADS];     // what the ranks have in this CTA's share of the bins, rank by rank
+    u64 all_w[THREADS];
     float list_x[MAX_LIST];      // first CTA: the tokens that it finishes, in index order
     int list_i[MAX_LIST];
 };
@@ -130,6 +135,48 @@ struct Group {
     }
     __device__ __forceinline__ Shared *of(Shared &S, int r) const { return CLUSTER ? g.map_shared_rank(&S, r) : &S; }
 };
+
+// Sums of the ranks' n_part and part: over all of them, and over those before this one.
+struct Parts {
+    unsigned n, n_before;
+    u64 w, w_before;
+};
+template <bool CLUSTER>
+__device__ __forceinline__ Parts parts_of(Shared &S, const Group<CLUSTER> &G) {
+    const int lane = threadIdx.x & 31;
+    Parts p{0, 0, 0, 0};
+    if (lane < G.size) {
+        const Shared *o = G.of(S, lane);
+        p.n = o->n_part, p.w = o->part;
+        if (lane < G.rank) p.n_before = p.n, p.w_before = p.w;
+    }
+    if (CLUSTER)
+        for (int o = MAX_CLUSTER / 2; o > 0; o >>= 1) {
+            p.n += __shfl_xor_sync(~0u, p.n, o);
+            p.w += __shfl_xor_sync(~0u, p.w, o);
+            p.n_before += __shfl_xor_sync(~0u, p.n_before, o);
+            p.w_before += __shfl_xor_sync(~0u, p.w_before, o);
+        }
+    p.n = __shfl_sync(~0u, p.n, 0);
+    p.w = __shfl_sync(~0u, p.w, 0);
+    p.n_before = __shfl_sync(~0u, p.n_before, 0);
+    p.w_before = __shfl_sync(~0u, p.w_before, 0);
+    return p;
+}
+// What lies in the warps before this one, and in all, of one number a warp (left in S.warp_sum by lane 0).
+__device__ __forceinline__ u64 warps_of(Shared &S, u64 mine, u64 &all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) S.warp_sum[warp] = mine;
+    __syncthreads();
+    u64 x = lane < WARPS ? S.warp_sum[lane] : 0, before = lane < warp ? x : 0;
+    for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(~0u, x, o);
+        before += __shfl_xor_sync(~0u, before, o);
+    }
+    all = x;
+    return before;
+}
 
 // Counts every token f(slot) -> bin >= 0 (and its weight) in the bins, adds the
 // group's bins up, and gives thread t of rank r bin r * BINS / size + t with what
@@ -149,13 +196,19 @@ __device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, in
     });
     G.sync();
     Bin b{0, 0, 0, 0};
-    if (tid < share)
-        for (int r = 0; r < G.size; ++r) {
-            const Shared *o = G.of(S, r);
-            const int at = G.rank * share + tid;
-            b.n += o->n[at];
-            b.w += o->lo[at] + ((u64)o->hi[at] << 16);
-        }
+    if (G.size > 1) {
+        // A rank's bins of the share by `share` threads each, then the ranks added up.
+        const Shared *o = G.of(S, tid / share);
+        const int at = G.rank * share + tid % share;
+        S.all_n[tid] = o->n[at];
+        S.all_w[tid] = o->lo[at] + ((u64)o->hi[at] << 16);
+        __syncthreads();
+        if (tid < share)
+            for (int r = 0; r < G.size; ++r) b.n += S.all_n[r * share + tid], b.w += S.all_w[r * share + tid];
+    } else {
+        b.n = S.n[tid];
+        b.w = S.lo[tid] + ((u64)S.hi[tid] << 16);
+    }
     unsigned ni = b.n;
     u64 wi = b.w;
     for (int o = 1; o < 32; o <<= 1) {
@@ -169,12 +222,9 @@ __device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, in
     if (tid == share - 1) S.n_part = ni, S.part = wi;
     if (tid == 0) S.found[search & 1].bin = -1;
     G.sync();
-    for (int r = 0; r < G.rank; ++r) {
-        const Shared *o = G.of(S, r);
-        ni += o->n_part, wi += o->part;
-    }
-    b.n_before = ni - b.n;
-    b.w_before = wi - b.w;
+    const Parts p = parts_of(S, G);
+    b.n_before = p.n_before + ni - b.n;
+    b.w_before = p.w_before + wi - b.w;
     return b;
 }
 // The bin that the target falls into, with `above` and `mass_above` before all bins, known to every rank.
@@ -199,9 +249,8 @@ __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &s
     // Keys that the bin can hold, a little more at both ends.
     cut.z_bin = f.bin;
     cut.last = 0x7FFFFFFF;
-    const double lo = (f.bin + 1) * (1 + 1e-5) / BINS_PER_Z * (double)T, hi = f.bin * (1 - 1e-5) / BINS_PER_Z * (double)T;
-    uint32_t k_lo = f.bin == BINS - 1 ? 0u : key_of(__double2float_rd((double)sc.top - lo) + 0.f);
-    uint32_t k_hi = key_of(__double2float_ru((double)sc.top - hi) + 0.f);
+    uint32_t k_lo = key_of(__fsub_rd(sc.top, (f.bin + 1) * (1.00001f / BINS_PER_Z) * T) + 0.f);
+    uint32_t k_hi = key_of(__fsub_ru(sc.top, f.bin * (0.99999f / BINS_PER_Z) * T) + 0.f);
     while (f.count > 1 && k_lo < k_hi && (t.by_mass || f.above + f.count != t.want)) {
         int shift = 0;
         while (((k_hi - k_lo) >> shift) >= (uint32_t)BINS) ++shift;
@@ -225,20 +274,15 @@ __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &s
     const u64 w = f.mass / f.count;              // (a bin that a weight is reached in has some)
     const unsigned need = t.by_mass ? (unsigned)((t.goal - f.mass_above + w - 1) / w) : t.want - f.above;
     if (need >= f.count) return f.mass_above + f.mass;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     unsigned mine = 0;
     each([&](float v, int) { mine += key_of(v) == k_lo; });
     mine = __reduce_add_sync(~0u, mine);
-    if (lane == 0) S.warp_at[warp] = (int)mine;
-    __syncthreads();
-    unsigned before = 0, all = 0;
-    for (int q = 0; q < WARPS; ++q) {
-        if (q == warp) before = all;
-        all += (unsigned)S.warp_at[q];
-    }
-    if (threadIdx.x == 0) S.n_part = all;
+    u64 all;
+    unsigned before = (unsigned)warps_of(S, mine, all);
+    if (threadIdx.x == 0) S.n_part = (unsigned)all;
     G.sync();
-    for (int r = 0; r < G.rank; ++r) before += G.of(S, r)->n_part;
+    before += parts_of(S, G).n_before;
     if (before < need && before + mine >= need)
         in_order([&](float v, int i) {
             const bool is = i >= 0 && key_of(v) == k_lo;
@@ -257,7 +301,7 @@ __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &s
 template <bool CLUSTER, class Each, class InOrder>
 __device__ __forceinline__ void draw(Shared &S, const Group<CLUSTER> &G, const Scale &sc, const Cut &cut, unsigned least, float u,
                                      int *token, float *prob, Each each, InOrder in_order) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     auto kept = [&](float v, int i) {
         const int b = sc.bin(v);
         if (b > cut.z_bin) return 0u;
@@ -270,24 +314,16 @@ __device__ __forceinline__ void draw(Shared &S, const Group<CLUSTER> &G, const S
     u64 mine = 0;
     each([&](float v, int i) { mine += kept(v, i); });
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    __syncthreads();
-    if (lane == 0) S.warp_sum[warp] = mine;
-    __syncthreads();
-    u64 before = 0, all = 0;
-    for (int q = 0; q < WARPS; ++q) {
-        if (q == warp) before = all;
-        all += S.warp_sum[q];
-    }
+    u64 all, before = warps_of(S, mine, all);
     if (threadIdx.x == 0) S.part = all;
     G.sync();
-    u64 total = 0;
-    for (int r = 0; r < G.size; ++r) {
-        const u64 o = G.of(S, r)->part;
-        if (r < G.rank) before += o;
-        total += o;
-    }
+    const Parts parts = parts_of(S, G);
+    const u64 total = parts.w;
+    before += parts.w_before;
     // The running sum exceeds u * total where it exceeds its whole part (u from 1 on: the last token).
-    const u64 goal = (u64)fmax(0.0, fmin((double)u * (double)total, (double)total - 0.5));
+    if (threadIdx.x == 0) S.goal = (u64)fmax(0.0, fmin((double)u * (double)total, (double)total - 0.5));
+    __syncthreads();
+    const u64 goal = S.goal;
     if (before <= goal && before + mine > goal)
         in_order([&](float v, int i) {
             const unsigned w = i >= 0 ? kept(v, i) : 0u;
@@ -394,10 +430,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     if (tid == 0) {
         for (int q = 0; q < WARPS; ++q) top = fmaxf(top, S.warp_max[q]);
         S.max = top;
+        // The least whole weight of at least min_p times the largest.
+        const float mp = P.min_p && (!P.temperature || P.temperature[row] > 0.f) ? P.min_p[row] : 0.f;
+        S.least = mp > 0.f ? (unsigned)fmax(1.0, ceil((double)fminf(mp, 1.f) * 2147483648.0)) : 1u;
     }
     G.sync();
     top = -INFINITY;
-    for (int r = 0; r < G.size; ++r) top = fmaxf(top, G.of(S, r)->max);
+    if (lane < G.size) top = G.of(S, lane)->max;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     const float T = fminf(P.temperature ? P.temperature[row] : 1.f, FLT_MAX);
     if (top == -INFINITY) {
         if (G.rank == 0 && tid == 0) {
@@ -411,14 +451,16 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     const Scale sc{top, greedy ? 1.f : __fdiv_rn(1.f, T)};
     const float p = P.top_p ? P.top_p[row] : 1.f;
     const int k = greedy ? 1 : P.top_k ? P.top_k[row] : 0;       // (the first of the largest: the one token that top-k 1 keeps)
-    // The least whole weight of at least min_p times the largest.
-    const float mp = P.min_p && !greedy ? P.min_p[row] : 0.f;
-    const unsigned least = mp > 0.f ? (unsigned)fmax(1.0, ceil((double)fminf(mp, 1.f) * 2147483648.0)) : 1u;
     const bool by_k = k > 0 && k < P.vocab, by_p = p < 1.f && !greedy;
     const float u = P.u[row], Tk = greedy ? 1.f : T;
     float *prob = P.probs ? P.probs + row : nullptr;
     // The goal of top-p over a weight: the least whole number that reaches it, at least 1 (the first token).
-    auto goal_of = [&](u64 whole) { return (u64)fmax(1.0, ceil((double)p * (double)whole)); };
+    auto goal_of = [&](u64 whole) {
+        __syncthreads();
+        if (tid == 0) S.goal = (u64)fmax(1.0, ceil((double)p * (double)whole));
+        __syncthreads();
+        return S.goal;
+    };
 
     Cut cut{BINS - 1, 0, 0x7FFFFFFF};
     int search = 0;
@@ -430,9 +472,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 if (zb < BINS) add(zb, mass ? sc.weight(v) : 0u);
             });
         });
-        unsigned tokens = 0;
-        u64 whole = 0;
-        for (int r = 0; r < G.size; ++r) tokens += G.of(S, r)->n_part, whole += G.of(S, r)->part;
+        const Parts parts = parts_of(S, G);
+        const unsigned tokens = parts.n;
+        u64 whole = parts.w;
         Found f = find_bin(S, G, search, b, 0, 0, Target{mass, (unsigned)k, mass ? goal_of(whole) : 0});
         // Tokens in bins down to the cut's: the set that it cuts.
         const int z_bin = f.bin < 0 ? BINS - 1 : f.bin;
@@ -442,21 +484,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
             unsigned mine = 0;
             each([&](float v, int) { mine += sc.bin(v) <= z_bin; });
             mine = __reduce_add_sync(~0u, mine);
-            if (lane == 0) S.warp_at[warp] = (int)mine;
-            __syncthreads();
-            unsigned before = 0, all = 0;
-            for (int q = 0; q < WARPS; ++q) {
-                if (q == warp) before = all;
-                all += (unsigned)S.warp_at[q];
-            }
-            if (tid == 0) S.n_part = all;
+            u64 all;
+            unsigned before = (unsigned)warps_of(S, mine, all);
+            if (tid == 0) S.n_part = (unsigned)all;
             G.sync();
-            unsigned n = 0;
-            for (int r = 0; r < G.size; ++r) {
-                const unsigned o = G.of(S, r)->n_part;
-                if (r < G.rank) before += o;
-                n += o;
-            }
+            const Parts parts = parts_of(S, G);
+            before += parts.n_before;
+            unsigned n = parts.n;
             Shared *to = G.of(S, 0);
             if (mine)
                 in_order([&](float v, int i) {
@@ -485,12 +519,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 u64 w = 0;
                 each_listed([&](float v, int) { w += sc.weight(v); });
                 for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
-                __syncthreads();
-                if (lane == 0) S.warp_sum[warp] = w;
-                __syncthreads();
-                w = 0;
-                for (int q = 0; q < WARPS; ++q) w += S.warp_sum[q];
-                return w;
+                u64 all;
+                warps_of(S, w, all);
+                return all;
             };
             if (!mass) whole = f.bin >= 0 ? refine(S, one, search, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each_listed, listed_in_order)
                                           : whole_listed();
@@ -503,11 +534,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                     if (zb < cut.z_bin || (zb == cut.z_bin && (key > cut.key || (key == cut.key && i <= cut.last)))) w += sc.weight(v);
                 });
                 for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
-                __syncthreads();
-                if (lane == 0) S.warp_sum[warp] = w;
-                __syncthreads();
-                whole = 0;
-                for (int q = 0; q < WARPS; ++q) whole += S.warp_sum[q];
+                warps_of(S, w, whole);
             }
             if (by_p) {
                 const Target t{true, 0, goal_of(whole)};
@@ -519,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 }
                 if (f.bin >= 0) refine(S, one, search, sc, Tk, f, t, cut, each_listed, listed_in_order);
             }
-            draw(S, one, sc, cut, least, u, P.tokens + row, prob, each_listed, listed_in_order);
+            draw(S, one, sc, cut, S.least, u, P.tokens + row, prob, each_listed, listed_in_order);
             return;
         }
         // Too many tokens for one CTA: the cluster goes on, with weights.
@@ -530,8 +557,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
             });
         });
         if (!mass) {
-            whole = 0;
-            for (int r = 0; r < G.size; ++r) whole += G.of(S, r)->part;
+            whole = parts_of(S, G).w;
             f = find_bin(S, G, search, wb, 0, 0, Target{false, (unsigned)k, 0});
             if (f.bin >= 0) whole = refine(S, G, search, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each, in_order);
             if (by_p) {
@@ -543,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
             refine(S, G, search, sc, Tk, f, Target{true, 0, goal_of(whole)}, cut, each, in_order);
         }
     }
-    draw(S, G, sc, cut, least, u, P.tokens + row, prob, each, in_order);
+    draw(S, G, sc, cut, S.least, u, P.tokens + row, prob, each, in_order);
     G.sync();                    // (the others may still read this CTA's sum)
 }
 
