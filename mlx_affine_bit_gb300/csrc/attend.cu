@@ -8,6 +8,7 @@
 #include <mutex>
 #include <utility>
 
+#include "attend_prompt.cuh"
 #include "attend_rows.cuh"
 #include "kv.h"
 
@@ -99,6 +100,31 @@ int launch_rows(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
     return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_attend launch");
 }
 
+// The same for the prompt kernel: one CTA an SM.
+template <int D>
+int launch_prompt(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
+    constexpr int rows = 128 * attend::p_tiles(D), smem = attend::p_smem(D);
+    static unsigned attr_set = 0;   // one bit per device: shared-memory limit raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    const unsigned bit = 1u << (dev & 31);
+    if (!(__atomic_load_n(&attr_set, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(attend::prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return cuda_error(e, "kv_attend set-up");
+        __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
+    }
+    const long long grid = std::min({steps, (long long)nsm, (long long)attend::MAX_PARTS});
+    Ws w;
+    const int rc = workspace(st, (size_t)grid * 2 * rows * (D + 4), (size_t)grid, &w);
+    if (rc) return rc;
+    P.part = w.part;
+    P.count = w.count;
+    attend::prompt_kernel<D><<<(unsigned)grid, attend::P_THREADS, smem, st>>>(P);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_attend launch");
+}
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -147,14 +173,25 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     P.q_f32 = (flags & TF_IN_F32) != 0;
     const long long max_group_rows = (long long)batch->max_rows * P.group;
     if (max_group_rows > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "too many rows of one sequence");
-    const int nt = max_group_rows <= 8 ? 1 : 2;
-    const long long tiles = (max_group_rows + 8 * nt - 1) / (8 * nt);
+#ifndef PROMPT_ROWS
+#define PROMPT_ROWS 17
+#endif
+    const bool prompt = max_group_rows >= PROMPT_ROWS;
+    const int nt = max_group_rows <= 8 ? 1 : 2, tile_rows = prompt ? 128 * attend::p_tiles(kv->dim) : 8 * nt;
+    const long long tiles = (max_group_rows + tile_rows - 1) / tile_rows;
     long long span = batch->max_len;
     if (window > 0) span = std::min(span, (long long)window + batch->max_rows + 32);
-    const int step = attend::step_of(kv->dim);
+    const int step = prompt ? attend::KEYS : attend::step_of(kv->dim);
     const long long most = std::max(1LL, (1LL << 40) / (batch->n_seqs * (long long)kv->kv_heads));
     const long long steps = batch->n_seqs * (long long)kv->kv_heads * std::min(most, tiles * ((span + step - 1) / step));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (prompt) {
+        switch (kv->dim) {
+            case 64: return launch_prompt<64>(P, steps, nsm, st);
+            case 128: return launch_prompt<128>(P, steps, nsm, st);
+            default: return launch_prompt<256>(P, steps, nsm, st);
+        }
+    }
     switch (kv->dim) {
         case 64: return nt == 1 ? launch_rows<64, 1>(P, steps, nsm, st) : launch_rows<64, 2>(P, steps, nsm, st);
         case 128: return nt == 1 ? launch_rows<128, 1>(P, steps, nsm, st) : launch_rows<128, 2>(P, steps, nsm, st);

@@ -1,0 +1,792 @@
+// attend_prompt.cuh -- attention of many rows (prompts, chunks of prompts) over the
+// 8-bit paged cache, on the fifth-generation tensor cores.
+//
+// For the rows r of one (sequence, key/value head) -- G query heads a token -- and
+// the tokens j they see, with q_r in fp16 times a power of two:
+//     s_rj = (q_r . c_j) * (scale log2(e) ks_page / f_r)
+//     p_rj = 2^(s_rj - m_r),  l_r = sum_j p_rj,  out_r = sum_j p_rj vs_page c'_j / l_r
+// The first product runs over the keys' bytes as fp16 subnormals (c + 128) 2^-24
+// (its offset, 128 2^-24 sum(q_r), goes into the exponent's constant), the second
+// over the codes, exact in fp16, and w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16,
+// n_r the running maximum of s_rj + log2(vs_page): 11 bits down to 2^-29 of the
+// row's largest contribution, nothing below 2^-40.
+//
+// Bound by the tensor cores and, closely, by the instructions around them: per row
+// and token one exponential and about four others, per token and dimension of the
+// cache about two to widen a code.  A CTA (one an SM) works on two tiles of 128 rows
+// (dim 256: one) by steps of 128 tokens, so that one widening serves 256 rows and
+// one tile's softmax runs beside the other's products:
+//     8 warps    softmax, a row a thread: S out of tensor memory, the running maxima,
+//                w back into tensor memory as the second product's A operand; the
+//                rows of q; the outputs
+//     4 warps    keys and values from global memory through registers into shared
+//                memory as fp16 (K-major and MN-major with the 128-byte swizzle)
+//     1 thread   the products
+// The work -- for every tile pair and head the steps of the tokens it sees -- is one
+// line that the CTAs cut into equal shares; an item (one pair and head) that several
+// CTAs share is joined by the last of them to arrive, in their order.  Every wait is
+// bounded.
+#pragma once
+#include "attend_rows.cuh"
+#include "prompt_kernel.cuh"
+
+namespace tfq {
+namespace attend {
+
+constexpr int P_SOFT = 8, P_CONV = 4;            // softmax and widening warps; then four whose first lane issues products
+constexpr int P_THREADS = (P_SOFT + P_CONV + 4) * 32;
+// Registers a thread after the split, by warpgroup: with the 512 threads' 128 at launch as their sum's limit.
+template <int D>
+struct PRegs {
+    static constexpr int SOFT = D == 256 ? 208 : 176, CONV = D == 256 ? 200 : 104, REST = D == 256 ? 48 : 56;
+    static_assert((D == 256 ? SOFT + REST : 2 * SOFT) + CONV + REST <= 4 * 128, "registers of the launch");
+};
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr int KEYS = 128;                        // tokens of a step
+TFQ_HD constexpr int p_tiles(int d) { return d == 256 ? 1 : 2; }
+TFQ_HD constexpr int p_slots(int d) { return d == 256 ? 2 : 4; }          // fp16 tiles of keys or values in flight
+TFQ_HD constexpr int p_tile_bytes(int d) { return KEYS * d * 2; }         // one of them, and 128 rows of q
+TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p_tile_bytes(d); }
+constexpr int SCALES = 4;                        // steps whose scales are kept
+
+// One tile pair's tokens: [from, to) in steps.
+struct TileWork {
+    int from, to, steps;
+};
+struct PSeq {
+    SeqRows q;
+    int tiles;               // tile pairs of the sequence's rows
+};
+template <int R>
+__device__ __forceinline__ PSeq p_seq(const Params &P, int s) {
+    PSeq w;
+    w.q = seq_rows(P.b, s);
+    if (!w.q.ok) {
+        // Rows that lie within the matrices get zeros (no token is seen).
+        w.q.end = 0;
+        if (w.q.row0 < 0 || w.q.n < 0 || w.q.n > P.b.max_rows || w.q.row0 + w.q.n > P.b.rows) w.q.n = 0;
+    }
+    w.tiles = (w.q.n * P.group + R - 1) / R;
+    return w;
+}
+template <int R>
+__device__ __forceinline__ TileWork p_tile(const Params &P, const PSeq &w, int tile) {
+    const int first = w.q.end - w.q.n, r0 = tile * R, r1 = min(r0 + R, w.q.n * P.group) - 1;
+    TileWork t{0, w.q.end, 0};
+    if (P.causal) {
+        t.to = max(0, min(w.q.end, first + r1 / P.group + 1));
+        if (P.window) t.from = max(0, first + r0 / P.group - P.window + 1) & ~31;
+    }
+    t.steps = max(1, (t.to - t.from + KEYS - 1) / KEYS);
+    return t;
+}
+
+// A CTA's place on the line: sequence, tile pair and head, and its steps of that item.
+template <int R>
+struct Walk {
+    int seq, tile, h, step0, step1;
+    PSeq s;
+    TileWork t;
+    long long item_at, line, end;            // the item's first step, the CTA's next, the CTA's end
+    __device__ __forceinline__ void open(const Params &P) {
+        t = p_tile<R>(P, s, tile);
+        span();
+    }
+    __device__ __forceinline__ void span() {
+        step0 = (int)(line - item_at);
+        step1 = (int)min((long long)t.steps, end - item_at);
+    }
+    __device__ __forceinline__ bool next(const Params &P) {
+        line = item_at + step1;
+        if (line >= end) return false;
+        item_at = line;
+        if (++h == P.kv.kv_heads) {
+            h = 0;
+            if (++tile == s.tiles) {
+                tile = 0;
+                do s = p_seq<R>(P, ++seq);
+                while (s.tiles == 0);
+            }
+            t = p_tile<R>(P, s, tile);
+        }
+        span();
+        return true;
+    }
+};
+
+struct PromptHdr {
+    uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2], scales[4], joined[2], done;
+    uint32_t tmem;
+    int abort, last, seq, tile, h;
+    long long item_at, total, sums[P_THREADS / 32];
+    float2 scale[SCALES][8];                 // key scale, log2 of the value scale, of each 16 tokens (-1: no page)
+    uint8_t tail[64];
+};
+static_assert(sizeof(PromptHdr) <= 1024, "header");
+
+// Descriptors with the 128-byte swizzle: rows of 128 bytes in groups of eight, 1024 bytes apart; blocks of 64 values
+// (of the dimension) 128 rows apart.  K-major: the rows are the product's rows; MN-major: they are its K.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(KEYS * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+__device__ __forceinline__ constexpr uint32_t f16_idesc(int n, bool b_mn) {
+    return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bd), "r"(id), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+// Completes the loads issued so far; names the registers, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_constant__ Params P) {
+    constexpr int NT = p_tiles(D), R = 128 * NT, SLOTS = p_slots(D), TB = p_tile_bytes(D);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PromptHdr &B = *reinterpret_cast<PromptHdr *>(smem);
+    uint8_t *const q_s = smem + 1024, *const kv_s = q_s + NT * TB;
+    volatile int *abort = &B.abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = P.kv.kv_heads, G = P.group, BL = P.block_log2, BM = P.kv.block - 1;
+
+    // Tensor memory: per tile S (128 columns; w over it, dim 256 beside it twice) and the outputs (D columns).
+    constexpr uint32_t S_COL = 0, O_COL = NT * 128, W_COL = O_COL + D;   // (W_COL: dim 256 only, 2 x 64)
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&B.kv_full[i], P_CONV);
+            mbar_init(&B.kv_empty[i], 1);
+        }
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(&B.s_full[i], 1);
+            mbar_init(&B.p_full[i], 4);
+            mbar_init(&B.pv_done[i], 1);
+            mbar_init(&B.q_full[i], 4);
+            mbar_init(&B.o_free[i], 4);
+        }
+        for (int i = 0; i < SCALES; ++i) mbar_init(&B.scales[i], P_CONV);
+        for (int i = 0; i < 2; ++i) mbar_init(&B.joined[i], 4 * NT);
+        mbar_init(&B.done, 1);
+        B.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+
+    // The line's length and this CTA's share: first the tile pairs of all sequences, thread by thread over the
+    // sequences, then their steps, thread by thread over the tile pairs.
+    long long *const flat = reinterpret_cast<long long *>(q_s), *const steps_at = flat + P_THREADS;   // (q's place, before q)
+    auto scan = [&](long long mine, long long *out) {        // exclusive, into out[tid]; returns the sum
+        long long x = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) B.sums[warp] = x;
+        __syncthreads();
+        long long all = 0;
+        for (int i = 0; i < P_THREADS / 32; ++i) {
+            if (i < warp) x += B.sums[i];
+            all += B.sums[i];
+        }
+        out[tid] = x - mine;
+        __syncthreads();
+        return all;
+    };
+    const int per = (P.b.n_seqs + P_THREADS - 1) / P_THREADS;
+    long long pairs = 0;
+    for (int s = tid * per; s < min(P.b.n_seqs, (tid + 1) * per); ++s) {
+        const PSeq w = p_seq<R>(P, s);
+        if (!w.q.ok && blockIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
+        pairs += w.tiles;
+    }
+    const long long n_pairs = scan(pairs, flat);
+    // Tile pair f of the line: its sequence and place there.
+    auto pair_at = [&](long long f, int &s, int &tile, PSeq &w) {
+        int lo = 0, hi = P_THREADS - 1;                      // the last thread whose sequences begin at or before f
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (flat[mid] <= f) lo = mid; else hi = mid - 1;
+        }
+        long long at = flat[lo];
+        for (s = lo * per;; ++s) {
+            w = p_seq<R>(P, s);
+            if (f < at + w.tiles) break;
+            at += w.tiles;
+        }
+        tile = (int)(f - at);
+    };
+    const long long per_f = (n_pairs + P_THREADS - 1) / P_THREADS, f0 = min(n_pairs, tid * per_f), f1 = min(n_pairs, f0 + per_f);
+    long long steps = 0;
+    if (f0 < f1) {
+        int s, tile;
+        PSeq w;
+        pair_at(f0, s, tile, w);
+        for (long long f = f0; f < f1; ++f) {
+            while (tile == w.tiles) w = p_seq<R>(P, ++s), tile = 0;
+            steps += p_tile<R>(P, w, tile++).steps;
+        }
+    }
+    const long long total = H * scan(steps, steps_at);
+    const int C = (int)min((long long)gridDim.x, total);     // CTAs that get a share
+    const bool idle = (int)blockIdx.x >= C;
+    const long long u0 = idle ? 0 : total * blockIdx.x / C, u1 = idle ? 0 : total * (blockIdx.x + 1) / C;
+    if (!idle && f0 < f1 && H * steps_at[tid] <= u0 && u0 < H * (steps_at[tid] + steps)) {
+        int s, tile;
+        PSeq w;
+        pair_at(f0, s, tile, w);
+        long long at = H * steps_at[tid];
+        for (;;) {
+            while (tile == w.tiles) w = p_seq<R>(P, ++s), tile = 0;
+            const int n = p_tile<R>(P, w, tile).steps;
+            if (u0 < at + (long long)H * n) {
+                B.seq = s;
+                B.tile = tile;
+                B.h = (int)((u0 - at) / n);
+                B.item_at = at + (long long)B.h * n;
+                break;
+            }
+            at += (long long)H * n;
+            ++tile;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = B.tmem;
+    Walk<R> w;
+    if (!idle) {
+        w.seq = B.seq;
+        w.tile = B.tile;
+        w.h = B.h;
+        w.item_at = B.item_at;
+        w.line = u0;
+        w.end = u1;
+        w.s = p_seq<R>(P, w.seq);
+        w.open(P);
+    }
+    __syncthreads();                             // (q's place is free)
+
+    if (idle) {
+    } else if (warp >= P_SOFT + P_CONV) {
+        regs_down<PRegs<D>::REST>();
+        if (warp == P_SOFT + P_CONV && lane == 0) {
+            const uint32_t id_s = f16_idesc(KEYS, false), id_o = f16_idesc(D, true);
+            const uint64_t q_d = sw128_desc(smem_u32(q_s)), kv_d = sw128_desc(smem_u32(kv_s));
+            uint32_t st = 0, item = 0;           // steps and items so far
+            auto scores = [&](uint32_t step) {   // S = q . keys
+                const uint32_t kt = 2 * step, slot = kt % SLOTS;
+                mbar_wait(&B.kv_full[slot], (kt / SLOTS) & 1, abort, P.status);
+                for (int t = 0; t < NT; ++t) {
+                    // (w lies over S: the product that read it is done.)
+                    if (NT > 1 && step > 0) mbar_wait(&B.pv_done[t], (step - 1) & 1, abort, P.status);
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = ((k >> 2) * (KEYS * 128) + (k & 3) * 32) >> 4;
+                        prompt::mma_issue(tmem + S_COL + t * 128, q_d + ((t * TB) >> 4) + o, kv_d + ((slot * TB) >> 4) + o, id_s, k > 0);
+                    }
+                    prompt::mma_commit(&B.s_full[t]);
+                }
+                prompt::mma_commit(&B.kv_empty[slot]);
+            };
+            auto outputs = [&](uint32_t step, int t, bool acc) {     // O (+)= w . values
+                const uint32_t slot = (2 * step + 1) % SLOTS;
+                const uint32_t w_at = tmem + (NT > 1 ? S_COL + t * 128 : W_COL + (step & 1) * 64);
+#pragma unroll
+                for (int k = 0; k < KEYS / 16; ++k)
+                    mma_ts(tmem + O_COL + t * D, w_at + k * 8, kv_d + ((slot * TB + k * 2048) >> 4), id_o, acc || k > 0);
+                prompt::mma_commit(&B.pv_done[t]);
+            };
+            do {
+                for (int t = 0; t < NT; ++t) mbar_wait(&B.q_full[t], item & 1, abort, P.status);
+                scores(st);
+                for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
+                    const uint32_t vt = 2 * st + 1;
+                    const bool more = i + 1 < w.step1;
+                    if (NT == 1) {
+                        mbar_wait(&B.p_full[0], st & 1, abort, P.status);
+                        if (more) scores(st + 1);
+                    }
+                    mbar_wait(&B.kv_full[vt % SLOTS], (vt / SLOTS) & 1, abort, P.status);
+                    for (int t = 0; t < NT; ++t) {
+                        if (NT > 1) mbar_wait(&B.p_full[t], st & 1, abort, P.status);
+                        if (i == w.step0) mbar_wait(&B.o_free[t], (item & 1) ^ 1, abort, P.status);
+                        fence_after();
+                        outputs(st, t, i > w.step0);
+                    }
+                    prompt::mma_commit(&B.kv_empty[vt % SLOTS]);
+                    if (NT > 1 && more) scores(st + 1);
+                }
+                ++item;
+            } while (w.next(P) && !*abort);
+            prompt::mma_commit(&B.done);
+            mbar_wait(&B.done, 0, abort, P.status, false);
+        }
+    } else if (warp >= P_SOFT) {
+        if constexpr (PRegs<D>::CONV > 128)
+            regs_up<PRegs<D>::CONV>();
+        else
+            regs_down<PRegs<D>::CONV>();
+        // Widening: warp v takes tokens 32 v .. 32 v + 31 of every step, a lane 16 bytes of a token at a time.
+        constexpr int LPT = D / 16;              // lanes a token, and loads a lane
+        const int v = warp - P_SOFT, sub = lane % LPT;
+        uint32_t st = 0;
+        do {
+            const long long seq_table = w.seq * P.b.table_stride;
+            uint4 kr[LPT], vr[LPT];
+            int pages = -1;                      // lane 2 s + half: page of 16 tokens of step (base + s), and its scales
+            float2 scale = make_float2(-1.f, -INFINITY);
+            auto look_up = [&](int step) {
+                const int t = w.t.from + (step + (lane >> 1)) * KEYS + 32 * v + 16 * (lane & 1);
+                pages = -1;
+                scale = make_float2(-1.f, -INFINITY);
+                if (t < w.t.to) {
+                    const int page = P.b.table[seq_table + (t >> BL)];
+                    if (page < 0 || page >= P.kv.n_blocks) {
+                        atomicOr(P.status, STATUS_BOUNDS);
+                    } else {
+                        pages = page;
+                        const long long ph = (long long)page * H + w.h;
+                        scale = make_float2(P.kv.k_scale[ph], log2f(P.kv.v_scale[ph]));
+                    }
+                }
+            };
+            auto load = [&](const int8_t *pool, int step, int at, uint4 (&r)[LPT]) {      // step `at` of those looked up
+                const int p0 = __shfl_sync(~0u, pages, 2 * at), p1 = __shfl_sync(~0u, pages, 2 * at + 1);
+                const int t0 = w.t.from + step * KEYS + 32 * v;
+#pragma unroll
+                for (int j = 0; j < LPT; ++j) {
+                    const int tk = j * (32 / LPT) + lane / LPT, page = j < LPT / 2 ? p0 : p1;
+                    r[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (page >= 0)
+                        r[j] = *reinterpret_cast<const uint4 *>(pool + (((((long long)page * H + w.h) << BL) + ((t0 + tk) & BM)) * D) + 16 * sub);
+                }
+            };
+            // Where this lane's 16 values of token tk go: two 16-byte chunks, 2 sub and 2 sub + 1 of the row of blocks of eight.
+            auto store = [&](uint8_t *tile, const uint4 (&r)[LPT], const bool tiny) {
+#pragma unroll
+                for (int j = 0; j < LPT; ++j) {
+                    const int tk = 32 * v + j * (32 / LPT) + lane / LPT;
+                    uint8_t *row = tile + (sub >> 2) * (KEYS * 128) + tk * 128;
+                    const uint32_t x[4] = {r[j].x ^ 0x80808080u, r[j].y ^ 0x80808080u, r[j].z ^ 0x80808080u, r[j].w ^ 0x80808080u};
+                    uint32_t y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[2 * i] = tiny ? lo2_tiny(x[i]) : lo2(x[i]);
+                        y[2 * i + 1] = tiny ? hi2_tiny(x[i]) : hi2(x[i]);
+                    }
+                    // (Lanes of the second block of 64 store their second chunk first: no bank twice at a time.)
+                    const int c = (sub & 3) * 2, first = (sub >> 2) & 1;
+                    const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+                    *reinterpret_cast<uint4 *>(row + (((c + first) ^ (tk & 7)) << 4)) = first ? b : a;
+                    *reinterpret_cast<uint4 *>(row + (((c + 1 - first) ^ (tk & 7)) << 4)) = first ? a : b;
+                }
+            };
+            auto publish = [&](uint32_t kt) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.kv_full[kt % SLOTS]);
+            };
+            look_up(w.step0);
+            load(P.kv.k, w.step0, 0, kr);
+            load(P.kv.v, w.step0, 0, vr);
+            for (int i = w.step0, at = 0; i < w.step1 && !*abort; ++i, ++st) {
+                const float2 mine = make_float2(__shfl_sync(~0u, scale.x, 2 * at + (lane & 1)), __shfl_sync(~0u, scale.y, 2 * at + (lane & 1)));
+                // The next step's pages (16 steps at a time).
+                if (++at == 16) {
+                    look_up(i + 1);
+                    at = 0;
+                }
+                uint32_t kt = 2 * st;
+                mbar_wait(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
+                store(kv_s + (kt % SLOTS) * TB, kr, true);
+                if (lane < 2) B.scale[st % SCALES][2 * v + lane] = mine;
+                publish(kt);
+                if (lane == 0) mbar_arrive(&B.scales[st % SCALES]);
+                if (i + 1 < w.step1) load(P.kv.k, i + 1, at, kr);
+                kt = 2 * st + 1;
+                mbar_wait(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
+                store(kv_s + (kt % SLOTS) * TB, vr, false);
+                publish(kt);
+                if (i + 1 < w.step1) load(P.kv.v, i + 1, at, vr);
+            }
+        } while (w.next(P) && !*abort);
+    } else if (warp >= 4 * NT) {
+        regs_down<PRegs<D>::REST>();
+    } else {
+        regs_up<PRegs<D>::SOFT>();
+        // Softmax: thread `row` of tile t.
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + S_COL + t * 128, o_at = tmem + lanes + O_COL + t * D;
+        const bool q16 = ((reinterpret_cast<uintptr_t>(P.q) | (uintptr_t)(P.q_stride * (P.q_f32 ? 4 : 2))) & 15) == 0;
+        const bool out16 = ((reinterpret_cast<uintptr_t>(P.out) | (uintptr_t)(P.out_stride * 2)) & 15) == 0;
+        uint32_t st = 0, item = 0, joins = 0;
+        RowSum sum{-INFINITY, -INFINITY, 0.f, 0.f};
+        // What the epilogue of an item needs after the walk has gone on.
+        struct Done {
+            uint16_t *out;       // null: not a row of the matrix
+            long long item_at;
+            int steps;
+        } last{nullptr, 0, 0};
+        auto epilogue = [&]() {
+            mbar_wait(&B.pv_done[t], (st - 1) & 1, abort, P.status);
+            fence_after();
+            auto store = [&](int d, const float (&y)[32]) {          // 32 values of the row
+                if (!last.out) return;
+                uint32_t h[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[e]) : "f"(y[2 * e + 1]), "f"(y[2 * e]));
+                if (out16) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint4 *>(last.out + d)[e] = make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        last.out[d + 2 * e] = (uint16_t)h[e];
+                        last.out[d + 2 * e + 1] = (uint16_t)(h[e] >> 16);
+                    }
+                }
+            };
+            auto cta_of = [&](long long u) { return (int)(((u + 1) * C - 1) / total); };
+            const int c_first = cta_of(last.item_at), parts = cta_of(last.item_at + last.steps - 1) - c_first + 1;
+            const int slot0 = 2 * c_first + (last.item_at > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
+            auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (c_first + k); };
+            // A part: [tile][D / 4][128 rows] of four outputs, after all parts [tile][128 rows] row sums.
+            float4 *const parts4 = reinterpret_cast<float4 *>(P.part);
+            float4 *const sums4 = parts4 + 2LL * gridDim.x * R * (D / 4);
+            const float f = out_factor(sum);
+            float4 *mine = parts4 + ((long long)slot(k_mine) * NT + t) * (D / 4) * 128 + row;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                uint32_t x[32];
+                tmem_ld32(o_at + d, x);
+                tmem_wait32(x);
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]);
+                if (parts == 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = sum.l == 0.f ? 0.f : y[e] * f;
+                    store(d, y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mine[(d / 4 + e) * 128] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.o_free[t]);
+            if (parts == 1) return;
+            sums4[((long long)slot(k_mine) * NT + t) * 128 + row] = make_float4(sum.m, sum.n, sum.l, 0.f);
+            __threadfence();
+            // (Bounded barriers of the softmax warps.)
+            auto meet = [&](int i) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.joined[i]);
+                mbar_wait(&B.joined[i], joins & 1, abort, P.status);
+            };
+            meet(0);
+            if (tid == 0) B.last = atomicAdd(P.count + c_first, 1) == parts - 1;
+            meet(1);
+            ++joins;
+            if (!B.last) return;
+            __threadfence();
+            if (tid == 0) P.count[c_first] = 0;
+            auto sum_of = [&](int k) {
+                const float4 x = __ldcg(sums4 + ((long long)slot(k) * NT + t) * 128 + row);
+                return RowSum{x.x, x.y, x.z, 0.f};
+            };
+            RowSum a{-INFINITY, -INFINITY, 0.f, 0.f};
+            for (int k = 0; k < parts; ++k) {
+                const RowSum x = sum_of(k);
+                a.m = fmaxf(a.m, x.m);
+                a.n = fmaxf(a.n, x.n);
+            }
+            for (int k = 0; k < parts; ++k) {
+                const RowSum x = sum_of(k);
+                a.l += x.l * l_factor(x, a.m);
+            }
+            const float fa = out_factor(a);
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = 0.f;
+                for (int k = 0; k < parts; ++k) {
+                    const float g = o_factor(sum_of(k), a.n);
+                    const float4 *src = parts4 + ((long long)slot(k) * NT + t) * (D / 4) * 128 + (d / 4) * 128 + row;
+                    float4 x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = __ldcg(src + e * 128);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // (a part that saw nothing of this row holds no numbers)
+                        y[4 * e] = g == 0.f ? y[4 * e] : fmaf(x[e].x, g, y[4 * e]);
+                        y[4 * e + 1] = g == 0.f ? y[4 * e + 1] : fmaf(x[e].y, g, y[4 * e + 1]);
+                        y[4 * e + 2] = g == 0.f ? y[4 * e + 2] : fmaf(x[e].z, g, y[4 * e + 2]);
+                        y[4 * e + 3] = g == 0.f ? y[4 * e + 3] : fmaf(x[e].w, g, y[4 * e + 3]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = a.l == 0.f ? 0.f : y[e] * fa;
+                store(d, y);
+            }
+        };
+        do {
+            // This thread's row of q.
+            const int n_rows = w.s.q.n * G, gr = w.tile * R + t * 128 + row;
+            const bool real = gr < n_rows;
+            const int gc = min(gr, n_rows - 1), i_tok = gc / G, head = w.h * G + gc - i_tok * G;
+            const long long q_at = (long long)(w.s.q.row0 + i_tok) * P.q_stride + (long long)head * D;
+            float amax = 0.f;
+            auto q8 = [&](int d, float (&x)[8]) {
+                if (P.q_f32) {
+                    const float *src = static_cast<const float *>(P.q) + q_at + d;
+                    if (q16) {
+                        const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
+                        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = src[e];
+                    }
+                } else {
+                    const uint16_t *src = static_cast<const uint16_t *>(P.q) + q_at + d;
+                    if (q16) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(src);
+                        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(u[e] << 16), x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((uint32_t)src[e] << 16);
+                    }
+                }
+            };
+#pragma unroll 4
+            for (int d = 0; d < D; d += 8) {
+                float x[8];
+                q8(d, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            }
+            const float fq = row_factor(amax), sq = P.scale < 0.f ? -fq : fq;
+            float sum_q = 0.f;
+            uint8_t *const q_row = q_s + t * TB + row * 128;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 8) {
+                float x[8];
+                q8(d, x);
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = pack_half(x[2 * e] * sq, x[2 * e + 1] * sq);
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+                    sum_q += y.x + y.y;
+                }
+                *reinterpret_cast<uint4 *>(q_row + (d >> 6) * (KEYS * 128) + ((((d >> 3) & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.q_full[t]);
+            if (item > 0) epilogue();
+            last.out = real ? P.out + (long long)(w.s.q.row0 + i_tok) * P.out_stride + (long long)head * D : nullptr;
+            last.item_at = w.item_at;
+            last.steps = w.t.steps;
+            ++item;
+
+            // Factor of a score in tensor memory, and the offset that comes off it first; tokens that the row sees.
+            const float rowf = fabsf(P.scale) * 1.44269504088896340736f / fq * (1.f / TINY), off = sum_q * (-128.f * TINY);
+            const int first = w.s.q.end - w.s.q.n, pos = first + i_tok;
+            const int see_to = P.causal ? min(w.s.q.end, pos + 1) : w.s.q.end, see_from = P.window ? pos - P.window + 1 : 0;
+            const int g0 = min(w.tile * R + t * 128, n_rows - 1), g1 = min(w.tile * R + t * 128 + 127, n_rows - 1);
+            const int all_to = P.causal ? min(w.s.q.end, first + g0 / G + 1) : w.s.q.end;
+            const int all_from = P.window ? first + g1 / G - P.window + 1 : 0;
+            sum = RowSum{-INFINITY, -INFINITY, 0.f, 0.f};
+            for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
+                const int t0 = w.t.from + i * KEYS;
+                mbar_wait(&B.s_full[t], st & 1, abort, P.status);
+                mbar_wait(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);
+                fence_after();
+                float2 sc[8];
+                bool full = t0 >= all_from && t0 + KEYS <= all_to;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    sc[g] = B.scale[st % SCALES][g];
+                    full = full && sc[g].x >= 0.f;
+                }
+                auto seen = [&](int j, int g) { return j >= see_from && j < see_to && sc[g].x >= 0.f; };
+                // The maxima of s and of s + log2(vs).
+                float mt = sum.m, nt = sum.n;
+                uint32_t xa[32], xb[32];
+                auto maxima = [&](int c, uint32_t (&x)[32]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * c + h;
+                        const float f = rowf * sc[g].x;
+                        float top = -INFINITY;
+                        if (full) {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
+                            top = (top + off) * f;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (seen(t0 + 16 * g + e, g)) top = fmaxf(top, (__uint_as_float(x[16 * h + e]) + off) * f);
+                        }
+                        mt = fmaxf(mt, top);
+                        nt = fmaxf(nt, top + sc[g].y);
+                    }
+                };
+                tmem_ld32(s_at, xa);
+                tmem_wait32(xa);
+                tmem_ld32(s_at + 32, xb);
+                maxima(0, xa);
+                tmem_wait32(xb);
+                tmem_ld32(s_at + 64, xa);
+                maxima(1, xb);
+                tmem_wait32(xa);
+                tmem_ld32(s_at + 96, xb);
+                maxima(2, xa);
+                tmem_wait32(xb);
+                maxima(3, xb);
+                const float mm = mt == -INFINITY ? 0.f : mt;
+                if (sum.l != 0.f) sum.l *= exp2_fast(sum.m - mt);
+                const bool grew = nt > sum.n;
+                const float shrink = sum.n == -INFINITY ? 0.f : exp2_fast(sum.n - nt);
+                sum.m = mt;
+                sum.n = nt;
+                auto rescale = [&]() {           // the outputs so far, to the new maximum
+                    if (i > w.step0 && __any_sync(~0u, grew)) {
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(o_at + d, x);
+                            tmem_wait32(x);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * shrink);
+                            tmem_st32(o_at + d, x);
+                        }
+                    }
+                };
+                tmem_ld32(s_at, xa);
+                if (NT > 1) rescale();           // (every earlier product is done: this step's scores were issued after them)
+                // The weights w, over S (dim 256: beside it).
+                const uint32_t w_at = NT > 1 ? s_at : tmem + lanes + W_COL + (st & 1) * 64;
+                float l0 = 0.f, l1 = 0.f;
+                auto weights = [&](int c, uint32_t (&x)[32]) {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * c + h;
+                        const float f = rowf * sc[g].x, k = off * f - mm;
+                        const float fw = nt == -INFINITY ? 0.f : exp2_fast(fminf(mm + sc[g].y - nt + W_EXP, 115.f));
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float a = fmaf(__uint_as_float(x[16 * h + e]), f, k), b = fmaf(__uint_as_float(x[16 * h + e + 1]), f, k);
+                            if (!full) {
+                                if (!seen(t0 + 16 * g + e, g)) a = -INFINITY;
+                                if (!seen(t0 + 16 * g + e + 1, g)) b = -INFINITY;
+                            }
+                            a = exp2_fast(a);
+                            b = exp2_fast(b);
+                            l0 += a;
+                            l1 += b;
+                            y[8 * h + e / 2] = pack_half(a * fw, b * fw);
+                        }
+                    }
+                    tmem_st16(w_at + 16 * c, y);
+                };
+                tmem_wait32(xa);
+                tmem_ld32(s_at + 32, xb);
+                weights(0, xa);
+                tmem_wait32(xb);
+                tmem_ld32(s_at + 64, xa);
+                weights(1, xb);
+                tmem_wait32(xa);
+                tmem_ld32(s_at + 96, xb);
+                weights(2, xa);
+                tmem_wait32(xb);
+                weights(3, xb);
+                sum.l += l0 + l1;
+                if (NT == 1 && i > w.step0) {
+                    // (The last step's product runs beside the exponentials.)
+                    mbar_wait(&B.pv_done[0], (st - 1) & 1, abort, P.status);
+                    fence_after();
+                    rescale();
+                }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.p_full[t]);
+            }
+        } while (w.next(P) && !*abort);
+        epilogue();
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+}  // namespace attend
+}  // namespace tfq
