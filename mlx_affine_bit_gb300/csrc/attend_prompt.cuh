@@ -21,7 +21,7 @@
 //                rows of q; the outputs
 //     4 warps    keys and values from global memory through registers into shared
 //                memory as fp16 (K-major and MN-major with the 128-byte swizzle)
-//     1 thread   the products
+//     1 thread   a tile: its products
 // The work -- for every tile pair and head the steps of the tokens it sees -- is one
 // line that the CTAs cut into equal shares; an item (one pair and head) that several
 // CTAs share is joined by the last of them to arrive, in their order.  Every wait is
@@ -38,7 +38,7 @@ constexpr int P_THREADS = (P_SOFT + P_CONV + 4) * 32;
 // Registers a thread after the split, by warpgroup: with the 512 threads' 128 at launch as their sum's limit.
 template <int D>
 struct PRegs {
-    static constexpr int SOFT = D == 256 ? 208 : 176, CONV = D == 256 ? 200 : 104, REST = D == 256 ? 48 : 56;
+    static constexpr int SOFT = D == 256 ? 200 : 168, CONV = D == 256 ? 168 : 104, REST = 72;
     static_assert((D == 256 ? SOFT + REST : 2 * SOFT) + CONV + REST <= 4 * 128, "registers of the launch");
 };
 template <int N>
@@ -55,6 +55,10 @@ TFQ_HD constexpr int p_slots(int d) { return d == 256 ? 2 : 4; }          // fp1
 TFQ_HD constexpr int p_tile_bytes(int d) { return KEYS * d * 2; }         // one of them, and 128 rows of q
 TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p_tile_bytes(d); }
 constexpr int SCALES = 4;                        // steps whose scales are kept
+#ifndef ITEM_COST
+#define ITEM_COST 2
+#endif
+constexpr int ITEM_STEPS = ITEM_COST;            // an item's beginning and end on the line, in steps
 
 // One tile pair's tokens: [from, to) in steps.
 struct TileWork {
@@ -63,13 +67,16 @@ struct TileWork {
 struct PSeq {
     SeqRows q;
     int tiles;               // tile pairs of the sequence's rows
+    int plan;                // tokens that its place on the line is for
 };
 template <int R>
 __device__ __forceinline__ PSeq p_seq(const Params &P, int s) {
     PSeq w;
     w.q = seq_rows(P.b, s);
+    w.plan = max(0, min(w.q.end, P.b.max_len));
     if (!w.q.ok) {
-        // Rows that lie within the matrices get zeros (no token is seen).
+        // Rows that lie within the matrices get zeros (no token is seen; the line, and with it the other
+        // sequences' bits, stay as they are).
         w.q.end = 0;
         if (w.q.row0 < 0 || w.q.n < 0 || w.q.n > P.b.max_rows || w.q.row0 + w.q.n > P.b.rows) w.q.n = 0;
     }
@@ -78,35 +85,42 @@ __device__ __forceinline__ PSeq p_seq(const Params &P, int s) {
 }
 template <int R>
 __device__ __forceinline__ TileWork p_tile(const Params &P, const PSeq &w, int tile) {
-    const int first = w.q.end - w.q.n, r0 = tile * R, r1 = min(r0 + R, w.q.n * P.group) - 1;
-    TileWork t{0, w.q.end, 0};
+    const int first = w.plan - w.q.n, r0 = tile * R, r1 = min(r0 + R, w.q.n * P.group) - 1;
+    TileWork t{0, w.plan, 0};
     if (P.causal) {
-        t.to = max(0, min(w.q.end, first + r1 / P.group + 1));
+        t.to = max(0, min(w.plan, first + r1 / P.group + 1));
         if (P.window) t.from = max(0, first + r0 / P.group - P.window + 1) & ~31;
     }
     t.steps = max(1, (t.to - t.from + KEYS - 1) / KEYS);
+    if (!w.q.ok) t.to = 0;
     return t;
 }
 
-// A CTA's place on the line: sequence, tile pair and head, and its steps of that item.
+// A CTA's place on the line: sequence, tile pair and head, and its steps of that
+// item.  An item takes ITEM_STEPS (its beginning and end) and its steps of the line;
+// a CTA whose share ends in the former has none of the latter.
 template <int R>
 struct Walk {
     int seq, tile, h, step0, step1;
     PSeq s;
     TileWork t;
-    long long item_at, line, end;            // the item's first step, the CTA's next, the CTA's end
-    __device__ __forceinline__ void open(const Params &P) {
-        t = p_tile<R>(P, s, tile);
-        span();
-    }
+    long long item_at, begin, end;           // the item's first step; the CTA's share
     __device__ __forceinline__ void span() {
-        step0 = (int)(line - item_at);
+        step0 = (int)max(0LL, begin - item_at);
         step1 = (int)min((long long)t.steps, end - item_at);
     }
+    // The first item with steps of this CTA (from the one that holds its share's beginning), false if there is none.
+    __device__ __forceinline__ bool first(const Params &P, int seq_, int tile_, int h_, long long at, long long begin_, long long end_) {
+        seq = seq_, tile = tile_, h = h_, begin = begin_, end = end_;
+        s = p_seq<R>(P, seq);
+        t = p_tile<R>(P, s, tile);
+        item_at = at + ITEM_STEPS;
+        span();
+        return step0 < step1;                // (a share that begins in an item's first part and ends there: no other has a part of it)
+    }
     __device__ __forceinline__ bool next(const Params &P) {
-        line = item_at + step1;
-        if (line >= end) return false;
-        item_at = line;
+        const long long at = item_at + t.steps;
+        if (at + ITEM_STEPS >= end) return false;
         if (++h == P.kv.kv_heads) {
             h = 0;
             if (++tile == s.tiles) {
@@ -116,6 +130,7 @@ struct Walk {
             }
             t = p_tile<R>(P, s, tile);
         }
+        item_at = at + ITEM_STEPS;
         span();
         return true;
     }
@@ -146,6 +161,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bd), "r"(id), "r"((uint32_t)acc)
         : "memory");
+}
+// mbar_wait in few instructions (the kernel has many waits).
+__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
+    if (mbar_try(bar, parity)) return;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try(bar, parity) && !*abort)
+        if (global_ns() - t0 > WAIT_LIMIT_NS) {
+            *abort = 1;
+            atomicOr(status, STATUS_WAIT);
+        }
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -188,6 +213,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Pairs of fp32 values at once, each rounded as by itself.
+__device__ __forceinline__ void mul2(uint32_t &a, uint32_t &b, float f) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+r"(a), "+r"(b)
+        : "r"(__float_as_uint(f)));
+}
+__device__ __forceinline__ void fma2(uint32_t &a, uint32_t &b, float f, float k) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+r"(a), "+r"(b)
+        : "r"(__float_as_uint(f)), "r"(__float_as_uint(k)));
+}
+__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -209,7 +251,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&B.kv_full[i], P_CONV);
-            mbar_init(&B.kv_empty[i], 1);
+            mbar_init(&B.kv_empty[i], NT);
         }
         for (int i = 0; i < NT; ++i) {
             mbar_init(&B.s_full[i], 1);
@@ -220,7 +262,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         }
         for (int i = 0; i < SCALES; ++i) mbar_init(&B.scales[i], P_CONV);
         for (int i = 0; i < 2; ++i) mbar_init(&B.joined[i], 4 * NT);
-        mbar_init(&B.done, 1);
+        mbar_init(&B.done, NT);
         B.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -280,12 +322,12 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         pair_at(f0, s, tile, w);
         for (long long f = f0; f < f1; ++f) {
             while (tile == w.tiles) w = p_seq<R>(P, ++s), tile = 0;
-            steps += p_tile<R>(P, w, tile++).steps;
+            steps += p_tile<R>(P, w, tile++).steps + ITEM_STEPS;
         }
     }
     const long long total = H * scan(steps, steps_at);
     const int C = (int)min((long long)gridDim.x, total);     // CTAs that get a share
-    const bool idle = (int)blockIdx.x >= C;
+    bool idle = (int)blockIdx.x >= C;
     const long long u0 = idle ? 0 : total * blockIdx.x / C, u1 = idle ? 0 : total * (blockIdx.x + 1) / C;
     if (!idle && f0 < f1 && H * steps_at[tid] <= u0 && u0 < H * (steps_at[tid] + steps)) {
         int s, tile;
@@ -294,7 +336,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         long long at = H * steps_at[tid];
         for (;;) {
             while (tile == w.tiles) w = p_seq<R>(P, ++s), tile = 0;
-            const int n = p_tile<R>(P, w, tile).steps;
+            const int n = p_tile<R>(P, w, tile).steps + ITEM_STEPS;
             if (u0 < at + (long long)H * n) {
                 B.seq = s;
                 B.tile = tile;
@@ -311,67 +353,51 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
     fence_after();
     const uint32_t tmem = B.tmem;
     Walk<R> w;
-    if (!idle) {
-        w.seq = B.seq;
-        w.tile = B.tile;
-        w.h = B.h;
-        w.item_at = B.item_at;
-        w.line = u0;
-        w.end = u1;
-        w.s = p_seq<R>(P, w.seq);
-        w.open(P);
-    }
+    if (!idle) idle = !w.first(P, B.seq, B.tile, B.h, B.item_at, u0, u1);
     __syncthreads();                             // (q's place is free)
 
     if (idle) {
     } else if (warp >= P_SOFT + P_CONV) {
         regs_down<PRegs<D>::REST>();
-        if (warp == P_SOFT + P_CONV && lane == 0) {
+        if (warp < P_SOFT + P_CONV + NT && lane == 0) {
+            const int t = warp - (P_SOFT + P_CONV);
             const uint32_t id_s = f16_idesc(KEYS, false), id_o = f16_idesc(D, true);
-            const uint64_t q_d = sw128_desc(smem_u32(q_s)), kv_d = sw128_desc(smem_u32(kv_s));
+            const uint64_t q_d = sw128_desc(smem_u32(q_s + t * TB)), kv_d = sw128_desc(smem_u32(kv_s));
+            const uint32_t s_at = tmem + S_COL + t * 128, o_at = tmem + O_COL + t * D;
             uint32_t st = 0, item = 0;           // steps and items so far
             auto scores = [&](uint32_t step) {   // S = q . keys
                 const uint32_t kt = 2 * step, slot = kt % SLOTS;
-                mbar_wait(&B.kv_full[slot], (kt / SLOTS) & 1, abort, P.status);
-                for (int t = 0; t < NT; ++t) {
-                    // (w lies over S: the product that read it is done.)
-                    if (NT > 1 && step > 0) mbar_wait(&B.pv_done[t], (step - 1) & 1, abort, P.status);
-                    fence_after();
+                wait_for(&B.kv_full[slot], (kt / SLOTS) & 1, abort, P.status);
+                // (w lies over S: the product that read it is done.)
+                if (NT > 1 && step > 0) wait_for(&B.pv_done[t], (step - 1) & 1, abort, P.status);
+                fence_after();
+                const uint64_t k_d = kv_d + ((slot * TB) >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t o = ((k >> 2) * (KEYS * 128) + (k & 3) * 32) >> 4;
-                        prompt::mma_issue(tmem + S_COL + t * 128, q_d + ((t * TB) >> 4) + o, kv_d + ((slot * TB) >> 4) + o, id_s, k > 0);
-                    }
-                    prompt::mma_commit(&B.s_full[t]);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = ((k >> 2) * (KEYS * 128) + (k & 3) * 32) >> 4;
+                    prompt::mma_issue(s_at, q_d + o, k_d + o, id_s, k > 0);
                 }
+                prompt::mma_commit(&B.s_full[t]);
                 prompt::mma_commit(&B.kv_empty[slot]);
             };
-            auto outputs = [&](uint32_t step, int t, bool acc) {     // O (+)= w . values
-                const uint32_t slot = (2 * step + 1) % SLOTS;
-                const uint32_t w_at = tmem + (NT > 1 ? S_COL + t * 128 : W_COL + (step & 1) * 64);
-#pragma unroll
-                for (int k = 0; k < KEYS / 16; ++k)
-                    mma_ts(tmem + O_COL + t * D, w_at + k * 8, kv_d + ((slot * TB + k * 2048) >> 4), id_o, acc || k > 0);
-                prompt::mma_commit(&B.pv_done[t]);
-            };
             do {
-                for (int t = 0; t < NT; ++t) mbar_wait(&B.q_full[t], item & 1, abort, P.status);
+                wait_for(&B.q_full[t], item & 1, abort, P.status);
                 scores(st);
                 for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
-                    const uint32_t vt = 2 * st + 1;
+                    const uint32_t vt = 2 * st + 1, slot = vt % SLOTS;
                     const bool more = i + 1 < w.step1;
-                    if (NT == 1) {
-                        mbar_wait(&B.p_full[0], st & 1, abort, P.status);
-                        if (more) scores(st + 1);
-                    }
-                    mbar_wait(&B.kv_full[vt % SLOTS], (vt / SLOTS) & 1, abort, P.status);
-                    for (int t = 0; t < NT; ++t) {
-                        if (NT > 1) mbar_wait(&B.p_full[t], st & 1, abort, P.status);
-                        if (i == w.step0) mbar_wait(&B.o_free[t], (item & 1) ^ 1, abort, P.status);
-                        fence_after();
-                        outputs(st, t, i > w.step0);
-                    }
-                    prompt::mma_commit(&B.kv_empty[vt % SLOTS]);
+                    wait_for(&B.p_full[t], st & 1, abort, P.status);
+                    if (NT == 1 && more) scores(st + 1);
+                    wait_for(&B.kv_full[slot], (vt / SLOTS) & 1, abort, P.status);
+                    if (i == w.step0) wait_for(&B.o_free[t], (item & 1) ^ 1, abort, P.status);
+                    fence_after();
+                    // O (+)= w . values
+                    const uint32_t w_at = NT > 1 ? s_at : tmem + W_COL + (st & 1) * 64;
+                    const uint64_t v_d = kv_d + ((slot * TB) >> 4);
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k) mma_ts(o_at, w_at + k * 8, v_d + ((k * 2048) >> 4), id_o, i > w.step0 || k > 0);
+                    prompt::mma_commit(&B.pv_done[t]);
+                    prompt::mma_commit(&B.kv_empty[slot]);
                     if (NT > 1 && more) scores(st + 1);
                 }
                 ++item;
@@ -455,14 +481,14 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     at = 0;
                 }
                 uint32_t kt = 2 * st;
-                mbar_wait(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
+                wait_for(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
                 store(kv_s + (kt % SLOTS) * TB, kr, true);
                 if (lane < 2) B.scale[st % SCALES][2 * v + lane] = mine;
                 publish(kt);
                 if (lane == 0) mbar_arrive(&B.scales[st % SCALES]);
                 if (i + 1 < w.step1) load(P.kv.k, i + 1, at, kr);
                 kt = 2 * st + 1;
-                mbar_wait(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
+                wait_for(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
                 store(kv_s + (kt % SLOTS) * TB, vr, false);
                 publish(kt);
                 if (i + 1 < w.step1) load(P.kv.v, i + 1, at, vr);
@@ -487,7 +513,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             int steps;
         } last{nullptr, 0, 0};
         auto epilogue = [&]() {
-            mbar_wait(&B.pv_done[t], (st - 1) & 1, abort, P.status);
+            wait_for(&B.pv_done[t], (st - 1) & 1, abort, P.status);
             fence_after();
             auto store = [&](int d, const float (&y)[32]) {          // 32 values of the row
                 if (!last.out) return;
@@ -509,8 +535,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             };
             auto cta_of = [&](long long u) { return (int)(((u + 1) * C - 1) / total); };
             const int c_first = cta_of(last.item_at), parts = cta_of(last.item_at + last.steps - 1) - c_first + 1;
-            const int slot0 = 2 * c_first + (last.item_at > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
-            auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (c_first + k); };
+            const int k_mine = (int)blockIdx.x - c_first;
+            auto slot = [&](int k) { return 2 * (c_first + k) + (k == 0); };     // (of a CTA's first item, which it goes on with; of its last, which it begins)
             // A part: [tile][D / 4][128 rows] of four outputs, after all parts [tile][128 rows] row sums.
             float4 *const parts4 = reinterpret_cast<float4 *>(P.part);
             float4 *const sums4 = parts4 + 2LL * gridDim.x * R * (D / 4);
@@ -543,7 +569,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             auto meet = [&](int i) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B.joined[i]);
-                mbar_wait(&B.joined[i], joins & 1, abort, P.status);
+                wait_for(&B.joined[i], joins & 1, abort, P.status);
             };
             meet(0);
             if (tid == 0) B.last = atomicAdd(P.count + c_first, 1) == parts - 1;
@@ -598,44 +624,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             const bool real = gr < n_rows;
             const int gc = min(gr, n_rows - 1), i_tok = gc / G, head = w.h * G + gc - i_tok * G;
             const long long q_at = (long long)(w.s.q.row0 + i_tok) * P.q_stride + (long long)head * D;
-            float amax = 0.f;
-            auto q8 = [&](int d, float (&x)[8]) {
-                if (P.q_f32) {
-                    const float *src = static_cast<const float *>(P.q) + q_at + d;
-                    if (q16) {
-                        const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
-                        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = src[e];
-                    }
-                } else {
-                    const uint16_t *src = static_cast<const uint16_t *>(P.q) + q_at + d;
-                    if (q16) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(src);
-                        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(u[e] << 16), x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((uint32_t)src[e] << 16);
-                    }
-                }
-            };
-#pragma unroll 4
-            for (int d = 0; d < D; d += 8) {
-                float x[8];
-                q8(d, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-            }
-            const float fq = row_factor(amax), sq = P.scale < 0.f ? -fq : fq;
-            float sum_q = 0.f;
+            float amax = 0.f, sum_q = 0.f, fq, sq;
             uint8_t *const q_row = q_s + t * TB + row * 128;
-#pragma unroll 4
-            for (int d = 0; d < D; d += 8) {
-                float x[8];
-                q8(d, x);
+            auto put8 = [&](int d, const float (&x)[8]) {
                 uint32_t h[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -644,6 +635,64 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     sum_q += y.x + y.y;
                 }
                 *reinterpret_cast<uint4 *>(q_row + (d >> 6) * (KEYS * 128) + ((((d >> 3) & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            };
+            auto factors = [&]() {
+                fq = row_factor(amax);
+                sq = P.scale < 0.f ? -fq : fq;
+            };
+            if (!P.q_f32 && q16) {
+                // The whole row at once.
+                uint4 r[D / 8];
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + q_at);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) r[i] = src[i];
+                uint32_t top = 0;                // magnitudes of bf16 are ordered as their bits
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t u[4] = {r[i].x & 0x7FFF7FFFu, r[i].y & 0x7FFF7FFFu, r[i].z & 0x7FFF7FFFu, r[i].w & 0x7FFF7FFFu};
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3])));
+                }
+                amax = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+                factors();
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t u[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(u[e] << 16), x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                    put8(8 * i, x);
+                }
+            } else {
+                auto q8 = [&](int d, float (&x)[8]) {
+                    if (P.q_f32) {
+                        const float *src = static_cast<const float *>(P.q) + q_at + d;
+                        if (q16) {
+                            const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
+                            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = src[e];
+                        }
+                    } else {
+                        const uint16_t *src = static_cast<const uint16_t *>(P.q) + q_at + d;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((uint32_t)src[e] << 16);
+                    }
+                };
+#pragma unroll 8
+                for (int d = 0; d < D; d += 8) {
+                    float x[8];
+                    q8(d, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+                }
+                factors();
+#pragma unroll 8
+                for (int d = 0; d < D; d += 8) {
+                    float x[8];
+                    q8(d, x);
+                    put8(d, x);
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -664,51 +713,55 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             sum = RowSum{-INFINITY, -INFINITY, 0.f, 0.f};
             for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
                 const int t0 = w.t.from + i * KEYS;
-                mbar_wait(&B.s_full[t], st & 1, abort, P.status);
-                mbar_wait(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);
+                wait_for(&B.s_full[t], st & 1, abort, P.status);
+                wait_for(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);
                 fence_after();
-                float2 sc[8];
+                // (All loops over the columns stay loops: unrolled, the code of a step would not stay in the instruction caches.)
+                const float2 *const sc = B.scale[st % SCALES];
                 bool full = t0 >= all_from && t0 + KEYS <= all_to;
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    sc[g] = B.scale[st % SCALES][g];
-                    full = full && sc[g].x >= 0.f;
-                }
-                auto seen = [&](int j, int g) { return j >= see_from && j < see_to && sc[g].x >= 0.f; };
-                // The maxima of s and of s + log2(vs).
+                for (int g = 0; g < 8; ++g) full = full && sc[g].x >= 0.f;
+                // The maxima of s and of s + log2(vs): of 32 columns at a time, two groups of 16 tokens.
                 float mt = sum.m, nt = sum.n;
-                uint32_t xa[32], xb[32];
-                auto maxima = [&](int c, uint32_t (&x)[32]) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * c + h;
-                        const float f = rowf * sc[g].x;
-                        float top = -INFINITY;
-                        if (full) {
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
-                            top = (top + off) * f;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (seen(t0 + 16 * g + e, g)) top = fmaxf(top, (__uint_as_float(x[16 * h + e]) + off) * f);
-                        }
-                        mt = fmaxf(mt, top);
-                        nt = fmaxf(nt, top + sc[g].y);
-                    }
+                auto top_of = [&](int g, float top) {
+                    mt = fmaxf(mt, top);
+                    nt = fmaxf(nt, top + sc[g].y);
                 };
-                tmem_ld32(s_at, xa);
-                tmem_wait32(xa);
-                tmem_ld32(s_at + 32, xb);
-                maxima(0, xa);
-                tmem_wait32(xb);
-                tmem_ld32(s_at + 64, xa);
-                maxima(1, xb);
-                tmem_wait32(xa);
-                tmem_ld32(s_at + 96, xb);
-                maxima(2, xa);
-                tmem_wait32(xb);
-                maxima(3, xb);
+                if (full) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait32(x);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                top[0] = max3(top[0], __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
+                                top[1] = max3(top[1], __uint_as_float(x[16 * h + e + 2]), __uint_as_float(x[16 * h + e + 3]));
+                            }
+                            top_of(2 * c + h, (fmaxf(top[0], top[1]) + off) * (rowf * sc[2 * c + h].x));
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait32(x);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int g = 2 * c + h, j0 = t0 + 16 * g;
+                            const float f = rowf * sc[g].x;
+                            float top = -INFINITY;
+                            if (sc[g].x >= 0.f)
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (j0 + e >= see_from && j0 + e < see_to) top = fmaxf(top, (__uint_as_float(x[16 * h + e]) + off) * f);
+                            top_of(g, top);
+                        }
+                    }
+                }
                 const float mm = mt == -INFINITY ? 0.f : mt;
                 if (sum.l != 0.f) sum.l *= exp2_fast(sum.m - mt);
                 const bool grew = nt > sum.n;
@@ -723,54 +776,52 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                             tmem_ld32(o_at + d, x);
                             tmem_wait32(x);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * shrink);
+                            for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], shrink);
                             tmem_st32(o_at + d, x);
                         }
                     }
                 };
-                tmem_ld32(s_at, xa);
                 if (NT > 1) rescale();           // (every earlier product is done: this step's scores were issued after them)
                 // The weights w, over S (dim 256: beside it).
                 const uint32_t w_at = NT > 1 ? s_at : tmem + lanes + W_COL + (st & 1) * 64;
                 float l0 = 0.f, l1 = 0.f;
-                auto weights = [&](int c, uint32_t (&x)[32]) {
-                    uint32_t y[16];
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32], y[16];
+                    tmem_ld32(s_at + 32 * c, x);
+                    float f[2], k[2], fw[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * c + h;
-                        const float f = rowf * sc[g].x, k = off * f - mm;
-                        const float fw = nt == -INFINITY ? 0.f : exp2_fast(fminf(mm + sc[g].y - nt + W_EXP, 115.f));
+                        const float2 z = sc[2 * c + h];
+                        f[h] = rowf * z.x;
+                        k[h] = off * f[h] - mm;
+                        fw[h] = nt == -INFINITY ? 0.f : exp2_fast(fminf(mm + z.y - nt + W_EXP, 115.f));
+                    }
+                    tmem_wait32(x);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float a = fmaf(__uint_as_float(x[16 * h + e]), f, k), b = fmaf(__uint_as_float(x[16 * h + e + 1]), f, k);
-                            if (!full) {
-                                if (!seen(t0 + 16 * g + e, g)) a = -INFINITY;
-                                if (!seen(t0 + 16 * g + e + 1, g)) b = -INFINITY;
-                            }
-                            a = exp2_fast(a);
-                            b = exp2_fast(b);
-                            l0 += a;
-                            l1 += b;
-                            y[8 * h + e / 2] = pack_half(a * fw, b * fw);
+                    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], f[e >> 4], k[e >> 4]);
+                    if (!full) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int j = t0 + 32 * c + e;
+                            if (!(j >= see_from && j < see_to && sc[2 * c + (e >> 4)].x >= 0.f)) x[e] = __float_as_uint(-INFINITY);
                         }
                     }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float a = exp2_fast(__uint_as_float(x[e])), b = exp2_fast(__uint_as_float(x[e + 1]));
+                        add2(l0, l1, a, b);
+                        x[e] = __float_as_uint(a);
+                        x[e + 1] = __float_as_uint(b);
+                        mul2(x[e], x[e + 1], fw[e >> 4]);
+                        y[e / 2] = pack_half(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    }
                     tmem_st16(w_at + 16 * c, y);
-                };
-                tmem_wait32(xa);
-                tmem_ld32(s_at + 32, xb);
-                weights(0, xa);
-                tmem_wait32(xb);
-                tmem_ld32(s_at + 64, xa);
-                weights(1, xb);
-                tmem_wait32(xa);
-                tmem_ld32(s_at + 96, xb);
-                weights(2, xa);
-                tmem_wait32(xb);
-                weights(3, xb);
+                }
                 sum.l += l0 + l1;
                 if (NT == 1 && i > w.step0) {
                     // (The last step's product runs beside the exponentials.)
-                    mbar_wait(&B.pv_done[0], (st - 1) & 1, abort, P.status);
+                    wait_for(&B.pv_done[0], (st - 1) & 1, abort, P.status);
                     fence_after();
                     rescale();
                 }

@@ -179,14 +179,16 @@ template <int D, int R>
 __device__ __forceinline__ SeqWork seq_work(const Params &P, int s) {
     SeqWork w;
     w.q = seq_rows(P.b, s);
+    const int plan = max(0, min(w.q.end, P.b.max_len));
     if (!w.q.ok) {
-        // Rows that lie within the matrices get zeros (no token is seen).
+        // Rows that lie within the matrices get zeros (no token is seen; the line, and with it the other
+        // sequences' bits, stay as they are).
         w.q.end = 0;
         if (w.q.row0 < 0 || w.q.n < 0 || w.q.n > P.b.max_rows || w.q.row0 + w.q.n > P.b.rows) w.q.n = 0;
     }
     w.tiles = (w.q.n * P.group + R - 1) / R;
-    w.base = P.window ? max(0, w.q.end - w.q.n - P.window + 1) & ~31 : 0;
-    w.steps = max(1, (w.q.end - w.base + step_of(D) - 1) / step_of(D));
+    w.base = P.window ? max(0, plan - w.q.n - P.window + 1) & ~31 : 0;
+    w.steps = max(1, (plan - w.base + step_of(D) - 1) / step_of(D));
     return w;
 }
 
