@@ -56,8 +56,9 @@ TFQ_HD constexpr int p_tile_bytes(int d) { return KEYS * d * 2; }         // one
 TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p_tile_bytes(d); }
 constexpr int SCALES = 4;                        // steps whose scales are kept
 #ifndef ITEM_COST
-#define ITEM_COST 2
+#define ITEM_COST 4
 #endif
+constexpr float SLACK = 0.9f;                    // growth of a maximum that is let be (in powers of two)
 constexpr int ITEM_STEPS = ITEM_COST;            // an item's beginning and end on the line, in steps
 
 // One tile pair's tokens: [from, to) in steps.
@@ -137,29 +138,38 @@ struct Walk {
 };
 
 struct PromptHdr {
-    uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2], scales[4], joined[2], done;
+    uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2], scales[4], joined[2], turn[2], done;
     uint32_t tmem;
     int abort, last, seq, tile, h;
     long long item_at, total, sums[P_THREADS / 32];
     float2 scale[SCALES][8];                 // key scale, log2 of the value scale, of each 16 tokens (-1: no page)
+    uint32_t pages[SCALES];                  // a byte a widening warp: 1 if its tokens' pages are there
     uint8_t tail[64];
 };
 static_assert(sizeof(PromptHdr) <= 1024, "header");
 
 // Descriptors with the 128-byte swizzle: rows of 128 bytes in groups of eight, 1024 bytes apart; blocks of 64 values
 // (of the dimension) 128 rows apart.  K-major: the rows are the product's rows; MN-major: they are its K.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(KEYS * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
+// (Shared addresses end below 2^18: an offset moves the low word only.)
+__device__ __forceinline__ uint32_t sw128_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFF) | ((uint32_t)(KEYS * 128 >> 4) << 16); }
+constexpr uint32_t SW128_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ constexpr uint32_t f16_idesc(int n, bool b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd, uint32_t id, bool acc) {
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t id) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bd), "r"(id), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(id), "n"(SW128_HI), "n"((int)ACC)
+        : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t id) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(id), "n"(SW128_HI), "n"((int)ACC)
         : "memory");
 }
 // mbar_wait in few instructions (the kernel has many waits).
@@ -262,6 +272,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         }
         for (int i = 0; i < SCALES; ++i) mbar_init(&B.scales[i], P_CONV);
         for (int i = 0; i < 2; ++i) mbar_init(&B.joined[i], 4 * NT);
+        mbar_init(&B.turn[0], 1);
+        mbar_init(&B.turn[1], 1);
         mbar_init(&B.done, NT);
         B.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         if (warp < P_SOFT + P_CONV + NT && lane == 0) {
             const int t = warp - (P_SOFT + P_CONV);
             const uint32_t id_s = f16_idesc(KEYS, false), id_o = f16_idesc(D, true);
-            const uint64_t q_d = sw128_desc(smem_u32(q_s + t * TB)), kv_d = sw128_desc(smem_u32(kv_s));
+            const uint32_t q_d = sw128_lo(smem_u32(q_s + t * TB)), kv_d = sw128_lo(smem_u32(kv_s));
             const uint32_t s_at = tmem + S_COL + t * 128, o_at = tmem + O_COL + t * D;
             uint32_t st = 0, item = 0;           // steps and items so far
             auto scores = [&](uint32_t step) {   // S = q . keys
@@ -371,11 +383,14 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 // (w lies over S: the product that read it is done.)
                 if (NT > 1 && step > 0) wait_for(&B.pv_done[t], (step - 1) & 1, abort, P.status);
                 fence_after();
-                const uint64_t k_d = kv_d + ((slot * TB) >> 4);
+                const uint32_t k_d = kv_d + ((slot * TB) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t o = ((k >> 2) * (KEYS * 128) + (k & 3) * 32) >> 4;
-                    prompt::mma_issue(s_at, q_d + o, k_d + o, id_s, k > 0);
+                    if (k == 0)
+                        mma_ss<false>(s_at, q_d + o, k_d + o, id_s);
+                    else
+                        mma_ss<true>(s_at, q_d + o, k_d + o, id_s);
                 }
                 prompt::mma_commit(&B.s_full[t]);
                 prompt::mma_commit(&B.kv_empty[slot]);
@@ -387,18 +402,27 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     const uint32_t vt = 2 * st + 1, slot = vt % SLOTS;
                     const bool more = i + 1 < w.step1;
                     wait_for(&B.p_full[t], st & 1, abort, P.status);
+                    // (The tiles' products take turns: one's run beside the other's softmax.)
+#ifndef NOTURN
+                    if (NT > 1) wait_for(&B.turn[t], (st & 1) ^ (t == 0), abort, P.status);
+#endif
                     if (NT == 1 && more) scores(st + 1);
                     wait_for(&B.kv_full[slot], (vt / SLOTS) & 1, abort, P.status);
                     if (i == w.step0) wait_for(&B.o_free[t], (item & 1) ^ 1, abort, P.status);
                     fence_after();
                     // O (+)= w . values
                     const uint32_t w_at = NT > 1 ? s_at : tmem + W_COL + (st & 1) * 64;
-                    const uint64_t v_d = kv_d + ((slot * TB) >> 4);
+                    const uint32_t v_d = kv_d + ((slot * TB) >> 4);
+                    if (i == w.step0)
+                        mma_ts<false>(o_at, w_at, v_d, id_o);
+                    else
+                        mma_ts<true>(o_at, w_at, v_d, id_o);
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k) mma_ts(o_at, w_at + k * 8, v_d + ((k * 2048) >> 4), id_o, i > w.step0 || k > 0);
+                    for (int k = 1; k < KEYS / 16; ++k) mma_ts<true>(o_at, w_at + k * 8, v_d + ((k * 2048) >> 4), id_o);
                     prompt::mma_commit(&B.pv_done[t]);
                     prompt::mma_commit(&B.kv_empty[slot]);
                     if (NT > 1 && more) scores(st + 1);
+                    if (NT > 1) mbar_arrive(&B.turn[t ^ 1]);
                 }
                 ++item;
             } while (w.next(P) && !*abort);
@@ -412,7 +436,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             regs_down<PRegs<D>::CONV>();
         // Widening: warp v takes tokens 32 v .. 32 v + 31 of every step, a lane 16 bytes of a token at a time.
         constexpr int LPT = D / 16;              // lanes a token, and loads a lane
-        const int v = warp - P_SOFT, sub = lane % LPT;
+        // The low two bits of a lane are its place in 64 bytes, the next the token's parity: the eight lanes of a
+        // 16-byte store then meet eight different chunks under the swizzle.
+        const int v = warp - P_SOFT, sub = (lane & 3) | (LPT > 4 ? (lane >> 1) & (LPT - 4) : 0);
+        const int tok = ((lane >> 2) & 1) | (LPT == 4 ? (lane >> 2) & 6 : LPT == 8 ? (lane >> 3) & 2 : 0);
         uint32_t st = 0;
         do {
             const long long seq_table = w.seq * P.b.table_stride;
@@ -439,7 +466,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 const int t0 = w.t.from + step * KEYS + 32 * v;
 #pragma unroll
                 for (int j = 0; j < LPT; ++j) {
-                    const int tk = j * (32 / LPT) + lane / LPT, page = j < LPT / 2 ? p0 : p1;
+                    const int tk = j * (32 / LPT) + tok, page = j < LPT / 2 ? p0 : p1;
                     r[j] = make_uint4(0u, 0u, 0u, 0u);
                     if (page >= 0)
                         r[j] = *reinterpret_cast<const uint4 *>(pool + (((((long long)page * H + w.h) << BL) + ((t0 + tk) & BM)) * D) + 16 * sub);
@@ -449,7 +476,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             auto store = [&](uint8_t *tile, const uint4 (&r)[LPT], const bool tiny) {
 #pragma unroll
                 for (int j = 0; j < LPT; ++j) {
-                    const int tk = 32 * v + j * (32 / LPT) + lane / LPT;
+                    const int tk = 32 * v + j * (32 / LPT) + tok;
                     uint8_t *row = tile + (sub >> 2) * (KEYS * 128) + tk * 128;
                     const uint32_t x[4] = {r[j].x ^ 0x80808080u, r[j].y ^ 0x80808080u, r[j].z ^ 0x80808080u, r[j].w ^ 0x80808080u};
                     uint32_t y[8];
@@ -458,11 +485,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                         y[2 * i] = tiny ? lo2_tiny(x[i]) : lo2(x[i]);
                         y[2 * i + 1] = tiny ? hi2_tiny(x[i]) : hi2(x[i]);
                     }
-                    // (Lanes of the second block of 64 store their second chunk first: no bank twice at a time.)
-                    const int c = (sub & 3) * 2, first = (sub >> 2) & 1;
-                    const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-                    *reinterpret_cast<uint4 *>(row + (((c + first) ^ (tk & 7)) << 4)) = first ? b : a;
-                    *reinterpret_cast<uint4 *>(row + (((c + 1 - first) ^ (tk & 7)) << 4)) = first ? a : b;
+                    const int c = (sub & 3) * 2;
+                    *reinterpret_cast<uint4 *>(row + ((c ^ (tk & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(row + (((c + 1) ^ (tk & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                 }
             };
             auto publish = [&](uint32_t kt) {
@@ -484,6 +509,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 wait_for(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
                 store(kv_s + (kt % SLOTS) * TB, kr, true);
                 if (lane < 2) B.scale[st % SCALES][2 * v + lane] = mine;
+                const bool there = __all_sync(~0u, mine.x >= 0.f);
+                if (lane == 0) reinterpret_cast<uint8_t *>(&B.pages[st % SCALES])[v] = there;
                 publish(kt);
                 if (lane == 0) mbar_arrive(&B.scales[st % SCALES]);
                 if (i + 1 < w.step1) load(P.kv.k, i + 1, at, kr);
@@ -716,54 +743,54 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 wait_for(&B.s_full[t], st & 1, abort, P.status);
                 wait_for(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);
                 fence_after();
-                // (All loops over the columns stay loops: unrolled, the code of a step would not stay in the instruction caches.)
+                // (Loops over the columns stay loops: unrolled, a step's code would not stay in the instruction caches.)
                 const float2 *const sc = B.scale[st % SCALES];
-                bool full = t0 >= all_from && t0 + KEYS <= all_to;
-                for (int g = 0; g < 8; ++g) full = full && sc[g].x >= 0.f;
-                // The maxima of s and of s + log2(vs): of 32 columns at a time, two groups of 16 tokens.
-                float mt = sum.m, nt = sum.n;
-                auto top_of = [&](int g, float top) {
-                    mt = fmaxf(mt, top);
-                    nt = fmaxf(nt, top + sc[g].y);
+                // f(c, x) on the columns 32 c ..
+                auto columns = [&](auto f) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait32(x);
+                        f(c, x);
+                    }
                 };
-                if (full) {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tmem_ld32(s_at + 32 * c, x);
-                        tmem_wait32(x);
+                // Factor of a score; never 0, so that -inf stays -inf (a page of zeros has scores of 0 all the same).
+                auto factor = [&](float ks) { return fmaxf(rowf * ks, 1e-30f); };
+                if (t0 < all_from || t0 + KEYS > all_to || B.pages[st % SCALES] != 0x01010101u) {
+                    // Tokens that the row does not see, first.
+                    columns([&](int c, uint32_t (&x)[32]) {
+                        const int from = see_from - t0 - 32 * c, to = see_to - t0 - 32 * c;
+                        const bool p0 = sc[2 * c].x >= 0.f, p1 = sc[2 * c + 1].x >= 0.f;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                top[0] = max3(top[0], __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
-                                top[1] = max3(top[1], __uint_as_float(x[16 * h + e + 2]), __uint_as_float(x[16 * h + e + 3]));
-                            }
-                            top_of(2 * c + h, (fmaxf(top[0], top[1]) + off) * (rowf * sc[2 * c + h].x));
-                        }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tmem_ld32(s_at + 32 * c, x);
-                        tmem_wait32(x);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int g = 2 * c + h, j0 = t0 + 16 * g;
-                            const float f = rowf * sc[g].x;
-                            float top = -INFINITY;
-                            if (sc[g].x >= 0.f)
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (j0 + e >= see_from && j0 + e < see_to) top = fmaxf(top, (__uint_as_float(x[16 * h + e]) + off) * f);
-                            top_of(g, top);
-                        }
-                    }
+                        for (int e = 0; e < 32; ++e)
+                            if (e < from || e >= to || !(e < 16 ? p0 : p1)) x[e] = __float_as_uint(-INFINITY);
+                        tmem_st32(s_at + 32 * c, x);
+                    });
+                    tmem_wait_st();
                 }
-                const float mm = mt == -INFINITY ? 0.f : mt;
-                if (sum.l != 0.f) sum.l *= exp2_fast(sum.m - mt);
+                // The maxima of s and of s + log2(vs), by groups of 16 tokens.
+                float mt = sum.m, nt = sum.n;
+                columns([&](int c, uint32_t (&x)[32]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 z = sc[2 * c + h];
+                        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            top[0] = max3(top[0], __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
+                            top[1] = max3(top[1], __uint_as_float(x[16 * h + e + 2]), __uint_as_float(x[16 * h + e + 3]));
+                        }
+                        const float m = (fmaxf(top[0], top[1]) + off) * factor(z.x);
+                        mt = fmaxf(mt, m);
+                        nt = fmaxf(nt, m + z.y);
+                    }
+                });
+                // Maxima that have grown by less than SLACK stay as they are: w then reaches 2^(15 + SLACK), below fp16's end.
+                mt = mt > sum.m + SLACK ? mt : sum.m;
+                nt = nt > sum.n + SLACK ? nt : sum.n;
+                const float mm = mt == -INFINITY ? 0.f : mt, nn = nt == -INFINITY ? INFINITY : nt;
+                if (mt != sum.m && sum.l != 0.f) sum.l *= exp2_fast(sum.m - mt);
                 const bool grew = nt > sum.n;
                 const float shrink = sum.n == -INFINITY ? 0.f : exp2_fast(sum.n - nt);
                 sum.m = mt;
@@ -784,41 +811,25 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 if (NT > 1) rescale();           // (every earlier product is done: this step's scores were issued after them)
                 // The weights w, over S (dim 256: beside it).
                 const uint32_t w_at = NT > 1 ? s_at : tmem + lanes + W_COL + (st & 1) * 64;
-                float l0 = 0.f, l1 = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32], y[16];
-                    tmem_ld32(s_at + 32 * c, x);
-                    float f[2], k[2], fw[2];
+                columns([&](int c, uint32_t (&x)[32]) {
+                    uint32_t y[16];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        // w = 2^(s - m + e), p = w 2^-e with the page's e; below 2^-45 w is 0 in fp16 whatever it is.
                         const float2 z = sc[2 * c + h];
-                        f[h] = rowf * z.x;
-                        k[h] = off * f[h] - mm;
-                        fw[h] = nt == -INFINITY ? 0.f : exp2_fast(fminf(mm + z.y - nt + W_EXP, 115.f));
-                    }
-                    tmem_wait32(x);
+                        const float e0 = fminf(fmaxf(mm + z.y - nn + W_EXP, -45.f), 115.f), f = factor(z.x), k = off * f - mm + e0;
+                        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], f[e >> 4], k[e >> 4]);
-                    if (!full) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int j = t0 + 32 * c + e;
-                            if (!(j >= see_from && j < see_to && sc[2 * c + (e >> 4)].x >= 0.f)) x[e] = __float_as_uint(-INFINITY);
+                        for (int e = 16 * h; e < 16 * h + 16; e += 2) {
+                            fma2(x[e], x[e + 1], f, k);
+                            const float a = exp2_fast(__uint_as_float(x[e])), b = exp2_fast(__uint_as_float(x[e + 1]));
+                            add2(l0, l1, a, b);
+                            y[e / 2] = pack_half(a, b);
                         }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float a = exp2_fast(__uint_as_float(x[e])), b = exp2_fast(__uint_as_float(x[e + 1]));
-                        add2(l0, l1, a, b);
-                        x[e] = __float_as_uint(a);
-                        x[e + 1] = __float_as_uint(b);
-                        mul2(x[e], x[e + 1], fw[e >> 4]);
-                        y[e / 2] = pack_half(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        sum.l = fmaf(l0 + l1, exp2_fast(-e0), sum.l);
                     }
                     tmem_st16(w_at + 16 * c, y);
-                }
-                sum.l += l0 + l1;
+                });
                 if (NT == 1 && i > w.step0) {
                     // (The last step's product runs beside the exponentials.)
                     wait_for(&B.pv_done[0], (st - 1) & 1, abort, P.status);
