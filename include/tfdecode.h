@@ -100,6 +100,10 @@ int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k
  *   flags    TF_IN_F32; TF_KV_CAUSAL: a row sees the tokens up to its own
  *            position (its place among the sequence's last tokens), otherwise
  *            all kv_len.
+ *            TF_KV_BY_ROWS, TF_KV_BY_TILES: the kernel for few rows (16 at a
+ *            time, any number works) or the one for prompts (256 rows at a time on
+ *            the tcgen05 tensor cores), instead of the call's own choice by its
+ *            sizes -- for a caller that has measured its own.
  *   window   0, or with TF_KV_CAUSAL the number of latest tokens (its own
  *            included) that a row sees.
  * Precision: q enters the tensor cores as fp16 after an exact power-of-two
@@ -108,12 +112,17 @@ int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k
  * to fp16 (11 bits) relative to the row's largest for the second product (11 bits
  * down to 2^-29 of it, nothing below 2^-40); scores, maxima, sums and accumulators
  * are fp32; out is rounded once to bf16.
+ * A row's bits do not change from call to call with the same arguments; between
+ * calls of another batch they may, within that precision, because sequences are
+ * cut between the CTAs by the whole call's tokens.
  * Allocates a per-(device, stream) workspace for the parts of split sequences
  * (grown on demand; the first call on a stream must precede any graph capture
  * on it).
  */
 #define TF_IN_F32 4
 #define TF_KV_CAUSAL 8
+#define TF_KV_BY_ROWS 64
+#define TF_KV_BY_TILES 128
 int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const void *q, int64_t q_stride, int heads, void *out,
                  int64_t out_stride, float scale, int window, int flags, void *stream);
 

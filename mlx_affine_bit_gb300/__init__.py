@@ -35,6 +35,7 @@ SYMBOLS = ("tf_qmm", "tf_qmm_ex", "tf_qmm_prompt", "tf_qmm_gather", "tf_qmm_noal
 TF_LAUNCH_PDL, TF_LAUNCH_EARLY_WEIGHTS, TF_LAUNCH_EARLY_X = 1, 2, 4
 TF_OUT_BF16, TF_EPI_RELU2 = 1, 2
 TF_IN_F32, TF_KV_CAUSAL, TF_IN_BF16 = 4, 8, 16
+TF_KV_BY_ROWS, TF_KV_BY_TILES = 64, 128
 
 
 class TfError(RuntimeError):
@@ -438,8 +439,10 @@ class KvCache:
                    TF_OUT_BF16 if out[0].dtype == torch.bfloat16 else 0, stream)
         return out[0], out[1]
 
-    def attend(self, q, batch, out=None, scale=None, causal=True, window=0, stream=None):
-        """Attention of q [rows][heads * dim] (bf16 or fp32) over the cache; out is bf16, scale 1/sqrt(dim) by default."""
+    def attend(self, q, batch, out=None, scale=None, causal=True, window=0, stream=None, kernel=0):
+        """Attention of q [rows][heads * dim] (bf16 or fp32) over the cache; out is bf16, scale 1/sqrt(dim) by default.
+
+        kernel: 0 (by the call's sizes), TF_KV_BY_ROWS or TF_KV_BY_TILES."""
         import torch
         rows, width = q.shape
         qs = _rows(q, "q", (torch.bfloat16, torch.float32), batch.rows, width)
@@ -450,7 +453,7 @@ class KvCache:
             raise ValueError("q's rows must hold heads * dim values")
         tf_kv_attend(self.c, self._batch(batch), q, qs, width // self.dim, out, os_,
                      self.dim ** -0.5 if scale is None else scale, window,
-                     (TF_KV_CAUSAL if causal else 0) | (TF_IN_F32 if q.dtype == torch.float32 else 0), stream)
+                     (TF_KV_CAUSAL if causal else 0) | (TF_IN_F32 if q.dtype == torch.float32 else 0) | kernel, stream)
         return out
 
 

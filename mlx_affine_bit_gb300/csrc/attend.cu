@@ -132,8 +132,10 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const void *q, int64_t q_stride, int heads,
                             void *out, int64_t out_stride, float scale, int window, int flags, void *stream) {
     fail_message(TF_OK, "");
-    if (flags & ~(TF_IN_F32 | TF_KV_CAUSAL))
-        return fail_message(TF_EINVAL_FLAGS, "tf_kv_attend takes TF_IN_F32 and TF_KV_CAUSAL only");
+    if (flags & ~(TF_IN_F32 | TF_KV_CAUSAL | TF_KV_BY_ROWS | TF_KV_BY_TILES))
+        return fail_message(TF_EINVAL_FLAGS, "unknown attention flags");
+    if ((flags & TF_KV_BY_ROWS) && (flags & TF_KV_BY_TILES))
+        return fail_message(TF_EINVAL_FLAGS, "TF_KV_BY_ROWS and TF_KV_BY_TILES exclude each other");
     int rc = check_kv(kv);
     if (!rc) rc = check_batch(kv, batch);
     if (rc) return rc;
@@ -173,14 +175,25 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     P.q_f32 = (flags & TF_IN_F32) != 0;
     const long long max_group_rows = (long long)batch->max_rows * P.group;
     if (max_group_rows > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "too many rows of one sequence");
-#ifndef PROMPT_ROWS
-#define PROMPT_ROWS 17
-#endif
-    const bool prompt = max_group_rows >= PROMPT_ROWS;
-    const int nt = max_group_rows <= 8 ? 1 : 2, tile_rows = prompt ? 128 * attend::p_tiles(kv->dim) : 8 * nt;
-    const long long tiles = (max_group_rows + tile_rows - 1) / tile_rows;
     long long span = batch->max_len;
     if (window > 0) span = std::min(span, (long long)window + batch->max_rows + 32);
+    // Rows or prompt kernel: the one that is expected to take less time, by what they measured over 17 to 400
+    // rows of 1 to 16 sequences of 4000 and 60000 tokens.  The rows kernel takes 16 rows at a time (some 6.5 ns
+    // for 128 tokens of dim 128 with all SMs at work, on top of 12 us), the prompt kernel 256 (dim 256: 128;
+    // some 2.9 us for 128 tokens on one SM, on top of 45 us).  64 rows of 16 x 4000 tokens, dim 128: 110
+    // against 115 us; 128 rows 194 against 115; 128 rows of 1 x 4000 tokens 35 against 51.
+    bool prompt = (flags & TF_KV_BY_TILES) != 0;
+    if (max_group_rows > 16 && !(flags & (TF_KV_BY_ROWS | TF_KV_BY_TILES))) {
+        const double blocks = (double)batch->n_seqs * kv->kv_heads * (double)((span + 127) / 128);
+        const int pair = 128 * attend::p_tiles(kv->dim);
+        const double pairs = (double)((max_group_rows + pair - 1) / pair), items = (double)batch->n_seqs * kv->kv_heads * pairs;
+        const double ctas = std::min((double)nsm, items * attend::MAX_SHARE);
+        const double t_rows = 12e3 + 6.5 * blocks * (double)((max_group_rows + 15) / 16) * kv->dim / 128;
+        const double t_prompt = 45e3 + 2900.0 * blocks * pairs / ctas;
+        prompt = t_prompt < t_rows;
+    }
+    const int nt = max_group_rows <= 8 ? 1 : 2, tile_rows = prompt ? 128 * attend::p_tiles(kv->dim) : 8 * nt;
+    const long long tiles = (max_group_rows + tile_rows - 1) / tile_rows;
     const int step = prompt ? attend::KEYS : attend::step_of(kv->dim);
     const long long most = std::max(1LL, (1LL << 40) / (batch->n_seqs * (long long)kv->kv_heads));
     const long long steps = batch->n_seqs * (long long)kv->kv_heads * std::min(most, tiles * ((span + step - 1) / step));

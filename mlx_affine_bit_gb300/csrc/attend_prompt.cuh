@@ -55,11 +55,9 @@ TFQ_HD constexpr int p_slots(int d) { return d == 256 ? 2 : 4; }          // fp1
 TFQ_HD constexpr int p_tile_bytes(int d) { return KEYS * d * 2; }         // one of them, and 128 rows of q
 TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p_tile_bytes(d); }
 constexpr int SCALES = 4;                        // steps whose scales are kept
-#ifndef ITEM_COST
-#define ITEM_COST 4
-#endif
 constexpr float SLACK = 0.9f;                    // growth of a maximum that is let be (in powers of two)
-constexpr int ITEM_STEPS = ITEM_COST;            // an item's beginning and end on the line, in steps
+constexpr int ITEM_STEPS = 3;                    // an item's beginning and end on the line, in steps (2 to 6: 3 is fastest)
+constexpr int MAX_SHARE = 8;                     // CTAs an item, on average: one of them joins their parts
 
 // One tile pair's tokens: [from, to) in steps.
 struct TileWork {
@@ -338,7 +336,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         }
     }
     const long long total = H * scan(steps, steps_at);
-    const int C = (int)min((long long)gridDim.x, total);     // CTAs that get a share
+    const int C = (int)min((long long)gridDim.x, min(total, n_pairs * H * MAX_SHARE));     // CTAs that get a share
     bool idle = (int)blockIdx.x >= C;
     const long long u0 = idle ? 0 : total * blockIdx.x / C, u1 = idle ? 0 : total * (blockIdx.x + 1) / C;
     if (!idle && f0 < f1 && H * steps_at[tid] <= u0 && u0 < H * (steps_at[tid] + steps)) {
@@ -403,9 +401,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     const bool more = i + 1 < w.step1;
                     wait_for(&B.p_full[t], st & 1, abort, P.status);
                     // (The tiles' products take turns: one's run beside the other's softmax.)
-#ifndef NOTURN
                     if (NT > 1) wait_for(&B.turn[t], (st & 1) ^ (t == 0), abort, P.status);
-#endif
                     if (NT == 1 && more) scores(st + 1);
                     wait_for(&B.kv_full[slot], (vt / SLOTS) & 1, abort, P.status);
                     if (i == w.step0) wait_for(&B.o_free[t], (item & 1) ^ 1, abort, P.status);
