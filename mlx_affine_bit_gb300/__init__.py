@@ -162,10 +162,28 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream of the current device.  (Its handle without a Stream object, where torch
+    gives it: 0.3 us instead of 3.)"""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.current_stream()             # (initializes CUDA)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+        else:
+            device = torch._C._cuda_getDevice
+            _raw_stream = lambda: raw(device())                             # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -324,7 +342,7 @@ def _tensor(t, name, dtypes, shape=None, contiguous=True):
     """Refuse a tensor that a call could not take: TypeError for its type, ValueError for the rest."""
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if contiguous and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -333,10 +351,12 @@ def _tensor(t, name, dtypes, shape=None, contiguous=True):
 
 def _rows(t, name, dtypes, rows, width):
     """The row stride of a [rows][width] matrix whose rows are contiguous."""
-    _tensor(t, name, dtypes, (rows, width), contiguous=False)
-    if width > 1 and t.stride(1) != 1:
+    if t.dtype not in dtypes or t.shape != (rows, width):
+        _tensor(t, name, dtypes, (rows, width), contiguous=False)
+    stride = t.stride()
+    if width > 1 and stride[1] != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    return t.stride(0) if rows > 1 else max(width, t.stride(0))
+    return stride[0] if rows > 1 else max(width, stride[0])
 
 
 class KvBatch:
@@ -420,9 +440,9 @@ class KvCache:
 
     def append(self, k, v, batch, stream=None) -> None:
         """Quantize rows k, v [rows][kv_heads * dim] (row stride free) in as the batch's last tokens."""
-        width = self.kv_heads * self.dim
-        ks = _rows(k, "k", (self.dtype,), batch.rows, width)
-        vs = _rows(v, "v", (self.dtype,), batch.rows, width)
+        width, types = self.kv_heads * self.dim, (self.dtype,)
+        ks = _rows(k, "k", types, batch.rows, width)
+        vs = _rows(v, "v", types, batch.rows, width)
         tf_kv_append(self.c, self._batch(batch), k, ks, v, vs, stream)
 
     def read(self, batch, dtype=None, k_out=None, v_out=None, stream=None):
@@ -430,14 +450,23 @@ class KvCache:
         import torch
         dtype = dtype or self.dtype
         width = self.kv_heads * self.dim
-        out = [torch.empty((batch.rows, width), dtype=dtype, device=self.k.device) if t is None else t
-               for t in (k_out, v_out)]
-        strides = [_rows(t, "output", (torch.bfloat16, torch.float32), batch.rows, width) for t in out]
-        if out[0].dtype != out[1].dtype:
-            raise TypeError("k_out and v_out must have one type")
-        tf_kv_read(self.c, self._batch(batch), out[0], strides[0], out[1], strides[1],
-                   TF_OUT_BF16 if out[0].dtype == torch.bfloat16 else 0, stream)
-        return out[0], out[1]
+        types = (torch.bfloat16, torch.float32)
+        if k_out is None and v_out is None:
+            k_out = torch.empty((batch.rows, width), dtype=dtype, device=self.k.device)
+            v_out = torch.empty_like(k_out)
+            ks = vs = width
+            if dtype not in types:
+                raise TypeError("read gives bf16 or fp32")
+        else:
+            k_out = torch.empty((batch.rows, width), dtype=dtype, device=self.k.device) if k_out is None else k_out
+            v_out = torch.empty((batch.rows, width), dtype=dtype, device=self.k.device) if v_out is None else v_out
+            ks = _rows(k_out, "k_out", types, batch.rows, width)
+            vs = _rows(v_out, "v_out", types, batch.rows, width)
+            if k_out.dtype != v_out.dtype:
+                raise TypeError("k_out and v_out must have one type")
+        tf_kv_read(self.c, self._batch(batch), k_out, ks, v_out, vs,
+                   TF_OUT_BF16 if k_out.dtype == torch.bfloat16 else 0, stream)
+        return k_out, v_out
 
     def attend(self, q, batch, out=None, scale=None, causal=True, window=0, stream=None, kernel=0):
         """Attention of q [rows][heads * dim] (bf16 or fp32) over the cache; out is bf16, scale 1/sqrt(dim) by default.
@@ -448,7 +477,9 @@ class KvCache:
         qs = _rows(q, "q", (torch.bfloat16, torch.float32), batch.rows, width)
         if out is None:
             out = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device)
-        os_ = _rows(out, "out", (torch.bfloat16,), rows, width)
+            os_ = width
+        else:
+            os_ = _rows(out, "out", (torch.bfloat16,), rows, width)
         if width % self.dim:
             raise ValueError("q's rows must hold heads * dim values")
         tf_kv_attend(self.c, self._batch(batch), q, qs, width // self.dim, out, os_,
@@ -464,10 +495,11 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     rows, vocab = logits.shape
     stride = _rows(logits, "logits", (torch.float32, torch.bfloat16), rows, vocab)
     f32, i32 = (torch.float32,), (torch.int32,)
+    shape = (rows,)
     for t, name, types in ((u, "u", f32), (temperature, "temperature", f32), (top_k, "top_k", i32), (top_p, "top_p", f32),
                            (min_p, "min_p", f32), (tokens, "tokens", i32), (probs, "probs", f32)):
-        if t is not None:
-            _tensor(t, name, types, (rows,))
+        if t is not None and (t.dtype not in types or t.shape != shape or not t.is_contiguous()):
+            _tensor(t, name, types, shape)
     if tokens is None:
         tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if probs is None:
