@@ -28,6 +28,7 @@ struct AppendParams {
     const void *src[2];
     long long stride[2];
     int nb;                 // pages that a sequence's new tokens may touch
+    int block_log2, dim_log2;
     int *status;
 };
 
@@ -37,12 +38,19 @@ __device__ __forceinline__ float finite_mag(float x) {
     return a <= FLT_MAX ? a : 0.f;
 }
 
-__device__ __forceinline__ uint32_t code_of(float x, float scale) {
-    // 0 / 0 and NaN convert to 0; an infinity saturates and is clamped.
-    int c = __float2int_rn(__fdiv_rn(x, scale));
-    c = max(-127, min(127, c));
-    return (uint32_t)(c & 255);
-}
+// x / scale rounded: as x * (1 / scale), which is within 2^-23 of it, relatively (3e-5 of a code at most), and by
+// the division where that leaves the nearest code open (or 1 / scale overflows).
+struct Step {
+    float scale, inv;
+    bool slow;
+    __device__ __forceinline__ uint32_t code(float x) const {
+        float q = __fmul_rn(x, inv), r = rintf(q);
+        if (slow || fabsf(q - r) > 0.4999f) r = rintf(__fdiv_rn(x, scale));
+        // 0 / 0 and NaN convert to 0; an infinity saturates and is clamped.
+        const int c = max(-127, min(127, __float2int_rn(r)));
+        return (uint32_t)(c & 255);
+    }
+};
 
 __device__ __forceinline__ void load8(float (&x)[8], const float *p, bool vec) {
     if (vec) {
@@ -80,10 +88,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
         w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Step &s) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i >> 2] |= code_of(x[i], scale) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= s.code(x[i]) << (8 * (i & 3));
     return make_uint2(w[0], w[1]);
 }
 
@@ -99,61 +107,62 @@ constexpr int VPT = 4;      // 8-value vectors a thread: block * dim / 32 thread
 template <typename T>
 __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendParams P) {
     const tf_kv &kv = P.kv;
-    const int H = kv.kv_heads, B = kv.block, D = kv.dim;
-    unsigned id = blockIdx.x;
-    const int side = id & 1;
-    id >>= 1;
-    const int h = id % H;
-    id /= H;
-    const int j = id % P.nb, s = id / P.nb;
+    const int H = kv.kv_heads, BL = P.block_log2, DL = P.dim_log2, B = 1 << BL, D = 1 << DL;
+    const int side = blockIdx.y & 1, h = blockIdx.y >> 1;
+    const int s = P.nb == 1 ? blockIdx.x : blockIdx.x / P.nb, j = blockIdx.x - s * P.nb;
 
     const SeqRows q = seq_rows(P.b, s);
     const int slot = P.b.slots ? P.b.slots[s] : s;
     const int first = q.end - q.n;
-    const int pg = first / B + j;                   // page of the sequence
+    const int pg = (first >> BL) + j;               // page of the sequence
     if (q.n == 0) return;
     if (!q.ok || first < 0 || slot < 0 || slot >= kv.n_slots) {
         if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
         return;
     }
-    const int base = pg * B;                        // the page's first token
+    const int base = pg << BL;                      // the page's first token
     if (base >= q.end) return;
     const int page = P.b.table[s * P.b.table_stride + pg];
-    if (page < 0 || page >= kv.n_blocks) {
-        if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
-        return;
-    }
     const int lo = max(first, base) - base, hi = min(q.end, base + B) - base;   // new tokens of the page
-    const int pg0 = first / B, last = (q.end - 1) / B;
-    const bool begun = first % B != 0;
+    const int pg0 = first >> BL, last = (q.end - 1) >> BL;
+    const bool begun = (first & (B - 1)) != 0;
     // The last two pages; one whose half of the ring the begun page occupies is left to that page's CTA.
     const bool keep = pg >= last - 1 && !(begun && pg > pg0 && ((pg - pg0) & 1) == 0);
     const T *src = static_cast<const T *>(P.src[side]);
     const bool vec = ((reinterpret_cast<uintptr_t>(src) | (P.stride[side] * sizeof(T))) & 15) == 0;
-    int8_t *codes = (side ? kv.v : kv.k) + ((long long)page * H + h) * B * D;
-    float *scales = (side ? kv.v_scale : kv.k_scale) + (long long)page * H + h;
-    T *ring = static_cast<T *>(side ? kv.open_v : kv.open_k) + (((long long)slot * H + h) * 2 * B + base % (2 * B)) * D;
-    float *ring_max = kv.open_max + (((long long)slot * 2 + side) * H + h) * 2 * B + base % (2 * B);
+    T *ring = static_cast<T *>(side ? kv.open_v : kv.open_k) + ((((long long)slot * H + h) * 2 << BL) + (base & (2 * B - 1))) * D;
+    float *ring_max = kv.open_max + ((((long long)slot * 2 + side) * H + h) * 2 << BL) + (base & (2 * B - 1));
 
-    const int vd = D / 8;                           // vectors a token: 8, 16 or 32 lanes of one warp
+    const int VL = DL - 3, vd = 1 << VL;            // vectors a token: 8, 16 or 32 lanes of one warp
     const int nt = blockDim.x, tid = threadIdx.x;
     float x[VPT][8];
     float amax = 0.f;
-    const float old_scale = lo > 0 ? *scales : 0.f;
-    for (int t = tid; t < lo; t += nt) amax = fmaxf(amax, ring_max[t]);
+    // The new rows (and the begun page's earlier magnitudes), while the page is looked up.
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * nt, t = v / vd, d = (v - t * vd) * 8;
+        const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
+        if (t >= lo && t < hi) load8(x[i], src + (long long)(q.row0 + base + t - first) * P.stride[side] + (h << DL) + d, vec);
+    }
+    for (int t = tid; t < lo; t += nt) amax = fmaxf(amax, ring_max[t]);
+    if (page < 0 || page >= kv.n_blocks) {
+        if (tid == 0) atomicOr(P.status, STATUS_BOUNDS);
+        return;
+    }
+    int8_t *codes = (side ? kv.v : kv.k) + (((long long)page * H + h) << (BL + DL));
+    float *scales = (side ? kv.v_scale : kv.k_scale) + (long long)page * H + h;
+    const float old_scale = lo > 0 ? *scales : 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
         const bool mine = t >= lo && t < hi;
         float m = 0.f;
         if (mine) {
-            load8(x[i], src + (long long)(q.row0 + base + t - first) * P.stride[side] + h * D + d, vec);
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(x[i][e]));
         }
         for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         if (mine && keep) {
-            store8(ring + t * D + d, x[i]);
+            store8(ring + (t << DL) + d, x[i]);
             if (d == 0) ring_max[t] = m;
         }
         amax = fmaxf(amax, m);
@@ -170,23 +179,24 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendParams P) {
     const bool leaves = pg == pg0 && begun && other > pg;
     const bool again = lo > 0 && (scale != old_scale || leaves);
     if (tid == 0) *scales = scale;
+    const Step step{scale, __fdiv_rn(1.f, scale), scale < 1e-30f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * nt, t = v / vd, d = (v - t * vd) * 8;
-        if (t < lo && again) load8(x[i], ring + t * D + d, true);
-        if (t < hi && (t >= lo || again)) *reinterpret_cast<uint2 *>(codes + t * D + d) = codes8(x[i], scale);
+        const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
+        if (t < lo && again) load8(x[i], ring + (t << DL) + d, true);
+        if (t < hi && (t >= lo || again)) *reinterpret_cast<uint2 *>(codes + (t << DL) + d) = codes8(x[i], step);
     }
     if (leaves) {
         __syncthreads();
-        const int first_t = other * B, n = min(q.end - first_t, B);
+        const int first_t = other << BL, n = min(q.end - first_t, B);
         for (int i = 0; i < VPT; ++i) {
-            const int v = tid + i * nt, t = v / vd, d = (v - t * vd) * 8;
+            const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
             float y[8], m = 0.f;
             if (t < n) {
-                load8(y, src + (long long)(q.row0 + first_t + t - first) * P.stride[side] + h * D + d, vec);
+                load8(y, src + (long long)(q.row0 + first_t + t - first) * P.stride[side] + (h << DL) + d, vec);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(y[e]));
-                store8(ring + t * D + d, y);
+                store8(ring + (t << DL) + d, y);
             }
             for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
             if (t < n && d == 0) ring_max[t] = m;
@@ -202,58 +212,79 @@ struct ReadParams {
     void *out[2];
     long long stride[2];
     int tiles;              // tiles of READ_TOKENS tokens that a sequence may have
+    int block_log2, dim_log2;
+    int row_log2;           // threads a row: the 16-code vectors of a row, rounded up to a power of two (256 at most)
     int *status;
 };
-constexpr int READ_TOKENS = 16;
+constexpr int READ_TOKENS = 16, READ_THREADS = 256;
 
 // One CTA a (sequence, 16 of its rows, keys or values): a thread turns 16 codes
-// into 16 values of a row.
+// into 16 values of a row, for up to four rows at a time.
 template <typename T>
-__global__ void kv_read_kernel(const ReadParams P) {
+__global__ void __launch_bounds__(READ_THREADS) kv_read_kernel(const ReadParams P) {
     const tf_kv &kv = P.kv;
-    const int H = kv.kv_heads, B = kv.block, D = kv.dim;
-    unsigned id = blockIdx.x;
-    const int side = id & 1;
-    id >>= 1;
-    const int tile = id % P.tiles, s = id / P.tiles;
+    const int H = kv.kv_heads, BL = P.block_log2, DL = P.dim_log2, BM = kv.block - 1;
+    const int side = blockIdx.y;
+    const int s = P.tiles == 1 ? blockIdx.x : blockIdx.x / P.tiles, tile = blockIdx.x - s * P.tiles;
     if (!P.out[side]) return;
     const SeqRows q = seq_rows(P.b, s);
     if (!q.ok || q.end < q.n) {
         if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
         return;
     }
-    const int t0 = tile * READ_TOKENS;
-    const int nt = min(READ_TOKENS, q.n - t0);
-    const int vd = D / 16, per = H * vd;            // 16-code vectors a head, a row
+    const int t0 = tile * READ_TOKENS, nt = min(READ_TOKENS, q.n - t0);
+    if (nt <= 0) return;
+    const int VL = DL - 4, per = H << VL;           // 16-code vectors a head, a row
     T *out = static_cast<T *>(P.out[side]);
     const bool vec = ((reinterpret_cast<uintptr_t>(out) | (P.stride[side] * sizeof(T))) & 15) == 0;
-    for (int v = threadIdx.x; v < nt * per; v += blockDim.x) {
-        const int t = v / per, c = v - t * per, h = c / vd, d = (c - h * vd) * 16;
-        const int pos = q.end - q.n + t0 + t;
-        const int page = P.b.table[s * P.b.table_stride + pos / B];
-        if (page < 0 || page >= kv.n_blocks) {
-            atomicOr(P.status, STATUS_BOUNDS);
-            continue;
-        }
-        const long long ph = (long long)page * H + h;
-        const uint4 w = *reinterpret_cast<const uint4 *>((side ? kv.v : kv.k) + (ph * B + pos % B) * D + d);
-        const float scale = (side ? kv.v_scale : kv.k_scale)[ph];
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        float y[2][8];
+    const int step = READ_THREADS >> P.row_log2;    // rows at a time
+    const int32_t *table = P.b.table + s * P.b.table_stride;
+    const int8_t *pool = side ? kv.v : kv.k;
+    const float *scales = side ? kv.v_scale : kv.k_scale;
+    for (int c = threadIdx.x & ((1 << P.row_log2) - 1); c < per; c += 1 << P.row_log2) {
+        const int h = c >> VL, d = (c & ((1 << VL) - 1)) * 16;
+        for (int tb = threadIdx.x >> P.row_log2; tb < nt; tb += 4 * step) {
+            uint4 w[4];
+            float scale[4];
+            int page[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i >> 3][i & 7] = scale * (float)(int8_t)(u[i >> 2] >> (8 * (i & 3)));
-        T *dst = out + (long long)(q.row0 + t0 + t) * P.stride[side] + h * D + d;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[k][i] = __bfloat162float(__float2bfloat16_rn(y[k][i]));
+            for (int k = 0; k < 4; ++k) {
+                const int t = tb + k * step, pos = q.end - q.n + t0 + t;
+                page[k] = t < nt ? table[pos >> BL] : 0;
             }
-            if (vec) {
-                store8(dst + 8 * k, y[k]);
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[8 * k + i] = (T)y[k][i];
+            for (int k = 0; k < 4; ++k) {
+                const int t = tb + k * step, pos = q.end - q.n + t0 + t;
+                if (page[k] < 0 || page[k] >= kv.n_blocks) {
+                    atomicOr(P.status, STATUS_BOUNDS);
+                    page[k] = -1;
+                } else if (t < nt) {
+                    const long long ph = (long long)page[k] * H + h;
+                    w[k] = *reinterpret_cast<const uint4 *>(pool + (((ph << BL) + (pos & BM)) << DL) + d);
+                    scale[k] = scales[ph];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = tb + k * step;
+                if (t >= nt || page[k] < 0) continue;
+                const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                T *dst = out + (long long)(q.row0 + t0 + t) * P.stride[side] + (h << DL) + d;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        y[i] = scale[k] * (float)(int8_t)(u[2 * e + (i >> 2)] >> (8 * (i & 3)));
+                        if constexpr (sizeof(T) == 2) y[i] = __bfloat162float(__float2bfloat16_rn(y[i]));
+                    }
+                    if (vec) {
+                        store8(dst + 8 * e, y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst[8 * e + i] = (T)y[i];
+                    }
+                }
             }
         }
     }
@@ -313,15 +344,17 @@ extern "C" int tf_kv_append(const tf_kv *kv, const tf_kv_batch *batch, const voi
     int nsm = 0, *status = nullptr;
     rc = device_info(&nsm, &status);
     if (rc) return rc;
-    AppendParams P{*kv, *batch, {k, v}, {k_stride, v_stride}, (batch->max_rows + kv->block - 2) / kv->block + 1, status};
-    const long long grid = 2LL * kv->kv_heads * P.nb * batch->n_seqs;
-    if (grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many pages in one call");
+    AppendParams P{*kv, *batch, {k, v}, {k_stride, v_stride}, (batch->max_rows + kv->block - 2) / kv->block + 1,
+                   __builtin_ctz(kv->block), __builtin_ctz(kv->dim), status};
+    const long long pages = (long long)P.nb * batch->n_seqs;
+    if (pages > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many pages in one call");
     const int threads = kv->block * kv->dim / (8 * VPT);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)pages, 2u * kv->kv_heads);
     if (kv->f32)
-        kv_append_kernel<float><<<(unsigned)grid, threads, 0, st>>>(P);
+        kv_append_kernel<float><<<grid, threads, 0, st>>>(P);
     else
-        kv_append_kernel<__nv_bfloat16><<<(unsigned)grid, threads, 0, st>>>(P);
+        kv_append_kernel<__nv_bfloat16><<<grid, threads, 0, st>>>(P);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_append launch");
 }
@@ -342,14 +375,17 @@ extern "C" int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out
     int nsm = 0, *status = nullptr;
     rc = device_info(&nsm, &status);
     if (rc) return rc;
-    ReadParams P{*kv, *batch, {k_out, v_out}, {k_stride, v_stride}, (batch->max_rows + READ_TOKENS - 1) / READ_TOKENS, status};
-    const long long grid = 2LL * P.tiles * batch->n_seqs;
-    if (grid > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");
+    ReadParams P{*kv, *batch, {k_out, v_out}, {k_stride, v_stride}, (batch->max_rows + READ_TOKENS - 1) / READ_TOKENS,
+                 __builtin_ctz(kv->block), __builtin_ctz(kv->dim), 0, status};
+    while (P.row_log2 < 8 && (1 << P.row_log2) < width / 16) ++P.row_log2;
+    const long long tiles = (long long)P.tiles * batch->n_seqs;
+    if (tiles > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)tiles, 2);
     if (flags & TF_OUT_BF16)
-        kv_read_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(P);
+        kv_read_kernel<__nv_bfloat16><<<grid, READ_THREADS, 0, st>>>(P);
     else
-        kv_read_kernel<float><<<(unsigned)grid, 256, 0, st>>>(P);
+        kv_read_kernel<float><<<grid, READ_THREADS, 0, st>>>(P);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_read launch");
 }
