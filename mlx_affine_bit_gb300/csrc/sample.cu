@@ -36,8 +36,8 @@ constexpr int BINS = 512;                        // bins of one counting step (a
 #endif
 constexpr int MAX_CLUSTER = MAXC;
 constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit: 2^31
-// exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest.
-constexpr float BINS_PER_Z = BINS / 23.f;
+// exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest, bin b the nearest to b.
+constexpr float BINS_PER_Z = BINS / 23.f, Z_END = -22.25f;
 static_assert(BINS == THREADS, "a thread a bin");
 constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone
 #ifndef SLICE_KB
@@ -64,14 +64,17 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 // The scaled distribution of a row.
 struct Scale {
     float top, inv;              // largest logit, 1 / temperature
-    __device__ __forceinline__ float z(float v) const { return v == top ? 0.f : __fmul_rn(__fsub_rn(v, top), inv); }
-    __device__ __forceinline__ unsigned weight(float v) const {
-        return v == -INFINITY ? 0u : __float2uint_rn(__fmul_rn(expf(z(v)), WEIGHT_ONE));
+    // 0 for the largest (also where it is inf, or 1 / temperature is).
+    __device__ __forceinline__ float z(float v) const { return fminf(__fmul_rn(__fsub_rn(v, top), inv), 0.f); }
+    __device__ __forceinline__ unsigned weight_of(float z) const { return __float2uint_rn(__fmul_rn(expf(z), WEIGHT_ONE)); }
+    __device__ __forceinline__ int bin_of(float z) const {       // for z from Z_END on
+        return __float_as_int(fmaf(z, -BINS_PER_Z, 8388608.f)) - 0x4B000000;
     }
-    // Bin of z; BINS for what has no weight (-inf, and z below ln 2^-32 = -22.18 and a little).
+    __device__ __forceinline__ unsigned weight(float v) const { return weight_of(z(v)); }
+    // BINS for what has no weight.
     __device__ __forceinline__ int bin(float v) const {
         const float x = z(v);
-        return v == -INFINITY || x < -22.25f ? BINS : (int)(x * -BINS_PER_Z);
+        return x < Z_END ? BINS : bin_of(x);
     }
 };
 
@@ -249,8 +252,8 @@ __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &s
     // Keys that the bin can hold, a little more at both ends.
     cut.z_bin = f.bin;
     cut.last = 0x7FFFFFFF;
-    uint32_t k_lo = key_of(__fsub_rd(sc.top, (f.bin + 1) * (1.00001f / BINS_PER_Z) * T) + 0.f);
-    uint32_t k_hi = key_of(__fsub_ru(sc.top, f.bin * (0.99999f / BINS_PER_Z) * T) + 0.f);
+    uint32_t k_lo = key_of(__fsub_rd(sc.top, (f.bin + 0.501f) * (1.00001f / BINS_PER_Z) * T) + 0.f);
+    uint32_t k_hi = key_of(__fsub_ru(sc.top, fmaxf(f.bin - 0.501f, 0.f) * (0.99999f / BINS_PER_Z) * T) + 0.f);
     while (f.count > 1 && k_lo < k_hi && (t.by_mass || f.above + f.count != t.want)) {
         int shift = 0;
         while (((k_hi - k_lo) >> shift) >= (uint32_t)BINS) ++shift;
@@ -303,13 +306,16 @@ __device__ __forceinline__ void draw(Shared &S, const Group<CLUSTER> &G, const S
                                      int *token, float *prob, Each each, InOrder in_order) {
     const int lane = threadIdx.x & 31;
     auto kept = [&](float v, int i) {
-        const int b = sc.bin(v);
+        const float z = sc.z(v);
+        if (z < Z_END) return 0u;
+        const int b = sc.bin_of(z);
         if (b > cut.z_bin) return 0u;
-        const unsigned w = sc.weight(v);
-        if (w < least) return 0u;
-        if (b < cut.z_bin) return w;
-        const uint32_t key = key_of(v);
-        return key > cut.key || (key == cut.key && i <= cut.last) ? w : 0u;
+        if (b == cut.z_bin) {
+            const uint32_t key = key_of(v);
+            if (key < cut.key || (key == cut.key && i > cut.last)) return 0u;
+        }
+        const unsigned w = sc.weight_of(z);
+        return w < least ? 0u : w;
     };
     u64 mine = 0;
     each([&](float v, int i) { mine += kept(v, i); });
@@ -356,16 +362,38 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     const float *g32 = static_cast<const float *>(P.logits) + (BF16 ? 0 : at0);
     auto value = [](float x) { return x != x ? -INFINITY : x + 0.f; };                  // NaN is -inf, -0 is 0
     auto of16 = [&](uint32_t h) { return value(__uint_as_float(h << 16)); };
+    // (A resident slice holds the values so.)
     auto at = [&](int i) {
-        if (BF16) return of16(RESIDENT ? reinterpret_cast<const uint16_t *>(slice)[i] : g16[i]);
-        return value(RESIDENT ? reinterpret_cast<const float *>(slice)[i] : g32[i]);
+        if (RESIDENT) return BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(slice)[i] << 16) : reinterpret_cast<const float *>(slice)[i];
+        return BF16 ? of16(g16[i]) : value(g32[i]);
     };
-    // A warp's part of the slice: indexes [i0, i1), lane by lane.
-    const int per = ((P.slice + WARPS - 1) / WARPS + 31) / 32 * 32;
+    // A warp's part of the slice: indexes [i0, i1), four by four and lane by lane.
+    const int per = ((P.slice + WARPS - 1) / WARPS + 127) / 128 * 128;
     const int i0 = min(len, warp * per), i1 = min(len, i0 + per);
     auto each = [&](auto f) {
-#pragma unroll 4
-        for (int i = i0 + lane; i < i1; i += 32) f(at(i), first + i);
+        int i = i0 + 4 * lane;
+        if (RESIDENT) {
+#pragma unroll 2
+            for (; i + 3 < i1; i += 128) {
+                if (BF16) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(slice) + i);
+                    f(__uint_as_float(x.x << 16), first + i), f(__uint_as_float(x.x & 0xFFFF0000u), first + i + 1);
+                    f(__uint_as_float(x.y << 16), first + i + 2), f(__uint_as_float(x.y & 0xFFFF0000u), first + i + 3);
+                } else {
+                    const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(slice) + i);
+                    f(x.x, first + i), f(x.y, first + i + 1), f(x.z, first + i + 2), f(x.w, first + i + 3);
+                }
+            }
+        } else {
+            for (; i + 3 < i1; i += 128) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = at(i + e);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f(x[e], first + i + e);
+            }
+        }
+        for (int e = 0; e < 4 && i + e < i1; ++e) f(at(i + e), first + i + e);
     };
     auto in_order = [&](auto f) {
         for (int i = i0; i < i1; i += 32) {
@@ -382,16 +410,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
         const int es = BF16 ? 2 : 4;
         const uintptr_t base = BF16 ? reinterpret_cast<uintptr_t>(g16) : reinterpret_cast<uintptr_t>(g32);
         const int head = min(len, (int)(((16 - base % 16) % 16) / es)), vecs = (len - head) / VEC;
+        auto keep16 = [](float x) { return __float_as_uint(x) >> 16; };
         auto one = [&](int i) {
-            if (BF16) {
-                const uint16_t h = g16[i];
-                reinterpret_cast<uint16_t *>(slice)[i] = h;
-                top = fmaxf(top, of16(h));
-            } else {
-                const float x = g32[i];
+            const float x = BF16 ? of16(g16[i]) : value(g32[i]);
+            if (BF16)
+                reinterpret_cast<uint16_t *>(slice)[i] = (uint16_t)keep16(x);
+            else
                 reinterpret_cast<float *>(slice)[i] = x;
-                top = fmaxf(top, value(x));
-            }
+            top = fmaxf(top, x);
         };
         if (tid < head) one(tid);
         for (int i = head + vecs * VEC + tid; i < len; i += THREADS) one(i);
@@ -401,24 +427,27 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
             const int i = head + v * VEC;
             if (BF16) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(g16 + i);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                if (head == 0) *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(slice) + i) = x;
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    const float a = of16(w[e] & 0xFFFFu), b = of16(w[e] >> 16);
+                    top = fmaxf(top, fmaxf(a, b));
+                    w[e] = keep16(a) | (__float_as_uint(b) & 0xFFFF0000u);
                     if (head) {
                         reinterpret_cast<uint16_t *>(slice)[i + 2 * e] = (uint16_t)w[e];
                         reinterpret_cast<uint16_t *>(slice)[i + 2 * e + 1] = (uint16_t)(w[e] >> 16);
                     }
-                    top = fmaxf(top, fmaxf(of16(w[e] & 0xFFFFu), of16(w[e] >> 16)));
                 }
+                if (head == 0) *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(slice) + i) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
-                const float4 x = *reinterpret_cast<const float4 *>(g32 + i);
+                float4 x = *reinterpret_cast<const float4 *>(g32 + i);
+                x = make_float4(value(x.x), value(x.y), value(x.z), value(x.w));
                 float *dst = reinterpret_cast<float *>(slice) + i;
                 if (head == 0)
                     *reinterpret_cast<float4 *>(dst) = x;
                 else
                     dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
-                top = fmaxf(top, fmaxf(fmaxf(value(x.x), value(x.y)), fmaxf(value(x.z), value(x.w))));
+                top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
             }
         }
     } else {
@@ -468,8 +497,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
         const bool mass = by_p && !by_k;         // (top-p after top-k is cut among the tokens that top-k leaves)
         const Bin b = count_bins(S, G, search, [&](auto add) {
             each([&](float v, int) {
-                const int zb = sc.bin(v);
-                if (zb < BINS) add(zb, mass ? sc.weight(v) : 0u);
+                const float z = sc.z(v);
+                if (z >= Z_END) add(sc.bin_of(z), mass ? sc.weight_of(z) : 0u);
             });
         });
         const Parts parts = parts_of(S, G);
@@ -552,8 +581,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
         // Too many tokens for one CTA: the cluster goes on, with weights.
         const Bin wb = mass ? b : count_bins(S, G, search, [&](auto add) {
             each([&](float v, int) {
-                const int zb = sc.bin(v);
-                if (zb < BINS) add(zb, sc.weight(v));
+                const float z = sc.z(v);
+                if (z >= Z_END) add(sc.bin_of(z), sc.weight_of(z));
             });
         });
         if (!mass) {
