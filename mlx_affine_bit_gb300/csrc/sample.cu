@@ -8,8 +8,8 @@
 // One cluster of CTAs a row, a slice of the row each, in shared memory where it
 // fits (the logits then leave global memory once).  The cut of a prefix is found
 // by counting tokens (and adding up weights) in bins: of z = (x - max) / T first,
-// each CTA its own slice, added up and searched a share of the bins a CTA over
-// distributed shared memory.  The tokens down to the bin that holds the cut are
+// each CTA its own slice, all of them added up by every CTA over distributed shared
+// memory.  The tokens down to the bin that holds the cut are
 // mostly few: they move, in index order, to the first CTA, which cuts them by
 // bins of the bits of x and draws, alone.  Where they are many the cluster goes on
 // together in the same way on its slices.  Reading the logits bounds many rows,
@@ -31,19 +31,13 @@ typedef unsigned long long u64;
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 512;                        // bins of one counting step (at most THREADS)
-#ifndef MAXC
-#define MAXC 16
-#endif
-constexpr int MAX_CLUSTER = MAXC;
+constexpr int MAX_CLUSTER = 16;
 constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit: 2^31
 // exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest, bin b the nearest to b.
 constexpr float BINS_PER_Z = BINS / 23.f, Z_END = -22.25f;
 static_assert(BINS == THREADS, "a thread a bin");
 constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone
-#ifndef SLICE_KB
-#define SLICE_KB 80
-#endif
-constexpr int MAX_SLICE_BYTES = SLICE_KB * 1024; // of a row in one CTA's shared memory (two CTAs an SM)
+constexpr int MAX_SLICE_BYTES = 80 * 1024; // of a row in one CTA's shared memory (two CTAs an SM)
 
 struct Params {
     const void *logits;
@@ -111,17 +105,16 @@ struct Shared {
     int warp_at[WARPS];
     u64 warp_sum[WARPS];
     float max;                   // of this CTA's slice
-    int at;                      // its index
-    unsigned n_part;             // this CTA's share of the bins (or of the tokens): tokens, weights
+    unsigned n_part;             // this CTA's tokens and weight of a kind that the ranks add up
     u64 part;
     u64 goal;                    // 64-bit products are one thread's work: the SM has few units for them
     unsigned least;
-    Found found[2];              // of alternate searches: a CTA may be one search ahead of another's readers
+    Found found;
     int tie_last;
-    unsigned n[BINS], lo[BINS], hi[BINS];       // tokens, and weights in 16-bit halves (a slice holds at most 2^16 tokens)
-    unsigned all_n[THREADS];     // what the ranks have in this CTA's share of the bins, rank by rank
-    u64 all_w[THREADS];
-    float list_x[MAX_LIST];      // first CTA: the tokens that it finishes, in index order
+    // Tokens by bin, and their weights in 16-bit halves (a slice holds at most 2^16 tokens); of alternate
+    // countings, so that a CTA may be one ahead of another's reading.
+    unsigned n[2][BINS], lo[2][BINS], hi[2][BINS];
+    float list_x[MAX_LIST];      // this CTA's tokens of the set that one CTA finishes, in index order; the first CTA's grows to all of them
     int list_i[MAX_LIST];
 };
 
@@ -136,6 +129,9 @@ struct Group {
         else
             __syncthreads();
     }
+    // The two halves of sync().
+    __device__ __forceinline__ void arrive() const { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+    __device__ __forceinline__ void wait() const { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
     __device__ __forceinline__ Shared *of(Shared &S, int r) const { return CLUSTER ? g.map_shared_rank(&S, r) : &S; }
 };
 
@@ -181,36 +177,30 @@ __device__ __forceinline__ u64 warps_of(Shared &S, u64 mine, u64 &all) {
     return before;
 }
 
-// Counts every token f(slot) -> bin >= 0 (and its weight) in the bins, adds the
-// group's bins up, and gives thread t of rank r bin r * BINS / size + t with what
-// lies before it.  The sums of all bins are left in the ranks' n_part and part.
+// Counts tokens (and adds up weights, where `weighted`) that each(add) gives as add(bin, weight), over the group; thread t holds
+// bin t with what lies before it.  The sums of all bins go to `all`.
 template <bool CLUSTER, class Each>
-__device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, int search, Each each) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, share = BINS / G.size;
-    __syncthreads();
-    for (int b = tid; b < BINS; b += THREADS) S.n[b] = S.lo[b] = S.hi[b] = 0;
+__device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, int &counting, bool weighted, Bin &all, Each each) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, now = counting++ & 1;
+    S.n[now][tid] = 0;
+    if (weighted) S.lo[now][tid] = S.hi[now][tid] = 0;
     __syncthreads();
     each([&](int b, unsigned w) {
-        atomicAdd(&S.n[b], 1u);
-        if (w) {
-            atomicAdd(&S.lo[b], w & 0xFFFFu);
-            if (w >> 16) atomicAdd(&S.hi[b], w >> 16);
+        atomicAdd(&S.n[now][b], 1u);
+        if (weighted) {
+            atomicAdd(&S.lo[now][b], w & 0xFFFFu);
+            if (w >> 16) atomicAdd(&S.hi[now][b], w >> 16);
         }
     });
     G.sync();
     Bin b{0, 0, 0, 0};
-    if (G.size > 1) {
-        // A rank's bins of the share by `share` threads each, then the ranks added up.
-        const Shared *o = G.of(S, tid / share);
-        const int at = G.rank * share + tid % share;
-        S.all_n[tid] = o->n[at];
-        S.all_w[tid] = o->lo[at] + ((u64)o->hi[at] << 16);
-        __syncthreads();
-        if (tid < share)
-            for (int r = 0; r < G.size; ++r) b.n += S.all_n[r * share + tid], b.w += S.all_w[r * share + tid];
-    } else {
-        b.n = S.n[tid];
-        b.w = S.lo[tid] + ((u64)S.hi[tid] << 16);
+#pragma unroll 8
+    for (int r = 0; r < (CLUSTER ? G.size : 1); ++r) b.n += G.of(S, r)->n[now][tid];
+    if (weighted) {
+        u64 lo = 0, hi = 0;
+#pragma unroll 4
+        for (int r = 0; r < (CLUSTER ? G.size : 1); ++r) lo += G.of(S, r)->lo[now][tid], hi += G.of(S, r)->hi[now][tid];
+        b.w = lo + (hi << 16);
     }
     unsigned ni = b.n;
     u64 wi = b.w;
@@ -220,34 +210,36 @@ __device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, in
         if (lane >= o) ni += a, wi += d;
     }
     if (lane == 31) S.warp_at[warp] = (int)ni, S.warp_sum[warp] = wi;
+    if (tid == 0) S.found.bin = -1;
     __syncthreads();
-    for (int q = 0; q < warp; ++q) ni += (unsigned)S.warp_at[q], wi += S.warp_sum[q];
-    if (tid == share - 1) S.n_part = ni, S.part = wi;
-    if (tid == 0) S.found[search & 1].bin = -1;
-    G.sync();
-    const Parts p = parts_of(S, G);
-    b.n_before = p.n_before + ni - b.n;
-    b.w_before = p.w_before + wi - b.w;
+    unsigned na = lane < WARPS ? (unsigned)S.warp_at[lane] : 0, nb = lane < warp ? na : 0;
+    u64 wa = lane < WARPS ? S.warp_sum[lane] : 0, wb = lane < warp ? wa : 0;
+    na = __reduce_add_sync(~0u, na);
+    nb = __reduce_add_sync(~0u, nb);
+    for (int o = 16; o > 0; o >>= 1) {
+        wa += __shfl_xor_sync(~0u, wa, o);
+        wb += __shfl_xor_sync(~0u, wb, o);
+    }
+    b.n_before = nb + ni - b.n;
+    b.w_before = wb + wi - b.w;
+    all = Bin{na, 0, wa, 0};
     return b;
 }
-// The bin that the target falls into, with `above` and `mass_above` before all bins, known to every rank.
-template <bool CLUSTER>
-__device__ __forceinline__ Found find_bin(Shared &S, const Group<CLUSTER> &G, int &search, const Bin &b, unsigned above,
-                                          u64 mass_above, const Target &t) {
-    const int share = BINS / G.size;
-    if ((int)threadIdx.x < share && t.in(above + b.n_before, b.n, mass_above + b.w_before, b.w)) {
-        const Found f{G.rank * share + (int)threadIdx.x, b.n, above + b.n_before, b.w, mass_above + b.w_before};
-        for (int r = 0; r < G.size; ++r) G.of(S, r)->found[search & 1] = f;
-    }
-    G.sync();
-    return S.found[search++ & 1];
+// The bin that the target falls into, with `above` and `mass_above` before all bins.  (After a counting, or
+// where one has been found before and there is one.)
+__device__ __forceinline__ Found find_bin(Shared &S, const Bin &b, unsigned above, u64 mass_above, const Target &t) {
+    __syncthreads();                             // (every thread has read the last one)
+    if (t.in(above + b.n_before, b.n, mass_above + b.w_before, b.w))
+        S.found = Found{(int)threadIdx.x, b.n, above + b.n_before, b.w, mass_above + b.w_before};
+    __syncthreads();
+    return S.found;
 }
 
 // Cuts the group's tokens, in bins of z down to `f.bin`, at the target, which lies in that bin; returns the weight kept.
 // each(g) calls g(logit, index) for this thread's tokens; in_order(g) does so warp by warp in index order,
 // 32 tokens at a time (index -1 past the end).
 template <bool CLUSTER, class Each, class InOrder>
-__device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &search, const Scale &sc, float T, Found f,
+__device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &counting, const Scale &sc, float T, Found f,
                                       const Target &t, Cut &cut, Each each, InOrder in_order) {
     // Keys that the bin can hold, a little more at both ends.
     cut.z_bin = f.bin;
@@ -257,13 +249,14 @@ __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &s
     while (f.count > 1 && k_lo < k_hi && (t.by_mass || f.above + f.count != t.want)) {
         int shift = 0;
         while (((k_hi - k_lo) >> shift) >= (uint32_t)BINS) ++shift;
-        const Bin b = count_bins(S, G, search, [&](auto add) {
+        Bin all;
+        const Bin b = count_bins(S, G, counting, true, all, [&](auto add) {
             each([&](float v, int) {
                 const uint32_t key = key_of(v);
                 if (key >= k_lo && key <= k_hi && sc.bin(v) == cut.z_bin) add((int)((k_hi - key) >> shift), sc.weight(v));
             });
         });
-        const Found g = find_bin(S, G, search, b, f.above, f.mass_above, t);
+        const Found g = find_bin(S, b, f.above, f.mass_above, t);
         if (g.bin < 0) break;
         f = g;
         const uint32_t hi2 = k_hi - ((uint32_t)f.bin << shift);
@@ -369,8 +362,10 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     };
     // A warp's part of the slice: indexes [i0, i1), four by four and lane by lane.
     const int per = ((P.slice + WARPS - 1) / WARPS + 127) / 128 * 128;
+    static_assert((1 << 20) / MAX_CLUSTER / WARPS <= 32 * 128 && MAX_SLICE_BYTES / 2 / WARPS <= 32 * 128, "32 times 128 tokens a warp at most");
     const int i0 = min(len, warp * per), i1 = min(len, i0 + per);
-    auto each = [&](auto f) {
+    // f of this thread's tokens, done(c) after those of the c-th 128.
+    auto each_done = [&](auto f, auto done) {
         int i = i0 + 4 * lane;
         if (RESIDENT) {
 #pragma unroll 2
@@ -383,6 +378,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                     const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(slice) + i);
                     f(x.x, first + i), f(x.y, first + i + 1), f(x.z, first + i + 2), f(x.w, first + i + 3);
                 }
+                done((i - i0) >> 7);
             }
         } else {
             for (; i + 3 < i1; i += 128) {
@@ -391,10 +387,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 for (int e = 0; e < 4; ++e) x[e] = at(i + e);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f(x[e], first + i + e);
+                done((i - i0) >> 7);
             }
         }
         for (int e = 0; e < 4 && i + e < i1; ++e) f(at(i + e), first + i + e);
+        if (i < i1) done((i - i0) >> 7);
     };
+    auto each = [&](auto f) { each_done(f, [](int) {}); };
     auto in_order = [&](auto f) {
         for (int i = i0; i < i1; i += 32) {
             const bool is = i + lane < i1;
@@ -492,47 +491,62 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     };
 
     Cut cut{BINS - 1, 0, 0x7FFFFFFF};
-    int search = 0;
+    int counting = 0;
     if (by_k || by_p) {
         const bool mass = by_p && !by_k;         // (top-p after top-k is cut among the tokens that top-k leaves)
-        const Bin b = count_bins(S, G, search, [&](auto add) {
+        Bin all_bins;
+        const Bin b = count_bins(S, G, counting, mass, all_bins, [&](auto add) {
             each([&](float v, int) {
                 const float z = sc.z(v);
                 if (z >= Z_END) add(sc.bin_of(z), mass ? sc.weight_of(z) : 0u);
             });
         });
-        const Parts parts = parts_of(S, G);
-        const unsigned tokens = parts.n;
-        u64 whole = parts.w;
-        Found f = find_bin(S, G, search, b, 0, 0, Target{mass, (unsigned)k, mass ? goal_of(whole) : 0});
+        u64 whole = all_bins.w;
+        Found f = find_bin(S, b, 0, 0, Target{mass, (unsigned)k, mass ? goal_of(whole) : 0});
         // Tokens in bins down to the cut's: the set that it cuts.
         const int z_bin = f.bin < 0 ? BINS - 1 : f.bin;
-        const unsigned set = f.bin < 0 ? tokens : f.above + f.count;
+        const unsigned set = f.bin < 0 ? all_bins.n : f.above + f.count;
         if (set <= MAX_LIST) {
-            // They move to the first CTA, in index order.
-            unsigned mine = 0;
-            each([&](float v, int) { mine += sc.bin(v) <= z_bin; });
+            // Each CTA lists its own, in index order, and the first takes them all.
+            const float last_bin = 8388608.f + z_bin;
+            auto in_set = [&](float v) {
+                const float z = sc.z(v);
+                return z >= Z_END && fmaf(z, -BINS_PER_Z, 8388608.f) <= last_bin;      // bin_of(z) <= z_bin
+            };
+            unsigned mine = 0, chunks = 0;       // chunks: which 128 of the warp's tokens (32 at most) hold some
+            unsigned mine_before = 0;
+            each_done([&](float v, int) { mine += in_set(v); },
+                      [&](int c) { chunks |= (unsigned)(mine != mine_before) << c, mine_before = mine; });
             mine = __reduce_add_sync(~0u, mine);
+            chunks = __reduce_or_sync(~0u, chunks);
             u64 all;
             unsigned before = (unsigned)warps_of(S, mine, all);
             if (tid == 0) S.n_part = (unsigned)all;
-            G.sync();
-            const Parts parts = parts_of(S, G);
-            before += parts.n_before;
-            unsigned n = parts.n;
-            Shared *to = G.of(S, 0);
-            if (mine)
-                in_order([&](float v, int i) {
-                    const bool is = i >= 0 && sc.bin(v) <= z_bin;
+            for (; chunks; chunks &= chunks - 1)
+                for (int i = i0 + (__ffs(chunks) - 1) * 128, end = min(i1, i + 128); i < end; i += 32) {
+                    const float v = i + lane < end ? at(i + lane) : -INFINITY;
+                    const bool is = in_set(v);
                     const unsigned mask = __ballot_sync(~0u, is), slot = before + __popc(mask & ((1u << lane) - 1));
-                    if (is && slot < MAX_LIST) to->list_x[slot] = v, to->list_i[slot] = i;
+                    if (is && slot < MAX_LIST) S.list_x[slot] = v, S.list_i[slot] = first + i + lane;
                     before += __popc(mask);
-                    return false;
-                });
+                }
             G.sync();
-            if (G.rank != 0) return;
+            if (G.rank != 0) {
+                G.sync();        // (the first CTA has read the list)
+                return;
+            }
+            // A warp takes a rank's list.
+            const unsigned count = lane < G.size ? G.of(S, lane)->n_part : 0;
+            const unsigned n_all = __reduce_add_sync(~0u, count), skip = __reduce_add_sync(~0u, lane < warp ? count : 0);
+            if (warp > 0 && warp < G.size) {
+                const Shared *o = G.of(S, warp);
+                const unsigned m = __shfl_sync(~0u, count, warp);
+                for (unsigned i = lane; i < m && skip + i < MAX_LIST; i += 32) S.list_x[skip + i] = o->list_x[i], S.list_i[skip + i] = o->list_i[i];
+            }
+            G.arrive();
+            __syncthreads();
             // From here on the first CTA alone.
-            n = min(n, (unsigned)MAX_LIST);
+            const unsigned n = min(n_all, (unsigned)MAX_LIST);
             const Group<false> one{G.g, 1, 0};
             const int per_warp = ((int)n + THREADS - 1) / THREADS * 32, l0 = min((int)n, warp * per_warp), l1 = min((int)n, l0 + per_warp);
             auto each_listed = [&](auto fn) {
@@ -552,7 +566,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 warps_of(S, w, all);
                 return all;
             };
-            if (!mass) whole = f.bin >= 0 ? refine(S, one, search, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each_listed, listed_in_order)
+            if (!mass) whole = f.bin >= 0 ? refine(S, one, counting, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each_listed, listed_in_order)
                                           : whole_listed();
             if (!mass && f.bin >= 0 && by_p) {
                 // (counted without weights: the weight that top-k keeps)
@@ -568,34 +582,36 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
             if (by_p) {
                 const Target t{true, 0, goal_of(whole)};
                 if (!mass) {
-                    const Bin lb = count_bins(S, one, search, [&](auto add) {
+                    Bin all_listed;
+                    const Bin lb = count_bins(S, one, counting, true, all_listed, [&](auto add) {
                         each_listed([&](float v, int) { add(sc.bin(v), sc.weight(v)); });
                     });
-                    f = find_bin(S, one, search, lb, 0, 0, t);
+                    f = find_bin(S, lb, 0, 0, t);
                 }
-                if (f.bin >= 0) refine(S, one, search, sc, Tk, f, t, cut, each_listed, listed_in_order);
+                if (f.bin >= 0) refine(S, one, counting, sc, Tk, f, t, cut, each_listed, listed_in_order);
             }
             draw(S, one, sc, cut, S.least, u, P.tokens + row, prob, each_listed, listed_in_order);
+            G.wait();
             return;
         }
         // Too many tokens for one CTA: the cluster goes on, with weights.
-        const Bin wb = mass ? b : count_bins(S, G, search, [&](auto add) {
+        const Bin wb = mass ? b : count_bins(S, G, counting, true, all_bins, [&](auto add) {
             each([&](float v, int) {
                 const float z = sc.z(v);
                 if (z >= Z_END) add(sc.bin_of(z), sc.weight_of(z));
             });
         });
         if (!mass) {
-            whole = parts_of(S, G).w;
-            f = find_bin(S, G, search, wb, 0, 0, Target{false, (unsigned)k, 0});
-            if (f.bin >= 0) whole = refine(S, G, search, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each, in_order);
+            whole = all_bins.w;
+            f = find_bin(S, wb, 0, 0, Target{false, (unsigned)k, 0});
+            if (f.bin >= 0) whole = refine(S, G, counting, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each, in_order);
             if (by_p) {
                 const Target t{true, 0, goal_of(whole)};
-                f = find_bin(S, G, search, wb, 0, 0, t);
-                if (f.bin >= 0) refine(S, G, search, sc, Tk, f, t, cut, each, in_order);
+                f = find_bin(S, wb, 0, 0, t);
+                if (f.bin >= 0) refine(S, G, counting, sc, Tk, f, t, cut, each, in_order);
             }
         } else if (f.bin >= 0) {
-            refine(S, G, search, sc, Tk, f, Target{true, 0, goal_of(whole)}, cut, each, in_order);
+            refine(S, G, counting, sc, Tk, f, Target{true, 0, goal_of(whole)}, cut, each, in_order);
         }
     }
     draw(S, G, sc, cut, S.least, u, P.tokens + row, prob, each, in_order);
