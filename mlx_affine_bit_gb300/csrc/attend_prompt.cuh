@@ -33,13 +33,12 @@
 namespace tfq {
 namespace attend {
 
-constexpr int P_SOFT = 8, P_CONV = 4;            // softmax and widening warps; then four whose first lane issues products
-constexpr int P_THREADS = (P_SOFT + P_CONV + 4) * 32;
+constexpr int P_THREADS = 512;
 // Registers a thread after the split, by warpgroup: with the 512 threads' 128 at launch as their sum's limit.
 template <int D>
 struct PRegs {
-    static constexpr int SOFT = D == 256 ? 200 : 168, CONV = D == 256 ? 168 : 104, REST = 72;
-    static_assert((D == 256 ? SOFT + REST : 2 * SOFT) + CONV + REST <= 4 * 128, "registers of the launch");
+    static constexpr int SOFT = D == 256 ? 232 : 168, CONV = 104, REST = 72;
+    static_assert((D == 256 ? SOFT + 2 * CONV : 2 * SOFT + CONV) + REST <= 4 * 128, "registers of the launch");
 };
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -51,6 +50,9 @@ __device__ __forceinline__ void regs_down() {
 }
 constexpr int KEYS = 128;                        // tokens of a step
 TFQ_HD constexpr int p_tiles(int d) { return d == 256 ? 1 : 2; }
+// Softmax warps (a row a thread) and widening warps; then four whose first lane issues a tile's products.
+TFQ_HD constexpr int p_soft(int d) { return 4 * p_tiles(d); }
+TFQ_HD constexpr int p_conv(int d) { return 12 - p_soft(d); }
 TFQ_HD constexpr int p_slots(int d) { return d == 256 ? 2 : 4; }          // fp16 tiles of keys or values in flight
 TFQ_HD constexpr int p_tile_bytes(int d) { return KEYS * d * 2; }         // one of them, and 128 rows of q
 TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p_tile_bytes(d); }
@@ -136,13 +138,12 @@ struct Walk {
 };
 
 struct PromptHdr {
-    uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2], scales[4], joined[2], turn[2], done;
+    uint64_t kv_full[4], kv_empty[4], s_full[2], s_free, p_full[2], pv_done[2], q_full[2], o_free[2], scales[4], joined[2], turn[2], done;
     uint32_t tmem;
     int abort, last, seq, tile, h;
     long long item_at, total, sums[P_THREADS / 32];
     float2 scale[SCALES][8];                 // key scale, log2 of the value scale, of each 16 tokens (-1: no page)
-    uint32_t pages[SCALES];                  // a byte a widening warp: 1 if its tokens' pages are there
-    uint8_t tail[64];
+    uint2 pages[SCALES];                     // a byte a widening warp: 1 if its tokens' pages are there
 };
 static_assert(sizeof(PromptHdr) <= 1024, "header");
 
@@ -247,6 +248,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <int D>
 __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_constant__ Params P) {
     constexpr int NT = p_tiles(D), R = 128 * NT, SLOTS = p_slots(D), TB = p_tile_bytes(D);
+    constexpr int P_SOFT = p_soft(D), P_CONV = p_conv(D);
     extern __shared__ __align__(1024) uint8_t smem[];
     PromptHdr &B = *reinterpret_cast<PromptHdr *>(smem);
     uint8_t *const q_s = smem + 1024, *const kv_s = q_s + NT * TB;
@@ -272,6 +274,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) mbar_init(&B.joined[i], 4 * NT);
         mbar_init(&B.turn[0], 1);
         mbar_init(&B.turn[1], 1);
+        mbar_init(&B.s_free, 4);
         mbar_init(&B.done, NT);
         B.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -399,10 +402,13 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
                     const uint32_t vt = 2 * st + 1, slot = vt % SLOTS;
                     const bool more = i + 1 < w.step1;
+                    if (NT == 1 && more) {
+                        wait_for(&B.s_free, st & 1, abort, P.status);
+                        scores(st + 1);
+                    }
                     wait_for(&B.p_full[t], st & 1, abort, P.status);
                     // (The tiles' products take turns: one's run beside the other's softmax.)
                     if (NT > 1) wait_for(&B.turn[t], (st & 1) ^ (t == 0), abort, P.status);
-                    if (NT == 1 && more) scores(st + 1);
                     wait_for(&B.kv_full[slot], (vt / SLOTS) & 1, abort, P.status);
                     if (i == w.step0) wait_for(&B.o_free[t], (item & 1) ^ 1, abort, P.status);
                     fence_after();
@@ -426,12 +432,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             mbar_wait(&B.done, 0, abort, P.status, false);
         }
     } else if (warp >= P_SOFT) {
-        if constexpr (PRegs<D>::CONV > 128)
-            regs_up<PRegs<D>::CONV>();
-        else
-            regs_down<PRegs<D>::CONV>();
-        // Widening: warp v takes tokens 32 v .. 32 v + 31 of every step, a lane 16 bytes of a token at a time.
-        constexpr int LPT = D / 16;              // lanes a token, and loads a lane
+        regs_down<PRegs<D>::CONV>();
+        // Widening: warp v takes tokens TW v .. TW v + TW - 1 of every step, a lane 16 bytes of a token at a time.
+        constexpr int TW = KEYS / P_CONV, NP = TW / 16;      // (and as many times 16 tokens, of a page each)
+        constexpr int LPT = D / 16, LOADS = TW * LPT / 32;   // lanes a token, loads a lane
         // The low two bits of a lane are its place in 64 bytes, the next the token's parity: the eight lanes of a
         // 16-byte store then meet eight different chunks under the swizzle.
         const int v = warp - P_SOFT, sub = (lane & 3) | (LPT > 4 ? (lane >> 1) & (LPT - 4) : 0);
@@ -439,11 +443,11 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         uint32_t st = 0;
         do {
             const long long seq_table = w.seq * P.b.table_stride;
-            uint4 kr[LPT], vr[LPT];
-            int pages = -1;                      // lane 2 s + half: page of 16 tokens of step (base + s), and its scales
+            uint4 kr[LOADS], vr[LOADS];
+            int pages = -1;                      // lane NP s + e: page of the e-th 16 tokens of step (base + s), and its scales
             float2 scale = make_float2(-1.f, -INFINITY);
             auto look_up = [&](int step) {
-                const int t = w.t.from + (step + (lane >> 1)) * KEYS + 32 * v + 16 * (lane & 1);
+                const int t = w.t.from + (step + lane / NP) * KEYS + TW * v + 16 * (lane % NP);
                 pages = -1;
                 scale = make_float2(-1.f, -INFINITY);
                 if (t < w.t.to) {
@@ -457,22 +461,33 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     }
                 }
             };
-            auto load = [&](const int8_t *pool, int step, int at, uint4 (&r)[LPT]) {      // step `at` of those looked up
-                const int p0 = __shfl_sync(~0u, pages, 2 * at), p1 = __shfl_sync(~0u, pages, 2 * at + 1);
-                const int t0 = w.t.from + step * KEYS + 32 * v;
+            int base = w.step0;                  // first step looked up
+            struct {
+                int p0, p1;                      // pages of a step's first and last 16 tokens of this warp
+                float2 scale;                    // lane e: scales of the e-th 16
+            } k_of;                              // of the step whose keys are on their way
+            auto find = [&](int step) {
+                if (step - base == 32 / NP) look_up(base = step);
+                const int at = NP * (step - base);
+                k_of.p0 = __shfl_sync(~0u, pages, at);
+                k_of.p1 = __shfl_sync(~0u, pages, at + NP - 1);
+                k_of.scale = make_float2(__shfl_sync(~0u, scale.x, at + lane % NP), __shfl_sync(~0u, scale.y, at + lane % NP));
+            };
+            auto load = [&](const int8_t *pool, int step, int p0, int p1, uint4 (&r)[LOADS]) {
+                const int t0 = w.t.from + step * KEYS + TW * v;
 #pragma unroll
-                for (int j = 0; j < LPT; ++j) {
-                    const int tk = j * (32 / LPT) + tok, page = j < LPT / 2 ? p0 : p1;
+                for (int j = 0; j < LOADS; ++j) {
+                    const int tk = j * (32 / LPT) + tok, page = j < LOADS / NP ? p0 : p1;
                     r[j] = make_uint4(0u, 0u, 0u, 0u);
                     if (page >= 0)
                         r[j] = *reinterpret_cast<const uint4 *>(pool + (((((long long)page * H + w.h) << BL) + ((t0 + tk) & BM)) * D) + 16 * sub);
                 }
             };
             // Where this lane's 16 values of token tk go: two 16-byte chunks, 2 sub and 2 sub + 1 of the row of blocks of eight.
-            auto store = [&](uint8_t *tile, const uint4 (&r)[LPT], const bool tiny) {
+            auto store = [&](uint8_t *tile, const uint4 (&r)[LOADS], const bool tiny) {
 #pragma unroll
-                for (int j = 0; j < LPT; ++j) {
-                    const int tk = 32 * v + j * (32 / LPT) + tok;
+                for (int j = 0; j < LOADS; ++j) {
+                    const int tk = TW * v + j * (32 / LPT) + tok;
                     uint8_t *row = tile + (sub >> 2) * (KEYS * 128) + tk * 128;
                     const uint32_t x[4] = {r[j].x ^ 0x80808080u, r[j].y ^ 0x80808080u, r[j].z ^ 0x80808080u, r[j].w ^ 0x80808080u};
                     uint32_t y[8];
@@ -491,34 +506,46 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B.kv_full[kt % SLOTS]);
             };
-            look_up(w.step0);
-            load(P.kv.k, w.step0, 0, kr);
-            load(P.kv.v, w.step0, 0, vr);
-            for (int i = w.step0, at = 0; i < w.step1 && !*abort; ++i, ++st) {
-                const float2 mine = make_float2(__shfl_sync(~0u, scale.x, 2 * at + (lane & 1)), __shfl_sync(~0u, scale.y, 2 * at + (lane & 1)));
-                // The next step's pages (16 steps at a time).
-                if (++at == 16) {
-                    look_up(i + 1);
-                    at = 0;
-                }
-                uint32_t kt = 2 * st;
+            auto put_keys = [&](uint32_t step) {
+                const uint32_t kt = 2 * step;
                 wait_for(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
                 store(kv_s + (kt % SLOTS) * TB, kr, true);
-                if (lane < 2) B.scale[st % SCALES][2 * v + lane] = mine;
-                const bool there = __all_sync(~0u, mine.x >= 0.f);
-                if (lane == 0) reinterpret_cast<uint8_t *>(&B.pages[st % SCALES])[v] = there;
+                if (lane < NP) B.scale[step % SCALES][NP * v + lane] = k_of.scale;
+                const bool there = __all_sync(~0u, k_of.scale.x >= 0.f);
+                if (lane == 0) reinterpret_cast<uint8_t *>(&B.pages[step % SCALES])[v] = there;
                 publish(kt);
-                if (lane == 0) mbar_arrive(&B.scales[st % SCALES]);
-                if (i + 1 < w.step1) load(P.kv.k, i + 1, at, kr);
-                kt = 2 * st + 1;
-                wait_for(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
-                store(kv_s + (kt % SLOTS) * TB, vr, false);
-                publish(kt);
-                if (i + 1 < w.step1) load(P.kv.v, i + 1, at, vr);
+                if (lane == 0) mbar_arrive(&B.scales[step % SCALES]);
+            };
+            look_up(w.step0);
+            find(w.step0);
+            load(P.kv.k, w.step0, k_of.p0, k_of.p1, kr);
+            load(P.kv.v, w.step0, k_of.p0, k_of.p1, vr);
+            // The slots are filled in the order in which the products free them.  One tile: a step's keys go before the
+            // values of the step before it (99 -> 95 us for three chunks of up to 509 tokens, 16 heads of 256, window
+            // 4096); two: after them.
+            constexpr int AHEAD = NT == 1;
+            if (AHEAD) {
+                put_keys(st);
+                if (w.step0 + 1 < w.step1) {
+                    find(w.step0 + 1);
+                    load(P.kv.k, w.step0 + 1, k_of.p0, k_of.p1, kr);
+                }
+            }
+            for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
+                int p0 = k_of.p0, p1 = k_of.p1;              // (of step i + AHEAD)
+                if (i + AHEAD < w.step1) put_keys(st + AHEAD);
+                if (i + AHEAD + 1 < w.step1) {
+                    find(i + AHEAD + 1);
+                    load(P.kv.k, i + AHEAD + 1, k_of.p0, k_of.p1, kr);
+                    if (!AHEAD) p0 = k_of.p0, p1 = k_of.p1;
+                }
+                const uint32_t vt = 2 * st + 1;
+                wait_for(&B.kv_empty[vt % SLOTS], ((vt / SLOTS) & 1) ^ 1, abort, P.status);
+                store(kv_s + (vt % SLOTS) * TB, vr, false);
+                publish(vt);
+                if (i + 1 < w.step1) load(P.kv.v, i + 1, p0, p1, vr);
             }
         } while (w.next(P) && !*abort);
-    } else if (warp >= 4 * NT) {
-        regs_down<PRegs<D>::REST>();
     } else {
         regs_up<PRegs<D>::SOFT>();
         // Softmax: thread `row` of tile t.
@@ -739,21 +766,38 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 wait_for(&B.s_full[t], st & 1, abort, P.status);
                 wait_for(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);
                 fence_after();
-                // (Loops over the columns stay loops: unrolled, a step's code would not stay in the instruction caches.)
                 const float2 *const sc = B.scale[st % SCALES];
-                // f(c, x) on the columns 32 c ..
+                // f(c, x) on the columns 32 c ..  One tile: all of them are taken into registers at once, so that the
+                // next step's scores can follow.  Two: they are read again each time, in a loop (unrolled, a step's
+                // code would not stay in the instruction caches).
+                uint32_t all[NT == 1 ? 4 : 1][32];
+                if constexpr (NT == 1) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, all[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait32(all[c]);
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B.s_free);
+                }
                 auto columns = [&](auto f) {
+                    if constexpr (NT == 1) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) f(c, all[c]);
+                    } else {
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tmem_ld32(s_at + 32 * c, x);
-                        tmem_wait32(x);
-                        f(c, x);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(s_at + 32 * c, x);
+                            tmem_wait32(x);
+                            f(c, x);
+                        }
                     }
                 };
                 // Factor of a score; never 0, so that -inf stays -inf (a page of zeros has scores of 0 all the same).
                 auto factor = [&](float ks) { return fmaxf(rowf * ks, 1e-30f); };
-                if (t0 < all_from || t0 + KEYS > all_to || B.pages[st % SCALES] != 0x01010101u) {
+                if (t0 < all_from || t0 + KEYS > all_to || B.pages[st % SCALES].x != 0x01010101u ||
+                    (P_CONV > 4 && B.pages[st % SCALES].y != 0x01010101u)) {
                     // Tokens that the row does not see, first.
                     columns([&](int c, uint32_t (&x)[32]) {
                         const int from = see_from - t0 - 32 * c, to = see_to - t0 - 32 * c;
@@ -761,9 +805,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (e < from || e >= to || !(e < 16 ? p0 : p1)) x[e] = __float_as_uint(-INFINITY);
-                        tmem_st32(s_at + 32 * c, x);
+                        if (NT > 1) tmem_st32(s_at + 32 * c, x);
                     });
-                    tmem_wait_st();
+                    if (NT > 1) tmem_wait_st();
                 }
                 // The maxima of s and of s + log2(vs), by groups of 16 tokens.
                 float mt = sum.m, nt = sum.n;
@@ -791,16 +835,21 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 const float shrink = sum.n == -INFINITY ? 0.f : exp2_fast(sum.n - nt);
                 sum.m = mt;
                 sum.n = nt;
+                                constexpr int AT = NT == 1 ? 1 : 2;          // 32 columns each at once (more measured no faster)
                 auto rescale = [&]() {           // the outputs so far, to the new maximum
                     if (i > w.step0 && __any_sync(~0u, grew)) {
 #pragma unroll 1
-                        for (int d = 0; d < D; d += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(o_at + d, x);
-                            tmem_wait32(x);
+                        for (int d = 0; d < D; d += 32 * AT) {
+                            uint32_t x[AT][32];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], shrink);
-                            tmem_st32(o_at + d, x);
+                            for (int c = 0; c < AT; ++c) tmem_ld32(o_at + d + 32 * c, x[c]);
+#pragma unroll
+                            for (int c = 0; c < AT; ++c) {
+                                tmem_wait32(x[c]);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) mul2(x[c][e], x[c][e + 1], shrink);
+                                tmem_st32(o_at + d + 32 * c, x[c]);
+                            }
                         }
                     }
                 };

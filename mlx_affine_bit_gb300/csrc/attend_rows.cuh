@@ -44,10 +44,7 @@ namespace attend {
 
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 // Tiles of 16 tokens that a warp takes at a time (dim 256: one, or its ring would leave one CTA an SM), and a CTA's tokens.
-#ifndef T128
-#define T128 2
-#endif
-TFQ_HD constexpr int tiles_of(int d) { return d == 256 ? 1 : d == 128 ? T128 : 2; }
+TFQ_HD constexpr int tiles_of(int d) { return d == 256 ? 1 : 2; }
 TFQ_HD constexpr int step_of(int d) { return 16 * tiles_of(d) * WARPS; }
 constexpr int CHUNK_TOKENS = 4096;       // tokens whose pages and scales a CTA keeps at a time
 constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
@@ -117,36 +114,11 @@ __device__ __forceinline__ float out_factor(const RowSum &a) {
     return a.l == 0.f ? 0.f : exp2f(a.n - a.m - W_EXP) / a.l;
 }
 
-#ifndef ST64
-#define ST64 2
-#endif
-#ifndef ST128
-#define ST128 2
-#endif
-#ifndef ST256
-#define ST256 3
-#endif
-#ifndef C64
-#define C64 5
-#endif
-#ifndef C64B
-#define C64B 4
-#endif
-#ifndef C128
-#define C128 3
-#endif
-#ifndef C128B
-#define C128B 3
-#endif
-#ifndef C256
-#define C256 2
-#endif
-#ifndef C256B
-#define C256B 2
-#endif
-// Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q take.
-TFQ_HD constexpr int stages(int d) { return d == 64 ? ST64 : d == 128 ? ST128 : ST256; }
-TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? C64 : C64B) : d == 128 ? (nt == 1 ? C128 : C128B) : (nt == 1 ? C256 : C256B); }
+// Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q
+// take.  48 sequences of up to 8000 tokens, 8 heads of 128: 79 us so, 81 with one tile a stage and four stages, 83
+// with three stages and two CTAs; one of 131072 tokens 52, 54 and 50.
+TFQ_HD constexpr int stages(int d) { return d == 256 ? 3 : 2; }
+TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? 5 : 4) : d == 128 ? 3 : 2; }
 TFQ_HD constexpr int tile_bytes(int d) { return 32 * d; }          // 16 tokens of keys and of values
 TFQ_HD constexpr int out_pitch(int d) { return d + 4; }            // floats between joined rows
 // Shared memory: the rings; after the tokens are done, every warp's outputs, then the parts' factors.
