@@ -32,67 +32,77 @@ struct AppendParams {
     int *status;
 };
 
-// Magnitude of a finite value; 0 for an infinity or NaN (see the header).
-__device__ __forceinline__ float finite_mag(float x) {
-    const float a = fabsf(x);
-    return a <= FLT_MAX ? a : 0.f;
-}
-
-// x / scale rounded: as x * (1 / scale), which is within 2^-23 of it, relatively (3e-5 of a code at most), and by
-// the division where that leaves the nearest code open (or 1 / scale overflows).
-struct Step {
-    float scale, inv;
-    bool slow;
-    __device__ __forceinline__ uint32_t code(float x) const {
-        float q = __fmul_rn(x, inv), r = rintf(q);
-        if (slow || fabsf(q - r) > 0.4999f) r = rintf(__fdiv_rn(x, scale));
-        // 0 / 0 and NaN convert to 0; an infinity saturates and is clamped.
-        const int c = max(-127, min(127, __float2int_rn(r)));
-        return (uint32_t)(c & 255);
+// Eight values as they came: fp32 in eight words, bf16 in four.
+template <typename T>
+struct Raw8 {
+    static constexpr int WORDS = sizeof(T) == 4 ? 8 : 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p, bool vec) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 a = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            }
+        } else if (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {      // (16-byte aligned)
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i) reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __device__ __forceinline__ float value(int i) const {
+        return __uint_as_float(sizeof(T) == 4 ? w[i] : i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+    // The largest magnitude; infinities and NaN left out (see the header).  Magnitudes are ordered as their bits.
+    __device__ __forceinline__ float amax() const {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) top = sizeof(T) == 4 ? max(top, w[i] & 0x7FFFFFFFu) : __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+        if (sizeof(T) == 2) top = max(top >> 16, top & 0xFFFFu) << 16;
+        if (top < 0x7F800000u) return __uint_as_float(top);
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = fabsf(value(i));
+            m = fmaxf(m, a <= FLT_MAX ? a : 0.f);
+        }
+        return m;
     }
 };
 
-__device__ __forceinline__ void load8(float (&x)[8], const float *p, bool vec) {
-    if (vec) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
+// x / scale rounded to the nearest, even in the middle.
+__device__ __forceinline__ int divided(float x, float scale) {
+    // 0 / 0 and NaN convert to 0; an infinity saturates and is clamped.
+    return max(-127, min(127, __float2int_rn(rintf(__fdiv_rn(x, scale)))));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {     // NaN if one is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// Codes of four values, and whether the division has to decide.  x * (1 / scale) is within 1.5 * 2^-23 of the
+// rounded x / scale, relatively (2.3e-5 of a code at most), and rounds to the same code unless it lies that near to
+// the middle of two; nor does it count for infinities and NaN (whose distance is NaN) and where 1 / scale
+// overflows.  A sum with 1.5 * 2^23 rounds to the code and holds it in its low byte.
+__device__ __forceinline__ uint32_t codes4(float x0, float x1, float x2, float x3, float scale, float inv, bool &open) {
+    const float x[4] = {x0, x1, x2, x3};
+    uint32_t t[4];
+    float far = scale < 1e-30f ? 1.f : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = p[i];
+    for (int i = 0; i < 4; ++i) {
+        const float q = __fmul_rn(x[i], inv), r = __fadd_rn(q, 12582912.f);
+        far = max_nan(far, fabsf(__fsub_rn(q, __fsub_rn(r, 12582912.f))));
+        t[i] = __float_as_uint(r);
     }
-}
-__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16 *p, bool vec) {
-    const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-    if (vec) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((uint32_t)h[i] << 16);
-    }
-}
-// The originals go back as they came (16-byte aligned destination).
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Step &s) {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i >> 2] |= s.code(x[i]) << (8 * (i & 3));
-    return make_uint2(w[0], w[1]);
+    open = !(far <= 0.49997f);
+    return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
 }
 
 constexpr int VPT = 4;      // 8-value vectors a thread: block * dim / 32 threads cover a page
@@ -135,13 +145,16 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendParams P) {
 
     const int VL = DL - 3, vd = 1 << VL;            // vectors a token: 8, 16 or 32 lanes of one warp
     const int nt = blockDim.x, tid = threadIdx.x;
-    float x[VPT][8];
+    // This thread's vectors: at d of tokens t0 + i * dt.
+    const int d = (tid & (vd - 1)) * 8, t0 = tid >> VL, dt = B / VPT;
+    Raw8<T> x[VPT];
     float amax = 0.f;
+    const T *rows = src + (long long)(q.row0 + base + t0 - first) * P.stride[side] + (h << DL) + d;
     // The new rows (and the begun page's earlier magnitudes), while the page is looked up.
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
-        if (t >= lo && t < hi) load8(x[i], src + (long long)(q.row0 + base + t - first) * P.stride[side] + (h << DL) + d, vec);
+        const int t = t0 + i * dt;
+        if (t >= lo && t < hi) x[i].load(rows + i * (dt * P.stride[side]), vec);
     }
     for (int t = tid; t < lo; t += nt) amax = fmaxf(amax, ring_max[t]);
     if (page < 0 || page >= kv.n_blocks) {
@@ -153,50 +166,60 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendParams P) {
     const float old_scale = lo > 0 ? *scales : 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
+        const int t = t0 + i * dt;
         const bool mine = t >= lo && t < hi;
-        float m = 0.f;
-        if (mine) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(x[i][e]));
-        }
-        for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        if (mine && keep) {
-            store8(ring + (t << DL) + d, x[i]);
-            if (d == 0) ring_max[t] = m;
-        }
+        float m = mine ? x[i].amax() : 0.f;
         amax = fmaxf(amax, m);
+        if (keep) {
+            for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            if (mine) x[i].store(ring + (t << DL) + d);
+            if (mine && d == 0) ring_max[t] = m;
+        }
     }
-    __shared__ float part[32];
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-    if ((tid & 31) == 0) part[tid >> 5] = amax;
+    __shared__ uint32_t part[32];
+    // (Magnitudes are ordered as their bits.)
+    uint32_t top = __reduce_max_sync(~0u, __float_as_uint(amax));
+    if ((tid & 31) == 0) part[tid >> 5] = top;
     __syncthreads();
-    amax = part[0];
-    for (int w = 1; w < nt / 32; ++w) amax = fmaxf(amax, part[w]);
+    top = (tid & 31) < nt / 32 ? part[tid & 31] : 0u;
+    amax = __uint_as_float(__reduce_max_sync(~0u, top));
     const float scale = __fmul_rn(amax, 1.f / 127.f);
     // (A long call, which takes these originals out of the ring, does so in any case.)
     const int other = (last - pg) & 1 ? last - 1 : last;      // the last page in this half of the ring
     const bool leaves = pg == pg0 && begun && other > pg;
     const bool again = lo > 0 && (scale != old_scale || leaves);
     if (tid == 0) *scales = scale;
-    const Step step{scale, __fdiv_rn(1.f, scale), scale < 1e-30f};
+    const float inv = __fdiv_rn(1.f, scale);
+    uint32_t open = 0;                               // bit 2 i + (0, 1): four values whose codes the division decides
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
-        if (t < lo && again) load8(x[i], ring + (t << DL) + d, true);
-        if (t < hi && (t >= lo || again)) *reinterpret_cast<uint2 *>(codes + (t << DL) + d) = codes8(x[i], step);
+        const int t = t0 + i * dt;
+        if (t < lo && again) x[i].load(ring + (t << DL) + d, true);
+        if (t < hi && (t >= lo || again)) {
+            bool a, b;
+            const uint32_t c0 = codes4(x[i].value(0), x[i].value(1), x[i].value(2), x[i].value(3), scale, inv, a);
+            const uint32_t c1 = codes4(x[i].value(4), x[i].value(5), x[i].value(6), x[i].value(7), scale, inv, b);
+            *reinterpret_cast<uint2 *>(codes + (t << DL) + d) = make_uint2(c0, c1);
+            open |= ((uint32_t)a | (uint32_t)b << 1) << (2 * i);
+        }
+    }
+    // The few that are left open (one value in some sixteen thousand) are read again, and divided.
+    for (; open; open &= open - 1) {
+        const int g = __ffs(open) - 1, t = t0 + (g >> 1) * dt, at = d + 4 * (g & 1);
+        const T *p = t < lo ? ring + (t << DL) + at : rows + (g >> 1) * (dt * P.stride[side]) + 4 * (g & 1);
+        for (int e = 0; e < 4; ++e) codes[(t << DL) + at + e] = (int8_t)divided((float)p[e], scale);
     }
     if (leaves) {
         __syncthreads();
         const int first_t = other << BL, n = min(q.end - first_t, B);
         for (int i = 0; i < VPT; ++i) {
-            const int v = tid + i * nt, t = v >> VL, d = (v & (vd - 1)) * 8;
-            float y[8], m = 0.f;
+            const int t = t0 + i * dt;
+            float m = 0.f;
             if (t < n) {
-                load8(y, src + (long long)(q.row0 + first_t + t - first) * P.stride[side] + (h << DL) + d, vec);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_mag(y[e]));
-                store8(ring + (t << DL) + d, y);
+                Raw8<T> y;
+                y.load(src + (long long)(q.row0 + first_t + t - first) * P.stride[side] + (h << DL) + d, vec);
+                m = y.amax();
+                y.store(ring + (t << DL) + d);
             }
             for (int o = 1; o < vd; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
             if (t < n && d == 0) ring_max[t] = m;
@@ -213,15 +236,16 @@ struct ReadParams {
     long long stride[2];
     int tiles;              // tiles of READ_TOKENS tokens that a sequence may have
     int block_log2, dim_log2;
-    int row_log2;           // threads a row: the 16-code vectors of a row, rounded up to a power of two (256 at most)
+    int row_log2;           // threads a row: its 16-byte vectors, rounded up to a power of two (256 at most)
     int *status;
 };
 constexpr int READ_TOKENS = 16, READ_THREADS = 256;
 
-// One CTA a (sequence, 16 of its rows, keys or values): a thread turns 16 codes
-// into 16 values of a row, for up to four rows at a time.
+// One CTA a (sequence, 16 of its rows, keys or values): a thread turns the codes of 16 bytes of output into
+// values of a row (a warp's stores are then of whole lines), for up to eight rows at a time.
 template <typename T>
 __global__ void __launch_bounds__(READ_THREADS) kv_read_kernel(const ReadParams P) {
+    constexpr int VEC = 16 / sizeof(T), AT = 8;
     const tf_kv &kv = P.kv;
     const int H = kv.kv_heads, BL = P.block_log2, DL = P.dim_log2, BM = kv.block - 1;
     const int side = blockIdx.y;
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(READ_THREADS) kv_read_kernel(const ReadParams 
     }
     const int t0 = tile * READ_TOKENS, nt = min(READ_TOKENS, q.n - t0);
     if (nt <= 0) return;
-    const int VL = DL - 4, per = H << VL;           // 16-code vectors a head, a row
+    const int VL = DL - (VEC == 4 ? 2 : 3), per = H << VL;      // vectors a head, a row
     T *out = static_cast<T *>(P.out[side]);
     const bool vec = ((reinterpret_cast<uintptr_t>(out) | (P.stride[side] * sizeof(T))) & 15) == 0;
     const int step = READ_THREADS >> P.row_log2;    // rows at a time
@@ -242,48 +266,55 @@ __global__ void __launch_bounds__(READ_THREADS) kv_read_kernel(const ReadParams 
     const int8_t *pool = side ? kv.v : kv.k;
     const float *scales = side ? kv.v_scale : kv.k_scale;
     for (int c = threadIdx.x & ((1 << P.row_log2) - 1); c < per; c += 1 << P.row_log2) {
-        const int h = c >> VL, d = (c & ((1 << VL) - 1)) * 16;
-        for (int tb = threadIdx.x >> P.row_log2; tb < nt; tb += 4 * step) {
-            uint4 w[4];
-            float scale[4];
-            int page[4];
+        const int h = c >> VL, d = (c & ((1 << VL) - 1)) * VEC;
+        for (int tb = threadIdx.x >> P.row_log2; tb < nt; tb += AT * step) {
+            uint2 w[AT];
+            float scale[AT];
+            int page[AT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < AT; ++k) {
                 const int t = tb + k * step, pos = q.end - q.n + t0 + t;
                 page[k] = t < nt ? table[pos >> BL] : 0;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < AT; ++k) {
                 const int t = tb + k * step, pos = q.end - q.n + t0 + t;
                 if (page[k] < 0 || page[k] >= kv.n_blocks) {
                     atomicOr(P.status, STATUS_BOUNDS);
                     page[k] = -1;
                 } else if (t < nt) {
                     const long long ph = (long long)page[k] * H + h;
-                    w[k] = *reinterpret_cast<const uint4 *>(pool + (((ph << BL) + (pos & BM)) << DL) + d);
+                    const int8_t *src = pool + (((ph << BL) + (pos & BM)) << DL) + d;
+                    if (VEC == 4)
+                        w[k].x = *reinterpret_cast<const uint32_t *>(src);
+                    else
+                        w[k] = *reinterpret_cast<const uint2 *>(src);
                     scale[k] = scales[ph];
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < AT; ++k) {
                 const int t = tb + k * step;
                 if (t >= nt || page[k] < 0) continue;
-                const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
                 T *dst = out + (long long)(q.row0 + t0 + t) * P.stride[side] + (h << DL) + d;
+                float y[VEC];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float y[8];
+                for (int i = 0; i < VEC; ++i) y[i] = scale[k] * (float)(int8_t)((i < 4 ? w[k].x : w[k].y) >> (8 * (i & 3)));
+                uint4 o;
+                if constexpr (VEC == 4) {
+                    o = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+                } else {
+                    uint32_t b[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[i] = scale[k] * (float)(int8_t)(u[2 * e + (i >> 2)] >> (8 * (i & 3)));
-                        if constexpr (sizeof(T) == 2) y[i] = __bfloat162float(__float2bfloat16_rn(y[i]));
-                    }
-                    if (vec) {
-                        store8(dst + 8 * e, y);
-                    } else {
+                    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[i]) : "f"(y[2 * i + 1]), "f"(y[2 * i]));
+                    o = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+                if (vec) {
+                    *reinterpret_cast<uint4 *>(dst) = o;
+                } else {
+                    const T *e = reinterpret_cast<const T *>(&o);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[8 * e + i] = (T)y[i];
-                    }
+                    for (int i = 0; i < VEC; ++i) dst[i] = e[i];
                 }
             }
         }
@@ -377,7 +408,7 @@ extern "C" int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out
     if (rc) return rc;
     ReadParams P{*kv, *batch, {k_out, v_out}, {k_stride, v_stride}, (batch->max_rows + READ_TOKENS - 1) / READ_TOKENS,
                  __builtin_ctz(kv->block), __builtin_ctz(kv->dim), 0, status};
-    while (P.row_log2 < 8 && (1 << P.row_log2) < width / 16) ++P.row_log2;
+    while (P.row_log2 < 8 && (1 << P.row_log2) < width / (16 / es)) ++P.row_log2;
     const long long tiles = (long long)P.tiles * batch->n_seqs;
     if (tiles > 0x7FFFFFFF) return fail_message(TF_EINVAL_SIZE, "too many rows in one call");
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -669,7 +669,7 @@ extern "C" int tf_sample(const void *logits, int rows, int vocab, int64_t stride
     // CTAs a row: as few as hold it in shared memory, more while SMs are idle and slices long.
     int cluster = 1;
     while (cluster < MAX_CLUSTER && ((long long)vocab * es > (long long)cluster * MAX_SLICE_BYTES ||
-                                     ((long long)rows * cluster <= nsm && vocab / cluster > 8192)))
+                                     ((long long)rows * cluster <= nsm && vocab / cluster > 4096)))
         cluster *= 2;
     const int slice = ((vocab + cluster - 1) / cluster + 7) / 8 * 8;
     const bool resident = (long long)slice * es <= MAX_SLICE_BYTES;
