@@ -61,7 +61,8 @@ extern "C" {
 #define TF_EINVAL_FLAGS (-12) /* output flags other than TF_OUT_BF16 | TF_EPI_RELU2 */
 #define TF_EGATHER (-13)      /* empty slot table, or a slot naming a missing expert or x row */
 #define TF_EBOUNDS (-14)      /* the bounds-checking debug build (libtfqmm_debug.so) found an index
-                                 outside its buffer (device status; the access was skipped) */
+                                 outside its buffer, or a call of tfdecode.h a length, row, slot or
+                                 page that does not fit (device status; the access was skipped) */
 
 /*
  * tf_qmm -- one quantized product.
@@ -261,8 +262,10 @@ int tf_qmm_bytes(int N, int K, int bits, int group, int64_t *w_bytes, int64_t *s
 
 /*
  * Reads and clears the device status word of the current device (synchronizes
- * the device).  TF_OK, TF_EDEVICE if a kernel gave up a bounded wait, or (debug
- * build only) TF_EBOUNDS if a kernel found an index outside its buffer.
+ * the device).  TF_OK, TF_EDEVICE if a kernel gave up a bounded wait, or
+ * TF_EBOUNDS if a kernel found an index outside its buffer (products: the debug
+ * build only; the calls of tfdecode.h check the numbers that they read in device
+ * memory in every build).
  */
 int tf_device_status(void);
 

@@ -2,7 +2,7 @@
  * tfqmm_debug.h -- entry points of the bounds-checking debug build only
  * (libtfqmm_debug.so, compiled from the same sources with TF_DEBUG_BOUNDS).
  * That library exports everything tfqmm.h declares, with the same results;
- * its kernels additionally check every shared- and global-memory index
+ * its product kernels additionally check every shared- and global-memory index
  * against its buffer before the access, skip an access that would fall
  * outside, and record it in the device status word, which tf_device_status
  * then reports as TF_EBOUNDS.  No check traps or faults.

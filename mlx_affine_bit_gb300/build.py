@@ -1,7 +1,7 @@
 """Build libtfqmm.so in-tree with nvcc for sm_103a (one -gencode, parallel units).
 
 Two libraries come out of the same sources: libtfqmm.so (the product) and
-libtfqmm_debug.so, built with TF_DEBUG_BOUNDS, whose kernels check every shared-
+libtfqmm_debug.so, built with TF_DEBUG_BOUNDS, whose products check every shared-
 and global-memory index against its buffer and report a violation through the
 device status word (TF_EBOUNDS) instead of making the access.  build_trace()
 makes a third on request, libtfqmm_trace.so (TF_TRACE): per-CTA phase times of

@@ -983,7 +983,7 @@ int tf_device_status(void) {
     if (v) {
         e = cudaMemset(d->status, 0, sizeof v);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(status)");
-        if (v & STATUS_BOUNDS) return fail(TF_EBOUNDS, "the debug build found an index outside its buffer");
+        if (v & STATUS_BOUNDS) return fail(TF_EBOUNDS, "a kernel found an index outside its buffer, or a sequence's numbers that do not fit theirs");
         return fail(TF_EDEVICE, "a kernel gave up a bounded wait");
     }
     return TF_OK;

@@ -1,6 +1,7 @@
 // attend.cu -- tf_kv_attend: attention over the 8-bit paged cache (tfdecode.h).
-// Host side: checks, the split of long sequences, the per-(device, stream)
-// workspace for the parts' sums; the kernels are in attend_rows.cuh.
+// Host side: checks, the choice of the kernel, the per-(device, stream) workspace
+// for the sums of tokens that several CTAs share; the kernels are in
+// attend_rows.cuh and attend_prompt.cuh.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -192,6 +193,8 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
         const double t_prompt = 45e3 + 2900.0 * blocks * pairs / ctas;
         prompt = t_prompt < t_rows;
     }
+    // Rows kernel: tiles of 8 rows where no sequence has more a head (4 rows of 48 x 4000 tokens, 8 heads of 128: 71 us,
+    // 77 in a tile of 16; 8 rows of 16 x 4000, 2 heads of 256: 28 and 33), else of 16.
     const int nt = max_group_rows <= 8 ? 1 : 2, tile_rows = prompt ? 128 * attend::p_tiles(kv->dim) : 8 * nt;
     const long long tiles = (max_group_rows + tile_rows - 1) / tile_rows;
     const int step = prompt ? attend::KEYS : attend::step_of(kv->dim);

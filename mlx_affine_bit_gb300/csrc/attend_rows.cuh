@@ -4,21 +4,28 @@
 // For the rows r of one (sequence, key/value head) -- G query heads a token --
 // and the tokens j they see:
 //     s_rj = (q_r . c_j) * (scale log2(e) ks_page / f_r)      q_r: fp16, times the power of two f_r
-// (the first product runs over bytes as they stand, fp16 subnormals (c + 128) 2^-24,
-// from a start of -128 2^-24 sum(q_r); the second needs the codes themselves: what
-// 128 sum(p) would round away is the small share of tokens that are far from the maximum)
 //     p_rj = 2^(s_rj - m_r),  l_r = sum_j p_rj,  out_r = sum_j p_rj vs_page c'_j / l_r
-// with the running maximum m_r of a warp's tokens.  Codes are exact in fp16.  What
-// enters the second product is w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16, with
-// the running maximum n_r of s_rj + log2(vs_page): relative to the row's largest
-// contribution, however far apart the scales are, it keeps 11 bits down to 2^-29
-// and comes to nothing below 2^-40.
+// with the running maximum m_r of a warp's tokens.  The first product runs over the
+// bytes as they stand, fp16 subnormals (c + 128) 2^-24, from a start of -128 2^-24
+// sum(q_r).  The second takes the codes themselves, exact in fp16: a start of that
+// kind would round away what tokens far from the maximum add.  What enters the
+// second product is w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16, with the running
+// maximum n_r of s_rj + log2(vs_page): relative to the row's largest contribution,
+// however far apart the scales are, it keeps 11 bits down to 2^-29 and comes to
+// nothing below 2^-40.
 //
-// Bound by reading the cache.  The work -- for every sequence, head and tile of
-// up to 8 * NT rows the tokens in steps of 128 -- is one line of steps that the
-// CTAs, as many as are resident at once, cut into equal shares, whatever the
-// lengths.  A CTA takes its share item by item; an item (one tile's tokens) that
-// several CTAs share is joined by the last of them to arrive, in their order.
+// Bound by reading the cache: 48 x 8000 tokens of 8 heads of 128, 32 query heads,
+// take 129 us, 6.1 TB/s of the codes; 1 x 131072 tokens 52 us (5.2 TB/s), of which
+// some 12 us are a call's beginning and end (a launch, the lengths, pages, codes,
+// the join of the parts): 1 x 700 tokens take 13 us.  Rows beyond 16 of a sequence
+// and head read the tokens again, out of L2 (16 sequences of up to 4100 tokens, 40
+// rows each: 32 us).
+//
+// The work -- for every sequence, head and tile of up to 8 * NT rows the tokens in
+// steps of 128 -- is one line of steps that the CTAs, as many as are resident at
+// once, cut into equal shares, whatever the lengths.  A CTA takes its share item by
+// item; an item (one tile's tokens) that several CTAs share is joined by the last of
+// them to arrive, in their order.
 // A warp takes 32 tokens at a time, in the fragments of mma.sync m16n8k16: a
 // lane's 16 bytes of a key are four k steps of a B fragment (the rows of q are
 // loaded in the same order), and 16 bytes of the values of four tokens are eight
@@ -394,163 +401,163 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 for (int e = 0; e < 4; ++e) o[p][u][e] = 0.f;
         }
         for (bool opened = true; c0 < t_end; c0 = c1, opened = false) {
-        if (!opened) {
-            open_chunk();
-            __syncthreads();
-        }
-        for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
-            if (lane == 0) fetch(ft);
-            ft += STEP;
-            mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
-            const uint8_t *tiles = mine + (it % NST) * STAGE;
-            // Tiles t and t + 16: their pages (a tile of no page is not seen).
-            int pi[TILES];
-            bool on[TILES];
-#pragma unroll
-            for (int h = 0; h < TILES; ++h) {
-                pi[h] = min(((t + 16 * h) >> BL) - pg0, npages - 1);
-                on[h] = s_page[pi[h]] >= 0 && !(h == 1 && single && t + 16 >= c1);
+            if (!opened) {
+                open_chunk();
+                __syncthreads();
             }
-            // Scores of the tiles' tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
-            float sc[2 * TILES][4];
-#pragma unroll
-            for (int nb = 0; nb < 2 * TILES; ++nb)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
-#pragma unroll
-            for (int v = 0; v < KV; ++v) {
-                uint32_t kw[2 * TILES][4];
-#pragma unroll
-                for (int nb = 0; nb < 2 * TILES; ++nb) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
-                    kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
-                    kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
-                    uint2 qa1 = make_uint2(0u, 0u);
-                    if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
-#pragma unroll
-                    for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
-                }
-            }
-            // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
-            const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
-            float ks[TILES], vs[TILES];
-#pragma unroll
-            for (int h = 0; h < TILES; ++h) ks[h] = s_ks[pi[h]], vs[h] = s_vs[pi[h]];
-            uint32_t pb[NT][2 * TILES];
-            bool grew = false;
-            float mt[NT], nt[NT];
-#pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
+                if (lane == 0) fetch(ft);
+                ft += STEP;
+                mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
+                const uint8_t *tiles = mine + (it % NST) * STAGE;
+                // Tiles t and t + 16: their pages (a tile of no page is not seen).
+                int pi[TILES];
+                bool on[TILES];
 #pragma unroll
                 for (int h = 0; h < TILES; ++h) {
-                    const float f = rowf[u] * ks[h];
-#pragma unroll
-                    for (int nb = 2 * h; nb < 2 * h + 2; ++nb) sc[nb][2 * u] *= f, sc[nb][2 * u + 1] *= f;
+                    pi[h] = min(((t + 16 * h) >> BL) - pg0, npages - 1);
+                    on[h] = s_page[pi[h]] >= 0 && !(h == 1 && single && t + 16 >= c1);
                 }
-            if (!full) {
+                // Scores of the tiles' tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
+                float sc[2 * TILES][4];
+#pragma unroll
+                for (int nb = 0; nb < 2 * TILES; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
+#pragma unroll
+                for (int v = 0; v < KV; ++v) {
+                    uint32_t kw[2 * TILES][4];
+#pragma unroll
+                    for (int nb = 0; nb < 2 * TILES; ++nb) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
+                        kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
+                        kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
+                        uint2 qa1 = make_uint2(0u, 0u);
+                        if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
+#pragma unroll
+                        for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
+                    }
+                }
+                // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
+                const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
+                float ks[TILES], vs[TILES];
+#pragma unroll
+                for (int h = 0; h < TILES; ++h) ks[h] = s_ks[pi[h]], vs[h] = s_vs[pi[h]];
+                uint32_t pb[NT][2 * TILES];
+                bool grew = false;
+                float mt[NT], nt[NT];
 #pragma unroll
                 for (int u = 0; u < NT; ++u)
 #pragma unroll
-                    for (int nb = 0; nb < 2 * TILES; ++nb)
+                    for (int h = 0; h < TILES; ++h) {
+                        const float f = rowf[u] * ks[h];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = t + 8 * nb + tok[e];
-                            if (!(on[nb >> 1] && j >= see_from[u] && j < see_to[u])) sc[nb][2 * u + e] = -INFINITY;
-                        }
-            }
+                        for (int nb = 2 * h; nb < 2 * h + 2; ++nb) sc[nb][2 * u] *= f, sc[nb][2 * u + 1] *= f;
+                    }
+                if (!full) {
 #pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                float top[TILES];
+                    for (int u = 0; u < NT; ++u)
 #pragma unroll
-                for (int h = 0; h < TILES; ++h)
-                    top[h] = fmaxf(fmaxf(sc[2 * h][2 * u], sc[2 * h][2 * u + 1]), fmaxf(sc[2 * h + 1][2 * u], sc[2 * h + 1][2 * u + 1]));
+                        for (int nb = 0; nb < 2 * TILES; ++nb)
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1)
-#pragma unroll
-                    for (int h = 0; h < TILES; ++h) top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], o));
-                mt[u] = m[u];
-                nt[u] = n[u];
-#pragma unroll
-                for (int h = 0; h < TILES; ++h) {
-                    mt[u] = fmaxf(mt[u], top[h]);
-                    nt[u] = fmaxf(nt[u], top[h] + vs[h]);
+                            for (int e = 0; e < 2; ++e) {
+                                const int j = t + 8 * nb + tok[e];
+                                if (!(on[nb >> 1] && j >= see_from[u] && j < see_to[u])) sc[nb][2 * u + e] = -INFINITY;
+                            }
                 }
-                grew |= mt[u] > m[u] || nt[u] > n[u];
-            }
-            if (__any_sync(~0u, grew)) {
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
-                    if (m[u] != -INFINITY) l[u] *= exp2_fast(m[u] - mt[u]);
-                    const float a = n[u] == -INFINITY ? 0.f : exp2_fast(n[u] - nt[u]);
-                    m[u] = mt[u];
-                    n[u] = nt[u];
-                    // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
-                    const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
+                    float top[TILES];
 #pragma unroll
-                    for (int p = 0; p < MT; ++p) {
-                        o[p][u][0] *= a0;
-                        o[p][u][1] *= a1;
-                        o[p][u][2] *= a0;
-                        o[p][u][3] *= a1;
+                    for (int h = 0; h < TILES; ++h)
+                        top[h] = fmaxf(fmaxf(sc[2 * h][2 * u], sc[2 * h][2 * u + 1]), fmaxf(sc[2 * h + 1][2 * u], sc[2 * h + 1][2 * u + 1]));
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+                        for (int h = 0; h < TILES; ++h) top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], o));
+                    mt[u] = m[u];
+                    nt[u] = n[u];
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) {
+                        mt[u] = fmaxf(mt[u], top[h]);
+                        nt[u] = fmaxf(nt[u], top[h] + vs[h]);
+                    }
+                    grew |= mt[u] > m[u] || nt[u] > n[u];
+                }
+                if (__any_sync(~0u, grew)) {
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        if (m[u] != -INFINITY) l[u] *= exp2_fast(m[u] - mt[u]);
+                        const float a = n[u] == -INFINITY ? 0.f : exp2_fast(n[u] - nt[u]);
+                        m[u] = mt[u];
+                        n[u] = nt[u];
+                        // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
+                        const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
+#pragma unroll
+                        for (int p = 0; p < MT; ++p) {
+                            o[p][u][0] *= a0;
+                            o[p][u][1] *= a1;
+                            o[p][u][2] *= a0;
+                            o[p][u][3] *= a1;
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const float mm = m[u] == -INFINITY ? 0.f : m[u];
+                for (int u = 0; u < NT; ++u) {
+                    const float mm = m[u] == -INFINITY ? 0.f : m[u];
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) {
+                        const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs[h] - n[u] + W_EXP, 115.f));
+#pragma unroll
+                        for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
+                            const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
+                            l[u] += p0 + p1;
+                            pb[u][nb] = pack_half(p0 * f, p1 * f);
+                        }
+                    }
+                }
+                // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 16 lr + .. (dim 64: 8 lr + ..).
 #pragma unroll
                 for (int h = 0; h < TILES; ++h) {
-                    const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs[h] - n[u] + W_EXP, 115.f));
+                    if (!on[h]) continue;                // (its codes were not fetched)
 #pragma unroll
-                    for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
-                        const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
-                        l[u] += p0 + p1;
-                        pb[u][nb] = pack_half(p0 * f, p1 * f);
-                    }
-                }
-            }
-            // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 16 lr + .. (dim 64: 8 lr + ..).
+                    for (int v = 0; v < NV; ++v) {
+                        uint32_t a[4][VB / 4];
 #pragma unroll
-            for (int h = 0; h < TILES; ++h) {
-                if (!on[h]) continue;                // (its codes were not fetched)
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    uint32_t a[4][VB / 4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
-                        if constexpr (VB == 16) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                            a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                            a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                            a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                        for (int k = 0; k < 4; ++k) {
+                            const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
+                            if constexpr (VB == 16) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                                a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                                a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                                a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < VB / 4; ++i) {
-                        // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
-                        const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
-                        const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
-                        const int p = v * VB / 2 + 2 * i;
-                        const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
-                        const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
+                        for (int i = 0; i < VB / 4; ++i) {
+                            // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
+                            const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
+                            const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
+                            const int p = v * VB / 2 + 2 * i;
+                            const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
+                            const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
 #pragma unroll
-                        for (int u = 0; u < NT; ++u) {
-                            mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
-                            mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
+                            for (int u = 0; u < NT; ++u) {
+                                mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
+                                mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
+                            }
                         }
                     }
                 }
+                __syncwarp();                        // (every lane has read the stage that is filled next)
             }
-            __syncwarp();                        // (every lane has read the stage that is filled next)
-        }
-        __syncthreads();                         // (and every warp this chunk's pages)
+            __syncthreads();                         // (and every warp this chunk's pages)
         }
 
         // Join the warps: row sums, and the outputs (in the rings' place) in warp order.

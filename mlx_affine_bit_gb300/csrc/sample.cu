@@ -9,11 +9,16 @@
 // fits (the logits then leave global memory once).  The cut of a prefix is found
 // by counting tokens (and adding up weights) in bins: of z = (x - max) / T first,
 // each CTA its own slice, all of them added up by every CTA over distributed shared
-// memory.  The tokens down to the bin that holds the cut are
-// mostly few: they move, in index order, to the first CTA, which cuts them by
-// bins of the bits of x and draws, alone.  Where they are many the cluster goes on
-// together in the same way on its slices.  Reading the logits bounds many rows,
-// the chain of cluster barriers (about ten) a few.
+// memory.  The tokens down to the bin that holds the cut are mostly few: they move,
+// in index order, to the first CTA, which cuts them by bins of the bits of x and
+// draws, alone.  Where they are many (more than MAX_LIST) the cluster goes on
+// together in the same way on its slices.
+//
+// One row of 248320 fp32 logits takes 18 us, bound by the chain of barriers and of
+// reads of the other CTAs' shared memory (four of the cluster, some twenty of the
+// first CTA alone); 48 rows 62 us (0.8 TB/s: some 50 instructions a logit in three
+// passes over the slice, and barriers, not the read of 48 MB); 300 rows of 32003
+// bf16 logits 33 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,8 +41,10 @@ constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit:
 // exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest, bin b the nearest to b.
 constexpr float BINS_PER_Z = BINS / 23.f, Z_END = -22.25f;
 static_assert(BINS == THREADS, "a thread a bin");
-constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone
-constexpr int MAX_SLICE_BYTES = 80 * 1024; // of a row in one CTA's shared memory (two CTAs an SM)
+constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone (300 rows of 32003, top-p 0.8: 40 us; 60 with 1024, 40 with 4096)
+// Of a row in one CTA's shared memory, for two CTAs an SM (300 x 32003 bf16: 33 us, 69 with the logits read from global
+// memory in each pass; 48 x 248320 fp32: 62 and 73).
+constexpr int MAX_SLICE_BYTES = 80 * 1024;
 
 struct Params {
     const void *logits;
@@ -168,8 +175,8 @@ __device__ __forceinline__ u64 warps_of(Shared &S, u64 mine, u64 &all) {
     __syncthreads();
     if (lane == 0) S.warp_sum[warp] = mine;
     __syncthreads();
-    u64 x = lane < WARPS ? S.warp_sum[lane] : 0, before = lane < warp ? x : 0;
-    for (int o = 16; o > 0; o >>= 1) {
+    u64 x = S.warp_sum[lane % WARPS], before = lane % WARPS < warp ? x : 0;
+    for (int o = WARPS / 2; o > 0; o >>= 1) {
         x += __shfl_xor_sync(~0u, x, o);
         before += __shfl_xor_sync(~0u, before, o);
     }
@@ -206,9 +213,13 @@ __device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, in
     u64 wi = b.w;
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned a = __shfl_up_sync(~0u, ni, o);
-        const u64 d = __shfl_up_sync(~0u, wi, o);
-        if (lane >= o) ni += a, wi += d;
+        if (lane >= o) ni += a;
     }
+    if (weighted)
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 d = __shfl_up_sync(~0u, wi, o);
+            if (lane >= o) wi += d;
+        }
     if (lane == 31) S.warp_at[warp] = (int)ni, S.warp_sum[warp] = wi;
     if (tid == 0) S.found.bin = -1;
     __syncthreads();
@@ -216,10 +227,13 @@ __device__ __forceinline__ Bin count_bins(Shared &S, const Group<CLUSTER> &G, in
     u64 wa = lane < WARPS ? S.warp_sum[lane] : 0, wb = lane < warp ? wa : 0;
     na = __reduce_add_sync(~0u, na);
     nb = __reduce_add_sync(~0u, nb);
-    for (int o = 16; o > 0; o >>= 1) {
-        wa += __shfl_xor_sync(~0u, wa, o);
-        wb += __shfl_xor_sync(~0u, wb, o);
-    }
+    if (weighted)
+        for (int o = WARPS / 2; o > 0; o >>= 1) {                // (the other lanes hold none)
+            wa += __shfl_xor_sync(~0u, wa, o);
+            wb += __shfl_xor_sync(~0u, wb, o);
+        }
+    wa = __shfl_sync(~0u, wa, 0);
+    wb = __shfl_sync(~0u, wb, 0);
     b.n_before = nb + ni - b.n;
     b.w_before = wb + wi - b.w;
     all = Bin{na, 0, wa, 0};
@@ -235,12 +249,13 @@ __device__ __forceinline__ Found find_bin(Shared &S, const Bin &b, unsigned abov
     return S.found;
 }
 
-// Cuts the group's tokens, in bins of z down to `f.bin`, at the target, which lies in that bin; returns the weight kept.
+// Cuts the group's tokens, in bins of z down to `f.bin`, at the target, which lies in that bin; returns the weight kept
+// (where `weighted`).
 // each(g) calls g(logit, index) for this thread's tokens; in_order(g) does so warp by warp in index order,
 // 32 tokens at a time (index -1 past the end).
 template <bool CLUSTER, class Each, class InOrder>
 __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &counting, const Scale &sc, float T, Found f,
-                                      const Target &t, Cut &cut, Each each, InOrder in_order) {
+                                      const Target &t, bool weighted, Cut &cut, Each each, InOrder in_order) {
     // Keys that the bin can hold, a little more at both ends.
     cut.z_bin = f.bin;
     cut.last = 0x7FFFFFFF;
@@ -250,10 +265,10 @@ __device__ __forceinline__ u64 refine(Shared &S, const Group<CLUSTER> &G, int &c
         int shift = 0;
         while (((k_hi - k_lo) >> shift) >= (uint32_t)BINS) ++shift;
         Bin all;
-        const Bin b = count_bins(S, G, counting, true, all, [&](auto add) {
+        const Bin b = count_bins(S, G, counting, weighted, all, [&](auto add) {
             each([&](float v, int) {
                 const uint32_t key = key_of(v);
-                if (key >= k_lo && key <= k_hi && sc.bin(v) == cut.z_bin) add((int)((k_hi - key) >> shift), sc.weight(v));
+                if (key >= k_lo && key <= k_hi && sc.bin(v) == cut.z_bin) add((int)((k_hi - key) >> shift), weighted ? sc.weight(v) : 0u);
             });
         });
         const Found g = find_bin(S, b, f.above, f.mass_above, t);
@@ -566,7 +581,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 warps_of(S, w, all);
                 return all;
             };
-            if (!mass) whole = f.bin >= 0 ? refine(S, one, counting, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each_listed, listed_in_order)
+            if (!mass) whole = f.bin >= 0 ? refine(S, one, counting, sc, Tk, f, Target{false, (unsigned)k, 0}, false, cut, each_listed, listed_in_order)
                                           : whole_listed();
             if (!mass && f.bin >= 0 && by_p) {
                 // (counted without weights: the weight that top-k keeps)
@@ -588,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                     });
                     f = find_bin(S, lb, 0, 0, t);
                 }
-                if (f.bin >= 0) refine(S, one, counting, sc, Tk, f, t, cut, each_listed, listed_in_order);
+                if (f.bin >= 0) refine(S, one, counting, sc, Tk, f, t, true, cut, each_listed, listed_in_order);
             }
             draw(S, one, sc, cut, S.least, u, P.tokens + row, prob, each_listed, listed_in_order);
             G.wait();
@@ -604,14 +619,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
         if (!mass) {
             whole = all_bins.w;
             f = find_bin(S, wb, 0, 0, Target{false, (unsigned)k, 0});
-            if (f.bin >= 0) whole = refine(S, G, counting, sc, Tk, f, Target{false, (unsigned)k, 0}, cut, each, in_order);
+            if (f.bin >= 0) whole = refine(S, G, counting, sc, Tk, f, Target{false, (unsigned)k, 0}, true, cut, each, in_order);
             if (by_p) {
                 const Target t{true, 0, goal_of(whole)};
                 f = find_bin(S, wb, 0, 0, t);
-                if (f.bin >= 0) refine(S, G, counting, sc, Tk, f, t, cut, each, in_order);
+                if (f.bin >= 0) refine(S, G, counting, sc, Tk, f, t, true, cut, each, in_order);
             }
         } else if (f.bin >= 0) {
-            refine(S, G, counting, sc, Tk, f, Target{true, 0, goal_of(whole)}, cut, each, in_order);
+            refine(S, G, counting, sc, Tk, f, Target{true, 0, goal_of(whole)}, true, cut, each, in_order);
         }
     }
     draw(S, G, sc, cut, S.least, u, P.tokens + row, prob, each, in_order);
@@ -666,7 +681,9 @@ extern "C" int tf_sample(const void *logits, int rows, int vocab, int64_t stride
     int nsm = 0, *status = nullptr;
     const int rc = device_info(&nsm, &status);
     if (rc) return rc;
-    // CTAs a row: as few as hold it in shared memory, more while SMs are idle and slices long.
+    // CTAs a row: as few as hold it in shared memory, more while SMs are idle and slices long: over 4096 logits (1 and 8
+    // rows of 32003 bf16: 14 and 17 us; over 8192: 15 and 18, over 2048: 15 and 23; one row of 248320 fp32 with 16 CTAs
+    // 18 us, with 8 30).
     int cluster = 1;
     while (cluster < MAX_CLUSTER && ((long long)vocab * es > (long long)cluster * MAX_SLICE_BYTES ||
                                      ((long long)rows * cluster <= nsm && vocab / cluster > 4096)))

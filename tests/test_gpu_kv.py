@@ -205,3 +205,23 @@ def test_another_stream():
     q.cache.append(k, v, b, stream=side)
     side.synchronize()
     q.check(0, 70)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("amax", [127.0, 1.0, 0.3, 3e-4, 1e-28, 3e-31, 5e36])
+def test_values_in_the_middle_of_two_codes(dtype, amax):
+    # (c + 1/2) scale, and its neighbours some fp32 steps away: nearest, even in the middle, of the rounded quotient.
+    q = Sequences([64 + 20], 1, 128, 64, dtype, 10)
+    scale = np.float32(amax) * (np.float32(1) / np.float32(127))
+    rng = np.random.default_rng(11)
+    for a in (q.k, q.v):
+        with np.errstate(under="ignore"):
+            x = (rng.integers(-126, 126, a[0].shape) + 0.5).astype(np.float32) * scale
+        steps = rng.integers(-40, 41, x.shape)
+        x = (x.view(np.int32) + np.where(x == 0, 0, steps).astype(np.int32)).view(np.float32)
+        x[0, 0, 0] = x[64, 0, 3] = amax
+        a[0] = bf16(x) if dtype == BF16 else x
+    q.append([(0, 70)])
+    q.append([(70, 84)])
+    status_clean()
+    q.check(0, 84)
