@@ -15,8 +15,8 @@
 // and token one exponential and about four others, per token and dimension of the
 // cache about two to widen a code.  Causal, 32 query heads of 128 over 8: 4000 tokens
 // of a prompt 201 us (652 TFLOP/s), 8000 653 us (803 TFLOP/s); 16 heads of 256: 4000
-// tokens 214 us; 16 heads of 64: 91 us; three chunks of up to 509 tokens, 16 heads of
-// 256, window 4096: 93 us.  A step of two tiles (256 rows, 128 tokens, dim 128) takes
+// tokens 196 us; 16 heads of 64: 91 us; three chunks of up to 509 tokens, 16 heads of
+// 256, window 4096: 89 us.  A step of two tiles (256 rows, 128 tokens, dim 128) takes
 // 2.7 us, 1.7 us of them the products: one with N = 128 takes 94 to 107 clocks for
 // 16 of K, measured alone, which is 60 to 68 % of the peak.  An item's beginning and end (the
 // rows of q, the first scores, the outputs) cost 6 us, the launch's plan 4.  A CTA (one an SM) works on two tiles of 128 rows
@@ -697,26 +697,34 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 sq = P.scale < 0.f ? -fq : fq;
             };
             if (!P.q_f32 && q16) {
-                // The whole row at once.
-                uint4 r[D / 8];
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + q_at);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) r[i] = src[i];
+                // The warp's 32 rows as they are to their places, LR lanes a row; then each thread its own row there.
+                constexpr int LR = D / 8, RPI = 32 / LR, CU = 2, QU = D == 256 ? 2 : 16;   // (measured: fewer are faster at dim 256, more at 128)
+#pragma unroll CU
+                for (int j = 0; j < LR; ++j) {
+                    const int r = j * RPI + lane / LR, c = lane % LR;
+                    const uint16_t *src = static_cast<const uint16_t *>(P.q) + __shfl_sync(~0u, q_at, r) + 8 * c;
+                    const uint32_t dst = smem_u32(q_s + t * TB + ((warp & 3) * 32 + r) * 128 + (c >> 3) * (KEYS * 128) + (((c & 7) ^ (r & 7)) << 4));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                auto at = [&](int d) { return *reinterpret_cast<const uint4 *>(q_row + (d >> 6) * (KEYS * 128) + ((((d >> 3) & 7) ^ (row & 7)) << 4)); };
                 uint32_t top = 0;                // magnitudes of bf16 are ordered as their bits
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t u[4] = {r[i].x & 0x7FFF7FFFu, r[i].y & 0x7FFF7FFFu, r[i].z & 0x7FFF7FFFu, r[i].w & 0x7FFF7FFFu};
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3])));
+#pragma unroll QU
+                for (int d = 0; d < D; d += 8) {
+                    const uint4 r = at(d);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu)));
                 }
                 amax = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
                 factors();
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t u[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll QU
+                for (int d = 0; d < D; d += 8) {
+                    const uint4 r = at(d);
+                    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(u[e] << 16), x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-                    put8(8 * i, x);
+                    put8(d, x);
                 }
             } else {
                 auto q8 = [&](int d, float (&x)[8]) {
