@@ -14,11 +14,11 @@
 // draws, alone.  Where they are many (more than MAX_LIST) the cluster goes on
 // together in the same way on its slices.
 //
-// One row of 248320 fp32 logits takes 18 us, bound by the chain of barriers and of
+// One row of 248320 fp32 logits takes 17 us, bound by the chain of barriers and of
 // reads of the other CTAs' shared memory (four of the cluster, some twenty of the
-// first CTA alone); 48 rows 62 us (0.8 TB/s: some 50 instructions a logit in three
-// passes over the slice, and barriers, not the read of 48 MB); 300 rows of 32003
-// bf16 logits 33 us.
+// first CTA alone); 48 rows 59 us (0.8 TB/s: some 55 instructions for 32 logits in
+// three passes over the slice, and barriers, not the read of 48 MB); 300 rows of
+// 32003 bf16 logits 32 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -114,8 +114,6 @@ struct Shared {
     float max;                   // of this CTA's slice
     unsigned n_part;             // this CTA's tokens and weight of a kind that the ranks add up
     u64 part;
-    u64 goal;                    // 64-bit products are one thread's work: the SM has few units for them
-    unsigned least;
     Found found;
     int tie_last;
     // Tokens by bin, and their weights in 16-bit halves (a slice holds at most 2^16 tokens); of alternate
@@ -124,6 +122,25 @@ struct Shared {
     float list_x[MAX_LIST];      // this CTA's tokens of the set that one CTA finishes, in index order; the first CTA's grows to all of them
     int list_i[MAX_LIST];
 };
+
+// f * whole in double precision (f in [0, 1), whole < 2^52), rounded to a whole number down, or up.  By whole numbers:
+// the SM has few units for doubles, and every thread can have it at once.
+__device__ __forceinline__ u64 product(float f, u64 whole, bool up) {
+    const uint32_t b = __float_as_uint(f), e = b >> 23;
+    const u64 m = e ? (b & 0x7FFFFFu) | 0x800000u : b;       // f = m 2^(max(e, 1) - 150)
+    const u64 hi = __umul64hi(m, whole), lo = m * whole;
+    const int length = hi ? 128 - __clzll(hi) : 64 - __clzll(lo), over = max(0, length - 53);
+    u64 q = lo;
+    if (over) {                                              // to 53 bits: the nearest, even in the middle
+        q = hi << (64 - over) | lo >> over;
+        const u64 rest = lo & ((1ull << over) - 1), half = 1ull << (over - 1);
+        q += rest > half || (rest == half && (q & 1));
+    }
+    const int down = 150 - (int)max(e, 1u) - over;
+    if (down <= 0) return q << -down;
+    if (down >= 64) return up && q;
+    return (q >> down) + (up && (q & ((1ull << down) - 1)));
+}
 
 // The CTAs that work together: the row's cluster, or one CTA.
 template <bool CLUSTER>
@@ -335,9 +352,7 @@ __device__ __forceinline__ void draw(Shared &S, const Group<CLUSTER> &G, const S
     const u64 total = parts.w;
     before += parts.w_before;
     // The running sum exceeds u * total where it exceeds its whole part (u from 1 on: the last token).
-    if (threadIdx.x == 0) S.goal = (u64)fmax(0.0, fmin((double)u * (double)total, (double)total - 0.5));
-    __syncthreads();
-    const u64 goal = S.goal;
+    const u64 goal = u < 1.f ? min(product(fmaxf(u, 0.f), total, false), total - 1) : total - 1;
     if (before <= goal && before + mine > goal)
         in_order([&](float v, int i) {
             const unsigned w = i >= 0 ? kept(v, i) : 0u;
@@ -416,6 +431,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
         }
     };
 
+    // The row's parameters (on their way while the logits are).
+    const float T = fminf(P.temperature ? P.temperature[row] : 1.f, FLT_MAX);
+    const float p = P.top_p ? P.top_p[row] : 1.f, u = P.u[row], min_p = P.min_p ? P.min_p[row] : 0.f;
+    const int top_k = P.top_k ? P.top_k[row] : 0;
+
     // The slice, and its largest logit.
     float top = -INFINITY;
     if (RESIDENT) {
@@ -473,15 +493,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     if (tid == 0) {
         for (int q = 0; q < WARPS; ++q) top = fmaxf(top, S.warp_max[q]);
         S.max = top;
-        // The least whole weight of at least min_p times the largest.
-        const float mp = P.min_p && (!P.temperature || P.temperature[row] > 0.f) ? P.min_p[row] : 0.f;
-        S.least = mp > 0.f ? (unsigned)fmax(1.0, ceil((double)fminf(mp, 1.f) * 2147483648.0)) : 1u;
     }
     G.sync();
     top = -INFINITY;
     if (lane < G.size) top = G.of(S, lane)->max;
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float T = fminf(P.temperature ? P.temperature[row] : 1.f, FLT_MAX);
     if (top == -INFINITY) {
         if (G.rank == 0 && tid == 0) {
             P.tokens[row] = -1;
@@ -492,18 +508,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     }
     const bool greedy = !(T > 0.f);
     const Scale sc{top, greedy ? 1.f : __fdiv_rn(1.f, T)};
-    const float p = P.top_p ? P.top_p[row] : 1.f;
-    const int k = greedy ? 1 : P.top_k ? P.top_k[row] : 0;       // (the first of the largest: the one token that top-k 1 keeps)
+    // The least whole weight of at least min_p times the largest (a power of two times min_p is exact).
+    const unsigned least = min_p > 0.f && !greedy ? max(1u, __float2uint_ru(fminf(min_p, 1.f) * WEIGHT_ONE)) : 1u;
+    const int k = greedy ? 1 : top_k;            // (the first of the largest: the one token that top-k 1 keeps)
     const bool by_k = k > 0 && k < P.vocab, by_p = p < 1.f && !greedy;
-    const float u = P.u[row], Tk = greedy ? 1.f : T;
+    const float Tk = greedy ? 1.f : T;
     float *prob = P.probs ? P.probs + row : nullptr;
     // The goal of top-p over a weight: the least whole number that reaches it, at least 1 (the first token).
-    auto goal_of = [&](u64 whole) {
-        __syncthreads();
-        if (tid == 0) S.goal = (u64)fmax(1.0, ceil((double)p * (double)whole));
-        __syncthreads();
-        return S.goal;
-    };
+    auto goal_of = [&](u64 whole) { return max(1ull, product(fmaxf(p, 0.f), whole, true)); };
 
     Cut cut{BINS - 1, 0, 0x7FFFFFFF};
     int counting = 0;
@@ -605,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
                 }
                 if (f.bin >= 0) refine(S, one, counting, sc, Tk, f, t, true, cut, each_listed, listed_in_order);
             }
-            draw(S, one, sc, cut, S.least, u, P.tokens + row, prob, each_listed, listed_in_order);
+            draw(S, one, sc, cut, least, u, P.tokens + row, prob, each_listed, listed_in_order);
             G.wait();
             return;
         }
@@ -629,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
             refine(S, G, counting, sc, Tk, f, Target{true, 0, goal_of(whole)}, true, cut, each, in_order);
         }
     }
-    draw(S, G, sc, cut, S.least, u, P.tokens + row, prob, each, in_order);
+    draw(S, G, sc, cut, least, u, P.tokens + row, prob, each, in_order);
     G.sync();                    // (the others may still read this CTA's sum)
 }
 
