@@ -41,10 +41,12 @@ constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit:
 // exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest, bin b the nearest to b.
 constexpr float BINS_PER_Z = BINS / 23.f, Z_END = -22.25f;
 static_assert(BINS == THREADS, "a thread a bin");
-constexpr int MAX_LIST = 2048;                   // tokens that one CTA finishes alone (300 rows of 32003, top-p 0.8: 40 us; 60 with 1024, 40 with 4096)
-// Of a row in one CTA's shared memory, for two CTAs an SM (300 x 32003 bf16: 33 us, 69 with the logits read from global
-// memory in each pass; 48 x 248320 fp32: 62 and 73).
-constexpr int MAX_SLICE_BYTES = 80 * 1024;
+// Tokens that one CTA finishes alone.  300 rows of 32003, top-p 0.8, some of which leave more than 2048: 34 us; 48 with
+// 2048 (the cluster goes on with its whole slices), 60 with 1024.
+constexpr int MAX_LIST = 4096;
+// Of a row in one CTA's shared memory, for two CTAs an SM beside the list (300 x 32003 bf16: 33 us, 69 with the logits
+// read from global memory in each pass; 48 x 248320 fp32: 62 and 73).
+constexpr int MAX_SLICE_BYTES = 66 * 1024;
 
 struct Params {
     const void *logits;
@@ -61,6 +63,8 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = __float_as_uint(x);
     return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
+
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k); }
 
 // The scaled distribution of a row.
 struct Scale {
@@ -108,10 +112,10 @@ struct Cut {
 };
 
 struct Shared {
-    float warp_max[WARPS];
+    uint32_t warp_max[WARPS];
     int warp_at[WARPS];
     u64 warp_sum[WARPS];
-    float max;                   // of this CTA's slice
+    uint32_t max;                // key of the largest logit of this CTA's slice
     unsigned n_part;             // this CTA's tokens and weight of a kind that the ranks add up
     u64 part;
     Found found;
@@ -487,17 +491,15 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     } else {
         each([&](float v, int) { top = fmaxf(top, v); });
     }
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (lane == 0) S.warp_max[warp] = top;
+    uint32_t top_key = __reduce_max_sync(~0u, key_of(top));
+    if (lane == 0) S.warp_max[warp] = top_key;
     __syncthreads();
-    if (tid == 0) {
-        for (int q = 0; q < WARPS; ++q) top = fmaxf(top, S.warp_max[q]);
-        S.max = top;
+    if (warp == 0) {
+        top_key = __reduce_max_sync(~0u, lane < WARPS ? S.warp_max[lane] : 0u);
+        if (lane == 0) S.max = top_key;
     }
     G.sync();
-    top = -INFINITY;
-    if (lane < G.size) top = G.of(S, lane)->max;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    top = of_key(__reduce_max_sync(~0u, lane < G.size ? G.of(S, lane)->max : 0u));
     if (top == -INFINITY) {
         if (G.rank == 0 && tid == 0) {
             P.tokens[row] = -1;
