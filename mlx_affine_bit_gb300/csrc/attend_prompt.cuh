@@ -18,10 +18,12 @@
 // tokens 196 us; 16 heads of 64: 91 us; three chunks of up to 509 tokens, 16 heads of
 // 256, window 4096: 89 us.  A step of two tiles (256 rows, 128 tokens, dim 128) takes
 // 2.7 us, 1.7 us of them the products: one with N = 128 takes 94 to 107 clocks for
-// 16 of K, measured alone, which is 60 to 68 % of the peak.  An item's beginning and end (the
-// rows of q, the first scores, the outputs) cost 6 us, the launch's plan 4.  A CTA (one an SM) works on two tiles of 128 rows
-// (dim 256: one) by steps of 128 tokens, so that one widening serves 256 rows and
-// one tile's softmax runs beside the other's products:
+// 16 of K, measured alone, which is 60 to 68 % of the peak.  An item's beginning and
+// end (the rows of q, the first scores, the outputs) cost 6 us, the launch's plan 4.
+//
+// A CTA (one an SM) works on two tiles of 128 rows (dim 256: one, tensor memory holds
+// no more) by steps of 128 tokens, so that one widening serves 256 rows and one
+// tile's softmax runs beside the other's products:
 //     8 warps    (dim 256: 4) softmax, a row a thread: S out of tensor memory, the
 //                running maxima, w back into tensor memory as the second product's
 //                A operand; the rows of q; the outputs
