@@ -87,7 +87,7 @@ __device__ __forceinline__ PSeq p_seq(const Params &P, int s) {
         // Rows that lie within the matrices get zeros (no token is seen; the line, and with it the other
         // sequences' bits, stay as they are).
         w.q.end = 0;
-        if (w.q.row0 < 0 || w.q.n < 0 || w.q.n > P.b.max_rows || w.q.row0 + w.q.n > P.b.rows) w.q.n = 0;
+        if (!w.q.placed) w.q.n = 0;
     }
     w.tiles = (w.q.n * P.group + R - 1) / R;
     return w;

@@ -225,3 +225,22 @@ def test_values_in_the_middle_of_two_codes(dtype, amax):
     q.append([(70, 84)])
     status_clean()
     q.check(0, 84)
+
+
+@pytest.mark.parametrize("wrong", [(2 ** 31 - 1, -2 ** 31, -2 ** 31 + 5), (0, 2 ** 31 - 1, -2 ** 31 + 3), (-2 ** 31, 2 ** 31 - 1, 20)])
+def test_row_starts_that_wrap_around_are_reported(wrong):
+    # Starts far outside whose 32-bit difference looks like a few rows: nothing is read or written there.
+    q = Sequences([20, 20], 1, 64, 16, BF16, 12)
+    b = q.batch([20, 20], [10, 10])
+    b._keep[2].copy_(torch.tensor(wrong, dtype=torch.int32))
+    x = torch.ones((20, 64), dtype=BF16, device=DEV)
+    out = [torch.full((20, 64), 3.0, dtype=BF16, device=DEV) for _ in range(2)]
+    for call in (lambda: q.cache.append(x, x, b), lambda: q.cache.read(b, k_out=out[0], v_out=out[1]),
+                 lambda: q.cache.attend(x, b, out=out[0], kernel=tf.TF_KV_BY_ROWS),
+                 lambda: q.cache.attend(x, b, out=out[0], kernel=tf.TF_KV_BY_TILES)):
+        call()
+        torch.cuda.synchronize()
+        with pytest.raises(tf.TfError) as e:
+            tf.tf_device_status()
+        assert e.value.rc == -14
+    assert torch.all(q.cache.k == 0) and torch.all(out[0] == 3.0) and torch.all(out[1] == 3.0)
