@@ -115,9 +115,13 @@ int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k
  * A row's bits do not change from call to call with the same arguments; between
  * calls of another batch they may, within that precision, because sequences are
  * cut between the CTAs by the whole call's tokens.
- * Allocates a per-(device, stream) workspace for the parts of split sequences
- * (grown on demand; the first call on a stream must precede any graph capture
- * on it).
+ * The first call on a (device, stream) allocates the stream's workspace for the
+ * parts of split sequences: some 41 MB, enough for every later call, held at the
+ * same address until exit.  It must precede any graph capture on the stream (a
+ * first call inside one is refused with TF_ECUDA and leaves the capture as it is);
+ * a captured graph stays valid whatever is called on the stream afterwards.
+ * Calls on one stream, and replays of the graphs captured on it, share that
+ * workspace: replay them on that stream, or after one another.
  */
 #define TF_IN_F32 4
 #define TF_KV_CAUSAL 8

@@ -17,46 +17,49 @@ using namespace tfq;
 
 namespace {
 
-// Parts of split sequences (floats) and their arrival counters (zero between launches).
+// Parts of split sequences and their arrival counters (zero between launches), one pair for each (device, stream).
+// Allocated once, for the largest launch of either kernel: captured graphs keep these addresses.
 struct Ws {
     float *part = nullptr;
-    size_t floats = 0;
     int *count = nullptr;
-    size_t counters = 0;
 };
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Ws> g_ws;
 
-int workspace(cudaStream_t st, size_t floats, size_t counters, Ws *out) {
+// Floats that a launch of `ctas` CTAs on tiles of `rows` rows needs: two parts a CTA, each of outputs and row sums.
+constexpr size_t part_floats(size_t ctas, int rows, int d) { return ctas * 2 * rows * (d + 4); }
+size_t most_floats(int nsm) {
+    size_t most = 0;
+    for (int d : {64, 128, 256})
+        most = std::max({most, part_floats(attend::MAX_PARTS, 16, d), part_floats(std::min(nsm, attend::MAX_PARTS), 128 * attend::p_tiles(d), d)});
+    return most;
+}
+
+int workspace(cudaStream_t st, int nsm, Ws *out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
     std::lock_guard<std::mutex> lk(g_mu);
     Ws &w = g_ws[{dev, st}];
-    if (w.floats < floats || w.counters < counters) {
-        if (w.part || w.count) {
-            // Earlier launches on this stream may still use it.
-            e = cudaStreamSynchronize(st);
-            if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
-        }
-        if (w.floats < floats) {
-            cudaFree(w.part);
-            w.part = nullptr;
-            w.floats = 0;
-            e = cudaMalloc(&w.part, floats * sizeof(float));
+    if (!w.count) {
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        e = cudaStreamIsCapturing(st, &capture);
+        if (e != cudaSuccess) return cuda_error(e, "cudaStreamIsCapturing");
+        if (capture != cudaStreamCaptureStatusNone)
+            return fail_message(TF_ECUDA, "the first attention call on a stream allocates its workspace and must precede a capture");
+        if (!w.part) {
+            e = cudaMalloc(&w.part, most_floats(nsm) * sizeof(float));
             if (e != cudaSuccess) return cuda_error(e, "cudaMalloc(attention parts)");
-            w.floats = floats;
         }
-        if (w.counters < counters) {
-            cudaFree(w.count);
-            w.count = nullptr;
-            w.counters = 0;
-            e = cudaMalloc(&w.count, counters * sizeof(int));
-            if (e != cudaSuccess) return cuda_error(e, "cudaMalloc(attention counters)");
-            e = cudaMemsetAsync(w.count, 0, counters * sizeof(int), st);
-            if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync(attention counters)");
-            w.counters = counters;
+        int *count = nullptr;
+        e = cudaMalloc(&count, attend::MAX_PARTS * sizeof(int));
+        if (e != cudaSuccess) return cuda_error(e, "cudaMalloc(attention counters)");
+        e = cudaMemsetAsync(count, 0, attend::MAX_PARTS * sizeof(int), st);
+        if (e != cudaSuccess) {
+            cudaFree(count);
+            return cuda_error(e, "cudaMemsetAsync(attention counters)");
         }
+        w.count = count;
     }
     *out = w;
     return TF_OK;
@@ -92,7 +95,7 @@ int launch_rows(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
     if (e != cudaSuccess) return cuda_error(e, "kv_attend set-up");
     const long long grid = std::min({steps, (long long)nsm * per_sm, (long long)attend::MAX_PARTS});
     Ws w;
-    const int rc = workspace(st, (size_t)grid * 2 * 8 * NT * (D + 4), (size_t)grid, &w);
+    const int rc = workspace(st, nsm, &w);
     if (rc) return rc;
     P.part = w.part;
     P.count = w.count;
@@ -104,7 +107,7 @@ int launch_rows(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
 // The same for the prompt kernel: one CTA an SM.
 template <int D>
 int launch_prompt(attend::Params &P, long long steps, int nsm, cudaStream_t st) {
-    constexpr int rows = 128 * attend::p_tiles(D), smem = attend::p_smem(D);
+    constexpr int smem = attend::p_smem(D);
     static unsigned attr_set = 0;   // one bit per device: shared-memory limit raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -117,7 +120,7 @@ int launch_prompt(attend::Params &P, long long steps, int nsm, cudaStream_t st) 
     }
     const long long grid = std::min({steps, (long long)nsm, (long long)attend::MAX_PARTS});
     Ws w;
-    const int rc = workspace(st, (size_t)grid * 2 * rows * (D + 4), (size_t)grid, &w);
+    const int rc = workspace(st, nsm, &w);
     if (rc) return rc;
     P.part = w.part;
     P.count = w.count;
