@@ -77,9 +77,10 @@ extern "C" {
  *            row alone -- the row / window gate of PR #788 extended past 16 rows.
  * Returns TF_OK or a negative status (checked on the host before any launch).
  * Allocation: the first call on a device allocates the device status word, and
- * a call whose plan splits K allocates (or grows, with cudaFree + cudaMalloc)
- * the split-K workspace of its (device, stream).  A caller that must not let
- * the library allocate uses tf_qmm_noalloc instead.
+ * a call whose plan splits K allocates the split-K workspace of its (device,
+ * stream), or a larger one (the old one is kept, since a graph captured on the
+ * stream may use it).  A caller that must not let the library allocate uses
+ * tf_qmm_noalloc instead.
  */
 int tf_qmm(const uint16_t *x, int rows, int K,
            const uint32_t *W, const uint16_t *scales, const uint16_t *biases,
@@ -199,7 +200,8 @@ int tf_qmm_ex(const uint16_t *x, int rows, int K,
  *   their group sums and, when the column tiles are fewer than the SMs and K
  *   holds more than one chunk, the chunk partials of one window (rows * K * 2 +
  *   (K / group) * ceil(rows / 64) * 256 + [(K / 2048) * 64 * N * 4] bytes, grown
- *   on demand; the first call on a stream must precede any graph capture on it).
+ *   on demand; what a captured graph uses is kept; a call inside a graph capture
+ *   needs one as large or larger before it on the stream).
  *   Plain launches: one prepass, then per 64 rows one launch and, with split
  *   chunks, one fold.  Measured on GB300 it overtakes 16-row windows of tf_qmm
  *   from about 24 rows (the 248320 x 2048 LM head; about 30 rows at 12288 x

@@ -353,23 +353,28 @@ int stream_ws(cudaStream_t st, size_t floats, size_t counters, StreamWs **out) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     StreamWs &w = g_ws[{dev, st}];
+    // Outgrown buffers stay allocated: a graph captured on the stream may use them at every replay.  Each is at least
+    // twice the one before, so that they come to less than the last.
     if (w.ws_floats < floats) {
-        if (w.ws) cudaFree(w.ws);
-        w.ws = nullptr;
-        w.ws_floats = 0;
-        e = cudaMalloc(&w.ws, floats * sizeof(float));
+        const size_t n = std::max(floats, 2 * w.ws_floats);
+        float *ws = nullptr;
+        e = cudaMalloc(&ws, n * sizeof(float));
         if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-        w.ws_floats = floats;
+        w.ws = ws;
+        w.ws_floats = n;
     }
     if (w.n_cnt < counters) {
-        if (w.cnt) cudaFree(w.cnt);
-        w.cnt = nullptr;
-        w.n_cnt = 0;
-        e = cudaMalloc(&w.cnt, counters * sizeof(int));
+        const size_t n = std::max(counters, 2 * w.n_cnt);
+        int *cnt = nullptr;
+        e = cudaMalloc(&cnt, n * sizeof(int));
         if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(counters)");
-        e = cudaMemsetAsync(w.cnt, 0, counters * sizeof(int), st);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(counters)");
-        w.n_cnt = counters;
+        e = cudaMemsetAsync(cnt, 0, n * sizeof(int), st);
+        if (e != cudaSuccess) {
+            cudaFree(cnt);
+            return cuda_fail(e, "cudaMemsetAsync(counters)");
+        }
+        w.cnt = cnt;
+        w.n_cnt = n;
     }
     *out = &w;
     return TF_OK;

@@ -77,6 +77,7 @@ __global__ void prompt_fold(const float *part, int nchunks, int N, int rows, int
 struct Ws {
     void *p = nullptr;
     size_t bytes = 0;
+    bool captured = false;      // a graph may use it at every replay: it stays allocated when it is outgrown
 };
 std::mutex g_pmu;
 std::map<std::pair<int, cudaStream_t>, Ws> g_pws;
@@ -85,21 +86,24 @@ int workspace(cudaStream_t st, size_t bytes, void **out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(st, &capture);
+    if (e != cudaSuccess) return cuda_error(e, "cudaStreamIsCapturing");
     std::lock_guard<std::mutex> lk(g_pmu);
     Ws &w = g_pws[{dev, st}];
     if (w.bytes < bytes) {
-        if (w.p) {
+        if (w.p && !w.captured) {
             // The previous launches on this stream may still read it.
             e = cudaStreamSynchronize(st);
             if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
             cudaFree(w.p);
         }
-        w.p = nullptr;
-        w.bytes = 0;
+        w = Ws{};
         e = cudaMalloc(&w.p, bytes);
         if (e != cudaSuccess) return cuda_error(e, "cudaMalloc(prompt workspace)");
         w.bytes = bytes;
     }
+    w.captured |= capture != cudaStreamCaptureStatusNone;
     *out = w.p;
     return TF_OK;
 }
