@@ -297,9 +297,10 @@ int tf_device_status(void);
 int tf_set_launch_mode(int mode);
 
 /*
- * Test hook for the bounded waits (no GPU fault is involved): the next product
- * launch withholds every CTA's first stage of codes, so the consumers' wait
- * for it runs out after about 2 s; the kernel records that in the device
+ * Test hook for the bounded waits (no GPU fault is involved): the next launch of
+ * a product or of tf_kv_attend withholds every CTA's first stage of codes (every
+ * warp's in attention of few rows), so the consumers' wait for it runs out after
+ * about 2 s; the kernel records that in the device
  * status word, stops waiting and runs to completion (its output is then
  * meaningless) and tf_device_status returns TF_EDEVICE.  The context stays
  * usable.  One shot; TF_OK.

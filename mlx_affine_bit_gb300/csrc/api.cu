@@ -477,7 +477,7 @@ int run_product(const uint16_t *x, int rows, int K, const uint32_t *W, const uin
     }
     P.early_x = overlap;
     P.early_w = (mode & TF_LAUNCH_EARLY_WEIGHTS) != 0 || P.early_x;
-    P.stall = g_stall.exchange(0);
+    P.stall = take_stall();
     // Runs of a stack read x and write disjoint columns: after the first, a run
     // without split-K overlaps the runs before it (see QmmParams::dep).
     P.dep = stack_pos < 0 || overlap ? 0 : stack_pos == 0 ? 1 : pl.nsl == 1 ? 2 : 0;
@@ -580,7 +580,7 @@ int window_with_scratch(const uint16_t *x, int w, int r0, int total_rows, int K,
     P.cs_dst[0] = 0;
     for (int r = 0; r < 16; ++r) P.xrow[r] = P.yrow[r] = r0 + std::min(r, w - 1);
     P.x_rows = P.y_rows = total_rows;
-    P.stall = g_stall.exchange(0);
+    P.stall = take_stall();
     cudaError_t e;
     if (pl.nsl > 1) {
         // The scratch keeps the last call's contents: the arrival counters must start at zero.
@@ -690,6 +690,8 @@ int tfq::tensor_map_2d(CUtensorMap *m, const void *base, int elem_bytes, long lo
                                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     return encode_2d(m, base, t, elem_bytes, cols, rows, box_cols, box_rows);
 }
+
+int tfq::take_stall() { return g_stall.exchange(0); }
 
 int tfq::tensor_map_rows128(CUtensorMap *m, const void *base, long long rows, int box_rows) {
     const int rc = get_encoder();

@@ -177,6 +177,7 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     P.block_log2 = __builtin_ctz(kv->block);
     P.causal = (flags & TF_KV_CAUSAL) != 0;
     P.q_f32 = (flags & TF_IN_F32) != 0;
+    P.stall = take_stall();
     const long long max_group_rows = (long long)batch->max_rows * P.group;
     if (max_group_rows > (1 << 30)) return fail_message(TF_EINVAL_SIZE, "too many rows of one sequence");
     long long span = batch->max_len;

@@ -149,7 +149,7 @@ struct PromptHdr {
     uint64_t kv_full[4], kv_empty[4], s_full[2], s_free, p_full[2], pv_done[2], q_full[2], o_free[2], scales[4], joined[2], turn[2], done;
     uint32_t tmem;
     int abort, last, seq, tile, h;
-    long long item_at, total, sums[P_THREADS / 32];
+    long long item_at, total, arrived, sums[P_THREADS / 32];     // (arrived: the last shared item of which a part was counted)
     float2 scale[SCALES][8];                 // key scale, log2 of the value scale, of each 16 tokens (-1: no page)
     uint2 pages[SCALES];                     // a byte a widening warp: 1 if its tokens' pages are there
 };
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         mbar_init(&B.s_free, 4);
         mbar_init(&B.done, NT);
         B.abort = 0;
+        B.arrived = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             auto publish = [&](uint32_t kt) {
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&B.kv_full[kt % SLOTS]);
+                if (lane == 0 && !(P.stall && kt == 0)) mbar_arrive(&B.kv_full[kt % SLOTS]);
             };
             auto put_keys = [&](uint32_t step) {
                 const uint32_t kt = 2 * step;
@@ -630,7 +631,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 wait_for(&B.joined[i], joins & 1, abort, P.status);
             };
             meet(0);
-            if (tid == 0) B.last = atomicAdd(P.count + c_first, 1) == parts - 1;
+            if (tid == 0) {
+                B.last = atomicAdd(P.count + c_first, 1) == parts - 1;
+                B.arrived = last.item_at;
+            }
             meet(1);
             ++joins;
             if (!B.last) return;
@@ -904,6 +908,17 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             }
         } while (w.next(P) && !*abort);
         epilogue();
+        if (tid == 0 && *abort) {
+            // A wait ran out, and the walk stopped.  If the last item of this CTA's share, which the CTAs after it may
+            // share, is among those left, its part is counted all the same: the counter comes back to zero, and the
+            // launches that follow join when their own parts are there.
+            Walk<R> z;
+            z.first(P, B.seq, B.tile, B.h, B.item_at, total * blockIdx.x / C, total * (blockIdx.x + 1) / C);
+            bool later = false;
+            while (z.next(P)) later = true;
+            const int parts = (int)(((z.item_at + z.t.steps) * C - 1) / total) - (int)blockIdx.x + 1;
+            if (later && parts > 1 && B.arrived != z.item_at && atomicAdd(P.count + blockIdx.x, 1) == parts - 1) P.count[blockIdx.x] = 0;
+        }
     }
     fence_before();
     __syncthreads();

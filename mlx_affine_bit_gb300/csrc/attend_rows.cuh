@@ -56,6 +56,7 @@ TFQ_HD constexpr int step_of(int d) { return 16 * tiles_of(d) * WARPS; }
 constexpr int CHUNK_TOKENS = 4096;       // tokens whose pages and scales a CTA keeps at a time
 constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
 constexpr int MAX_PARTS = 768;           // CTAs of a launch, at most
+constexpr int NO_TOKEN = 1 << 30;        // past every chunk
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
 
 struct Params {
@@ -71,6 +72,7 @@ struct Params {
     float scale;
     int group, window, causal, q_f32;
     int block_log2;         // of kv.block
+    int stall;              // test hook: every CTA's first keys are withheld (rows kernel: every warp's first copies)
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -306,7 +308,8 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         int c0 = max(t_begin, from), c1 = c0, pg0 = 0, npages = 0, ft = 0;
         auto fetch = [&](int t) {                // (the warp's first lane)
             if (t >= c1) return;
-            const int stage = fit++ % NST;
+            const uint32_t stage = fit++ % NST;
+            if (P.stall && fit == 1) return;
             const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < c1 ? s_page[(t >> BL) + 1 - pg0] : -1;
             mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : TILES) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
             uint8_t *dst = mine + stage * STAGE;
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 s_page[i] = page;
             }
             __syncthreads();
-            ft = c0 + TP * warp;
+            ft = *abort ? NO_TOKEN : c0 + TP * warp;
             for (int i = 0; i < NST - 1; ++i, ft += STEP)
                 if (lane == 0) fetch(ft);
             for (int i = tid; i < npages; i += THREADS) {
@@ -408,7 +411,10 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
                 if (lane == 0) fetch(ft);
                 ft += STEP;
-                mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
+                if (!mbar_try(&bar[it % NST], (it / NST) & 1)) {
+                    if (!*abort) mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
+                    if (*abort) ft = NO_TOKEN;       // (a wait ran out: nothing more is fetched, the stages may be on their way)
+                }
                 const uint8_t *tiles = mine + (it % NST) * STAGE;
                 // Tiles t and t + 16: their pages (a tile of no page is not seen).
                 int pi[TILES];
@@ -684,8 +690,10 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         line = item_at + step1;
     }
     if (*abort && lane == 0) {
-        // A wait ran out: no copy may be in flight when the CTA ends.
-        for (uint32_t j = it > NST ? it - NST : 0; j < it; ++j) mbar_wait(&bar[j % NST], (j / NST) & 1, abort, P.status, false);
+        // A wait ran out (the items were gone through all the same, so that every part has arrived and the counters
+        // are zero again): no copy may be in flight when the CTA ends.
+        for (uint32_t j = fit > NST ? fit - NST : 0; j < fit; ++j)
+            if (!(P.stall && j == 0)) mbar_wait(&bar[j % NST], (j / NST) & 1, abort, P.status, false);
     }
 }
 

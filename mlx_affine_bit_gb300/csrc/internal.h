@@ -49,6 +49,9 @@ int tensor_map_3d(CUtensorMap *m, const void *base, int elem_bytes, long long d0
 // swizzle (16-byte chunk c of a box's row r at c ^ (r & 7)).
 int tensor_map_rows128(CUtensorMap *m, const void *base, long long rows, int box_rows);
 
+// Whether tf_inject_stall armed the test hook for this launch; disarms it (api.cu).
+int take_stall();
+
 // SM count and device status word of the current device (allocated on first use).
 int device_info(int *nsm, int **status);
 
