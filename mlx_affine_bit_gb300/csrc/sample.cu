@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
     };
 
     // The row's parameters (on their way while the logits are).
-    const float T = fminf(P.temperature ? P.temperature[row] : 1.f, FLT_MAX);
+    const float temperature = P.temperature ? P.temperature[row] : 1.f, T = fminf(temperature, FLT_MAX);
     const float p = P.top_p ? P.top_p[row] : 1.f, u = P.u[row], min_p = P.min_p ? P.min_p[row] : 0.f;
     const int top_k = P.top_k ? P.top_k[row] : 0;
 
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Params P) {
         G.sync();                // (the others may still read this CTA's maximum)
         return;
     }
-    const bool greedy = !(T > 0.f);
+    const bool greedy = !(temperature > 0.f);    // (NaN too, which T is not)
     const Scale sc{top, greedy ? 1.f : __fdiv_rn(1.f, T)};
     // The least whole weight of at least min_p times the largest (a power of two times min_p is exact).
     const unsigned least = min_p > 0.f && !greedy ? max(1u, __float2uint_ru(fminf(min_p, 1.f) * WEIGHT_ONE)) : 1u;

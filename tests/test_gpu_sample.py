@@ -207,3 +207,28 @@ def test_again_and_on_other_streams():
         tf.sample(x, u, tokens=tokens, probs=probs, stream=stream, **par)
         torch.cuda.synchronize()
         assert torch.equal(tokens, first[0]) and torch.equal(probs, first[1])
+
+
+@pytest.mark.parametrize("vocab", [1000, 32003, 248320])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_temperatures_that_are_not_above_zero(vocab, dtype):
+    # NaN and negative ones too: the first largest logit, whatever the other parameters.
+    rng = np.random.default_rng(vocab + 1)
+    cold = [np.nan, -np.nan, -1.0, -np.inf, -0.0, 0.0]
+    par = [(t, k, p, m) for t in cold for k, p, m in ((0, 1.0, 0.0), (50, 0.9, 0.05), (0, 0.3, 0.0))]
+    x = logits(rng, len(par), vocab, "broad")
+    check(x, par, 6, dtype)
+    m = torch.from_numpy(x).to(DEV).to(dtype)
+    tokens, probs = tf.sample(m, torch.rand(len(par), device=DEV), temperature=torch.tensor([p[0] for p in par], device=DEV))
+    assert torch.equal(tokens.long(), m.float().argmax(1)) and torch.all(probs == 1)
+
+
+def test_other_parameters_that_are_not_numbers():
+    # top-p and min-p of NaN keep everything (they are not below 1, not above 0).
+    rng = np.random.default_rng(3)
+    m = torch.from_numpy(logits(rng, 4, 5000, "sharp")).to(DEV)
+    u, nan = torch.rand(4, device=DEV), torch.full((4,), float("nan"), device=DEV)
+    want = tf.sample(m, u)
+    for par in (dict(top_p=nan), dict(min_p=nan), dict(top_p=nan, min_p=nan)):
+        got = tf.sample(m, u, **par)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
