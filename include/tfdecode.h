@@ -111,7 +111,8 @@ int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k
  * to 11), codes are exact there; each p times its page's value scale is rounded
  * to fp16 (11 bits) relative to the row's largest for the second product (11 bits
  * down to 2^-29 of it, nothing below 2^-40); scores, maxima, sums and accumulators
- * are fp32; out is rounded once to bf16.
+ * are fp32 (a score of 2^20 is held to 2^-3: larger ones are told apart no better
+ * than fp32 does, but lose nothing else); out is rounded once to bf16.
  * A row's bits do not change from call to call with the same arguments; between
  * calls of another batch they may, within that precision, because sequences are
  * cut between the CTAs by the whole call's tokens.

@@ -9,7 +9,10 @@
 // (its offset, 128 2^-24 sum(q_r), goes into the exponent's constant), the second
 // over the codes, exact in fp16, and w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16,
 // n_r the running maximum of s_rj + log2(vs_page): 11 bits down to 2^-29 of the
-// row's largest contribution, nothing below 2^-40.
+// row's largest contribution, nothing below 2^-40.  The exponent of w is one fused
+// product and sum on what the tensor cores leave; where its terms could be so large
+// (FAR) that their rounding showed, a pass of its own turns them into scores less a
+// common base first.
 //
 // Bound by the tensor cores and, closely, by the instructions around them: per row
 // and token one exponential and about four others, per token and dimension of the
@@ -64,8 +67,10 @@ TFQ_HD constexpr int p_conv(int d) { return 12 - p_soft(d); }
 TFQ_HD constexpr int p_slots(int d) { return d == 256 ? 2 : 4; }          // fp16 tiles of keys or values in flight
 TFQ_HD constexpr int p_tile_bytes(int d) { return KEYS * d * 2; }         // one of them, and 128 rows of q
 TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p_tile_bytes(d); }
+constexpr uint32_t PAGES_THERE = 0x8000;         // (the sign of a key scale)
 constexpr int SCALES = 4;                        // steps whose scales are kept
 constexpr float SLACK = 0.9f;                    // growth of a maximum that is let be, in powers of two (w stays in fp16's range)
+constexpr float FAR = 4096.f;                    // bound (in powers of two) of the terms of an exponent that are summed as they stand
 constexpr int ITEM_STEPS = 3;                    // an item's beginning and end on the line, in steps (2 to 6: 3 is fastest)
 constexpr int MAX_SHARE = 8;                     // CTAs an item, on average: one of them joins their parts
 
@@ -151,7 +156,9 @@ struct PromptHdr {
     int abort, last, seq, tile, h;
     long long item_at, total, arrived, sums[P_THREADS / 32];     // (arrived: the last shared item of which a part was counted)
     float2 scale[SCALES][8];                 // key scale, log2 of the value scale, of each 16 tokens (-1: no page)
-    uint2 pages[SCALES];                     // a byte a widening warp: 1 if its tokens' pages are there
+    // A number a widening warp: the largest key scale of its tokens' pages (the upper half of its bits, rounded up, at least
+    // 1; 0 if there is no page), and PAGES_THERE if all of them are there.
+    __align__(16) uint16_t top_ks[SCALES][8];
 };
 static_assert(sizeof(PromptHdr) <= 1024, "header");
 
@@ -521,7 +528,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 store(kv_s + (kt % SLOTS) * TB, kr, true);
                 if (lane < NP) B.scale[step % SCALES][NP * v + lane] = k_of.scale;
                 const bool there = __all_sync(~0u, k_of.scale.x >= 0.f);
-                if (lane == 0) reinterpret_cast<uint8_t *>(&B.pages[step % SCALES])[v] = there;
+                const float top_ks = NP > 1 ? fmaxf(k_of.scale.x, __shfl_xor_sync(~0u, k_of.scale.x, 1)) : k_of.scale.x;
+                if (lane == 0)
+                    B.top_ks[step % SCALES][v] = (there ? PAGES_THERE : 0u) | (top_ks < 0.f ? 0u : max(1u, (__float_as_uint(top_ks) + 0xFFFFu) >> 16));
                 publish(kt);
                 if (lane == 0) mbar_arrive(&B.scales[step % SCALES]);
             };
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.o_free[t]);
             if (parts == 1) return;
-            sums4[((long long)slot(k_mine) * NT + t) * 128 + row] = make_float4(sum.m, sum.n, sum.l, 0.f);
+            sums4[((long long)slot(k_mine) * NT + t) * 128 + row] = make_float4(sum.m, sum.d, sum.l, 0.f);
             __threadfence();
             // (Bounded barriers of the softmax warps.)
             auto meet = [&](int i) {
@@ -644,15 +653,25 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 const float4 x = __ldcg(sums4 + ((long long)slot(k) * NT + t) * 128 + row);
                 return RowSum{x.x, x.y, x.z, 0.f};
             };
-            RowSum a{-INFINITY, -INFINITY, 0.f, 0.f};
-            for (int k = 0; k < parts; ++k) {
-                const RowSum x = sum_of(k);
-                a.m = fmaxf(a.m, x.m);
-                a.n = fmaxf(a.n, x.n);
+            // (The first parts' sums in one round of loads: mostly there are no more.)
+            constexpr int AHEAD = 4;
+            RowSum a{-INFINITY, -INFINITY, 0.f, 0.f}, first[AHEAD];
+            float g[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) first[k] = sum_of(min(k, parts - 1));
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) join_maxima(a, first[k]);
+#pragma unroll 1
+            for (int k = AHEAD; k < parts; ++k) join_maxima(a, sum_of(k));
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                g[k] = o_factor(first[k], a);
+                if (k < parts) a.l += first[k].l * l_factor(first[k], a);
             }
-            for (int k = 0; k < parts; ++k) {
+#pragma unroll 1
+            for (int k = AHEAD; k < parts; ++k) {
                 const RowSum x = sum_of(k);
-                a.l += x.l * l_factor(x, a.m);
+                a.l += x.l * l_factor(x, a);
             }
             const float fa = out_factor(a);
 #pragma unroll 1
@@ -660,8 +679,15 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = 0.f;
+#pragma unroll 1
                 for (int k = 0; k < parts; ++k) {
-                    const float g = o_factor(sum_of(k), a.n);
+                    float f = 0.f;
+                    if (k < AHEAD) {
+#pragma unroll
+                        for (int e = 0; e < AHEAD; ++e) f = k == e ? g[e] : f;
+                    } else {
+                        f = o_factor(sum_of(k), a);
+                    }
                     const float4 *src = parts4 + ((long long)slot(k) * NT + t) * (D / 4) * 128 + (d / 4) * 128 + row;
                     float4 x[8];
 #pragma unroll
@@ -669,10 +695,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         // (a part that saw nothing of this row holds no numbers)
-                        y[4 * e] = g == 0.f ? y[4 * e] : fmaf(x[e].x, g, y[4 * e]);
-                        y[4 * e + 1] = g == 0.f ? y[4 * e + 1] : fmaf(x[e].y, g, y[4 * e + 1]);
-                        y[4 * e + 2] = g == 0.f ? y[4 * e + 2] : fmaf(x[e].z, g, y[4 * e + 2]);
-                        y[4 * e + 3] = g == 0.f ? y[4 * e + 3] : fmaf(x[e].w, g, y[4 * e + 3]);
+                        y[4 * e] = f == 0.f ? y[4 * e] : fmaf(x[e].x, f, y[4 * e]);
+                        y[4 * e + 1] = f == 0.f ? y[4 * e + 1] : fmaf(x[e].y, f, y[4 * e + 1]);
+                        y[4 * e + 2] = f == 0.f ? y[4 * e + 2] : fmaf(x[e].z, f, y[4 * e + 2]);
+                        y[4 * e + 3] = f == 0.f ? y[4 * e + 3] : fmaf(x[e].w, f, y[4 * e + 3]);
                     }
                 }
 #pragma unroll
@@ -686,7 +712,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             const bool real = gr < n_rows;
             const int gc = min(gr, n_rows - 1), i_tok = gc / G, head = w.h * G + gc - i_tok * G;
             const long long q_at = (long long)(w.s.q.row0 + i_tok) * P.q_stride + (long long)head * D;
-            float amax = 0.f, sum_q = 0.f, fq, sq;
+            float amax = 0.f, sum_q = 0.f, sum_abs = 0.f, fq, sq;
             uint8_t *const q_row = q_s + t * TB + row * 128;
             auto put8 = [&](int d, const float (&x)[8]) {
                 uint32_t h[4];
@@ -695,6 +721,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     h[e] = pack_half(x[2 * e] * sq, x[2 * e + 1] * sq);
                     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
                     sum_q += y.x + y.y;
+                    sum_abs += fabsf(y.x) + fabsf(y.y);
                 }
                 *reinterpret_cast<uint4 *>(q_row + (d >> 6) * (KEYS * 128) + ((((d >> 3) & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             };
@@ -781,10 +808,28 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             const int all_to = P.causal ? min(w.s.q.end, first + g0 / G + 1) : w.s.q.end;
             const int all_from = P.window ? first + g1 / G - P.window + 1 : 0;
             sum = RowSum{-INFINITY, -INFINITY, 0.f, 0.f};
+            float n = -INFINITY;                 // the maximum of s + log2(vs)
+            // Where the terms of an exponent could pass FAR, which is with a key scale above far_ks (of the warp's rows, twice
+            // in its upper half), the warp's scores, m and n are relative to `base` from there on.
+            float base = 0.f;
+            uint32_t far_ks = __reduce_min_sync(~0u, __float_as_uint(FAR / (sum_abs * (128.f * TINY) * rowf)) >> 16) * 0x10001u;
             for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
                 const int t0 = w.t.from + i * KEYS;
-                wait_for(&B.s_full[t], st & 1, abort, P.status);
                 wait_for(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);
+                constexpr uint32_t THERE = PAGES_THERE * 0x10001u;
+                uint32_t top_ks, there;          // of pairs of the widening warps' numbers
+                if (P_CONV > 4) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(B.top_ks[st % SCALES]);
+                    top_ks = __vmaxu2(__vmaxu2(k.x & ~THERE, k.y & ~THERE), __vmaxu2(k.z & ~THERE, k.w & ~THERE));
+                    there = k.x & k.y & k.z & k.w & THERE;
+                } else {
+                    const uint2 k = *reinterpret_cast<const uint2 *>(B.top_ks[st % SCALES]);
+                    top_ks = __vmaxu2(k.x & ~THERE, k.y & ~THERE);
+                    there = k.x & k.y & THERE;
+                }
+                const bool far = __vmaxu2(top_ks, far_ks) != far_ks;
+                const bool masked = t0 < all_from || t0 + KEYS > all_to || there != THERE || far;
+                wait_for(&B.s_full[t], st & 1, abort, P.status);
                 fence_after();
                 const float2 *const sc = B.scale[st % SCALES];
                 // f(c, x) on the columns 32 c ..  One tile: all of them are taken into registers at once, so that the
@@ -814,10 +859,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                         }
                     }
                 };
-                // Factor of a score; never 0, so that -inf stays -inf (a page of zeros has scores of 0 all the same).
-                auto factor = [&](float ks) { return fmaxf(rowf * ks, 1e-30f); };
-                if (t0 < all_from || t0 + KEYS > all_to || B.pages[st % SCALES].x != 0x01010101u ||
-                    (P_CONV > 4 && B.pages[st % SCALES].y != 0x01010101u)) {
+                // Factor of a score (`least`: never 0, so that -inf stays -inf; a page of zeros has scores of 0 all the same).
+                float row_f = rowf, least = 1e-30f, off_s = off;
+                auto factor = [&](float ks) { return fmaxf(row_f * ks, least); };
+                if (masked) {
                     // Tokens that the row does not see, first.
                     columns([&](int c, uint32_t (&x)[32]) {
                         const int from = see_from - t0 - 32 * c, to = see_to - t0 - 32 * c;
@@ -828,9 +873,36 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                         if (NT > 1) tmem_st32(s_at + 32 * c, x);
                     });
                     if (NT > 1) tmem_wait_st();
+                    if (far) {
+                        // The scores as fp32 numbers less the largest so far, which is the new base; m and n move with it.
+                        float top = base + sum.m;
+                        columns([&](int c, uint32_t (&x)[32]) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float y = -INFINITY;
+#pragma unroll
+                                for (int e = 16 * h; e < 16 * h + 16; ++e) y = fmaxf(y, __uint_as_float(x[e]));
+                                top = fmaxf(top, __fmul_rn(y + off, factor(sc[2 * c + h].x)));
+                            }
+                        });
+                        const float to = base_of(top), by = base - to;
+                        columns([&](int c, uint32_t (&x)[32]) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[e]) + off, factor(sc[2 * c + e / 16].x)), to));
+                            if (NT > 1) tmem_st32(s_at + 32 * c, x);
+                        });
+                        if (NT > 1) tmem_wait_st();
+                        sum.l *= exp2_fast(sum.m + by);
+                        n += by;
+                        sum.m = top == -INFINITY ? -INFINITY : 0.f;
+                        base = to;
+                        far_ks = 0;                          // (and so in the steps that follow)
+                        row_f = off_s = 0.f, least = 1.f;    // (a factor of 1, and no offset)
+                    }
                 }
                 // The maxima of s and of s + log2(vs), by groups of 16 tokens.
-                float mt = sum.m, nt = sum.n;
+                float mt = sum.m, nt = n;
                 columns([&](int c, uint32_t (&x)[32]) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -841,21 +913,21 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                             top[0] = max3(top[0], __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
                             top[1] = max3(top[1], __uint_as_float(x[16 * h + e + 2]), __uint_as_float(x[16 * h + e + 3]));
                         }
-                        const float m = (fmaxf(top[0], top[1]) + off) * factor(z.x);
+                        const float m = (fmaxf(top[0], top[1]) + off_s) * factor(z.x);
                         mt = fmaxf(mt, m);
                         nt = fmaxf(nt, m + z.y);
                     }
                 });
                 // Maxima that have grown by less than SLACK stay as they are: w then reaches 2^(15 + SLACK), below fp16's end.
                 mt = mt > sum.m + SLACK ? mt : sum.m;
-                nt = nt > sum.n + SLACK ? nt : sum.n;
+                nt = nt > n + SLACK ? nt : n;
                 const float mm = mt == -INFINITY ? 0.f : mt, nn = nt == -INFINITY ? INFINITY : nt;
                 if (mt != sum.m && sum.l != 0.f) sum.l *= exp2_fast(sum.m - mt);
-                const bool grew = nt > sum.n;
-                const float shrink = sum.n == -INFINITY ? 0.f : exp2_fast(sum.n - nt);
+                const bool grew = nt > n;
+                const float shrink = n == -INFINITY ? 0.f : exp2_fast(n - nt);
                 sum.m = mt;
-                sum.n = nt;
-                                constexpr int AT = NT == 1 ? 1 : 2;          // 32 columns each at once (more measured no faster)
+                n = nt;
+                constexpr int AT = NT == 1 ? 1 : 2;          // 32 columns each at once (more measured no faster)
                 auto rescale = [&]() {           // the outputs so far, to the new maximum
                     if (i > w.step0 && __any_sync(~0u, grew)) {
 #pragma unroll 1
@@ -882,7 +954,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     for (int h = 0; h < 2; ++h) {
                         // w = 2^(s - m + e), p = w 2^-e with the page's e; below 2^-45 w is 0 in fp16 whatever it is.
                         const float2 z = sc[2 * c + h];
-                        const float e0 = fminf(fmaxf(mm + z.y - nn + W_EXP, -45.f), 115.f), f = factor(z.x), k = off * f - mm + e0;
+                        const float e0 = fminf(fmaxf(mm + z.y - nn + W_EXP, -45.f), 115.f), f = factor(z.x), k = off_s * f - mm + e0;
                         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
                         for (int e = 16 * h; e < 16 * h + 16; e += 2) {
@@ -906,6 +978,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B.p_full[t]);
             }
+            sum.d = n - base_of(sum.m);
+            sum.m += base;
         } while (w.next(P) && !*abort);
         epilogue();
         if (tid == 0 && *abort) {

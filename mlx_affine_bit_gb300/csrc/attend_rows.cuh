@@ -9,10 +9,11 @@
 // bytes as they stand, fp16 subnormals (c + 128) 2^-24, from a start of -128 2^-24
 // sum(q_r).  The second takes the codes themselves, exact in fp16: a start of that
 // kind would round away what tokens far from the maximum add.  What enters the
-// second product is w_rj = 2^15 p_rj vs_page 2^(m_r - n_r) in fp16, with the running
-// maximum n_r of s_rj + log2(vs_page): relative to the row's largest contribution,
+// second product is w_rj = 2^15 p_rj vs_page 2^-d_r in fp16, with the running maximum
+// d_r of s_rj - m_r + log2(vs_page): relative to the row's largest contribution,
 // however far apart the scales are, it keeps 11 bits down to 2^-29 and comes to
-// nothing below 2^-40.
+// nothing below 2^-40.  (Relative to m_r: beside a large score the logarithm's bits
+// would be rounded away.)
 //
 // Bound by reading the cache: 48 x 8000 tokens of 8 heads of 128, 32 query heads,
 // take 129 us, 6.1 TB/s of the codes; 1 x 131072 tokens 52 us (5.2 TB/s), of which
@@ -110,18 +111,26 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// What has been summed of a row: maxima m of s and n of s + log2(vs), sum l of p.
+// What has been summed of a row: maxima m of s and d of s - m + log2(vs), sum l of p.
 struct __align__(16) RowSum {
-    float m, n, l, unused;
+    float m, d, l, unused;
 };
-// Factors of a part's l and outputs in a join of maxima m and n: 0 for a part that
-// saw no token (l = 0) or only values of scale 0; NaN scores (l NaN) stay NaN.
-__device__ __forceinline__ float l_factor(const RowSum &p, float m) { return p.l == 0.f ? 0.f : exp2_fast(p.m - m); }
-__device__ __forceinline__ float o_factor(const RowSum &p, float n) { return p.n == -INFINITY ? 0.f : exp2_fast(p.n - n); }
-// Factor of the joined outputs: to the maximum of s, and by the sum.
-__device__ __forceinline__ float out_factor(const RowSum &a) {
-    return a.l == 0.f ? 0.f : exp2f(a.n - a.m - W_EXP) / a.l;
+// A maximum to subtract: 0 where there is none (what is below it is then -inf, not NaN).
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// p's d relative to a base that is no smaller than p.m (-inf: no token, or only values of scale 0).
+__device__ __forceinline__ float d_at(const RowSum &p, float base) { return p.d + (p.m - base); }
+// a's maxima, joined with p's.
+__device__ __forceinline__ void join_maxima(RowSum &a, const RowSum &p) {
+    const float m = fmaxf(a.m, p.m), base = base_of(m);
+    a.d = fmaxf(d_at(a, base), d_at(p, base));
+    a.m = m;
 }
+// Factors of a part's l and outputs in a join of the maxima of `a`: 0 for a part that
+// saw no token or only values of scale 0; NaN scores (l NaN) stay NaN.
+__device__ __forceinline__ float l_factor(const RowSum &p, const RowSum &a) { return exp2_fast(p.m - base_of(a.m)); }
+__device__ __forceinline__ float o_factor(const RowSum &p, const RowSum &a) { return exp2_fast(d_at(p, base_of(a.m)) - base_of(a.d)); }
+// Factor of the joined outputs: to the maximum of s, and by the sum.
+__device__ __forceinline__ float out_factor(const RowSum &a) { return a.l == 0.f ? 0.f : exp2f(a.d - W_EXP) / a.l; }
 
 // Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q
 // take.  48 sequences of up to 8000 tokens, 8 heads of 128: 79 us so, 81 with one tile a stage and four stages, 83
@@ -193,7 +202,8 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     __shared__ int s_abort;
     __shared__ __align__(16) __half sq[R][D + 8];
     __shared__ float2 s_row[R];
-    __shared__ RowSum s_sum[WARPS][R];
+    __shared__ RowSum s_sum[WARPS][R], s_join[R];    // of each warp, and of all of them
+    __shared__ float s_wfac[WARPS][R];               // factors of the warps' outputs in the join
     __shared__ float s_ks[MAX_PAGES], s_vs[MAX_PAGES];
     __shared__ int s_page[MAX_PAGES];
     __shared__ long long s_warp[WARPS], s_first;
@@ -393,10 +403,10 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         }
 
         float o[MT][NT][4];
-        float m[NT], n[NT], l[NT];
+        float m[NT], d[NT], l[NT];
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            m[u] = n[u] = -INFINITY;
+            m[u] = d[u] = -INFINITY;
             l[u] = 0.f;
 #pragma unroll
             for (int p = 0; p < MT; ++p)
@@ -455,14 +465,18 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 for (int h = 0; h < TILES; ++h) ks[h] = s_ks[pi[h]], vs[h] = s_vs[pi[h]];
                 uint32_t pb[NT][2 * TILES];
                 bool grew = false;
-                float mt[NT], nt[NT];
+                float mt[NT], mm[NT], dt[NT];
 #pragma unroll
                 for (int u = 0; u < NT; ++u)
 #pragma unroll
                     for (int h = 0; h < TILES; ++h) {
                         const float f = rowf[u] * ks[h];
 #pragma unroll
-                        for (int nb = 2 * h; nb < 2 * h + 2; ++nb) sc[nb][2 * u] *= f, sc[nb][2 * u + 1] *= f;
+                        for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
+                            // (rounded here, so that the largest less the maximum is 0)
+                            sc[nb][2 * u] = __fmul_rn(sc[nb][2 * u], f);
+                            sc[nb][2 * u + 1] = __fmul_rn(sc[nb][2 * u + 1], f);
+                        }
                     }
                 if (!full) {
 #pragma unroll
@@ -486,21 +500,22 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                         for (int h = 0; h < TILES; ++h) top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], o));
                     mt[u] = m[u];
-                    nt[u] = n[u];
 #pragma unroll
-                    for (int h = 0; h < TILES; ++h) {
-                        mt[u] = fmaxf(mt[u], top[h]);
-                        nt[u] = fmaxf(nt[u], top[h] + vs[h]);
-                    }
-                    grew |= mt[u] > m[u] || nt[u] > n[u];
+                    for (int h = 0; h < TILES; ++h) mt[u] = fmaxf(mt[u], top[h]);
+                    mm[u] = base_of(mt[u]);
+                    dt[u] = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) dt[u] = fmaxf(dt[u], (top[h] - mm[u]) + vs[h]);
+                    grew |= mt[u] > m[u] || dt[u] > d[u];
                 }
                 if (__any_sync(~0u, grew)) {
 #pragma unroll
                     for (int u = 0; u < NT; ++u) {
                         if (m[u] != -INFINITY) l[u] *= exp2_fast(m[u] - mt[u]);
-                        const float a = n[u] == -INFINITY ? 0.f : exp2_fast(n[u] - nt[u]);
+                        const float d0 = d[u] + (m[u] - mm[u]);
                         m[u] = mt[u];
-                        n[u] = nt[u];
+                        d[u] = fmaxf(d0, dt[u]);
+                        const float a = exp2_fast(d0 - base_of(d[u]));
                         // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
                         const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
 #pragma unroll
@@ -514,13 +529,12 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 }
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
-                    const float mm = m[u] == -INFINITY ? 0.f : m[u];
 #pragma unroll
                     for (int h = 0; h < TILES; ++h) {
-                        const float f = n[u] == -INFINITY ? 0.f : exp2_fast(fminf(mm + vs[h] - n[u] + W_EXP, 115.f));
+                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf(vs[h] + (W_EXP - d[u]), 115.f));
 #pragma unroll
                         for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
-                            const float p0 = exp2_fast(sc[nb][2 * u] - mm), p1 = exp2_fast(sc[nb][2 * u + 1] - mm);
+                            const float p0 = exp2_fast(sc[nb][2 * u] - mm[u]), p1 = exp2_fast(sc[nb][2 * u + 1] - mm[u]);
                             l[u] += p0 + p1;
                             pb[u][nb] = pack_half(p0 * f, p1 * f);
                         }
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         for (int u = 0; u < NT; ++u) {
             l[u] += __shfl_xor_sync(~0u, l[u], 1);
             l[u] += __shfl_xor_sync(~0u, l[u], 2);
-            if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], n[u], l[u], 0.f};
+            if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], d[u], l[u], 0.f};
         }
 #pragma unroll
         for (int u = 0; u < NT; ++u)
@@ -586,18 +600,22 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 }
             }
         __syncthreads();
-        auto joined = [&](int r) {
-            RowSum a = s_sum[0][r];
-            for (int k = 1; k < WARPS; ++k) a.m = fmaxf(a.m, s_sum[k][r].m), a.n = fmaxf(a.n, s_sum[k][r].n);
+        if (tid < R) {
+            RowSum a = s_sum[0][tid];
+            for (int k = 1; k < WARPS; ++k) join_maxima(a, s_sum[k][tid]);
             a.l = 0.f;
-            for (int k = 0; k < WARPS; ++k) a.l += s_sum[k][r].l * l_factor(s_sum[k][r], a.m);
-            return a;
-        };
-        auto joined4 = [&](int r, int d, const RowSum &a) {
+            for (int k = 0; k < WARPS; ++k) {
+                a.l += s_sum[k][tid].l * l_factor(s_sum[k][tid], a);
+                s_wfac[k][tid] = o_factor(s_sum[k][tid], a);
+            }
+            s_join[tid] = a;
+        }
+        __syncthreads();
+        auto joined4 = [&](int r, int d) {
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k = 0; k < WARPS; ++k) {
                 const float4 x = *reinterpret_cast<const float4 *>(out_of(k, r) + d);
-                const float f = o_factor(s_sum[k][r], a.n);
+                const float f = s_wfac[k][r];
                 y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
             }
             return y;
@@ -613,10 +631,8 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         // The CTAs that share the item, in order.
         const int c_first = cta_of(item_at), parts = cta_of(item_at + sw.steps - 1) - c_first + 1;
         if (parts == 1) {
-            for (int v = 4 * tid; v < rows * D; v += 4 * THREADS) {
-                const RowSum a = joined(v / D);
-                store4(v / D, v % D, joined4(v / D, v % D, a), out_factor(a));
-            }
+            for (int v = 4 * tid; v < rows * D; v += 4 * THREADS)
+                store4(v / D, v % D, joined4(v / D, v % D), out_factor(s_join[v / D]));
         } else {
             // A CTA's first item's part is in its slot 0, that of a later one (its last) in slot 1.
             const int slot0 = 2 * c_first + (item_at > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
@@ -624,11 +640,8 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             float4 *sums = reinterpret_cast<float4 *>(P.part + 2LL * gridDim.x * R * D);
             float *part = P.part + (long long)slot(k_mine) * R * D;
             for (int v = 4 * tid; v < rows * D; v += 4 * THREADS)
-                *reinterpret_cast<float4 *>(part + v) = joined4(v / D, v % D, joined(v / D));
-            if (tid < rows) {
-                const RowSum a = joined(tid);
-                sums[slot(k_mine) * R + tid] = make_float4(a.m, a.n, a.l, 0.f);
-            }
+                *reinterpret_cast<float4 *>(part + v) = joined4(v / D, v % D);
+            if (tid < rows) sums[slot(k_mine) * R + tid] = make_float4(s_join[tid].m, s_join[tid].d, s_join[tid].l, 0.f);
             __threadfence();
             __syncthreads();
             if (tid == 0) s_last = atomicAdd(P.count + c_first, 1) == parts - 1;
@@ -636,7 +649,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             if (s_last) {
                 __threadfence();
                 if (tid == 0) P.count[c_first] = 0;
-                // The row sums of all parts (in s_sum[0]) and the parts' factors, a warp a row.
+                // The row sums of all parts (in s_join) and the parts' factors, a warp a row.
                 float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (the outputs in the ring have been read)
                 for (int r = warp; r < rows; r += WARPS) {
                     auto sum_of = [&](int k) {
@@ -645,23 +658,19 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                     };
                     const RowSum own = sum_of(min(lane, parts - 1));
                     RowSum a = own;
-                    for (int k = lane + 32; k < parts; k += 32) {
-                        const RowSum x = sum_of(k);
-                        a.m = fmaxf(a.m, x.m);
-                        a.n = fmaxf(a.n, x.n);
-                    }
+                    for (int k = lane + 32; k < parts; k += 32) join_maxima(a, sum_of(k));
                     for (int o = 16; o > 0; o >>= 1) {
-                        a.m = fmaxf(a.m, __shfl_xor_sync(~0u, a.m, o));
-                        a.n = fmaxf(a.n, __shfl_xor_sync(~0u, a.n, o));
+                        const float m = __shfl_xor_sync(~0u, a.m, o), d = __shfl_xor_sync(~0u, a.d, o);
+                        join_maxima(a, RowSum{m, d, 0.f, 0.f});
                     }
                     a.l = 0.f;
                     for (int k = lane; k < parts; k += 32) {
                         const RowSum x = k < 32 ? own : sum_of(k);
-                        a.l += x.l * l_factor(x, a.m);
-                        s_fac[k][r] = o_factor(x, a.n);
+                        a.l += x.l * l_factor(x, a);
+                        s_fac[k][r] = o_factor(x, a);
                     }
                     for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
-                    if (lane == 0) s_sum[0][r] = a;
+                    if (lane == 0) s_join[r] = a;
                 }
                 __syncthreads();
                 // The outputs, in the parts' order, eight loads at a time.
@@ -680,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                             y.z = fmaf(x[k].z, f, y.z), y.w = fmaf(x[k].w, f, y.w);
                         }
                     }
-                    store4(r, v % D, y, out_factor(s_sum[0][r]));
+                    store4(r, v % D, y, out_factor(s_join[r]));
                 }
             }
         }
