@@ -105,7 +105,7 @@ int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k
  *            the tcgen05 tensor cores), instead of the call's own choice by its
  *            sizes -- for a caller that has measured its own.
  *   window   0, or with TF_KV_CAUSAL the number of latest tokens (its own
- *            included) that a row sees.
+ *            included) that a row sees (any number: from max_len on, all).
  * Precision: q enters the tensor cores as fp16 after an exact power-of-two
  * scaling of its row (bf16 values keep all their bits, fp32 values are rounded
  * to 11), codes are exact there; each p times its page's value scale is rounded

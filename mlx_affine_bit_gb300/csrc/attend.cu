@@ -173,7 +173,8 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     P.status = status;
     P.group = heads / kv->kv_heads;
     P.scale = scale;
-    P.window = window;
+    // (A window that holds every token is none; the kernels' positions less a window then stay within 32 bits.)
+    P.window = window = window < batch->max_len ? window : 0;
     P.block_log2 = __builtin_ctz(kv->block);
     P.causal = (flags & TF_KV_CAUSAL) != 0;
     P.q_f32 = (flags & TF_IN_F32) != 0;

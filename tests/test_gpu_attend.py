@@ -264,3 +264,18 @@ def test_captured_decode_step():
     tf.tf_device_status()
     q.check(0, 90)
     q.check(1, 40)
+
+
+@pytest.mark.parametrize("rows", [[6, 1, 9], [160, 2, 300]])
+def test_windows_of_any_size(rows):
+    # As large as a window can be given: every token is seen, also by sequences that have fewer tokens than rows.
+    lens = [2, 300, 7]
+    q = filled(lens, 2, 64, 16, 17)
+    x = torch.randn((sum(rows), 256), device=DEV).to(BF16)
+    b = q.batch(lens, rows)
+    want = q.cache.attend(x, b)
+    for window in (300, 301, 1 << 20, 2 ** 31 - 300, 2 ** 31 - 2, 2 ** 31 - 1):
+        assert torch.equal(q.cache.attend(x, b, window=window), want), window
+    torch.cuda.synchronize()
+    tf.tf_device_status()
+    assert torch.all(torch.any(want[rows[0] - 2:rows[0]] != 0, dim=1))
