@@ -33,10 +33,18 @@ extern "C" {
  * Infinities are left out of the maximum and held as +-127, NaN as 0, so that a
  * bad token does not spoil the others of its page.  A page's content depends on
  * its tokens only, not on how the calls that wrote them cut the sequence: the
- * originals of a sequence's last two pages stay in an open ring, and a page
- * whose scale changes is quantized again from there.  A sequence may therefore
- * be rewound by up to `block` tokens (rejected drafts) and written anew, with
- * the same result as if the rejected tokens had never been there.
+ * originals of the two pages that a sequence reached last stay in an open ring,
+ * and a page whose scale changes is quantized again from there.  A sequence may
+ * therefore be rewound (rejected drafts) and written anew, with the same result
+ * as if the rejected tokens had never been there, while the ring has the
+ * originals of the page that is gone on with:
+ *     - to no more than `block` tokens before the longest length that the sequence
+ *       has had, however often it was rewound meanwhile (rejected tokens, too,
+ *       take their places in the ring);
+ *     - or to the first token of any page, which needs no originals.  The sequence
+ *       then counts as begun there: its longest length is that from there on.
+ * A call that goes on elsewhere is not detected: it quantizes the page's earlier
+ * tokens from what stands in their places.
  */
 typedef struct tf_kv {
     int8_t *k, *v;            /* [n_blocks][kv_heads][block][dim], 16-byte aligned */

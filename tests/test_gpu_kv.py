@@ -244,3 +244,43 @@ def test_row_starts_that_wrap_around_are_reported(wrong):
             tf.tf_device_status()
         assert e.value.rc == -14
     assert torch.all(q.cache.k == 0) and torch.all(out[0] == 3.0) and torch.all(out[1] == 3.0)
+
+
+@pytest.mark.parametrize("block,dtype", [(16, BF16), (32, F32)])
+def test_rewinding_again_and_again_leaves_no_trace(block, dtype):
+    # Back and forth between the longest length and a page before it, drafts of any size in between; every kept token in
+    # the end is the one written last.
+    n = 6 * block + 5
+    q = Sequences([n], 2, 64, block, dtype, 13)
+    good = [a[0].copy() for a in (q.k, q.v)]
+    rng = np.random.default_rng(block)
+    longest = length = 0
+    while length < n:
+        for _ in range(4):
+            start = int(rng.integers(max(0, longest - block), length + 1))
+            end = min(n, start + int(rng.integers(1, block + 1)))
+            for a in (q.k, q.v):
+                a[0][start:end] = bf16(100 * rng.standard_normal(a[0][start:end].shape))
+            q.append([(start, end)])
+            longest, length = max(longest, end), end
+        # What is kept: from the lowest place that may be gone on from.
+        start = max(0, longest - block) if longest < n else max(0, min(length, n - block))
+        for a, g in zip((q.k, q.v), good):
+            a[0][start:] = g[start:]
+        end = min(n, start + block + 1)
+        q.append([(start, end)])
+        longest, length = max(longest, end), end
+        q.check(0, length)
+    # And to a page's first token, from anywhere.
+    for a, g in zip((q.k, q.v), good):
+        a[0][:] = bf16(0.01 * g)
+    q.append([(block, n - 3)])
+    for a, g in zip((q.k, q.v), good):
+        a[0][2 * block:] = g[2 * block:]
+    q.append([(2 * block, n)])
+    q.append([(n - 7, n)])
+    status_clean()
+    kc, ks, vc, vs = q.stored(0, n)
+    for x, c, sc in ((q.k[0], kc, ks), (q.v[0], vc, vs)):
+        want_c, want_s = cache_of(x[block:], block)
+        assert np.array_equal(c[block:], want_c) and np.array_equal(sc[1:], want_s)
