@@ -30,8 +30,8 @@ extern "C" {
  *     value[t][d] = scale * code[t][d],   scale = max |x[t][d]| * (1/127) over the page's tokens,
  *     code = x / scale rounded to nearest even   (fp32 product, division and rounding; scale 0: code 0)
  *
- * Infinities are left out of the maximum and held as +-127, NaN as 0, so that a
- * bad token does not spoil the others of its page.  A page's content depends on
+ * Infinities are left out of the maximum and held as +-127 (0 in a page of scale
+ * 0), NaN as 0, so that a bad token does not spoil the others of its page.  A page's content depends on
  * its tokens only, not on how the calls that wrote them cut the sequence: the
  * originals of the two pages that a sequence reached last stay in an open ring,
  * and a page whose scale changes is quantized again from there.  A sequence may

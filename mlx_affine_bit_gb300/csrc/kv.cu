@@ -85,8 +85,8 @@ struct Raw8 {
 
 // x / scale rounded to the nearest, even in the middle.
 __device__ __forceinline__ int divided(float x, float scale) {
-    // 0 / 0 and NaN convert to 0; an infinity saturates and is clamped.
-    return max(-127, min(127, __float2int_rn(rintf(__fdiv_rn(x, scale)))));
+    // NaN converts to 0; an infinity saturates and is clamped.
+    return scale == 0.f ? 0 : max(-127, min(127, __float2int_rn(rintf(__fdiv_rn(x, scale)))));
 }
 __device__ __forceinline__ float max_nan(float a, float b) {     // NaN if one is
     float r;

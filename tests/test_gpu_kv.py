@@ -284,3 +284,28 @@ def test_rewinding_again_and_again_leaves_no_trace(block, dtype):
     for x, c, sc in ((q.k[0], kc, ks), (q.v[0], vc, vs)):
         want_c, want_s = cache_of(x[block:], block)
         assert np.array_equal(c[block:], want_c) and np.array_equal(sc[1:], want_s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("small", [0.0, 1e-45, 7e-44, 8e-44])
+def test_pages_of_scale_zero_hold_zeros(dtype, small):
+    # Nothing but zeros (or what max / 127 rounds to 0: up to 63 of the smallest subnormals) beside infinities and NaN.
+    q = Sequences([40], 2, 64, 16, dtype, 14)
+    for a in (q.k, q.v):
+        x = np.full(a[0].shape, np.float32(small), np.float32)
+        x[::2] *= -1
+        x[3, 0, 5], x[20, 1, 0], x[17, 1, 63], x[36, 0, 1] = np.inf, -np.inf, np.nan, np.inf
+        a[0] = bf16(x) if dtype == BF16 else x
+    amax = np.max(np.abs(q.k[0][np.isfinite(q.k[0])]))
+    scale = np.float32(amax) * (np.float32(1) / np.float32(127))
+    q.append([(0, 30)])
+    q.append([(30, 40)])
+    status_clean()
+    kc, ks, vc, vs = q.stored(0, 40)
+    assert np.all(ks == scale) and np.all(vs == scale)
+    if scale == 0:
+        assert np.all(kc == 0) and np.all(vc == 0)
+    else:
+        assert kc[3, 0, 5] == 127 and kc[20, 1, 0] == -127 and kc[17, 1, 63] == 0
+    for x in q.values(0, 40):
+        assert np.all(np.isfinite(x))
