@@ -5,8 +5,10 @@ Argument marshalling only: every step of the product runs in the library's
 CUDA kernels (``csrc/``).  The names and arguments follow ``include/tfqmm.h`` and
 ``include/tfdecode.h``.
 Tensors may be passed as torch tensors (their ``data_ptr()`` is used) or as
-raw integer addresses; ``stream`` is a ``torch.cuda.Stream``, a raw
-``cudaStream_t`` integer, or None for torch's current stream.
+raw integer addresses; ``KvCache``, ``KvBatch`` and ``sample`` take tensors, and
+check their types, shapes, strides and devices.  ``stream`` is a
+``torch.cuda.Stream``, a raw ``cudaStream_t`` integer, or None for torch's current
+stream.
 
 The library must be built first (``mlx_affine_bit_gb300.build.build()``);
 loading fails loudly when it is missing.  There is no CPU fallback.
@@ -338,24 +340,44 @@ def qmm(x, W, scales, biases, bits, group, y=None, y_stride=None, stream=None):
     return y
 
 
-def _tensor(t, name, dtypes, shape=None, contiguous=True):
-    """Refuse a tensor that a call could not take: TypeError for its type, ValueError for the rest."""
+def _tensor(t, name, dtypes, shape=None, contiguous=True, device=None):
+    """Refuse a tensor that a call could not take: TypeError for its type, ValueError for the rest.
+    device: the number of the device that it must be on (get_device())."""
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
     if shape is not None and t.shape != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if contiguous and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+    if device is not None and t.get_device() != device:
+        raise ValueError("%s must be on %s, is on %s" % (name, "the host" if device < 0 else "cuda:%d" % device, t.device))
     return t
 
 
-def _rows(t, name, dtypes, rows, width):
-    """The row stride of a [rows][width] matrix whose rows are contiguous."""
+_get_device = None
+
+
+def _on_gpu(device, what):
+    """Refuse tensors that are not on the current GPU, where the kernels run."""
+    global _get_device
+    if device < 0:
+        raise ValueError("%s must be on a GPU" % what)
+    if _get_device is None:
+        import torch
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if device != _get_device():
+        raise ValueError("%s is on cuda:%d, which is not the current device" % (what, device))
+
+
+def _rows(t, name, dtypes, rows, width, device):
+    """The row stride of a [rows][width] matrix on that device whose rows are contiguous."""
     if t.dtype not in dtypes or t.shape != (rows, width):
         _tensor(t, name, dtypes, (rows, width), contiguous=False)
     stride = t.stride()
     if width > 1 and stride[1] != 1:
         raise ValueError("%s must have contiguous rows" % name)
+    if t.get_device() != device:
+        _tensor(t, name, dtypes, contiguous=False, device=device)
     return stride[0] if rows > 1 else max(width, stride[0])
 
 
@@ -372,15 +394,16 @@ class KvBatch:
         i32 = (torch.int32,)
         n = kv_len.shape[0]
         _tensor(kv_len, "kv_len", i32, (n,))
-        _tensor(table, "table", i32, (n, table.shape[-1]), contiguous=False)
+        self.device = kv_len.get_device()
+        _tensor(table, "table", i32, (n, table.shape[-1]), contiguous=False, device=self.device)
         if table.shape[1] > 1 and table.stride(1) != 1:
             raise ValueError("table must have contiguous rows")
         if row_start is not None:
-            _tensor(row_start, "row_start", i32, (n + 1,))
+            _tensor(row_start, "row_start", i32, (n + 1,), device=self.device)
             if rows is None:
                 raise ValueError("row_start needs rows")
         if slots is not None:
-            _tensor(slots, "slots", i32, (n,))
+            _tensor(slots, "slots", i32, (n,), device=self.device)
         if max_len > table.shape[1] * 128:
             raise ValueError("max_len exceeds the table")
         self.rows = n * max_rows if row_start is None else rows
@@ -404,16 +427,17 @@ class KvCache:
             raise ValueError("k must be [n_blocks][kv_heads][block][dim]")
         n_blocks, heads, block, dim = k.shape
         _tensor(k, "k", (torch.int8,))
-        _tensor(v, "v", (torch.int8,), k.shape)
-        _tensor(k_scale, "k_scale", (torch.float32,), (n_blocks, heads))
-        _tensor(v_scale, "v_scale", (torch.float32,), (n_blocks, heads))
+        self.device = device = k.get_device()
+        _tensor(v, "v", (torch.int8,), k.shape, device=device)
+        _tensor(k_scale, "k_scale", (torch.float32,), (n_blocks, heads), device=device)
+        _tensor(v_scale, "v_scale", (torch.float32,), (n_blocks, heads), device=device)
         n_slots = 0
         self.dtype = torch.bfloat16
         if open_k is not None:
             n_slots, self.dtype = open_k.shape[0], open_k.dtype
-            _tensor(open_k, "open_k", (torch.bfloat16, torch.float32), (n_slots, heads, 2 * block, dim))
-            _tensor(open_v, "open_v", (self.dtype,), open_k.shape)
-            _tensor(open_max, "open_max", (torch.float32,), (n_slots, 2, heads, 2 * block))
+            _tensor(open_k, "open_k", (torch.bfloat16, torch.float32), (n_slots, heads, 2 * block, dim), device=device)
+            _tensor(open_v, "open_v", (self.dtype,), open_k.shape, device=device)
+            _tensor(open_max, "open_max", (torch.float32,), (n_slots, 2, heads, 2 * block), device=device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.open_k, self.open_v, self.open_max = open_k, open_v, open_max
         self.kv_heads, self.block, self.dim = heads, block, dim
@@ -436,13 +460,16 @@ class KvCache:
     def _batch(self, batch):
         if batch.c.max_len > batch._pages * self.block:
             raise ValueError("max_len exceeds the table's pages")
+        if batch.device != self.device:
+            raise ValueError("the batch's tensors must be on the cache's device")
+        _on_gpu(self.device, "the cache")
         return batch.c
 
     def append(self, k, v, batch, stream=None) -> None:
         """Quantize rows k, v [rows][kv_heads * dim] (row stride free) in as the batch's last tokens."""
         width, types = self.kv_heads * self.dim, (self.dtype,)
-        ks = _rows(k, "k", types, batch.rows, width)
-        vs = _rows(v, "v", types, batch.rows, width)
+        ks = _rows(k, "k", types, batch.rows, width, self.device)
+        vs = _rows(v, "v", types, batch.rows, width, self.device)
         tf_kv_append(self.c, self._batch(batch), k, ks, v, vs, stream)
 
     def read(self, batch, dtype=None, k_out=None, v_out=None, stream=None):
@@ -460,8 +487,8 @@ class KvCache:
         else:
             k_out = torch.empty((batch.rows, width), dtype=dtype, device=self.k.device) if k_out is None else k_out
             v_out = torch.empty((batch.rows, width), dtype=dtype, device=self.k.device) if v_out is None else v_out
-            ks = _rows(k_out, "k_out", types, batch.rows, width)
-            vs = _rows(v_out, "v_out", types, batch.rows, width)
+            ks = _rows(k_out, "k_out", types, batch.rows, width, self.device)
+            vs = _rows(v_out, "v_out", types, batch.rows, width, self.device)
             if k_out.dtype != v_out.dtype:
                 raise TypeError("k_out and v_out must have one type")
         tf_kv_read(self.c, self._batch(batch), k_out, ks, v_out, vs,
@@ -474,12 +501,12 @@ class KvCache:
         kernel: 0 (by the call's sizes), TF_KV_BY_ROWS or TF_KV_BY_TILES."""
         import torch
         rows, width = q.shape
-        qs = _rows(q, "q", (torch.bfloat16, torch.float32), batch.rows, width)
+        qs = _rows(q, "q", (torch.bfloat16, torch.float32), batch.rows, width, self.device)
         if out is None:
             out = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device)
             os_ = width
         else:
-            os_ = _rows(out, "out", (torch.bfloat16,), rows, width)
+            os_ = _rows(out, "out", (torch.bfloat16,), rows, width, self.device)
         if width % self.dim:
             raise ValueError("q's rows must hold heads * dim values")
         tf_kv_attend(self.c, self._batch(batch), q, qs, width // self.dim, out, os_,
@@ -493,13 +520,15 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     numbers, per-row temperature, top_p, min_p (fp32) and top_k (int32) or None.  Returns (tokens, probs)."""
     import torch
     rows, vocab = logits.shape
-    stride = _rows(logits, "logits", (torch.float32, torch.bfloat16), rows, vocab)
+    device = logits.get_device()
+    stride = _rows(logits, "logits", (torch.float32, torch.bfloat16), rows, vocab, device)
     f32, i32 = (torch.float32,), (torch.int32,)
     shape = (rows,)
     for t, name, types in ((u, "u", f32), (temperature, "temperature", f32), (top_k, "top_k", i32), (top_p, "top_p", f32),
                            (min_p, "min_p", f32), (tokens, "tokens", i32), (probs, "probs", f32)):
-        if t is not None and (t.dtype not in types or t.shape != shape or not t.is_contiguous()):
-            _tensor(t, name, types, shape)
+        if t is not None and (t.dtype not in types or t.shape != shape or not t.is_contiguous() or t.get_device() != device):
+            _tensor(t, name, types, shape, device=device)
+    _on_gpu(device, "logits")
     if tokens is None:
         tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if probs is None:

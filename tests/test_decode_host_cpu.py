@@ -67,3 +67,75 @@ def test_rewinding_twice_goes_further_than_the_ring():
     assert ring.append(0, 32) and ring.append(32, 33) and ring.append(17, 18)
     assert not ring.may(2)
     assert not ring.append(2, 3)
+
+
+class Elsewhere:
+    """A tensor that says it is on another device; a call that passed it on would show (no library is loaded here)."""
+
+    def __init__(self, t, device):
+        self.t, self.device_number = t, device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.device_number
+
+
+@pytest.fixture
+def tf(monkeypatch):
+    import mlx_affine_bit_gb300 as tf
+
+    def called(*a, **k):
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(tf, "lib", called)
+    monkeypatch.setattr(tf, "_get_device", lambda: 0)
+    return tf
+
+
+def test_tensors_on_other_devices_are_refused(tf):
+    import torch
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)      # noqa: E731
+    at = Elsewhere
+    pools = [torch.zeros((4, 2, 16, 64), dtype=torch.int8) for _ in range(2)] + [torch.zeros((4, 2)) for _ in range(2)] + \
+        [torch.zeros((2, 2, 32, 64), dtype=torch.bfloat16) for _ in range(2)] + [torch.zeros((2, 2, 2, 32))]
+    lens, table, slots, starts = i32(3, 5), torch.zeros((2, 2), dtype=torch.int32), i32(0, 1), i32(0, 1, 2)
+    cache = lambda *d: tf.KvCache(*[at(t, n) for t, n in zip(pools, d)])         # noqa: E731
+    # A cache and a batch are on one device ...
+    for wrong in range(1, 7):
+        with pytest.raises(ValueError, match="on"):
+            cache(*[-1 if i == wrong else 0 for i in range(7)])
+    for d in ((0, -1, 0, 0), (0, 0, 1, 0), (0, 0, 0, -1), (-1, 0, 0, 0)):
+        with pytest.raises(ValueError, match="on"):
+            tf.KvBatch(at(lens, d[0]), at(table, d[1]), 5, row_start=at(starts, d[2]), rows=2, slots=at(slots, d[3]))
+    # ... the same, and the current GPU; so are the rows of each call.
+    good, b = cache(*[0] * 7), tf.KvBatch(at(lens, 0), at(table, 0), 5)
+    rows = lambda d: at(torch.zeros((2, 128), dtype=torch.bfloat16), d)          # noqa: E731
+    for c, batch, where in ((good, b, -1), (good, b, 1), (good, tf.KvBatch(lens, table, 5), 0), (cache(*[-1] * 7), tf.KvBatch(lens, table, 5), -1),
+                            (cache(*[1] * 7), tf.KvBatch(at(lens, 1), at(table, 1), 5), 1)):
+        home = c.device
+        for call in (lambda: c.append(rows(where), rows(home), batch, stream=0), lambda: c.append(rows(home), rows(where), batch, stream=0),
+                     lambda: c.read(batch, k_out=rows(where), v_out=rows(home), stream=0),
+                     lambda: c.attend(rows(where), batch, out=rows(home), stream=0),
+                     lambda: c.attend(rows(home), batch, out=rows(where), stream=0)):
+            with pytest.raises(ValueError, match="on|device"):
+                call()
+    with pytest.raises(AssertionError):          # (and what fits goes on to the library)
+        good.append(rows(0), rows(0), b, stream=0)
+
+
+def test_sampling_on_other_devices_is_refused(tf):
+    import torch
+    x, u, k = torch.zeros((2, 10)), torch.zeros(2), torch.zeros(2, dtype=torch.int32)
+    at = Elsewhere
+    for name, t in (("u", u), ("temperature", u), ("top_k", k), ("top_p", u), ("min_p", u), ("tokens", k), ("probs", u)):
+        par = dict(u=at(u, 0), tokens=at(k, 0), probs=at(u, 0))
+        par[name] = t
+        with pytest.raises(ValueError, match=name):
+            tf.sample(at(x, 0), stream=0, **par)
+    for d in (-1, 1):
+        with pytest.raises(ValueError, match="logits"):
+            tf.sample(at(x, d), at(u, d), tokens=at(k, d), probs=at(u, d), stream=0)
+    with pytest.raises(AssertionError):
+        tf.sample(at(x, 0), at(u, 0), tokens=at(k, 0), probs=at(u, 0), stream=0)
