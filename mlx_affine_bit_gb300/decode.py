@@ -77,7 +77,18 @@ class Decoder:
         return self.head(x if last is None else x[last])
 
     def generate(self, prompts, n, temperature=0.8, top_k=50, top_p=0.95, seed=1, graph=True):
-        """n tokens [n][seqs] after the prompts (lists of tokens, one a sequence), and the last step's seconds."""
+        """n tokens [n][seqs] after the prompts (lists of tokens, one a sequence), and the last step's seconds.
+
+        graph: single-token steps after the first as one CUDA graph, captured on the current stream (torch's default
+        stream cannot be captured: then on one of the call's own)."""
+        if graph and torch.cuda.current_stream() == torch.cuda.default_stream():
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                result = self.generate(prompts, n, temperature, top_k, top_p, seed, graph)
+            torch.cuda.current_stream().wait_stream(side)
+            result[0].record_stream(torch.cuda.current_stream())
+            return result
         dev, seqs = self.table.device, len(prompts)
         if seqs != self.seqs or max(map(len, prompts)) + n > self.max_len:
             raise ValueError("the decoder was made for %d sequences of up to %d tokens" % (self.seqs, self.max_len))

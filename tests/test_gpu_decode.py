@@ -98,3 +98,14 @@ def test_refuses_other_sequences():
         d.generate([[1]], 2)
     with pytest.raises(ValueError):
         d.generate([[1], [2] * 31], 2)
+
+
+def test_generation_on_the_default_stream():
+    # With a graph, although that stream cannot be captured; the tokens of a stream of one's own.
+    prompts = [[(31 * s + 7 * i) % 4096 for i in range(n)] for s, n in enumerate((20, 1, 33, 64))]
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    got = Decoder(max_len=100).generate(prompts, 12)[0].clone()
+    assert torch.equal(got, Decoder(max_len=100).generate(prompts, 12, graph=False)[0])
+    with torch.cuda.stream(torch.cuda.Stream()):
+        want = Decoder(max_len=100).generate(prompts, 12)[0].cpu()
+    assert torch.equal(got.cpu(), want)
