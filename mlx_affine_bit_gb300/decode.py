@@ -81,6 +81,10 @@ class Decoder:
 
         graph: single-token steps after the first as one CUDA graph, captured on the current stream (torch's default
         stream cannot be captured: then on one of the call's own)."""
+        if len(prompts) != self.seqs or max(map(len, prompts)) + n > self.max_len:
+            raise ValueError("the decoder was made for %d sequences of up to %d tokens" % (self.seqs, self.max_len))
+        if n < 1 or min(map(len, prompts)) < 1:
+            raise ValueError("every prompt, and what is generated, must have a token at least")
         if graph and torch.cuda.current_stream() == torch.cuda.default_stream():
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
@@ -90,8 +94,6 @@ class Decoder:
             result[0].record_stream(torch.cuda.current_stream())
             return result
         dev, seqs = self.table.device, len(prompts)
-        if seqs != self.seqs or max(map(len, prompts)) + n > self.max_len:
-            raise ValueError("the decoder was made for %d sequences of up to %d tokens" % (self.seqs, self.max_len))
         gen = torch.Generator(device=dev).manual_seed(seed)
         u = torch.rand((n, seqs), generator=gen, device=dev)
         row_u = torch.empty(seqs, device=dev)

@@ -139,3 +139,12 @@ def test_sampling_on_other_devices_is_refused(tf):
             tf.sample(at(x, d), at(u, d), tokens=at(k, d), probs=at(u, d), stream=0)
     with pytest.raises(AssertionError):
         tf.sample(at(x, 0), at(u, 0), tokens=at(k, 0), probs=at(u, 0), stream=0)
+
+
+def test_generation_refuses_empty_prompts(tf):
+    # (The last row of a prompt without rows would be another's.)
+    from mlx_affine_bit_gb300.decode import Decoder
+    d = Decoder(layers=1, width=256, heads=2, kv_heads=1, dim=64, vocab=64, seqs=2, max_len=32, device="cpu")
+    for prompts, n in (([[1], []], 2), ([[], []], 2), ([[1], [2]], 0), ([[1], [2]], -1), ([[1]], 2), ([], 2), ([[1], [2] * 31], 2)):
+        with pytest.raises(ValueError):
+            d.generate(prompts, n)
