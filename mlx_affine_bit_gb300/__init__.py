@@ -473,9 +473,11 @@ class KvCache:
         tf_kv_append(self.c, self._batch(batch), k, ks, v, vs, stream)
 
     def read(self, batch, dtype=None, k_out=None, v_out=None, stream=None):
-        """The batch's tokens as k, v rows [rows][kv_heads * dim] of dtype (the appended rows' type by default)."""
+        """The batch's tokens as k, v rows [rows][kv_heads * dim] of dtype (by default the type of the output that is
+        given, or of the appended rows).  An output that is not given is made."""
         import torch
-        dtype = dtype or self.dtype
+        given = k_out if k_out is not None else v_out
+        dtype = dtype or (self.dtype if given is None else given.dtype)
         width = self.kv_heads * self.dim
         types = (torch.bfloat16, torch.float32)
         if k_out is None and v_out is None:

@@ -148,3 +148,24 @@ def test_generation_refuses_empty_prompts(tf):
     for prompts, n in (([[1], []], 2), ([[], []], 2), ([[1], [2]], 0), ([[1], [2]], -1), ([[1]], 2), ([], 2), ([[1], [2] * 31], 2)):
         with pytest.raises(ValueError):
             d.generate(prompts, n)
+
+
+def test_reading_with_one_output_given(tf, monkeypatch):
+    # The other is made, of the same type, whatever the cache was appended from.
+    import torch
+    cache = tf.KvCache.empty(4, 2, 64, 16, 2, torch.float32, "cpu")
+    b = tf.KvBatch(torch.tensor([3, 5], dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32), 5)
+    monkeypatch.setattr(tf, "_on_gpu", lambda *a: None)
+    calls = []
+    monkeypatch.setattr(tf, "tf_kv_read", lambda *a: calls.append(a))
+    for dtype, flags in ((torch.bfloat16, tf.TF_OUT_BF16), (torch.float32, 0)):
+        mine = torch.zeros((2, 128), dtype=dtype)
+        for k, v in ((mine, None), (None, mine)):
+            got = cache.read(b, k_out=k, v_out=v)
+            assert got[0 if k is not None else 1] is mine and got[0].dtype == got[1].dtype == dtype
+            assert calls[-1][6] == flags
+    assert cache.read(b)[0].dtype == torch.float32 and cache.read(b, torch.bfloat16)[1].dtype == torch.bfloat16
+    with pytest.raises(TypeError):               # (two types are refused as before)
+        cache.read(b, k_out=torch.zeros((2, 128)), v_out=torch.zeros((2, 128), dtype=torch.bfloat16))
+    with pytest.raises(TypeError):
+        cache.read(b, torch.bfloat16, k_out=torch.zeros((2, 128)))
