@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendParams P) {
     const int slot = P.b.slots ? P.b.slots[s] : s;
     const int first = q.end - q.n;
     const int pg = (first >> BL) + j;               // page of the sequence
-    if (q.n == 0) return;
+    if (q.ok && q.n == 0) return;
     if (!q.ok || first < 0 || slot < 0 || slot >= kv.n_slots) {
         if (threadIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
         return;

@@ -309,3 +309,29 @@ def test_pages_of_scale_zero_hold_zeros(dtype, small):
         assert kc[3, 0, 5] == 127 and kc[20, 1, 0] == -127 and kc[17, 1, 63] == 0
     for x in q.values(0, 40):
         assert np.all(np.isfinite(x))
+
+
+@pytest.mark.parametrize("wrong", ["length", "rows"])
+def test_sequences_without_rows_are_checked_too(wrong):
+    # Each call reports numbers that do not fit, also of a sequence that has nothing to write or read; the other is served.
+    q = Sequences([20, 20], 1, 64, 16, BF16, 15)
+    b = q.batch([20, 20], [20, 0])
+    if wrong == "length":
+        b._keep[0][1] = 21
+    else:
+        b._keep[2][2] = 41
+    x, y = q.rows([q.k[0]]), q.rows([q.v[0]])
+    calls = [lambda: q.cache.append(x, y, b), lambda: q.cache.read(b), lambda: q.cache.attend(x, b)]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        with pytest.raises(tf.TfError) as e:
+            tf.tf_device_status()
+        assert e.value.rc == -14
+    q.check(0, 20)
+    # A slot stands for nothing where there is nothing to write.
+    c = tf.KvBatch(*b._keep[:2], 20, torch.tensor([0, 20, 20], dtype=torch.int32, device=DEV), 20, 20,
+                   torch.tensor([0, -1], dtype=torch.int32, device=DEV))
+    c._keep[0][1] = 20
+    q.cache.append(x, y, c)
+    status_clean()
