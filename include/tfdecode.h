@@ -155,7 +155,8 @@ int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const void *q, int64
  * min_p keeps those of at least min_p times the largest weight (min_p above 1
  * counts as 1).  The token is the first, in index order, at which the running
  * sum of the kept weights exceeds u times their sum.  A temperature that is not
- * above 0, NaN included, takes the first largest logit (probability 1).  A row of
+ * above 0, NaN included, takes the first largest logit (probability 1); one above
+ * the largest float counts as that.  top_p or min_p of NaN are off.  A row of
  * -inf gives token -1 and probability 0.
  */
 #define TF_IN_BF16 16

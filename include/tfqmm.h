@@ -33,6 +33,8 @@
  * asynchronous on `stream` (a cudaStream_t; NULL = the legacy default stream).
  * The library keeps, per device and stream, a small workspace for split-K
  * partials and a device status word (allocated on first use, held until exit).
+ * Calls on one stream, and replays of the graphs captured on it, share that
+ * workspace: replay them on that stream, or after one another.
  * Errors are returned as negative status codes; nothing throws across the ABI.
  */
 #ifndef TFQMM_H

@@ -186,8 +186,11 @@ extern "C" int tf_kv_attend(const tf_kv *kv, const tf_kv_batch *batch, const voi
     // Rows or prompt kernel: the one that is expected to take less time, by what they measured over 17 to 400
     // rows of 1 to 16 sequences of 4000 and 60000 tokens.  The rows kernel takes 16 rows at a time (some 6.5 ns
     // for 128 tokens of dim 128 with all SMs at work, on top of 12 us), the prompt kernel 256 (dim 256: 128;
-    // some 2.9 us for 128 tokens on one SM, on top of 45 us).  64 rows of 16 x 4000 tokens, dim 128: 110
-    // against 115 us; 128 rows 194 against 115; 128 rows of 1 x 4000 tokens 35 against 51.
+    // some 2.9 us for 128 tokens on one SM, on top of 45 us).  64 rows of 16 x 4000 tokens, dim 128: 109
+    // against 107 us; 128 rows 197 against 107; 128 rows of 1 x 4000 tokens 32 against 42.
+    // The host knows the largest number of rows and the largest length of a sequence only, and takes them for all:
+    // a chunk of 500 rows beside 47 single tokens over 4000 to 4500 tokens goes to the prompt kernel as a whole and takes
+    // 334 us (by rows 272), where a call for the chunk and one for the others take 70 and 74.
     bool prompt = (flags & TF_KV_BY_TILES) != 0;
     if (max_group_rows > 16 && !(flags & (TF_KV_BY_ROWS | TF_KV_BY_TILES))) {
         const double blocks = (double)batch->n_seqs * kv->kv_heads * (double)((span + 127) / 128);

@@ -17,9 +17,10 @@
 // Bound by the tensor cores and, closely, by the instructions around them: per row
 // and token one exponential and about four others, per token and dimension of the
 // cache about two to widen a code.  Causal, 32 query heads of 128 over 8: 4000 tokens
-// of a prompt 201 us (652 TFLOP/s), 8000 653 us (803 TFLOP/s); 16 heads of 256: 4000
-// tokens 196 us; 16 heads of 64: 91 us; three chunks of up to 509 tokens, 16 heads of
-// 256, window 4096: 89 us.  A step of two tiles (256 rows, 128 tokens, dim 128) takes
+// of a prompt 201 us (652 TFLOP/s), 8000 646 us (812 TFLOP/s); 16 heads of 256: 4000
+// tokens 202 us; 16 heads of 64: 88 us; three chunks of up to 509 tokens, 16 heads of
+// 256, window 4096: 91 us (scores past FAR: 4000 tokens of 32 heads 323 us, the chunks
+// 136).  A step of two tiles (256 rows, 128 tokens, dim 128) takes
 // 2.7 us, 1.7 us of them the products: one with N = 128 takes 94 to 107 clocks for
 // 16 of K, measured alone, which is 60 to 68 % of the peak.  An item's beginning and
 // end (the rows of q, the first scores, the outputs) cost 6 us, the launch's plan 4.
@@ -70,7 +71,10 @@ TFQ_HD constexpr int p_smem(int d) { return 1024 + (p_tiles(d) + p_slots(d)) * p
 constexpr uint32_t PAGES_THERE = 0x8000;         // (the sign of a key scale)
 constexpr int SCALES = 4;                        // steps whose scales are kept
 constexpr float SLACK = 0.9f;                    // growth of a maximum that is let be, in powers of two (w stays in fp16's range)
-constexpr float FAR = 4096.f;                    // bound (in powers of two) of the terms of an exponent that are summed as they stand
+// Bound (in powers of two) of the terms of an exponent that are summed as they stand: below it their sums, of up to
+// 2^13, round by 2^-11 at most.  The check of a step comes before the wait for its scores (after it: 4 us of 204 for 4000
+// tokens of 32 heads of 128).
+constexpr float FAR = 4096.f;
 constexpr int ITEM_STEPS = 3;                    // an item's beginning and end on the line, in steps (2 to 6: 3 is fastest)
 constexpr int MAX_SHARE = 8;                     // CTAs an item, on average: one of them joins their parts
 

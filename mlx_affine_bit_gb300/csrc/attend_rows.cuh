@@ -16,11 +16,14 @@
 // would be rounded away.)
 //
 // Bound by reading the cache: 48 x 8000 tokens of 8 heads of 128, 32 query heads,
-// take 129 us, 6.1 TB/s of the codes; 1 x 131072 tokens 52 us (5.2 TB/s), of which
+// take 125 us, 6.3 TB/s of the codes; 1 x 131072 tokens 54 us (5.0 TB/s), of which
 // some 12 us are a call's beginning and end (a launch, the lengths, pages, codes,
 // the join of the parts): 1 x 700 tokens take 13 us.  Rows beyond 16 of a sequence
-// and head read the tokens again, out of L2 (16 sequences of up to 4100 tokens, 40
-// rows each: 32 us).
+// and head read the tokens again, out of L2 (16 sequences of up to 4100 tokens, up to
+// 40 rows each: 34 us).
+//
+// q is rounded to fp16's 11 bits where it comes as fp32: each of its values moves by no
+// more than 2^-11 of itself, where a key's code is off by up to 2^-8 of its page's largest.
 //
 // The work -- for every sequence, head and tile of up to 8 * NT rows the tokens in
 // steps of 128 -- is one line of steps that the CTAs, as many as are resident at

@@ -18,7 +18,9 @@
 // reads of the other CTAs' shared memory (four of the cluster, some twenty of the
 // first CTA alone); 48 rows 59 us (0.8 TB/s: some 55 instructions for 32 logits in
 // three passes over the slice, and barriers, not the read of 48 MB); 300 rows of
-// 32003 bf16 logits 32 us.
+// 32003 bf16 logits 34 to 41 us where no row's top-p leaves more than MAX_LIST tokens
+// (ten of twelve random inputs), 47 and 62 us where one does: all rows run at once,
+// and the slowest is the call's time.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,8 +43,9 @@ constexpr float WEIGHT_ONE = 2147483648.f;       // weight of the largest logit:
 // exp(z) * 2^31 rounds to 0 below z = -22.18: BINS / 23 bins a unit of z cover the rest, bin b the nearest to b.
 constexpr float BINS_PER_Z = BINS / 23.f, Z_END = -22.25f;
 static_assert(BINS == THREADS, "a thread a bin");
-// Tokens that one CTA finishes alone.  300 rows of 32003, top-p 0.8, some of which leave more than 2048: 34 us; 48 with
-// 2048 (the cluster goes on with its whole slices), 60 with 1024.
+// Tokens that one CTA finishes alone.  300 rows of 32003, top-p 0.8, of one input whose rows leave up to some 4000: 34 us;
+// 48 with 2048 (the cluster goes on with its whole slices), 60 with 1024.  Inputs with longer lists pay the same way
+// with 4096: 62 us with a list of 5738.  The list is 32 KB of the CTA's shared memory.
 constexpr int MAX_LIST = 4096;
 // Of a row in one CTA's shared memory, for two CTAs an SM beside the list (300 x 32003 bf16: 33 us, 69 with the logits
 // read from global memory in each pass; 48 x 248320 fp32: 62 and 73).
