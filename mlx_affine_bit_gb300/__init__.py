@@ -1,12 +1,13 @@
 """Python binding of libtfqmm, the MLX-affine quantized row product for GB300, and
-of the 8-bit cache, attention and sampling around it.
+of the 8-bit cache, attention and sampling around it, and the pages, positions and
+4-bit cache that serving adds.
 
 Argument marshalling only: every step of the product runs in the library's
-CUDA kernels (``csrc/``).  The names and arguments follow ``include/tfqmm.h`` and
-``include/tfdecode.h``.
+CUDA kernels (``csrc/``).  The names and arguments follow ``include/tfqmm.h``,
+``include/tfdecode.h`` and ``include/tfserve.h``.
 Tensors may be passed as torch tensors (their ``data_ptr()`` is used) or as
-raw integer addresses; ``KvCache``, ``KvBatch`` and ``sample`` take tensors, and
-check their types, shapes, strides and devices.  ``stream`` is a
+raw integer addresses; ``KvCache``, ``KvBatch``, ``sample``, ``KvPages``, ``Rope`` and
+``Kv4Cache`` take tensors, and check their types, shapes, strides and devices.  ``stream`` is a
 ``torch.cuda.Stream``, a raw ``cudaStream_t`` integer, or None for torch's current
 stream.
 
@@ -33,11 +34,13 @@ STATUS = {
 SYMBOLS = ("tf_qmm", "tf_qmm_ex", "tf_qmm_prompt", "tf_qmm_gather", "tf_qmm_noalloc", "tf_noalloc_status", "tf_qmm_stack", "tf_widen",
            "tf_widen_host", "tf_common_width", "tf_qmm_bytes", "tf_device_status", "tf_set_launch_mode",
            "tf_inject_stall", "tf_last_error_string", "tf_version",
-           "tf_kv_append", "tf_kv_read", "tf_kv_attend", "tf_sample")
+           "tf_kv_append", "tf_kv_read", "tf_kv_attend", "tf_sample",
+           "tf_kv_plan", "tf_rope", "tf_kv4_append", "tf_kv4_read", "tf_kv4_attend")
 TF_LAUNCH_PDL, TF_LAUNCH_EARLY_WEIGHTS, TF_LAUNCH_EARLY_X = 1, 2, 4
 TF_OUT_BF16, TF_EPI_RELU2 = 1, 2
 TF_IN_F32, TF_KV_CAUSAL, TF_IN_BF16 = 4, 8, 16
 TF_KV_BY_ROWS, TF_KV_BY_TILES = 64, 128
+TF_ROPE_PAIRS, TF_ROPE_BACK = 256, 512
 
 
 class TfError(RuntimeError):
@@ -65,6 +68,17 @@ class TfKvBatch(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("n_seqs", "rows", "max_rows", "max_len")] + \
                [(n, ctypes.c_void_p) for n in ("row_start", "kv_len", "table")] + \
                [("table_stride", ctypes.c_int64), ("slots", ctypes.c_void_p)]
+
+
+class TfKvPages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_void_p) for n in ("kv_len", "free_pages", "n_free")] + \
+               [(n, ctypes.c_int) for n in ("n_seqs", "n_blocks", "max_pages", "block")]
+
+
+class TfKv4(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_affine", "v_affine")] + \
+               [(n, ctypes.c_int) for n in ("n_blocks", "kv_heads", "block", "dim")]
 
 
 _lib = None
@@ -147,11 +161,18 @@ def _load(path):
     L.tf_kv_read.argtypes = [kv, batch, P, i64, P, i64, i32, P]
     L.tf_kv_attend.argtypes = [kv, batch, P, i64, i32, P, i64, ctypes.c_float, i32, i32, P]
     L.tf_sample.argtypes = [P, i32, i32, i64, P, P, P, P, P, P, P, i32, P]
+    pages, kv4 = ctypes.POINTER(TfKvPages), ctypes.POINTER(TfKv4)
+    L.tf_kv_plan.argtypes = [pages, P, i32, i32, i32, P, P, P, P, P]
+    L.tf_rope.argtypes = [P, i32, ctypes.c_float, P, i32, P, i64, P, i64, i32, i32, i32, P]
+    L.tf_kv4_append.argtypes = [kv4, P, i32, P, i64, P, i64, i32, P]
+    L.tf_kv4_read.argtypes = [kv4, batch, P, i64, P, i64, i32, P]
+    L.tf_kv4_attend.argtypes = [kv4, batch, P, i64, i32, P, i64, ctypes.c_float, i32, i32, P]
     L.tf_last_error_string.restype = ctypes.c_char_p
     L.tf_version.restype = ctypes.c_char_p
     for name in ("tf_qmm", "tf_qmm_ex", "tf_qmm_prompt", "tf_qmm_gather", "tf_qmm_noalloc", "tf_qmm_stack", "tf_widen",
                  "tf_widen_host", "tf_common_width", "tf_qmm_bytes", "tf_device_status", "tf_noalloc_status",
-                 "tf_set_launch_mode", "tf_inject_stall", "tf_kv_append", "tf_kv_read", "tf_kv_attend", "tf_sample"):
+                 "tf_set_launch_mode", "tf_inject_stall", "tf_kv_append", "tf_kv_read", "tf_kv_attend", "tf_sample",
+                 "tf_kv_plan", "tf_rope", "tf_kv4_append", "tf_kv4_read", "tf_kv4_attend"):
         getattr(L, name).restype = i32
     return L
 
@@ -318,6 +339,35 @@ def tf_sample(logits, rows, vocab, stride, u, temperature, top_k, top_p, min_p, 
     """One token per row of logits from the random numbers u (see include/tfdecode.h)."""
     _check(lib().tf_sample(_ptr(logits), rows, vocab, stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p),
                            _ptr(min_p), _ptr(tokens), _ptr(probs), flags, _stream(stream)))
+
+
+def tf_kv_plan(pages: TfKvPages, change, rows, max_rows, max_len, row_start, positions, slots, info, stream=None) -> None:
+    """One step of growing and shrinking sequences: their pages, row starts, positions and slots (see include/tfserve.h)."""
+    _check(lib().tf_kv_plan(pages, _ptr(change), rows, max_rows, max_len, _ptr(row_start), _ptr(positions), _ptr(slots),
+                            _ptr(info), _stream(stream)))
+
+
+def tf_rope(turns, rot, factor, positions, rows, x, x_stride, out, out_stride, heads, dim, flags=0, stream=None) -> None:
+    """Rotary positions of rows of heads (see include/tfserve.h)."""
+    _check(lib().tf_rope(_ptr(turns), rot, factor, _ptr(positions), rows, _ptr(x), x_stride, _ptr(out), out_stride, heads,
+                         dim, flags, _stream(stream)))
+
+
+def tf_kv4_append(kv: TfKv4, slots, rows, k, k_stride, v, v_stride, flags=0, stream=None) -> None:
+    """Quantize rows of keys and values into their slots of the 4-bit cache (see include/tfserve.h)."""
+    _check(lib().tf_kv4_append(kv, _ptr(slots), rows, _ptr(k), k_stride, _ptr(v), v_stride, flags, _stream(stream)))
+
+
+def tf_kv4_read(kv: TfKv4, batch: TfKvBatch, k_out, k_stride, v_out, v_stride, flags=0, stream=None) -> None:
+    """Read the batch's tokens back from the 4-bit cache; either output may be None."""
+    _check(lib().tf_kv4_read(kv, batch, _ptr(k_out), k_stride, _ptr(v_out), v_stride, flags, _stream(stream)))
+
+
+def tf_kv4_attend(kv: TfKv4, batch: TfKvBatch, q, q_stride, heads, out, out_stride, scale, window=0, flags=TF_KV_CAUSAL,
+                  stream=None) -> None:
+    """Attention of the batch's rows over the 4-bit cache; out is bf16 (see include/tfserve.h)."""
+    _check(lib().tf_kv4_attend(kv, batch, _ptr(q), q_stride, heads, _ptr(out), out_stride, scale, window, flags,
+                               _stream(stream)))
 
 
 def tf_version() -> str:
@@ -538,3 +588,6 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     tf_sample(logits, rows, vocab, stride, u, temperature, top_k, top_p, min_p, tokens, probs,
               TF_IN_BF16 if logits.dtype == torch.bfloat16 else 0, stream)
     return tokens, probs
+
+
+from .serve import Kv4Cache, KvPages, KvPlan, Rope   # noqa: E402,F401

@@ -264,7 +264,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-template <int D>
+// Place in a 16-byte chunk of the fp16 tiles of eight dimensions' e-th: with 4-bit codes, the order in which a word's come
+// out in pairs (d, d + 4), the same for q and keys, and undone where outputs are stored.
+TFQ_HD constexpr int chunk_place(int f, int e) { return f == 4 ? (e & 3) * 2 + (e >> 2) : e; }
+// Eight codes of a word as fp16 (exact: 1024 + c and 64 + c, less that) times a scale plus a bias, in that order.
+__device__ __forceinline__ uint4 widened(uint32_t w, __half2 scale, __half2 bias) {
+    auto value = [&](uint32_t bits, uint16_t base) {
+        const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&bits), __half2half2(__ushort_as_half(base)));
+        const __half2 y = __hfma2(c, scale, bias);
+        return *reinterpret_cast<const uint32_t *>(&y);
+    };
+    const uint32_t v = w >> 8;
+    return make_uint4(value((w & 0x000F000Fu) | 0x64006400u, 0x6400), value((w & 0x00F000F0u) | 0x54005400u, 0x5400),
+                      value((v & 0x000F000Fu) | 0x64006400u, 0x6400), value((v & 0x00F000F0u) | 0x54005400u, 0x5400));
+}
+
+// F: bits of a code (8 or 4).
+template <int F, int D>
 __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_constant__ Params P) {
     constexpr int NT = p_tiles(D), R = 128 * NT, SLOTS = p_slots(D), TB = p_tile_bytes(D);
     constexpr int P_SOFT = p_soft(D), P_CONV = p_conv(D);
@@ -455,11 +471,14 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         regs_down<PRegs<D>::CONV>();
         // Widening: warp v takes tokens TW v .. TW v + TW - 1 of every step, a lane 16 bytes of a token at a time.
         constexpr int TW = KEYS / P_CONV, NP = TW / 16;      // (and as many times 16 tokens, of a page each)
-        constexpr int LPT = D / 16, LOADS = TW * LPT / 32;   // lanes a token, loads a lane
-        // The low two bits of a lane are its place in 64 bytes, the next the token's parity: the eight lanes of a
-        // 16-byte store then meet eight different chunks under the swizzle.
-        const int v = warp - P_SOFT, sub = (lane & 3) | (LPT > 4 ? (lane >> 1) & (LPT - 4) : 0);
-        const int tok = ((lane >> 2) & 1) | (LPT == 4 ? (lane >> 2) & 6 : LPT == 8 ? (lane >> 3) & 2 : 0);
+        constexpr int TOK = D * F / 8, LPT = TOK / 16, LOADS = TW * LPT / 32;   // bytes and lanes a token, loads a lane
+        // The eight lanes of a 16-byte store meet eight different chunks under the swizzle.  8 bits, two chunks a lane: its
+        // low two bits are its place in 64 bytes, the next the token's parity.  4 bits, four chunks a lane: the low bit
+        // is its half of a row of 128 bytes, the next two the token's.
+        const int v = warp - P_SOFT;
+        const int sub = F == 4 ? (lane & 1) | (LPT > 2 ? (lane >> 2) & (LPT - 2) : 0) : (lane & 3) | (LPT > 4 ? (lane >> 1) & (LPT - 4) : 0);
+        const int tok = F == 4 ? (LPT == 2 ? lane >> 1 : LPT == 4 ? (lane >> 1 & 3) | (lane >> 2 & 4) : lane >> 1 & 3)
+                               : ((lane >> 2) & 1) | (LPT == 4 ? (lane >> 2) & 6 : LPT == 8 ? (lane >> 3) & 2 : 0);
         uint32_t st = 0;
         do {
             const long long seq_table = w.seq * P.b.table_stride;
@@ -477,7 +496,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     } else {
                         pages = page;
                         const long long ph = (long long)page * H + w.h;
-                        scale = make_float2(P.kv.k_scale[ph], log2f(P.kv.v_scale[ph]));
+                        if constexpr (F == 8)
+                            scale = make_float2(P.kv.k_scale[ph], log2f(P.kv.v_scale[ph]));
+                        else
+                            scale = make_float2(1.f, 0.f);
                     }
                 }
             };
@@ -500,14 +522,58 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     const int tk = j * (32 / LPT) + tok, page = j < LOADS / NP ? p0 : p1;
                     r[j] = make_uint4(0u, 0u, 0u, 0u);
                     if (page >= 0)
-                        r[j] = *reinterpret_cast<const uint4 *>(pool + (((((long long)page * H + w.h) << BL) + ((t0 + tk) & BM)) * D) + 16 * sub);
+                        r[j] = *reinterpret_cast<const uint4 *>(pool + (((((long long)page * H + w.h) << BL) + ((t0 + tk) & BM)) * TOK) + 16 * sub);
                 }
             };
+            // 4 bits: scales and biases of a step's keys and values, (0, 0) of tokens that no row of the pair sees (whatever
+            // may stand there); those of the values whose turn is next, as fp16 over their unit.
+            uint32_t ka[F == 4 ? LOADS : 1], va[F == 4 ? LOADS : 1], v_now[F == 4 ? LOADS : 1];
+            const int seen_from = P.window ? max(0, w.s.plan - w.s.q.n + w.tile * R / G - P.window + 1) : 0;
+            auto load_affine = [&](int step, int p0, int p1) {
+                if constexpr (F == 4) {
+                    const int t0 = w.t.from + step * KEYS + TW * v;
+#pragma unroll
+                    for (int j = 0; j < LOADS; ++j) {
+                        const int tk = j * (32 / LPT) + tok, page = j < LOADS / NP ? p0 : p1;
+                        ka[j] = va[j] = 0;
+                        if (page >= 0 && t0 + tk >= seen_from && t0 + tk < w.t.to) {
+                            const long long at = ((((long long)page * H + w.h) << BL) + ((t0 + tk) & BM)) * (D / 64) + (sub >> 1);
+                            ka[j] = P.k_affine[at];
+                            va[j] = P.v_affine[at];
+                        }
+                    }
+                }
+            };
+            // Units of the 16 tokens of loads j0 ..: the power of two above every value; scales and biases become fp16 over it.
+            // Returns its exponent, biased (0: only zeros).
+            auto over_unit = [&](uint32_t (&a)[F == 4 ? LOADS : 1], int j0) {
+                float most = 0.f;
+#pragma unroll
+                for (int j = j0; j < j0 + LOADS / NP; ++j) {
+                    const float sc = __uint_as_float(a[j] << 16), bias = __uint_as_float(a[j] & 0xFFFF0000u);
+                    most = fmaxf(most, fmaxf(fabsf(bias), fabsf(fmaf(15.f, sc, bias))));
+                }
+                const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(most)), unit = top == 0 ? 0 : min((top >> 23) + 1, 253u);
+                const float inv = __uint_as_float((254u - unit) << 23);
+#pragma unroll
+                for (int j = j0; j < j0 + LOADS / NP; ++j)
+                    a[j] = pack_half(__uint_as_float(a[j] << 16) * inv, __uint_as_float(a[j] & 0xFFFF0000u) * inv);
+                return unit;
+            };
             // Where this lane's 16 values of token tk go: two 16-byte chunks, 2 sub and 2 sub + 1 of the row of blocks of eight.
-            auto store = [&](uint8_t *tile, const uint4 (&r)[LOADS], const bool tiny) {
+            auto store = [&](uint8_t *tile, const uint4 (&r)[LOADS], const bool tiny, const uint32_t (&affine)[F == 4 ? LOADS : 1]) {
 #pragma unroll
                 for (int j = 0; j < LOADS; ++j) {
                     const int tk = TW * v + j * (32 / LPT) + tok;
+                    if constexpr (F == 4) {
+                        uint8_t *row4 = tile + (sub >> 1) * (KEYS * 128) + tk * 128;
+                        const __half2 a = *reinterpret_cast<const __half2 *>(&affine[j]), sc = __low2half2(a), bias = __high2half2(a);
+                        const uint32_t x4[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4 *>(row4 + (((4 * (sub & 1) + i) ^ (tk & 7)) << 4)) = widened(x4[i], sc, bias);
+                        continue;
+                    }
                     uint8_t *row = tile + (sub >> 2) * (KEYS * 128) + tk * 128;
                     const uint32_t x[4] = {r[j].x ^ 0x80808080u, r[j].y ^ 0x80808080u, r[j].z ^ 0x80808080u, r[j].w ^ 0x80808080u};
                     uint32_t y[8];
@@ -528,8 +594,22 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             };
             auto put_keys = [&](uint32_t step) {
                 const uint32_t kt = 2 * step;
+                if constexpr (F == 4) {
+                    uint32_t k_unit[NP], v_unit[NP];
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) {
+                        k_unit[e] = over_unit(ka, e * (LOADS / NP));
+                        v_unit[e] = over_unit(va, e * (LOADS / NP));
+                    }
+                    // (Keys of zeros only: scores of 0 with any unit.)
+                    const uint32_t ku = lane % NP == 0 ? k_unit[0] : k_unit[NP - 1], vu = lane % NP == 0 ? v_unit[0] : v_unit[NP - 1];
+                    if (k_of.scale.x >= 0.f)
+                        k_of.scale = make_float2(ku == 0 ? 1.f : __uint_as_float(ku << 23), vu == 0 ? -INFINITY : (float)((int)vu - 127));
+#pragma unroll
+                    for (int j = 0; j < LOADS; ++j) v_now[j] = va[j];
+                }
                 wait_for(&B.kv_empty[kt % SLOTS], ((kt / SLOTS) & 1) ^ 1, abort, P.status);
-                store(kv_s + (kt % SLOTS) * TB, kr, true);
+                store(kv_s + (kt % SLOTS) * TB, kr, true, ka);
                 if (lane < NP) B.scale[step % SCALES][NP * v + lane] = k_of.scale;
                 const bool there = __all_sync(~0u, k_of.scale.x >= 0.f);
                 const float top_ks = NP > 1 ? fmaxf(k_of.scale.x, __shfl_xor_sync(~0u, k_of.scale.x, 1)) : k_of.scale.x;
@@ -541,6 +621,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             look_up(w.step0);
             find(w.step0);
             load(P.kv.k, w.step0, k_of.p0, k_of.p1, kr);
+            load_affine(w.step0, k_of.p0, k_of.p1);
             load(P.kv.v, w.step0, k_of.p0, k_of.p1, vr);
             // The slots are filled in the order in which the products free them.  One tile: a step's keys go before the
             // values of the step before it (99 -> 95 us for three chunks of up to 509 tokens, 16 heads of 256, window
@@ -551,19 +632,28 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 if (w.step0 + 1 < w.step1) {
                     find(w.step0 + 1);
                     load(P.kv.k, w.step0 + 1, k_of.p0, k_of.p1, kr);
+                    load_affine(w.step0 + 1, k_of.p0, k_of.p1);
                 }
             }
             for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
                 int p0 = k_of.p0, p1 = k_of.p1;              // (of step i + AHEAD)
+                uint32_t v_affine[F == 4 ? LOADS : 1];       // (of step i)
+                if (F == 4 && AHEAD)
+#pragma unroll
+                    for (int j = 0; j < (F == 4 ? LOADS : 1); ++j) v_affine[j] = v_now[j];
                 if (i + AHEAD < w.step1) put_keys(st + AHEAD);
+                if (F == 4 && !AHEAD)
+#pragma unroll
+                    for (int j = 0; j < (F == 4 ? LOADS : 1); ++j) v_affine[j] = v_now[j];
                 if (i + AHEAD + 1 < w.step1) {
                     find(i + AHEAD + 1);
                     load(P.kv.k, i + AHEAD + 1, k_of.p0, k_of.p1, kr);
+                    load_affine(i + AHEAD + 1, k_of.p0, k_of.p1);
                     if (!AHEAD) p0 = k_of.p0, p1 = k_of.p1;
                 }
                 const uint32_t vt = 2 * st + 1;
                 wait_for(&B.kv_empty[vt % SLOTS], ((vt / SLOTS) & 1) ^ 1, abort, P.status);
-                store(kv_s + (vt % SLOTS) * TB, vr, false);
+                store(kv_s + (vt % SLOTS) * TB, vr, false, v_affine);
                 publish(vt);
                 if (i + 1 < w.step1) load(P.kv.v, i + 1, p0, p1, vr);
             }
@@ -592,7 +682,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 uint32_t h[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[e]) : "f"(y[2 * e + 1]), "f"(y[2 * e]));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                        : "=r"(h[e])
+                        : "f"(y[(2 * e & ~7) + chunk_place(F, 2 * e + 1 & 7)]), "f"(y[(2 * e & ~7) + chunk_place(F, 2 * e & 7)]));
                 if (out16) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -722,7 +814,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 uint32_t h[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    h[e] = pack_half(x[2 * e] * sq, x[2 * e + 1] * sq);
+                    h[e] = F == 4 ? pack_half(x[e] * sq, x[e + 4] * sq) : pack_half(x[2 * e] * sq, x[2 * e + 1] * sq);
                     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
                     sum_q += y.x + y.y;
                     sum_abs += fabsf(y.x) + fabsf(y.y);
@@ -805,7 +897,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             ++item;
 
             // Factor of a score in tensor memory, and the offset that comes off it first; tokens that the row sees.
-            const float rowf = fabsf(P.scale) * 1.44269504088896340736f / fq * (1.f / TINY), off = sum_q * (-128.f * TINY);
+            constexpr float CODE = F == 8 ? TINY : 1.f, TOP = F == 8 ? 128.f * TINY : 1.f;   // of a key in shared memory: its unit, a bound
+            const float rowf = fabsf(P.scale) * 1.44269504088896340736f / fq * (1.f / CODE), off = F == 8 ? sum_q * (-128.f * TINY) : 0.f;
             const int first = w.s.q.end - w.s.q.n, pos = first + i_tok;
             const int see_to = P.causal ? min(w.s.q.end, pos + 1) : w.s.q.end, see_from = P.window ? pos - P.window + 1 : 0;
             const int g0 = min(w.tile * R + t * 128, n_rows - 1), g1 = min(w.tile * R + t * 128 + 127, n_rows - 1);
@@ -816,7 +909,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             // Where the terms of an exponent could pass FAR, which is with a key scale above far_ks (of the warp's rows, twice
             // in its upper half), the warp's scores, m and n are relative to `base` from there on.
             float base = 0.f;
-            uint32_t far_ks = __reduce_min_sync(~0u, __float_as_uint(FAR / (sum_abs * (128.f * TINY) * rowf)) >> 16) * 0x10001u;
+            uint32_t far_ks = __reduce_min_sync(~0u, __float_as_uint(FAR / (sum_abs * TOP * rowf)) >> 16) * 0x10001u;
             for (int i = w.step0; i < w.step1 && !*abort; ++i, ++st) {
                 const int t0 = w.t.from + i * KEYS;
                 wait_for(&B.scales[st % SCALES], (st / SCALES) & 1, abort, P.status);

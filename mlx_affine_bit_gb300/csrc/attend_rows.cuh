@@ -62,10 +62,13 @@ constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
 constexpr int MAX_PARTS = 768;           // CTAs of a launch, at most
 constexpr int NO_TOKEN = 1 << 30;        // past every chunk
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
+// ... by the cache's bits: of 4, w is p times the scale of a code, at most a 15th of what d stands for.
+TFQ_HD constexpr float w_exp(int f) { return f == 4 ? 18.f : W_EXP; }
 
 struct Params {
     CUtensorMap tm_k, tm_v;  // the pools as rows of 128 bytes; a box is a pair of tiles, or one of 16-token pages
-    tf_kv kv;
+    tf_kv kv;                // (the 4-bit cache: pools and sizes, no scales)
+    const uint32_t *k_affine, *v_affine;     // of the 4-bit cache: a bf16 scale and, above it, a bf16 bias
     tf_kv_batch b;
     const void *q;
     uint16_t *out;
@@ -114,6 +117,18 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+__device__ __forceinline__ float log2_fast(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Consecutive bytes (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // What has been summed of a row: maxima m of s and d of s - m + log2(vs), sum l of p.
 struct __align__(16) RowSum {
     float m, d, l, unused;
@@ -133,18 +148,20 @@ __device__ __forceinline__ void join_maxima(RowSum &a, const RowSum &p) {
 __device__ __forceinline__ float l_factor(const RowSum &p, const RowSum &a) { return exp2_fast(p.m - base_of(a.m)); }
 __device__ __forceinline__ float o_factor(const RowSum &p, const RowSum &a) { return exp2_fast(d_at(p, base_of(a.m)) - base_of(a.d)); }
 // Factor of the joined outputs: to the maximum of s, and by the sum.
-__device__ __forceinline__ float out_factor(const RowSum &a) { return a.l == 0.f ? 0.f : exp2f(a.d - W_EXP) / a.l; }
+template <int F = 8>
+__device__ __forceinline__ float out_factor(const RowSum &a) { return a.l == 0.f ? 0.f : exp2f(a.d - w_exp(F)) / a.l; }
 
 // Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q
 // take.  48 sequences of up to 8000 tokens, 8 heads of 128: 79 us so, 81 with one tile a stage and four stages, 83
 // with three stages and two CTAs; one of 131072 tokens 52, 54 and 50.
-TFQ_HD constexpr int stages(int d) { return d == 256 ? 3 : 2; }
+TFQ_HD constexpr int stages(int f, int d) { return f == 4 ? (d == 256 ? 5 : d == 128 ? 3 : 4) : d == 256 ? 3 : 2; }
 TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? 5 : 4) : d == 128 ? 3 : 2; }
-TFQ_HD constexpr int tile_bytes(int d) { return 32 * d; }          // 16 tokens of keys and of values
+TFQ_HD constexpr int tile_bytes(int f, int d) { return 4 * f * d; }     // 16 tokens of keys and of values
+TFQ_HD constexpr int affine_bytes(int f, int d) { return f == 4 ? 2 * d : 0; }   // ... and their scales and biases
 TFQ_HD constexpr int out_pitch(int d) { return d + 4; }            // floats between joined rows
 // Shared memory: the rings; after the tokens are done, every warp's outputs, then the parts' factors.
-TFQ_HD constexpr int smem_bytes(int d, int nt) {
-    const int ring = WARPS * stages(d) * tiles_of(d) * tile_bytes(d), outs = WARPS * 8 * nt * out_pitch(d) * 4;
+TFQ_HD constexpr int smem_bytes(int f, int d, int nt) {
+    const int ring = WARPS * stages(f, d) * tiles_of(d) * (tile_bytes(f, d) + affine_bytes(f, d)), outs = WARPS * 8 * nt * out_pitch(d) * 4;
     const int join = MAX_PARTS * 8 * nt * 4, most = outs > join ? outs : join;
     return ring > most ? ring : most;
 }
@@ -152,8 +169,16 @@ TFQ_HD constexpr int smem_bytes(int d, int nt) {
 // Token of a tile (in eights) that column n of the scores stands for.  A quarter
 // of a warp reads 16 bytes a lane of the keys of tokens order(2 a), order(2 a + 1),
 // and of the values of the four tokens order(2 a) (or the four order(2 a + 1)).
-template <int D>
+template <int F, int D>
 __device__ __forceinline__ int order(int n) {
+    if (F == 4) {
+        // Half a warp reads 8 bytes a lane of the keys of tokens order(0) .. order(3) (or the other four), a warp 4
+        // bytes a lane of the values of the even columns' tokens (or the odd ones').
+        const int n0 = n & 1, n1 = n >> 1 & 1, n2 = n >> 2;
+        if (D == 64) return n ^ n2;
+        if (D == 128) return (n0 ^ n2) * 4 + n0 * 2 + n1;
+        return (n0 ^ n2) * 4 + n1 * 2 + n0;
+    }
     const int a = n >> 1;
     if (D == 64) return (a + (a & 2)) ^ (n & 1 ? 3 : 0);
     if (D == 128) return n ^ (n & 1 ? 4 : 0);
@@ -192,14 +217,18 @@ __device__ __forceinline__ float row_factor(float amax) {
     return __uint_as_float((e >= 253 ? 1u : 254u - e) << 23);
 }
 
-template <int D, int NT>
+// F: bits of a code (8 or 4).
+template <int F, int D, int NT>
 __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid_constant__ Params P) {
     constexpr int R = 8 * NT;                    // rows of a tile
-    constexpr int KV = D / 64;                   // 16-byte vectors of a key a lane (a quad covers 64 bytes)
+    constexpr int KV = D / 64;                   // vectors of a key a lane: its 16 of each 64 values
     constexpr int MT = D / 16;                   // m tiles of the transposed values
-    constexpr int VB = D >= 128 ? 16 : 8;        // bytes that a lane takes of a token's values at once
+    constexpr int VB = F == 8 && D >= 128 ? 16 : 8;   // values of a token that a lane takes at once
     constexpr int NV = D / (8 * VB);             // ... and how often
-    constexpr int NST = stages(D), TILES = tiles_of(D), TP = 16 * TILES, STEP = step_of(D);
+    constexpr int NST = stages(F, D), TILES = tiles_of(D), TP = 16 * TILES, STEP = step_of(D);
+    constexpr int TOK = D * F / 8;               // bytes of a token
+    constexpr int SECOND = 16 * TOK == 512 ? 64 : 0;  // what the swizzle adds in a second tile that begins in the middle of 1024 bytes
+    constexpr float WX = w_exp(F);
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ uint64_t bars[WARPS][NST];
     __shared__ int s_abort;
@@ -207,7 +236,8 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     __shared__ float2 s_row[R];
     __shared__ RowSum s_sum[WARPS][R], s_join[R];    // of each warp, and of all of them
     __shared__ float s_wfac[WARPS][R];               // factors of the warps' outputs in the join
-    __shared__ float s_ks[MAX_PAGES], s_vs[MAX_PAGES];
+    __shared__ float s_ks[F == 8 ? MAX_PAGES : 1], s_vs[F == 8 ? MAX_PAGES : 1];
+    __shared__ float s_qs[F == 4 ? R : 1][KV];       // sums of a row's 64s of q
     __shared__ int s_page[MAX_PAGES];
     __shared__ long long s_warp[WARPS], s_first;
     __shared__ int s_seq;
@@ -260,24 +290,26 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     }
     __syncthreads();
 
-    // A warp's ring: stages of a pair of tiles' keys, then their values.
-    constexpr int STAGE = TILES * tile_bytes(D);
+    // A warp's ring: stages of a pair of tiles' keys, then their values.  (4 bits: after all rings, in the same way,
+    // scales and biases.)
+    constexpr int STAGE = TILES * tile_bytes(F, D), AFFINE = TILES * affine_bytes(F, D);
     uint8_t *mine = ring + warp * NST * STAGE;
+    uint8_t *const mine_affine = ring + WARPS * NST * STAGE + warp * NST * AFFINE;
     uint64_t *bar = bars[warp];
     volatile int *abort = &s_abort;
     const bool single = TILES == 2 && BL == 4;   // pages of one tile only: a stage's tiles come from two
     uint32_t fit = 0, it = 0;                    // pairs fetched and taken, over all items
     // Offsets of this lane's reads in a stage: keys of token order(lr) (+ 8, + 16, + 24), values of four tokens of a tile.
     int k_at[KV][2], v_at[NV][4];
-    const int tok[2] = {order<D>(2 * lc), order<D>(2 * lc + 1)};
+    const int tok[2] = {order<F, D>(2 * lc), order<F, D>(2 * lc + 1)};
 #pragma unroll
     for (int v = 0; v < KV; ++v)
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) k_at[v][nb] = swizzled((order<D>(lr) + 8 * nb) * D + 64 * v + 16 * lc);
+        for (int nb = 0; nb < 2; ++nb) k_at[v][nb] = swizzled((order<F, D>(lr) + 8 * nb) * TOK + 8 * F * v + 2 * F * lc);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v_at[v][k] = swizzled((tok[k & 1] + 8 * (k >> 1)) * D + v * 8 * VB + VB * lr) + STAGE / 2;
+        for (int k = 0; k < 4; ++k) v_at[v][k] = swizzled((tok[k & 1] + 8 * (k >> 1)) * TOK + (v * 8 * VB + VB * lr) * F / 8) + STAGE / 2;
 
     int seq = s_seq;
     long long seq_at = s_first;                  // the sequence's first step on the line
@@ -317,22 +349,30 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             }
         }
         // Tokens [c0, c1): their pages, the first stages under way, and their scales (of the values' the logarithm).
-        const int from = P.window ? max(0, first + i0 - P.window + 1) & ~31 : 0;
+        const int any_from = P.window ? max(0, first + i0 - P.window + 1) : 0, from = any_from & ~31;   // (the first token that any of them sees)
         int c0 = max(t_begin, from), c1 = c0, pg0 = 0, npages = 0, ft = 0;
         auto fetch = [&](int t) {                // (the warp's first lane)
             if (t >= c1) return;
             const uint32_t stage = fit++ % NST;
             if (P.stall && fit == 1) return;
             const int p0 = s_page[(t >> BL) - pg0], p1 = single && t + 16 < c1 ? s_page[(t >> BL) + 1 - pg0] : -1;
-            mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : TILES) : 0) + (p1 >= 0 ? 1 : 0)) * tile_bytes(D));
+            mbar_arrive_tx(&bar[stage], (uint32_t)((p0 >= 0 ? (single ? 1 : TILES) : 0) + (p1 >= 0 ? 1 : 0)) * (tile_bytes(F, D) + affine_bytes(F, D)));
             uint8_t *dst = mine + stage * STAGE;
-            auto copy = [&](int page, int at, uint8_t *to) {
-                const int row = (int)((((((long long)page * H + h) << BL) + (at & BM)) * D) >> 7);
+            auto copy = [&](int page, int at, int tile) {
+                const long long token = (((long long)page * H + h) << BL) + (at & BM);
+                const int row = (int)((token * TOK) >> 7);
+                uint8_t *to = dst + tile * 16 * TOK;
                 tma_2d(to, &P.tm_k, 0, row, &bar[stage]);
                 tma_2d(to + STAGE / 2, &P.tm_v, 0, row, &bar[stage]);
+                if constexpr (F == 4) {
+                    uint8_t *pairs = mine_affine + stage * AFFINE + tile * D;
+                    const uint32_t bytes = (single ? 1 : TILES) * D;
+                    bulk_copy(pairs, P.k_affine + token * KV, bytes, &bar[stage]);
+                    bulk_copy(pairs + AFFINE / 2, P.v_affine + token * KV, bytes, &bar[stage]);
+                }
             };
-            if (p0 >= 0) copy(p0, t, dst);
-            if (p1 >= 0) copy(p1, t + 16, dst + 16 * D);
+            if (p0 >= 0) copy(p0, t, 0);
+            if (p1 >= 0) copy(p1, t + 16, 1);
         };
         auto open_chunk = [&]() {
             c1 = min(c0 + CHUNK_TOKENS, t_end);
@@ -350,7 +390,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             ft = *abort ? NO_TOKEN : c0 + TP * warp;
             for (int i = 0; i < NST - 1; ++i, ft += STEP)
                 if (lane == 0) fetch(ft);
-            for (int i = tid; i < npages; i += THREADS) {
+            for (int i = tid; F == 8 && i < npages; i += THREADS) {
                 const long long ph = (long long)s_page[i] * H + h;
                 s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
                 s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
@@ -360,19 +400,30 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < R / WARPS; ++k) {
             const int r = warp + k * WARPS;
-            float m = 0.f, sum = 0.f;
+            float m = 0.f, sum[F == 8 ? 1 : KV] = {};
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) m = fmaxf(m, fabsf(qx[k][e]));
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
             const float f = row_factor(m);
+            // (4 bits: times 2^8, and of odd dimensions 2^4, whose codes stand 2^4 higher; the eight of a word in the
+            // order in which its codes come.)
+            constexpr float Q = F == 4 ? 256.f : 1.f;
+            const int at4 = (lane & ~7) | (lane & 3) << 1 | (lane >> 2 & 1);
+            const float odd = lane & 1 ? 0.0625f : 1.f;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
-                const __half x = __float2half_rn(qx[k][e] * f);
-                sq[r][e * 32 + lane] = x;
-                sum += __half2float(x);
+                const __half x = F == 4 ? __float2half_rn(qx[k][e] * f * (Q * odd)) : __float2half_rn(qx[k][e] * f);
+                sq[r][e * 32 + (F == 4 ? at4 : lane)] = x;
+                sum[F == 4 ? e / 2 : 0] += F == 4 ? __half2float(x) * (1.f / odd) : __half2float(x);
             }
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            if (lane == 0) s_row[r] = make_float2(P.scale * 1.44269504088896340736f / f * (1.f / TINY), sum * (-128.f * TINY));
+#pragma unroll
+            for (int g = 0; g < (F == 8 ? 1 : KV); ++g)
+                for (int o = 16; o > 0; o >>= 1) sum[g] += __shfl_xor_sync(~0u, sum[g], o);
+            if (lane == 0) {
+                s_row[r] = make_float2(P.scale * 1.44269504088896340736f / f * (1.f / (Q * TINY)), sum[0] * (-128.f * TINY));
+#pragma unroll
+                for (int g = 0; F == 4 && g < KV; ++g) s_qs[r][g] = sum[g] * TINY;
+            }
         }
         __syncthreads();
 
@@ -388,13 +439,16 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qa[u][v][i] = q_at(u, v, i);
         }
-        float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24
+        float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24 (8 bits)
+        float qs[NT][KV];                            // 2^-24 sums of q's 64s (4 bits)
         int see_from[NT], see_to[NT];                // tokens that rows lr (+ 8) see
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             const int r = min(lr + 8 * u, rows - 1);   // (rows past the tile's end are computed, never stored)
             rowf[u] = s_row[r].x;
             off[u] = s_row[r].y;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) qs[u][v] = F == 4 ? s_qs[r][v] : 0.f;
             const int pos = first + (r0 + r) / G;
             see_to[u] = P.causal ? min(end, pos + 1) : end;
             see_from[u] = P.window ? pos - P.window + 1 : 0;
@@ -407,10 +461,13 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 
         float o[MT][NT][4];
         float m[NT], d[NT], l[NT];
+        float ob[NT][KV];                            // 4 bits: sums of w times the biases, rows lr (+ 8), this lane's tokens
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             m[u] = d[u] = -INFINITY;
             l[u] = 0.f;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) ob[u][v] = 0.f;
 #pragma unroll
             for (int p = 0; p < MT; ++p)
 #pragma unroll
@@ -442,31 +499,99 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                 for (int nb = 0; nb < 2 * TILES; ++nb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
+                    for (int e = 0; e < 4; ++e) sc[nb][e] = F == 8 && e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
+                auto q_pair = [&](int u, int v, int i) {
+                    if constexpr (NT == 1) if (u > 0) return make_uint2(0u, 0u);
+                    return Q_REGS ? qa[u < NT ? u : 0][Q_REGS ? v : 0][i] : q_at(u, v, i);
+                };
+                const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(mine_affine + (it % NST) * AFFINE);
+                if constexpr (F == 8) {
 #pragma unroll
-                for (int v = 0; v < KV; ++v) {
-                    uint32_t kw[2 * TILES][4];
+                    for (int v = 0; v < KV; ++v) {
+                        uint32_t kw[2 * TILES][4];
 #pragma unroll
-                    for (int nb = 0; nb < 2 * TILES; ++nb) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
-                        kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
-                        kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
+                        for (int nb = 0; nb < 2 * TILES; ++nb) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * TOK + k_at[v][nb & 1]);
+                            kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
+                            kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint2 qa0 = q_pair(0, v, i), qa1 = q_pair(1, v, i);
+#pragma unroll
+                            for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
+                        }
                     }
+                } else {
+                    // 64 dimensions at a time: their products with the codes, times the token's scale, and the sum of
+                    // q times its bias.
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
-                        uint2 qa1 = make_uint2(0u, 0u);
-                        if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
+                    for (int v = 0; v < KV; ++v) {
+                        float raw[2 * TILES][4];
+                        uint32_t kw[2 * TILES][2];
 #pragma unroll
-                        for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
+                        for (int nb = 0; nb < 2 * TILES; ++nb) {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(tiles + (nb >> 1) * 16 * TOK + (k_at[v][nb & 1] ^ (nb >> 1) * SECOND));
+                            kw[nb][0] = x.x, kw[nb][1] = x.y;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) raw[nb][e] = 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint2 qa0 = q_pair(0, v, i), qa1 = q_pair(1, v, i);
+#pragma unroll
+                            for (int nb = 0; nb < 2 * TILES; ++nb) {
+                                const uint32_t w = kw[nb][i >> 1] >> (8 * (i & 1));
+                                mma_f16(raw[nb], qa0.x, qa1.x, qa0.y, qa1.y, w & 0x000F000Fu, w & 0x00F000F0u);
+                            }
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < 2 * TILES; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t a = pairs[(8 * nb + tok[e]) * KV + v];
+#pragma unroll
+                                for (int u = 0; u < NT; ++u)
+                                    sc[nb][2 * u + e] = fmaf(raw[nb][2 * u + e], __uint_as_float(a << 16),
+                                                             fmaf(__uint_as_float(a & 0xFFFF0000u), qs[u][v], sc[nb][2 * u + e]));
+                            }
                     }
                 }
                 // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
                 const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
                 float ks[TILES], vs[TILES];
 #pragma unroll
-                for (int h = 0; h < TILES; ++h) ks[h] = s_ks[pi[h]], vs[h] = s_vs[pi[h]];
-                uint32_t pb[NT][2 * TILES];
+                for (int h = 0; h < TILES; ++h) ks[h] = F == 8 ? s_ks[pi[h]] : 1.f, vs[h] = F == 8 ? s_vs[pi[h]] : 0.f;
+                // 4 bits: scale and bias of the values of token t + 8 nb + tok[e] (0 where no row sees it: whatever may stand
+                // there, infinities and NaN too, meets weights of 0); and of a tile's tokens, what no value passes by more
+                // than a factor of 2.
+                const uint32_t *const v_pairs = pairs + AFFINE / 8;
+                auto v_pair = [&](int nb, int e, int g) {
+                    const uint32_t a = v_pairs[(8 * nb + tok[e]) * KV + g];
+                    const int j = t + 8 * nb + tok[e];
+                    return full || (j >= any_from && j < to) ? a : 0u;
+                };
+                if constexpr (F == 4) {
+                    float most[TILES];
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) {
+                        most[h] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int g = 0; g < KV; ++g) {
+                                const uint32_t a = v_pair(2 * h + (i >> 1), i & 1, g);
+                                most[h] = fmaxf(most[h], fmaxf(fabsf(__uint_as_float(a << 16)) * 15.f, fabsf(__uint_as_float(a & 0xFFFF0000u))));
+                            }
+                    }
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+                        for (int h = 0; h < TILES; ++h) most[h] = fmaxf(most[h], __shfl_xor_sync(~0u, most[h], o));
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) vs[h] = on[h] ? log2_fast(most[h]) : -INFINITY;
+                }
+                uint32_t pb[F == 8 ? 1 : KV][NT][2 * TILES];     // (4 bits: of each 64 dimensions)
                 bool grew = false;
                 float mt[NT], mm[NT], dt[NT];
 #pragma unroll
@@ -522,6 +647,8 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                         // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
                         const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
 #pragma unroll
+                        for (int v = 0; F == 4 && v < KV; ++v) ob[u][v] *= a;
+#pragma unroll
                         for (int p = 0; p < MT; ++p) {
                             o[p][u][0] *= a0;
                             o[p][u][1] *= a1;
@@ -534,12 +661,22 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 for (int u = 0; u < NT; ++u) {
 #pragma unroll
                     for (int h = 0; h < TILES; ++h) {
-                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf(vs[h] + (W_EXP - d[u]), 115.f));
+                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf((F == 8 ? vs[h] : 0.f) + (WX - d[u]), 115.f));
 #pragma unroll
                         for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
                             const float p0 = exp2_fast(sc[nb][2 * u] - mm[u]), p1 = exp2_fast(sc[nb][2 * u + 1] - mm[u]);
                             l[u] += p0 + p1;
-                            pb[u][nb] = pack_half(p0 * f, p1 * f);
+                            if constexpr (F == 8) {
+                                pb[0][u][nb] = pack_half(p0 * f, p1 * f);
+                            } else {
+                                const float w0 = p0 * f, w1 = p1 * f;
+#pragma unroll
+                                for (int g = 0; g < KV; ++g) {
+                                    const uint32_t a = v_pair(nb, 0, g), b = v_pair(nb, 1, g);
+                                    pb[g][u][nb] = pack_half(w0 * __uint_as_float(a << 16), w1 * __uint_as_float(b << 16));
+                                    if (on[h]) ob[u][g] = fmaf(w0, __uint_as_float(a & 0xFFFF0000u), fmaf(w1, __uint_as_float(b & 0xFFFF0000u), ob[u][g]));
+                                }
+                            }
                         }
                     }
                 }
@@ -547,33 +684,52 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                 for (int h = 0; h < TILES; ++h) {
                     if (!on[h]) continue;                // (its codes were not fetched)
+                    if constexpr (F == 8) {
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        uint32_t a[4][VB / 4];
+                        for (int v = 0; v < NV; ++v) {
+                            uint32_t a[4][VB / 4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
-                            if constexpr (VB == 16) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                                a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                                a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
-                            } else {
-                                const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                                a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                            for (int k = 0; k < 4; ++k) {
+                                const uint8_t *src = tiles + h * 16 * TOK + v_at[v][k];
+                                if constexpr (VB == 16) {
+                                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                                    a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                                    a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
+                                } else {
+                                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                                    a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < VB / 4; ++i) {
+                                // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
+                                const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
+                                const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
+                                const int p = v * VB / 2 + 2 * i;
+                                const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
+                                const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
+#pragma unroll
+                                for (int u = 0; u < NT; ++u) {
+                                    mma_f16(o[p][u], f0, f1, f2, f3, pb[0][u][2 * h], pb[0][u][2 * h + 1]);
+                                    mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[0][u][2 * h], pb[0][u][2 * h + 1]);
+                                }
                             }
                         }
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < VB / 4; ++i) {
-                            // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
-                            const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
-                            const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
-                            const int p = v * VB / 2 + 2 * i;
-                            const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
-                            const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
+                        for (int v = 0; v < NV; ++v) {
+                            uint32_t a[4];
 #pragma unroll
-                            for (int u = 0; u < NT; ++u) {
-                                mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
-                                mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
+                            for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const uint32_t *>(tiles + h * 16 * TOK + (v_at[v][k] ^ h * SECOND));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                // Codes of d + 2 i and d + 2 i + 1 of tokens tok[0], tok[1]; and of the two eight further.
+                                const uint32_t sel = i < 2 ? 0x5410u : 0x7632u;
+                                const uint32_t x = prmt(a[0], a[1], sel) >> (8 * (i & 1)), y = prmt(a[2], a[3], sel) >> (8 * (i & 1));
+#pragma unroll
+                                for (int u = 0; u < NT; ++u)
+                                    mma_f16(o[4 * v + i][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u,
+                                            pb[v][u][2 * h], pb[v][u][2 * h + 1]);
                             }
                         }
                     }
@@ -591,15 +747,31 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             l[u] += __shfl_xor_sync(~0u, l[u], 2);
             if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], d[u], l[u], 0.f};
         }
+        if constexpr (F == 4) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int v = 0; v < KV; ++v) {
+                    ob[u][v] += __shfl_xor_sync(~0u, ob[u][v], 1);
+                    ob[u][v] += __shfl_xor_sync(~0u, ob[u][v], 2);
+                }
+        }
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float *dst = out_of(warp, 2 * lc + e + 8 * u);
+                float b[KV];
+#pragma unroll
+                for (int v = 0; F == 4 && v < KV; ++v) b[v] = __shfl_sync(~0u, ob[u][v], 8 * lc + 4 * e);
 #pragma unroll
                 for (int p = 0; p < MT; ++p) {
                     const int d = p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2));
-                    *reinterpret_cast<float2 *>(dst + d) = make_float2(o[p][u][e], o[p][u][2 + e]);
+                    if constexpr (F == 4)        // (the odd dimensions' codes stood 2^4 higher)
+                        *reinterpret_cast<float2 *>(dst + d) =
+                            make_float2(fmaf(o[p][u][e], 1.f / TINY, b[p / 4]), fmaf(o[p][u][2 + e], 0.0625f / TINY, b[p / 4]));
+                    else
+                        *reinterpret_cast<float2 *>(dst + d) = make_float2(o[p][u][e], o[p][u][2 + e]);
                 }
             }
         __syncthreads();
@@ -635,7 +807,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         const int c_first = cta_of(item_at), parts = cta_of(item_at + sw.steps - 1) - c_first + 1;
         if (parts == 1) {
             for (int v = 4 * tid; v < rows * D; v += 4 * THREADS)
-                store4(v / D, v % D, joined4(v / D, v % D), out_factor(s_join[v / D]));
+                store4(v / D, v % D, joined4(v / D, v % D), out_factor<F>(s_join[v / D]));
         } else {
             // A CTA's first item's part is in its slot 0, that of a later one (its last) in slot 1.
             const int slot0 = 2 * c_first + (item_at > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
@@ -692,7 +864,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                             y.z = fmaf(x[k].z, f, y.z), y.w = fmaf(x[k].w, f, y.w);
                         }
                     }
-                    store4(r, v % D, y, out_factor(s_join[r]));
+                    store4(r, v % D, y, out_factor<F>(s_join[r]));
                 }
             }
         }

@@ -343,7 +343,7 @@ int tfq::check_kv(const tf_kv *kv) {
     return TF_OK;
 }
 
-int tfq::check_batch(const tf_kv *kv, const tf_kv_batch *b) {
+int tfq::check_batch(int block, const tf_kv_batch *b) {
     if (!b) return fail_message(TF_EINVAL_PTR, "NULL batch");
     if (!b->kv_len || !b->table) return fail_message(TF_EINVAL_PTR, "NULL kv_len or table");
     if (!aligned(b->kv_len, 4) || !aligned(b->table, 4) || !aligned(b->row_start, 4) || !aligned(b->slots, 4))
@@ -354,7 +354,7 @@ int tfq::check_batch(const tf_kv *kv, const tf_kv_batch *b) {
     if (!b->row_start && (long long)b->n_seqs * b->max_rows != b->rows)
         return fail_message(TF_EINVAL_ROWS, "without row_start, rows must be n_seqs * max_rows");
     if (b->max_len < 1 || b->max_len > (1 << 20)) return fail_message(TF_EINVAL_SIZE, "max_len must be in [1, 2^20]");
-    if (b->table_stride < (b->max_len + kv->block - 1) / kv->block)
+    if (b->table_stride < (b->max_len + block - 1) / block)
         return fail_message(TF_EINVAL_STRIDE, "table_stride holds fewer pages than max_len needs");
     return TF_OK;
 }
@@ -363,7 +363,7 @@ extern "C" int tf_kv_append(const tf_kv *kv, const tf_kv_batch *batch, const voi
                             int64_t v_stride, void *stream) {
     fail_message(TF_OK, "");
     int rc = check_kv(kv);
-    if (!rc) rc = check_batch(kv, batch);
+    if (!rc) rc = check_batch(kv->block, batch);
     if (rc) return rc;
     if (kv->f32 != 0 && kv->f32 != 1) return fail_message(TF_EINVAL_FLAGS, "f32 must be 0 or 1");
     if (!kv->open_k || !kv->open_v || !kv->open_max || !aligned(kv->open_k, 16) || !aligned(kv->open_v, 16) ||
@@ -401,7 +401,7 @@ extern "C" int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out
     fail_message(TF_OK, "");
     if (flags & ~TF_OUT_BF16) return fail_message(TF_EINVAL_FLAGS, "tf_kv_read takes TF_OUT_BF16 only");
     int rc = check_kv(kv);
-    if (!rc) rc = check_batch(kv, batch);
+    if (!rc) rc = check_batch(kv->block, batch);
     if (rc) return rc;
     const int es = flags & TF_OUT_BF16 ? 2 : 4;
     if ((!k_out && !v_out) || !aligned(k_out, es) || !aligned(v_out, es))

@@ -3,14 +3,15 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "../../include/tfdecode.h"
+#include "../../include/tfserve.h"
 #include "internal.h"
 
 namespace tfq {
 
-// Host checks of the structs (kv.cu): TF_OK or a status with the message recorded.
+// Host checks of the structs (kv.cu, kv4.cu): TF_OK or a status with the message recorded.
 int check_kv(const tf_kv *kv);
-int check_batch(const tf_kv *kv, const tf_kv_batch *b);
+int check_kv4(const tf_kv4 *kv);
+int check_batch(int block, const tf_kv_batch *b);
 
 // A sequence's rows and tokens: rows row0 .. row0 + n - 1 are its tokens end - n .. end - 1.
 struct SeqRows {
