@@ -217,6 +217,344 @@ __device__ __forceinline__ float row_factor(float amax) {
     return __uint_as_float((e >= 253 ? 1u : 254u - e) << 23);
 }
 
+// Two fp32 numbers at a time.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 two(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 of_two(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Products that begin at 0.
+__device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of a warp's 8 x 8 numbers of 16 bits (lane 4 r + c holds row r's 2 c and 2 c + 1).
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// The larger magnitudes of two pairs of bf16 numbers (signs mean nothing then; NaN is passed over).
+__device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// What a warp of the rows kernel holds of a tile of 8 NT rows, over the 4-bit cache, and how it takes 16 or 32 tokens.
+//
+//     s_rj = f_r sum_g (scale_jg (q_rg . c_jg) + bias_jg sum(q_rg))        g: groups of 64 dimensions
+//     p_rj = 2^(s_rj - m_r),  l_r = sum_j p_rj,  out_rg = sum_j p_rj (scale_jg c'_jg + bias_jg) / l_r
+// Codes are bits 0 to 3 or 4 to 7 of a half word, as fp16 subnormals c 2^-24 and c 2^-20: one mask makes two of them
+// (the 2^4 goes into q for the first product and into the output for the second).
+// First product: the tokens are its 16 rows and the rows of q its 8 columns, so that no part of it is idle with up to 8
+// rows; a lane gets the scores of two tokens a tile and two rows, two numbers to an instruction.  The sums with the
+// biases are a product of bf16: the cache's pairs (scale, bias) as they lie with (0, a third of sum(q)'s bits).
+// Second product: w_rj scale_jg in fp16 (w as over 8 bits: 2^18 p 2^-d, d the running maximum of s - m + log2(15 scale
+// or bias)), transposed in the warp, with the codes' tokens put side by side by byte permutes; the biases' part in fp32.
+// The maxima m and d are joined over the warp's lanes only where a lane finds one passed by more than SLACK4.
+//
+// Bound by the issue of instructions and the latency between them: 48 x 8000 tokens of 8 heads of 128, 32 query heads, 71 us, 1 x 131000
+// tokens 44 us (with the rows of q as the first product's 16 rows, maxima joined at every step and the biases' sums in fp32:
+// 84 and 53 us).
+constexpr float SLACK4 = 1.f;            // in powers of two (w stays below fp16's largest: 2^18 / 15 times 2^SLACK4)
+template <int D, int NT>
+struct Rows4 {
+    static constexpr int KV = D / 64, MT = D / 16, TILES = tiles_of(D), NB = KV == 4 ? 2 : 1;
+    static constexpr bool Q_REGS = D < 256 || NT == 1;
+    static constexpr int TOK = D / 2;
+    static constexpr int SECOND = 16 * TOK == 512 ? 64 : 0;   // what the swizzle adds in a second tile that begins in the middle of 1024 bytes
+
+    uint2 q[NT][Q_REGS ? 4 * KV : 1];    // k step (v, i) of row lr (+ 8): d = 64 v + 16 lc + 4 i + {0, 1 | 2, 3} as stored
+    uint32_t qb[NT][NB][2];              // of sum(q): (0, a part), by the lane's place among the pairs
+    F2 rowf[NT], mm[NT], f[NT], l[NT];   // of rows 2 lc, 2 lc + 1 (+ 8): factor of a score, base of m, 2^18 2^-d, sum
+    F2 ob[NT][KV];                       // sums of w times the biases, this lane's tokens
+    float m[NT][2], d[NT][2];
+    float o[MT][NT][4];
+
+    template <typename Q, typename S>
+    __device__ __forceinline__ void begin(const Q &sq, const float2 *s_row, const S &s_qs, int lr, int lc, int rows) {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            if constexpr (Q_REGS) {
+#pragma unroll
+                for (int i = 0; i < 4 * KV; ++i) q[u][i] = *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * (i >> 2) + 16 * lc + 4 * (i & 3)]);
+            }
+            // Parts of 8 bits each of the sum of group lc % KV.
+            const float x = s_qs[lr + 8 * u][lc & (KV - 1)];
+            auto top = [](float y) { return __float_as_uint(y) & 0xFFFF0000u; };
+            const uint32_t p0 = top(x), p1 = top(x - __uint_as_float(p0)), p2 = top(x - __uint_as_float(p0) - __uint_as_float(p1));
+            const int k = lc / KV;
+            auto part = [&](int i) { return i == 0 ? p0 : i == 1 ? p1 : i == 2 ? p2 : 0u; };
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) qb[u][b][e] = part(k + (2 * b + e) * (4 / KV));
+            rowf[u] = two(s_row[min(2 * lc + 8 * u, rows - 1)].x, s_row[min(2 * lc + 1 + 8 * u, rows - 1)].x);
+            mm[u] = f[u] = l[u] = 0;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) ob[u][v] = 0;
+            m[u][0] = m[u][1] = d[u][0] = d[u][1] = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < MT; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[p][u][e] = 0.f;
+        }
+    }
+
+    // Tokens t + 16 h + 8 nb + ..: their codes in `tiles` (at k_at, and v_at), scales and biases in k_pairs and v_pairs.
+    // full: every row sees every token.  Else seen(i) is whether token t + i is there and any row sees it, and
+    // sees(r, i) whether row r does.
+    template <typename Q, typename Seen, typename Sees>
+    __device__ __forceinline__ void step(const uint8_t *tiles, const uint32_t *k_pairs, const uint32_t *v_pairs, const int (&k_at)[KV][2],
+                                         const int (&v_at)[KV][4], int mine, const Q &sq, int lr, int lc, bool full, Seen seen, Sees sees) {
+        // Scores: tokens t + 8 nb + mine (mine: order(lr)) of rows 2 lc, 2 lc + 1 (+ 8).
+        uint32_t pair[2 * TILES][KV];
+        auto load_pairs = [&](const uint32_t *src) {
+#pragma unroll
+            for (int nb = 0; nb < 2 * TILES; ++nb) {
+                const uint32_t *at = src + (8 * nb + mine) * KV;
+                if constexpr (KV == 1) pair[nb][0] = *at;
+                if constexpr (KV == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                    pair[nb][0] = x.x, pair[nb][1] = x.y;
+                }
+                if constexpr (KV == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                    pair[nb][0] = x.x, pair[nb][1] = x.y, pair[nb][2] = x.z, pair[nb][3] = x.w;
+                }
+            }
+        };
+        load_pairs(k_pairs);
+        F2 sc[2 * TILES][NT];
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) {
+            uint32_t a[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t(&x)[KV] = pair[2 * h + e];
+                if constexpr (KV == 1) a[e] = x[0];
+                if constexpr (KV == 2) a[e] = lc & 1 ? x[1] : x[0];
+                if constexpr (KV == 4) a[e] = lc & 2 ? (lc & 1 ? x[3] : x[2]) : (lc & 1 ? x[1] : x[0]);
+            }
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                float c[4];
+                mma_bf16_0(c, a[0], a[1], KV == 1 ? 0u : a[0], KV == 1 ? 0u : a[1], qb[u][0][0], qb[u][0][1]);
+                if constexpr (NB == 2) mma_bf16(c, a[0], a[1], a[0], a[1], qb[u][NB - 1][0], qb[u][NB - 1][1]);
+                sc[2 * h][u] = two(c[0], c[1]);
+                sc[2 * h + 1][u] = two(c[2], c[3]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < KV; ++v) {
+            float raw[TILES][NT][4];
+            uint2 x[2 * TILES];
+#pragma unroll
+            for (int nb = 0; nb < 2 * TILES; ++nb) x[nb] = *reinterpret_cast<const uint2 *>(tiles + (nb >> 1) * 16 * TOK + (k_at[v][nb & 1] ^ (nb >> 1) * SECOND));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < TILES; ++h) {
+                    const uint32_t w0 = (i >> 1 ? x[2 * h].y : x[2 * h].x) >> (8 * (i & 1)), w1 = (i >> 1 ? x[2 * h + 1].y : x[2 * h + 1].x) >> (8 * (i & 1));
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        const uint2 b = Q_REGS ? q[u][Q_REGS ? 4 * v + i : 0] : *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]);
+                        if (i == 0)
+                            mma_f16_0(raw[h][u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
+                        else
+                            mma_f16(raw[h][u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
+                    }
+                }
+#pragma unroll
+            for (int nb = 0; nb < 2 * TILES; ++nb) {
+                const float s = __uint_as_float(pair[nb][v] << 16);
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+                    sc[nb][u] = fma2(two(raw[nb >> 1][u][2 * (nb & 1)], raw[nb >> 1][u][2 * (nb & 1) + 1]), two(s, s), sc[nb][u]);
+            }
+        }
+        load_pairs(v_pairs);
+#pragma unroll
+        for (int nb = 0; nb < 2 * TILES; ++nb)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) sc[nb][u] = mul2(sc[nb][u], rowf[u]);     // (rounded here: the largest less the maximum is 0)
+        if (!full) {
+#pragma unroll
+            for (int nb = 0; nb < 2 * TILES; ++nb) {
+                const int i = 8 * nb + mine;
+                // (Where no row sees a token its values' pairs are 0: whatever stands there, infinities and NaN too, meets
+                // weights of 0.)
+                if (!seen(i))
+#pragma unroll
+                    for (int v = 0; v < KV; ++v) pair[nb][v] = 0;
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const float2 x = of_two(sc[nb][u]);
+                    sc[nb][u] = two(seen(i) && sees(2 * lc + 8 * u, i) ? x.x : -INFINITY, seen(i) && sees(2 * lc + 1 + 8 * u, i) ? x.y : -INFINITY);
+                }
+            }
+        }
+        // Of this lane's tokens of each tile: the logarithm of what no value passes by more than a factor of 2, and the
+        // largest scores.
+        float vs[TILES], top[TILES][NT][2];
+        bool grew = false;
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) most = larger_bf16x2(most, larger_bf16x2(pair[2 * h][v], pair[2 * h + 1][v]));
+            vs[h] = log2_fast(fmaxf(fabsf(__uint_as_float(most << 16)) * 15.f, fabsf(__uint_as_float(most & 0xFFFF0000u))));
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float2 x = of_two(sc[2 * h][u]), y = of_two(sc[2 * h + 1][u]), b = of_two(mm[u]);
+                const float t0 = top[h][u][0] = fmaxf(x.x, y.x), t1 = top[h][u][1] = fmaxf(x.y, y.y);
+                grew |= t0 > m[u][0] + SLACK4 || t1 > m[u][1] + SLACK4 || (t0 - b.x) + vs[h] > d[u][0] + SLACK4 || (t1 - b.y) + vs[h] > d[u][1] + SLACK4;
+            }
+        }
+        if (__any_sync(~0u, grew)) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                float base[2], scale[2], fac[2], fl[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mt = m[u][e], dt = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) mt = fmaxf(mt, top[h][u][e]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, x));
+                    base[e] = base_of(mt);
+#pragma unroll
+                    for (int h = 0; h < TILES; ++h) dt = fmaxf(dt, (top[h][u][e] - base[e]) + vs[h]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) dt = fmaxf(dt, __shfl_xor_sync(~0u, dt, x));
+                    const float d0 = d[u][e] + (m[u][e] - base[e]);
+                    fl[e] = m[u][e] == -INFINITY ? 1.f : exp2_fast(m[u][e] - mt);
+                    m[u][e] = mt;
+                    d[u][e] = fmaxf(d0, dt);
+                    fac[e] = exp2_fast(d0 - base_of(d[u][e]));
+                    scale[e] = d[u][e] == -INFINITY ? 0.f : exp2_fast(fminf(w_exp(4) - d[u][e], 115.f));
+                }
+                mm[u] = two(base[0], base[1]);
+                f[u] = two(scale[0], scale[1]);
+                l[u] = mul2(l[u], two(fl[0], fl[1]));
+                const F2 a = two(fac[0], fac[1]);
+#pragma unroll
+                for (int v = 0; v < KV; ++v) ob[u][v] = mul2(ob[u][v], a);
+#pragma unroll
+                for (int p = 0; p < MT; ++p) {
+                    const float2 x = of_two(mul2(two(o[p][u][0], o[p][u][1]), a)), y = of_two(mul2(two(o[p][u][2], o[p][u][3]), a));
+                    o[p][u][0] = x.x, o[p][u][1] = x.y, o[p][u][2] = y.x, o[p][u][3] = y.y;
+                }
+            }
+        }
+        uint32_t pb[KV][NT][2 * TILES];
+#pragma unroll
+        for (int nb = 0; nb < 2 * TILES; ++nb) {
+            F2 w[NT];
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const float2 x = of_two(sc[nb][u]), b = of_two(mm[u]);
+                const F2 p = two(exp2_fast(x.x - b.x), exp2_fast(x.y - b.y));
+                l[u] = add2(l[u], p);
+                w[u] = mul2(p, f[u]);
+            }
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                const float s = __uint_as_float(pair[nb][v] << 16), b = __uint_as_float(pair[nb][v] & 0xFFFF0000u);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const float2 x = of_two(mul2(w[u], two(s, s)));
+                    pb[v][u][nb] = transposed(pack_half(x.x, x.y));
+                    ob[u][v] = fma2(w[u], two(b, b), ob[u][v]);
+                }
+            }
+        }
+        // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 64 v + 8 lr + ...
+#pragma unroll
+        for (int h = 0; h < TILES; ++h)
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                uint32_t a[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const uint32_t *>(tiles + h * 16 * TOK + (v_at[v][k] ^ h * SECOND));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // Codes of d + 2 i and d + 2 i + 1 of tokens tok[0], tok[1]; and of the two eight further.
+                    const uint32_t sel = i < 2 ? 0x5410u : 0x7632u;
+                    const uint32_t x = prmt(a[0], a[1], sel) >> (8 * (i & 1)), y = prmt(a[2], a[3], sel) >> (8 * (i & 1));
+#pragma unroll
+                    for (int u = 0; u < NT; ++u)
+                        mma_f16(o[4 * v + i][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, pb[v][u][2 * h], pb[v][u][2 * h + 1]);
+                }
+            }
+    }
+
+    // The sums over the lanes' tokens: row sums by store(row, sum), the values of a row's dimensions dim, dim + 1 by put.
+    template <typename Store, typename Put>
+    __device__ __forceinline__ void end(int lr, int lc, Store store, Put put) {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            float2 b[KV], s = of_two(l[u]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) s.x += __shfl_xor_sync(~0u, s.x, x), s.y += __shfl_xor_sync(~0u, s.y, x);
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                b[v] = of_two(ob[u][v]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) b[v].x += __shfl_xor_sync(~0u, b[v].x, x), b[v].y += __shfl_xor_sync(~0u, b[v].y, x);
+            }
+            if (lr == 0) {
+                store(2 * lc + 8 * u, RowSum{m[u][0], d[u][0], s.x, 0.f});
+                store(2 * lc + 1 + 8 * u, RowSum{m[u][1], d[u][1], s.y, 0.f});
+            }
+            // (the odd dimensions' codes stood 2^4 higher)
+#pragma unroll
+            for (int p = 0; p < MT; ++p)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = e ? b[p / 4].y : b[p / 4].x;
+                    put(2 * lc + e + 8 * u, p / 4 * 64 + 8 * lr + 2 * (p % 4), make_float2(fmaf(o[p][u][e], 1.f / TINY, x), fmaf(o[p][u][2 + e], 0.0625f / TINY, x)));
+                }
+        }
+    }
+};
+
 // F: bits of a code (8 or 4).
 template <int F, int D, int NT>
 __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid_constant__ Params P) {
@@ -227,8 +565,6 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     constexpr int NV = D / (8 * VB);             // ... and how often
     constexpr int NST = stages(F, D), TILES = tiles_of(D), TP = 16 * TILES, STEP = step_of(D);
     constexpr int TOK = D * F / 8;               // bytes of a token
-    constexpr int SECOND = 16 * TOK == 512 ? 64 : 0;  // what the swizzle adds in a second tile that begins in the middle of 1024 bytes
-    constexpr float WX = w_exp(F);
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ uint64_t bars[WARPS][NST];
     __shared__ int s_abort;
@@ -238,6 +574,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     __shared__ float s_wfac[WARPS][R];               // factors of the warps' outputs in the join
     __shared__ float s_ks[F == 8 ? MAX_PAGES : 1], s_vs[F == 8 ? MAX_PAGES : 1];
     __shared__ float s_qs[F == 4 ? R : 1][KV];       // sums of a row's 64s of q
+    __shared__ int2 s_see[F == 4 ? R : 1];           // tokens that a row sees
     __shared__ int s_page[MAX_PAGES];
     __shared__ long long s_warp[WARPS], s_first;
     __shared__ int s_seq;
@@ -390,10 +727,12 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             ft = *abort ? NO_TOKEN : c0 + TP * warp;
             for (int i = 0; i < NST - 1; ++i, ft += STEP)
                 if (lane == 0) fetch(ft);
-            for (int i = tid; F == 8 && i < npages; i += THREADS) {
-                const long long ph = (long long)s_page[i] * H + h;
-                s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
-                s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
+            if constexpr (F == 8) {
+                for (int i = tid; i < npages; i += THREADS) {
+                    const long long ph = (long long)s_page[i] * H + h;
+                    s_ks[i] = s_page[i] < 0 ? 0.f : P.kv.k_scale[ph];
+                    s_vs[i] = s_page[i] < 0 ? -INFINITY : log2f(P.kv.v_scale[ph]);
+                }
             }
         };
         if (c0 < t_end) open_chunk();            // (the loads of q are on their way meanwhile)
@@ -423,6 +762,10 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 s_row[r] = make_float2(P.scale * 1.44269504088896340736f / f * (1.f / (Q * TINY)), sum[0] * (-128.f * TINY));
 #pragma unroll
                 for (int g = 0; F == 4 && g < KV; ++g) s_qs[r][g] = sum[g] * TINY;
+                if constexpr (F == 4) {
+                    const int pos = first + (r0 + min(r, rows - 1)) / G;
+                    s_see[r] = make_int2(P.window ? pos - P.window + 1 : 0, P.causal ? min(end, pos + 1) : end);
+                }
             }
         }
         __syncthreads();
@@ -431,7 +774,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         constexpr bool Q_REGS = D < 256;
         uint2 qa[NT][Q_REGS ? KV : 1][4];
         auto q_at = [&](int u, int v, int i) { return *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]); };
-        if constexpr (Q_REGS) {
+        if constexpr (F == 8 && Q_REGS) {
 #pragma unroll
             for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -439,16 +782,13 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qa[u][v][i] = q_at(u, v, i);
         }
-        float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24 (8 bits)
-        float qs[NT][KV];                            // 2^-24 sums of q's 64s (4 bits)
+        float rowf[NT], off[NT];                     // factor of a score; its start, -128 sum(q) 2^-24
         int see_from[NT], see_to[NT];                // tokens that rows lr (+ 8) see
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             const int r = min(lr + 8 * u, rows - 1);   // (rows past the tile's end are computed, never stored)
             rowf[u] = s_row[r].x;
             off[u] = s_row[r].y;
-#pragma unroll
-            for (int v = 0; v < KV; ++v) qs[u][v] = F == 4 ? s_qs[r][v] : 0.f;
             const int pos = first + (r0 + r) / G;
             see_to[u] = P.causal ? min(end, pos + 1) : end;
             see_from[u] = P.window ? pos - P.window + 1 : 0;
@@ -461,13 +801,12 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 
         float o[MT][NT][4];
         float m[NT], d[NT], l[NT];
-        float ob[NT][KV];                            // 4 bits: sums of w times the biases, rows lr (+ 8), this lane's tokens
+        Rows4<D, NT> rows4;                          // (4 bits: all of these, and q)
+        if constexpr (F == 4) rows4.begin(sq, s_row, s_qs, lr, lc, rows);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             m[u] = d[u] = -INFINITY;
             l[u] = 0.f;
-#pragma unroll
-            for (int v = 0; v < KV; ++v) ob[u][v] = 0.f;
 #pragma unroll
             for (int p = 0; p < MT; ++p)
 #pragma unroll
@@ -494,104 +833,45 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                     pi[h] = min(((t + 16 * h) >> BL) - pg0, npages - 1);
                     on[h] = s_page[pi[h]] >= 0 && !(h == 1 && single && t + 16 >= c1);
                 }
+                const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
+                if constexpr (F == 4) {
+                    const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(mine_affine + (it % NST) * AFFINE);
+                    rows4.step(
+                        tiles, pairs, pairs + AFFINE / 8, k_at, v_at, order<F, D>(lr), sq, lr, lc, full,
+                        [&](int i) { return on[i < 16 ? 0 : TILES - 1] && t + i >= any_from && t + i < to; },
+                        [&](int r, int i) { return t + i >= s_see[r].x && t + i < s_see[r].y; });
+                    __syncwarp();                    // (every lane has read the stage that is filled next)
+                    continue;
+                }
                 // Scores of the tiles' tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
                 float sc[2 * TILES][4];
 #pragma unroll
                 for (int nb = 0; nb < 2 * TILES; ++nb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nb][e] = F == 8 && e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
-                auto q_pair = [&](int u, int v, int i) {
-                    if constexpr (NT == 1) if (u > 0) return make_uint2(0u, 0u);
-                    return Q_REGS ? qa[u < NT ? u : 0][Q_REGS ? v : 0][i] : q_at(u, v, i);
-                };
-                const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(mine_affine + (it % NST) * AFFINE);
-                if constexpr (F == 8) {
+                    for (int e = 0; e < 4; ++e) sc[nb][e] = e >> 1 < NT ? off[NT > 1 ? e >> 1 : 0] : 0.f;
 #pragma unroll
-                    for (int v = 0; v < KV; ++v) {
-                        uint32_t kw[2 * TILES][4];
+                for (int v = 0; v < KV; ++v) {
+                    uint32_t kw[2 * TILES][4];
 #pragma unroll
-                        for (int nb = 0; nb < 2 * TILES; ++nb) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * TOK + k_at[v][nb & 1]);
-                            kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
-                            kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint2 qa0 = q_pair(0, v, i), qa1 = q_pair(1, v, i);
-#pragma unroll
-                            for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
-                        }
+                    for (int nb = 0; nb < 2 * TILES; ++nb) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(tiles + (nb >> 1) * 16 * D + k_at[v][nb & 1]);
+                        kw[nb][0] = x.x ^ 0x80808080u, kw[nb][1] = x.y ^ 0x80808080u;
+                        kw[nb][2] = x.z ^ 0x80808080u, kw[nb][3] = x.w ^ 0x80808080u;
                     }
-                } else {
-                    // 64 dimensions at a time: their products with the codes, times the token's scale, and the sum of
-                    // q times its bias.
 #pragma unroll
-                    for (int v = 0; v < KV; ++v) {
-                        float raw[2 * TILES][4];
-                        uint32_t kw[2 * TILES][2];
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 qa0 = Q_REGS ? qa[0][Q_REGS ? v : 0][i] : q_at(0, v, i);
+                        uint2 qa1 = make_uint2(0u, 0u);
+                        if constexpr (NT > 1) qa1 = Q_REGS ? qa[NT - 1][Q_REGS ? v : 0][i] : q_at(NT - 1, v, i);
 #pragma unroll
-                        for (int nb = 0; nb < 2 * TILES; ++nb) {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(tiles + (nb >> 1) * 16 * TOK + (k_at[v][nb & 1] ^ (nb >> 1) * SECOND));
-                            kw[nb][0] = x.x, kw[nb][1] = x.y;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) raw[nb][e] = 0.f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint2 qa0 = q_pair(0, v, i), qa1 = q_pair(1, v, i);
-#pragma unroll
-                            for (int nb = 0; nb < 2 * TILES; ++nb) {
-                                const uint32_t w = kw[nb][i >> 1] >> (8 * (i & 1));
-                                mma_f16(raw[nb], qa0.x, qa1.x, qa0.y, qa1.y, w & 0x000F000Fu, w & 0x00F000F0u);
-                            }
-                        }
-#pragma unroll
-                        for (int nb = 0; nb < 2 * TILES; ++nb)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t a = pairs[(8 * nb + tok[e]) * KV + v];
-#pragma unroll
-                                for (int u = 0; u < NT; ++u)
-                                    sc[nb][2 * u + e] = fmaf(raw[nb][2 * u + e], __uint_as_float(a << 16),
-                                                             fmaf(__uint_as_float(a & 0xFFFF0000u), qs[u][v], sc[nb][2 * u + e]));
-                            }
+                        for (int nb = 0; nb < 2 * TILES; ++nb) mma_f16(sc[nb], qa0.x, qa1.x, qa0.y, qa1.y, lo2_tiny(kw[nb][i]), hi2_tiny(kw[nb][i]));
                     }
                 }
                 // Rows lr and lr + 8: tokens t + 8 nb + tok[e] in sc[nb][2 u + e].
-                const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
                 float ks[TILES], vs[TILES];
 #pragma unroll
-                for (int h = 0; h < TILES; ++h) ks[h] = F == 8 ? s_ks[pi[h]] : 1.f, vs[h] = F == 8 ? s_vs[pi[h]] : 0.f;
-                // 4 bits: scale and bias of the values of token t + 8 nb + tok[e] (0 where no row sees it: whatever may stand
-                // there, infinities and NaN too, meets weights of 0); and of a tile's tokens, what no value passes by more
-                // than a factor of 2.
-                const uint32_t *const v_pairs = pairs + AFFINE / 8;
-                auto v_pair = [&](int nb, int e, int g) {
-                    const uint32_t a = v_pairs[(8 * nb + tok[e]) * KV + g];
-                    const int j = t + 8 * nb + tok[e];
-                    return full || (j >= any_from && j < to) ? a : 0u;
-                };
-                if constexpr (F == 4) {
-                    float most[TILES];
-#pragma unroll
-                    for (int h = 0; h < TILES; ++h) {
-                        most[h] = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int g = 0; g < KV; ++g) {
-                                const uint32_t a = v_pair(2 * h + (i >> 1), i & 1, g);
-                                most[h] = fmaxf(most[h], fmaxf(fabsf(__uint_as_float(a << 16)) * 15.f, fabsf(__uint_as_float(a & 0xFFFF0000u))));
-                            }
-                    }
-#pragma unroll
-                    for (int o = 1; o < 4; o <<= 1)
-#pragma unroll
-                        for (int h = 0; h < TILES; ++h) most[h] = fmaxf(most[h], __shfl_xor_sync(~0u, most[h], o));
-#pragma unroll
-                    for (int h = 0; h < TILES; ++h) vs[h] = on[h] ? log2_fast(most[h]) : -INFINITY;
-                }
-                uint32_t pb[F == 8 ? 1 : KV][NT][2 * TILES];     // (4 bits: of each 64 dimensions)
+                for (int h = 0; h < TILES; ++h) ks[h] = s_ks[pi[h]], vs[h] = s_vs[pi[h]];
+                uint32_t pb[NT][2 * TILES];
                 bool grew = false;
                 float mt[NT], mm[NT], dt[NT];
 #pragma unroll
@@ -647,8 +927,6 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                         // Accumulators hold rows 2 lc + {0, 1} (+ 8 u): their factors sit in lanes 4 (2 lc + e).
                         const float a0 = __shfl_sync(~0u, a, 8 * lc), a1 = __shfl_sync(~0u, a, 8 * lc + 4);
 #pragma unroll
-                        for (int v = 0; F == 4 && v < KV; ++v) ob[u][v] *= a;
-#pragma unroll
                         for (int p = 0; p < MT; ++p) {
                             o[p][u][0] *= a0;
                             o[p][u][1] *= a1;
@@ -661,22 +939,12 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 for (int u = 0; u < NT; ++u) {
 #pragma unroll
                     for (int h = 0; h < TILES; ++h) {
-                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf((F == 8 ? vs[h] : 0.f) + (WX - d[u]), 115.f));
+                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf(vs[h] + (W_EXP - d[u]), 115.f));
 #pragma unroll
                         for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
                             const float p0 = exp2_fast(sc[nb][2 * u] - mm[u]), p1 = exp2_fast(sc[nb][2 * u + 1] - mm[u]);
                             l[u] += p0 + p1;
-                            if constexpr (F == 8) {
-                                pb[0][u][nb] = pack_half(p0 * f, p1 * f);
-                            } else {
-                                const float w0 = p0 * f, w1 = p1 * f;
-#pragma unroll
-                                for (int g = 0; g < KV; ++g) {
-                                    const uint32_t a = v_pair(nb, 0, g), b = v_pair(nb, 1, g);
-                                    pb[g][u][nb] = pack_half(w0 * __uint_as_float(a << 16), w1 * __uint_as_float(b << 16));
-                                    if (on[h]) ob[u][g] = fmaf(w0, __uint_as_float(a & 0xFFFF0000u), fmaf(w1, __uint_as_float(b & 0xFFFF0000u), ob[u][g]));
-                                }
-                            }
+                            pb[u][nb] = pack_half(p0 * f, p1 * f);
                         }
                     }
                 }
@@ -684,52 +952,33 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 #pragma unroll
                 for (int h = 0; h < TILES; ++h) {
                     if (!on[h]) continue;                // (its codes were not fetched)
-                    if constexpr (F == 8) {
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) {
-                            uint32_t a[4][VB / 4];
+                    for (int v = 0; v < NV; ++v) {
+                        uint32_t a[4][VB / 4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint8_t *src = tiles + h * 16 * TOK + v_at[v][k];
-                                if constexpr (VB == 16) {
-                                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                                    a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                                    a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
-                                } else {
-                                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                                    a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < VB / 4; ++i) {
-                                // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
-                                const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
-                                const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
-                                const int p = v * VB / 2 + 2 * i;
-                                const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
-                                const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
-#pragma unroll
-                                for (int u = 0; u < NT; ++u) {
-                                    mma_f16(o[p][u], f0, f1, f2, f3, pb[0][u][2 * h], pb[0][u][2 * h + 1]);
-                                    mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[0][u][2 * h], pb[0][u][2 * h + 1]);
-                                }
+                        for (int k = 0; k < 4; ++k) {
+                            const uint8_t *src = tiles + h * 16 * D + v_at[v][k];
+                            if constexpr (VB == 16) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                                a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
+                                a[k][2] = x.z ^ 0x80808080u, a[k][3] = x.w ^ 0x80808080u;
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                                a[k][0] = x.x ^ 0x80808080u, a[k][1] = x.y ^ 0x80808080u;
                             }
                         }
-                    } else {
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) {
-                            uint32_t a[4];
+                        for (int i = 0; i < VB / 4; ++i) {
+                            // Bytes (token, token + 1) of d + 0, d + 1 and of d + 2, d + 3.
+                            const uint32_t x0 = prmt(a[0][i], a[1][i], 0x5140u), x1 = prmt(a[0][i], a[1][i], 0x7362u);
+                            const uint32_t y0 = prmt(a[2][i], a[3][i], 0x5140u), y1 = prmt(a[2][i], a[3][i], 0x7362u);
+                            const int p = v * VB / 2 + 2 * i;
+                            const uint32_t f0 = lo2(x0), f1 = hi2(x0), f2 = lo2(y0), f3 = hi2(y0);
+                            const uint32_t g0 = lo2(x1), g1 = hi2(x1), g2 = lo2(y1), g3 = hi2(y1);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const uint32_t *>(tiles + h * 16 * TOK + (v_at[v][k] ^ h * SECOND));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                // Codes of d + 2 i and d + 2 i + 1 of tokens tok[0], tok[1]; and of the two eight further.
-                                const uint32_t sel = i < 2 ? 0x5410u : 0x7632u;
-                                const uint32_t x = prmt(a[0], a[1], sel) >> (8 * (i & 1)), y = prmt(a[2], a[3], sel) >> (8 * (i & 1));
-#pragma unroll
-                                for (int u = 0; u < NT; ++u)
-                                    mma_f16(o[4 * v + i][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u,
-                                            pb[v][u][2 * h], pb[v][u][2 * h + 1]);
+                            for (int u = 0; u < NT; ++u) {
+                                mma_f16(o[p][u], f0, f1, f2, f3, pb[u][2 * h], pb[u][2 * h + 1]);
+                                mma_f16(o[p + 1][u], g0, g1, g2, g3, pb[u][2 * h], pb[u][2 * h + 1]);
                             }
                         }
                     }
@@ -741,39 +990,26 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
 
         // Join the warps: row sums, and the outputs (in the rings' place) in warp order.
         auto out_of = [&](int wi, int r) { return reinterpret_cast<float *>(ring) + (wi * R + r) * out_pitch(D); };
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            l[u] += __shfl_xor_sync(~0u, l[u], 1);
-            l[u] += __shfl_xor_sync(~0u, l[u], 2);
-            if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], d[u], l[u], 0.f};
-        }
         if constexpr (F == 4) {
+            rows4.end(lr, lc, [&](int r, const RowSum &x) { s_sum[warp][r] = x; },
+                      [&](int r, int d, float2 x) { *reinterpret_cast<float2 *>(out_of(warp, r) + d) = x; });
+        } else {
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                l[u] += __shfl_xor_sync(~0u, l[u], 1);
+                l[u] += __shfl_xor_sync(~0u, l[u], 2);
+                if (lc == 0) s_sum[warp][lr + 8 * u] = RowSum{m[u], d[u], l[u], 0.f};
+            }
 #pragma unroll
             for (int u = 0; u < NT; ++u)
 #pragma unroll
-                for (int v = 0; v < KV; ++v) {
-                    ob[u][v] += __shfl_xor_sync(~0u, ob[u][v], 1);
-                    ob[u][v] += __shfl_xor_sync(~0u, ob[u][v], 2);
+                for (int e = 0; e < 2; ++e) {
+                    float *dst = out_of(warp, 2 * lc + e + 8 * u);
+#pragma unroll
+                    for (int p = 0; p < MT; ++p)
+                        *reinterpret_cast<float2 *>(dst + p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2))) = make_float2(o[p][u][e], o[p][u][2 + e]);
                 }
         }
-#pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float *dst = out_of(warp, 2 * lc + e + 8 * u);
-                float b[KV];
-#pragma unroll
-                for (int v = 0; F == 4 && v < KV; ++v) b[v] = __shfl_sync(~0u, ob[u][v], 8 * lc + 4 * e);
-#pragma unroll
-                for (int p = 0; p < MT; ++p) {
-                    const int d = p / (VB / 2) * 8 * VB + VB * lr + 2 * (p % (VB / 2));
-                    if constexpr (F == 4)        // (the odd dimensions' codes stood 2^4 higher)
-                        *reinterpret_cast<float2 *>(dst + d) =
-                            make_float2(fmaf(o[p][u][e], 1.f / TINY, b[p / 4]), fmaf(o[p][u][2 + e], 0.0625f / TINY, b[p / 4]));
-                    else
-                        *reinterpret_cast<float2 *>(dst + d) = make_float2(o[p][u][e], o[p][u][2 + e]);
-                }
-            }
         __syncthreads();
         if (tid < R) {
             RowSum a = s_sum[0][tid];
