@@ -169,16 +169,8 @@ TFQ_HD constexpr int smem_bytes(int f, int d, int nt) {
 // Token of a tile (in eights) that column n of the scores stands for.  A quarter
 // of a warp reads 16 bytes a lane of the keys of tokens order(2 a), order(2 a + 1),
 // and of the values of the four tokens order(2 a) (or the four order(2 a + 1)).
-template <int F, int D>
+template <int D>
 __device__ __forceinline__ int order(int n) {
-    if (F == 4) {
-        // Half a warp reads 8 bytes a lane of the keys of tokens order(0) .. order(3) (or the other four), a warp 4
-        // bytes a lane of the values of the even columns' tokens (or the odd ones').
-        const int n0 = n & 1, n1 = n >> 1 & 1, n2 = n >> 2;
-        if (D == 64) return n ^ n2;
-        if (D == 128) return (n0 ^ n2) * 4 + n0 * 2 + n1;
-        return (n0 ^ n2) * 4 + n1 * 2 + n0;
-    }
     const int a = n >> 1;
     if (D == 64) return (a + (a & 2)) ^ (n & 1 ? 3 : 0);
     if (D == 128) return n ^ (n & 1 ? 4 : 0);
@@ -244,21 +236,27 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// As mma_f16, for the compiler to move.
+__device__ __forceinline__ void mma_f16_free(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 // Products that begin at 0.
 __device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -266,8 +264,17 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // The transpose of a warp's 8 x 8 numbers of 16 bits (lane 4 r + c holds row r's 2 c and 2 c + 1).
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+// Four 8 x 8 matrices of 16-bit units out of shared memory (lane 8 i + r gives matrix i's row r, 16 bytes): lane 4 r + c
+// gets row r's units 2 c, 2 c + 1 of each; TRANS: unit r of rows 2 c, 2 c + 1.
+template <bool TRANS>
+__device__ __forceinline__ void load_matrices(uint32_t (&x)[4], const uint8_t *row) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(smem_u32(row)));
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(smem_u32(row)));
 }
 // The larger magnitudes of two pairs of bf16 numbers (signs mean nothing then; NaN is passed over).
 __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
@@ -286,7 +293,7 @@ __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
 // rows; a lane gets the scores of two tokens a tile and two rows, two numbers to an instruction.  The sums with the
 // biases are a product of bf16: the cache's pairs (scale, bias) as they lie with (0, a third of sum(q)'s bits).
 // Second product: w_rj scale_jg in fp16 (w as over 8 bits: 2^18 p 2^-d, d the running maximum of s - m + log2(15 scale
-// or bias)), transposed in the warp, with the codes' tokens put side by side by byte permutes; the biases' part in fp32.
+// or bias)), transposed in the warp, with the codes transposed by the loads (four of a token at a time); the biases' part in fp32.
 // The maxima m and d are joined over the warp's lanes only where a lane finds one passed by more than SLACK4.
 //
 // Bound by the issue of instructions and the latency between them: 48 x 8000 tokens of 8 heads of 128, 32 query heads, 71 us, 1 x 131000
@@ -300,20 +307,24 @@ struct Rows4 {
     static constexpr int TOK = D / 2;
     static constexpr int SECOND = 16 * TOK == 512 ? 64 : 0;   // what the swizzle adds in a second tile that begins in the middle of 1024 bytes
 
-    uint2 q[NT][Q_REGS ? 4 * KV : 1];    // k step (v, i) of row lr (+ 8): d = 64 v + 16 lc + 4 i + {0, 1 | 2, 3} as stored
+    uint2 q[NT][Q_REGS ? 4 * KV : 1];    // k steps 2 c, 2 c + 1 of row lr (+ 8): d = 32 c + 8 lc + {0, 1 | 2, 3}, + 4, as stored
     uint32_t qb[NT][NB][2];              // of sum(q): (0, a part), by the lane's place among the pairs
     F2 rowf[NT], mm[NT], f[NT], l[NT];   // of rows 2 lc, 2 lc + 1 (+ 8): factor of a score, base of m, 2^18 2^-d, sum
     F2 ob[NT][KV];                       // sums of w times the biases, this lane's tokens
     float m[NT][2], d[NT][2];
     float o[MT][NT][4];
 
+    template <typename Q>
+    static __device__ __forceinline__ uint2 q_at(const Q &sq, int r, int lc, int i) {
+        return *reinterpret_cast<const uint2 *>(&sq[r][32 * (i >> 1) + 8 * lc + 4 * (i & 1)]);
+    }
     template <typename Q, typename S>
     __device__ __forceinline__ void begin(const Q &sq, const float2 *s_row, const S &s_qs, int lr, int lc, int rows) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             if constexpr (Q_REGS) {
 #pragma unroll
-                for (int i = 0; i < 4 * KV; ++i) q[u][i] = *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * (i >> 2) + 16 * lc + 4 * (i & 3)]);
+                for (int i = 0; i < 4 * KV; ++i) q[u][i] = q_at(sq, lr + 8 * u, lc, i);
             }
             // Parts of 8 bits each of the sum of group lc % KV.
             const float x = s_qs[lr + 8 * u][lc & (KV - 1)];
@@ -337,12 +348,13 @@ struct Rows4 {
         }
     }
 
-    // Tokens t + 16 h + 8 nb + ..: their codes in `tiles` (at k_at, and v_at), scales and biases in k_pairs and v_pairs.
+    // Tokens t + 16 h + 8 nb + ..: their keys' codes in `tiles` and their values' in `values` (rows of matrices: at `at`),
+    // scales and biases in k_pairs and v_pairs.
     // full: every row sees every token.  Else seen(i) is whether token t + i is there and any row sees it, and
     // sees(r, i) whether row r does.
     template <typename Q, typename Seen, typename Sees>
-    __device__ __forceinline__ void step(const uint8_t *tiles, const uint32_t *k_pairs, const uint32_t *v_pairs, const int (&k_at)[KV][2],
-                                         const int (&v_at)[KV][4], int mine, const Q &sq, int lr, int lc, bool full, Seen seen, Sees sees) {
+    __device__ __forceinline__ void step(const uint8_t *tiles, const uint8_t *values, const uint32_t *k_pairs, const uint32_t *v_pairs,
+                                         const int (&at)[KV], int mine, const Q &sq, int lr, int lc, bool full, Seen seen, Sees sees) {
         // Scores: tokens t + 8 nb + mine (mine: order(lr)) of rows 2 lc, 2 lc + 1 (+ 8).
         uint32_t pair[2 * TILES][KV];
         auto load_pairs = [&](const uint32_t *src) {
@@ -384,21 +396,21 @@ struct Rows4 {
 #pragma unroll
         for (int v = 0; v < KV; ++v) {
             float raw[TILES][NT][4];
-            uint2 x[2 * TILES];
+            uint32_t x[TILES][4];                // tokens 0 .. 7 and 8 .. 15 of the first 32 dimensions, and of the others
 #pragma unroll
-            for (int nb = 0; nb < 2 * TILES; ++nb) x[nb] = *reinterpret_cast<const uint2 *>(tiles + (nb >> 1) * 16 * TOK + (k_at[v][nb & 1] ^ (nb >> 1) * SECOND));
+            for (int h = 0; h < TILES; ++h) load_matrices<false>(x[h], tiles + h * 16 * TOK + (at[v] ^ h * SECOND));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int h = 0; h < TILES; ++h) {
-                    const uint32_t w0 = (i >> 1 ? x[2 * h].y : x[2 * h].x) >> (8 * (i & 1)), w1 = (i >> 1 ? x[2 * h + 1].y : x[2 * h + 1].x) >> (8 * (i & 1));
+                    const uint32_t w0 = x[h][2 * (i >> 1)] >> (8 * (i & 1)), w1 = x[h][2 * (i >> 1) + 1] >> (8 * (i & 1));
 #pragma unroll
                     for (int u = 0; u < NT; ++u) {
-                        const uint2 b = Q_REGS ? q[u][Q_REGS ? 4 * v + i : 0] : *reinterpret_cast<const uint2 *>(&sq[lr + 8 * u][64 * v + 16 * lc + 4 * i]);
+                        const uint2 b = Q_REGS ? q[u][Q_REGS ? 4 * v + i : 0] : q_at(sq, lr + 8 * u, lc, 4 * v + i);
                         if (i == 0)
                             mma_f16_0(raw[h][u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
                         else
-                            mma_f16(raw[h][u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
+                            mma_f16_free(raw[h][u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
                     }
                 }
 #pragma unroll
@@ -505,22 +517,19 @@ struct Rows4 {
                 }
             }
         }
-        // Transposed values: tokens tok[0], tok[1] (+ 8) of d = 64 v + 8 lr + ...
+        // Transposed values: tokens 2 lc, 2 lc + 1 (+ 8) of a tile, d = 32 c + 4 lr + ...
 #pragma unroll
         for (int h = 0; h < TILES; ++h)
 #pragma unroll
             for (int v = 0; v < KV; ++v) {
-                uint32_t a[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const uint32_t *>(tiles + h * 16 * TOK + (v_at[v][k] ^ h * SECOND));
+                uint32_t x[4];
+                load_matrices<true>(x, values + h * 16 * TOK + (at[v] ^ h * SECOND));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // Codes of d + 2 i and d + 2 i + 1 of tokens tok[0], tok[1]; and of the two eight further.
-                    const uint32_t sel = i < 2 ? 0x5410u : 0x7632u;
-                    const uint32_t x = prmt(a[0], a[1], sel) >> (8 * (i & 1)), y = prmt(a[2], a[3], sel) >> (8 * (i & 1));
+                    const uint32_t a = x[2 * (i >> 1)] >> (8 * (i & 1)), b = x[2 * (i >> 1) + 1] >> (8 * (i & 1));
 #pragma unroll
                     for (int u = 0; u < NT; ++u)
-                        mma_f16(o[4 * v + i][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, pb[v][u][2 * h], pb[v][u][2 * h + 1]);
+                        mma_f16_free(o[4 * v + i][u], a & 0x000F000Fu, a & 0x00F000F0u, b & 0x000F000Fu, b & 0x00F000F0u, pb[v][u][2 * h], pb[v][u][2 * h + 1]);
                 }
             }
     }
@@ -549,7 +558,7 @@ struct Rows4 {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float x = e ? b[p / 4].y : b[p / 4].x;
-                    put(2 * lc + e + 8 * u, p / 4 * 64 + 8 * lr + 2 * (p % 4), make_float2(fmaf(o[p][u][e], 1.f / TINY, x), fmaf(o[p][u][2 + e], 0.0625f / TINY, x)));
+                    put(2 * lc + e + 8 * u, p / 2 * 32 + 4 * lr + 2 * (p % 2), make_float2(fmaf(o[p][u][e], 1.f / TINY, x), fmaf(o[p][u][2 + e], 0.0625f / TINY, x)));
                 }
         }
     }
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     constexpr int R = 8 * NT;                    // rows of a tile
     constexpr int KV = D / 64;                   // vectors of a key a lane: its 16 of each 64 values
     constexpr int MT = D / 16;                   // m tiles of the transposed values
-    constexpr int VB = F == 8 && D >= 128 ? 16 : 8;   // values of a token that a lane takes at once
+    constexpr int VB = D >= 128 ? 16 : 8;   // values of a token that a lane takes at once
     constexpr int NV = D / (8 * VB);             // ... and how often
     constexpr int NST = stages(F, D), TILES = tiles_of(D), TP = 16 * TILES, STEP = step_of(D);
     constexpr int TOK = D * F / 8;               // bytes of a token
@@ -581,6 +590,20 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane >> 2, lc = lane & 3;
     const int H = P.kv.kv_heads, G = P.group, BL = P.block_log2, BM = P.kv.block - 1;
+
+    if constexpr (F == 4) {
+        // The rows of q and of the table, a line of 128 bytes a thread where there are no more, on their way to L2 while the
+        // lengths are read.
+        const int es = P.q_f32 ? 4 : 2, q_lines = H * G * D * es / 128 + 1, t_lines = ((((P.b.max_len - 1) >> BL) + 1) >> 5) + 1;
+        const long long nq = (long long)P.b.rows * q_lines, nt = (long long)P.b.n_seqs * t_lines, all = (long long)gridDim.x * THREADS;
+        const long long i = (long long)blockIdx.x * THREADS + tid;
+        if (nq + nt <= all && i < nq + nt) {
+            const long long j = i < nq ? i : i - nq, row = i < nq ? j / q_lines : j / t_lines, line = i < nq ? j - row * q_lines : j - row * t_lines;
+            const char *at = i < nq ? static_cast<const char *>(P.q) + row * P.q_stride * es + min(line * 128, (long long)H * G * D * es - 1)
+                                    : reinterpret_cast<const char *>(P.b.table + row * P.b.table_stride + min(line * 32, (long long)((P.b.max_len - 1) >> BL)));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+    }
 
     // This CTA's share: steps [u0, u1) of the line, whose first sequence is s_seq, at s_first of the line.
     const int per = (P.b.n_seqs + THREADS - 1) / THREADS;
@@ -637,16 +660,19 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     const bool single = TILES == 2 && BL == 4;   // pages of one tile only: a stage's tiles come from two
     uint32_t fit = 0, it = 0;                    // pairs fetched and taken, over all items
     // Offsets of this lane's reads in a stage: keys of token order(lr) (+ 8, + 16, + 24), values of four tokens of a tile.
-    int k_at[KV][2], v_at[NV][4];
-    const int tok[2] = {order<F, D>(2 * lc), order<F, D>(2 * lc + 1)};
+    // (4 bits: rows of matrices, 16 bytes of a token; natural order, whose eight tokens meet eight chunks under the swizzle.)
+    int k_at[KV][2], v_at[NV][4], at4[KV];
+    const int tok[2] = {order<D>(2 * lc), order<D>(2 * lc + 1)};
 #pragma unroll
-    for (int v = 0; v < KV; ++v)
+    for (int v = 0; v < KV; ++v) {
+        at4[v] = swizzled((lane & 15) * TOK + 32 * v + 16 * (lane >> 4));
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) k_at[v][nb] = swizzled((order<F, D>(lr) + 8 * nb) * TOK + 8 * F * v + 2 * F * lc);
+        for (int nb = 0; nb < 2; ++nb) k_at[v][nb] = swizzled((order<D>(lr) + 8 * nb) * D + 64 * v + 16 * lc);
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v_at[v][k] = swizzled((tok[k & 1] + 8 * (k >> 1)) * TOK + (v * 8 * VB + VB * lr) * F / 8) + STAGE / 2;
+        for (int k = 0; k < 4; ++k) v_at[v][k] = swizzled((tok[k & 1] + 8 * (k >> 1)) * D + v * 8 * VB + VB * lr) + STAGE / 2;
 
     int seq = s_seq;
     long long seq_at = s_first;                  // the sequence's first step on the line
@@ -711,10 +737,12 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
             if (p0 >= 0) copy(p0, t, 0);
             if (p1 >= 0) copy(p1, t + 16, 1);
         };
+        bool holes = false;                      // any of the chunk's pages is none
         auto open_chunk = [&]() {
             c1 = min(c0 + CHUNK_TOKENS, t_end);
             pg0 = c0 >> BL;
             npages = ((c1 - 1) >> BL) - pg0 + 1;
+            bool hole = false;
             for (int i = tid; i < npages; i += THREADS) {
                 int page = P.b.table[seq * P.b.table_stride + pg0 + i];
                 if (page < 0 || page >= P.kv.n_blocks) {
@@ -722,8 +750,9 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                     page = -1;
                 }
                 s_page[i] = page;
+                hole |= page < 0;
             }
-            __syncthreads();
+            holes = __syncthreads_or(hole);
             ft = *abort ? NO_TOKEN : c0 + TP * warp;
             for (int i = 0; i < NST - 1; ++i, ft += STEP)
                 if (lane == 0) fetch(ft);
@@ -826,23 +855,23 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 }
                 const uint8_t *tiles = mine + (it % NST) * STAGE;
                 // Tiles t and t + 16: their pages (a tile of no page is not seen).
-                int pi[TILES];
-                bool on[TILES];
-#pragma unroll
-                for (int h = 0; h < TILES; ++h) {
-                    pi[h] = min(((t + 16 * h) >> BL) - pg0, npages - 1);
-                    on[h] = s_page[pi[h]] >= 0 && !(h == 1 && single && t + 16 >= c1);
-                }
-                const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
+                auto page_of = [&](int h) { return min(((t + 16 * h) >> BL) - pg0, npages - 1); };
+                auto there = [&](int h) { return s_page[page_of(h)] >= 0 && !(h == 1 && single && t + 16 >= c1); };
                 if constexpr (F == 4) {
+                    const bool full = t >= all_from && t + TP <= all_to && !holes;
                     const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(mine_affine + (it % NST) * AFFINE);
                     rows4.step(
-                        tiles, pairs, pairs + AFFINE / 8, k_at, v_at, order<F, D>(lr), sq, lr, lc, full,
-                        [&](int i) { return on[i < 16 ? 0 : TILES - 1] && t + i >= any_from && t + i < to; },
+                        tiles, tiles + STAGE / 2, pairs, pairs + AFFINE / 8, at4, lr, sq, lr, lc, full,
+                        [&](int i) { return there(i < 16 ? 0 : 1) && t + i >= any_from && t + i < to; },
                         [&](int r, int i) { return t + i >= s_see[r].x && t + i < s_see[r].y; });
                     __syncwarp();                    // (every lane has read the stage that is filled next)
                     continue;
                 }
+                int pi[TILES];
+                bool on[TILES];
+#pragma unroll
+                for (int h = 0; h < TILES; ++h) pi[h] = page_of(h), on[h] = there(h);
+                const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
                 // Scores of the tiles' tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
                 float sc[2 * TILES][4];
 #pragma unroll
@@ -1067,34 +1096,44 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                         const float4 x = __ldcg(sums + slot(k) * R + r);
                         return RowSum{x.x, x.y, x.z, 0.f};
                     };
-                    const RowSum own = sum_of(min(lane, parts - 1));
-                    RowSum a = own;
-                    for (int k = lane + 32; k < parts; k += 32) join_maxima(a, sum_of(k));
+                    // (a lane's first parts' in one round of loads)
+                    constexpr int AT = 3;
+                    RowSum own[AT];
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) own[i] = sum_of(min(lane + 32 * i, parts - 1));
+                    RowSum a = own[0];
+#pragma unroll
+                    for (int i = 1; i < AT; ++i) join_maxima(a, own[i]);
+                    for (int k = lane + 32 * AT; k < parts; k += 32) join_maxima(a, sum_of(k));
                     for (int o = 16; o > 0; o >>= 1) {
                         const float m = __shfl_xor_sync(~0u, a.m, o), d = __shfl_xor_sync(~0u, a.d, o);
                         join_maxima(a, RowSum{m, d, 0.f, 0.f});
                     }
                     a.l = 0.f;
-                    for (int k = lane; k < parts; k += 32) {
-                        const RowSum x = k < 32 ? own : sum_of(k);
+                    auto take = [&](int k, const RowSum &x) {
                         a.l += x.l * l_factor(x, a);
                         s_fac[k][r] = o_factor(x, a);
-                    }
+                    };
+#pragma unroll
+                    for (int i = 0; i < AT; ++i)
+                        if (lane + 32 * i < parts) take(lane + 32 * i, own[i]);
+                    for (int k = lane + 32 * AT; k < parts; k += 32) take(k, sum_of(k));
                     for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
                     if (lane == 0) s_join[r] = a;
                 }
                 __syncthreads();
-                // The outputs, in the parts' order, eight loads at a time.
+                // The outputs, in the parts' order, JOIN loads at a time.
+                constexpr int JOIN = F == 4 ? 16 : 8;
                 for (int v = 4 * tid; v < rows * D; v += 4 * THREADS) {
                     const int r = v / D;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k0 = 0; k0 < parts; k0 += 8) {
-                        float4 x[8];
+                    for (int k0 = 0; k0 < parts; k0 += JOIN) {
+                        float4 x[JOIN];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
+                        for (int k = 0; k < JOIN; ++k)
                             x[k] = __ldcg(reinterpret_cast<const float4 *>(P.part + (long long)slot(min(k0 + k, parts - 1)) * R * D + v));
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < JOIN; ++k) {
                             const float f = k0 + k < parts ? s_fac[min(k0 + k, parts - 1)][r] : 0.f;
                             y.x = fmaf(x[k].x, f, y.x), y.y = fmaf(x[k].y, f, y.y);
                             y.z = fmaf(x[k].z, f, y.z), y.w = fmaf(x[k].w, f, y.w);
