@@ -60,6 +60,7 @@ TFQ_HD constexpr int step_of(int d) { return 16 * tiles_of(d) * WARPS; }
 constexpr int CHUNK_TOKENS = 4096;       // tokens whose pages and scales a CTA keeps at a time
 constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
 constexpr int MAX_PARTS = 768;           // CTAs of a launch, at most
+constexpr int ITEM_ROWS = 3;             // an item's beginning and end, in steps (4 bits)
 constexpr int NO_TOKEN = 1 << 30;        // past every chunk
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
 // ... by the cache's bits: of 4, w is p times the scale of a code, at most a 15th of what d stands for.
@@ -79,6 +80,7 @@ struct Params {
     float scale;
     int group, window, causal, q_f32;
     int block_log2;         // of kv.block
+    int item_steps;         // what an item's beginning and end count for on the line (rows kernel)
     int stall;              // test hook: every CTA's first keys are withheld (rows kernel: every warp's first copies)
 };
 
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     __shared__ int s_seq;
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane >> 2, lc = lane & 3;
-    const int H = P.kv.kv_heads, G = P.group, BL = P.block_log2, BM = P.kv.block - 1;
+    const int H = P.kv.kv_heads, G = P.group, BL = P.block_log2, BM = P.kv.block - 1, item = F == 4 ? P.item_steps : 0;
 
     if constexpr (F == 4) {
         // The rows of q and of the table, a line of 128 bytes a thread where there are no more, on their way to L2 while the
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     for (int s = s0; s < s1; ++s) {
         const SeqWork w = seq_work<D, R>(P, s);
         if (!w.q.ok && blockIdx.x == 0) atomicOr(P.status, STATUS_BOUNDS);
-        mine_sum += (long long)H * w.tiles * w.steps;
+        mine_sum += (long long)H * w.tiles * (w.steps + item);
     }
     long long incl = mine_sum;
     for (int o = 1; o < 32; o <<= 1) {
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
         int s = s0;
         for (;; ++s) {
             const SeqWork w = seq_work<D, R>(P, s);
-            const long long n = (long long)H * w.tiles * w.steps;
+            const long long n = (long long)H * w.tiles * (w.steps + item);
             if (u0 < at + n) break;
             at += n;
         }
@@ -678,14 +680,15 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
     long long seq_at = s_first;                  // the sequence's first step on the line
     SeqWork sw = seq_work<D, R>(P, seq);
     for (long long line = u0; line < u1;) {
-        while (line >= seq_at + (long long)H * sw.tiles * sw.steps) {
-            seq_at += (long long)H * sw.tiles * sw.steps;
+        while (line >= seq_at + (long long)H * sw.tiles * (sw.steps + item)) {
+            seq_at += (long long)H * sw.tiles * (sw.steps + item);
             sw = seq_work<D, R>(P, ++seq);
         }
         // The item: a head and a tile of the sequence's rows; this CTA's steps of it.
-        const int index = (int)((line - seq_at) / sw.steps), h = index / sw.tiles, tile = index - h * sw.tiles;
-        const long long item_at = seq_at + (long long)index * sw.steps;
-        const int step0 = (int)(line - item_at), step1 = (int)min((long long)sw.steps, u1 - item_at);
+        const int index = (int)((line - seq_at) / (sw.steps + item)), h = index / sw.tiles, tile = index - h * sw.tiles;
+        const long long item_at = seq_at + (long long)index * (sw.steps + item) + item;      // (its first step)
+        const int step0 = (int)max(0LL, line - item_at), step1 = (int)min((long long)sw.steps, u1 - item_at);
+        if (step0 >= step1) break;               // (the share ends in the item's beginning)
         const int r0 = tile * R, rows = min(R, sw.q.n * G - r0);
         const int end = sw.q.end, first = end - sw.q.n;              // (position of the sequence's first row)
         const int i0 = r0 / G, i1 = (r0 + rows - 1) / G;             // first and last of the tile's tokens
@@ -1075,7 +1078,7 @@ __global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid
                 store4(v / D, v % D, joined4(v / D, v % D), out_factor<F>(s_join[v / D]));
         } else {
             // A CTA's first item's part is in its slot 0, that of a later one (its last) in slot 1.
-            const int slot0 = 2 * c_first + (item_at > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
+            const int slot0 = 2 * c_first + (item_at - item > total * c_first / C ? 1 : 0), k_mine = (int)blockIdx.x - c_first;
             auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (c_first + k); };
             float4 *sums = reinterpret_cast<float4 *>(P.part + 2LL * gridDim.x * R * D);
             float *part = P.part + (long long)slot(k_mine) * R * D;
