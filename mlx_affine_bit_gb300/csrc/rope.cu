@@ -7,7 +7,7 @@
 //
 // Bound by memory: 4000 rows of 40 heads of 128, fp32 to bf16, are 123 MB.  A CTA
 // takes a few rows: their cosines and sines once, into shared memory, for all heads;
-// then a thread a place in the row, for each of the CTA's rows.
+// then a thread a place in the row, for four of the CTA's rows at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -17,7 +17,7 @@ using namespace tfq;
 
 namespace {
 
-constexpr int THREADS = 256, MAX_PAIRS = 512;
+constexpr int THREADS = 256, MAX_PAIRS = 512, MAX_ROWS = 8;
 
 struct RopeParams {
     const uint64_t *turns;
@@ -29,6 +29,8 @@ struct RopeParams {
     int per_head;           // items of a head: of N pairs of the turned part, of 2 N values of the rest
     float factor;
     bool back, copy;        // turn the other way; the rest is copied (else it stands there already)
+    int rows_cta = 1;       // rows of a CTA
+    uint32_t by_items = 0, by_head = 0;      // reciprocals of a row's items and a head's
 };
 
 // N values: fp32, or bf16; in as few accesses as N and their size allow where VEC.
@@ -80,22 +82,25 @@ __device__ __forceinline__ void store(T *p, const float (&v)[N]) {
     }
 }
 
-// N pairs an item; ROWS rows a CTA.
-template <typename TI, typename TO, int N, bool PAIRS, int ROWS>
+// n / d by ceil(2^32 / d), which is too large by less than 1: exact where n d < 2^32.  (0: a division.)
+__device__ __forceinline__ int over(int n, uint32_t reciprocal, int d) { return reciprocal ? (int)__umulhi((uint32_t)n, reciprocal) : n / d; }
+
+// N pairs an item; a CTA has P.rows_cta rows, and where there are few of those a part of their items (blockIdx.y).
+template <typename TI, typename TO, int N, bool PAIRS, int AT, bool WIDE>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeParams P) {
     constexpr bool VEC = N > 1;
-    extern __shared__ float2 s_turn[];                  // [ROWS][rot / 2] cosine, sine
-    __shared__ int s_pos[ROWS];
+    extern __shared__ float2 s_turn[];                  // [rows_cta][rot / 2] cosine, sine
+    __shared__ int s_pos[MAX_ROWS];
     const int tid = threadIdx.x, half = P.rot / 2;
-    const long long r0 = (long long)blockIdx.x * ROWS;
-    for (int i = tid; i < ROWS * half; i += THREADS) {
+    const long long r0 = (long long)blockIdx.x * P.rows_cta;
+    for (int i = tid; i < P.rows_cta * half; i += THREADS) {
         const int k = i / half, j = i - k * half;
         const int pos = r0 + k < P.rows ? P.positions[r0 + k] : -1;
         if (j == 0) s_pos[k] = pos;
-        const uint32_t turn = (uint32_t)(((unsigned long long)(unsigned)pos * P.turns[j]) >> 32);
-        const uint32_t quarter = (turn + (1u << 29)) >> 30;
+        const uint32_t angle = (uint32_t)(((unsigned long long)(unsigned)pos * P.turns[j]) >> 32);
+        const uint32_t quarter = (angle + (1u << 29)) >> 30;
         float s, c;
-        sincospif((float)(int)(turn - (quarter << 30)) * (1.f / 2147483648.f), &s, &c);
+        sincospif((float)(int)(angle - (quarter << 30)) * (1.f / 2147483648.f), &s, &c);
         if (quarter & 1) {
             const float t = c;
             c = -s, s = t;
@@ -104,65 +109,87 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeParams P) {
         s_turn[i] = make_float2(P.factor * c, P.back ? -P.factor * s : P.factor * s);
     }
     __syncthreads();
-    const int turned = half / N, items = P.heads * P.per_head;
-    for (int item = blockIdx.y * THREADS + tid; item < items; item += gridDim.y * THREADS) {
-        const int h = item / P.per_head, e = item - h * P.per_head;
-        const bool rest = e >= turned;
-        // The item's first and second values: pairs as they lie, or 2 N values of the rest.
-        const int at = h * P.dim + (rest ? P.rot + (e - turned) * 2 * N : PAIRS ? e * 2 * N : e * N);
-        const int second = rest || PAIRS ? N : half;
-        if (rest && !P.copy) continue;
-        const TI *x = static_cast<const TI *>(P.x) + r0 * P.x_stride + at;
-        TO *out = static_cast<TO *>(P.out) + r0 * P.out_stride + at;
-        float a[ROWS][N], b[ROWS][N];
+    const int turned = half / N, items = P.heads * P.per_head, all = WIDE ? items : items * P.rows_cta;
+    // A thread takes AT items at a time.  WIDE: one place of the row, in AT rows.  Else items go over the row and then over
+    // the CTA's rows.
+    for (int n = blockIdx.y * THREADS + tid; n < all; n += gridDim.y * THREADS * (WIDE ? 1 : AT)) {
+        int row[AT], at[AT], second[AT];                // row -1: nothing to do; second: from the item's first values to its others
+        int turn[AT];                                   // place of its first turn, -1: of the rest
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            if (s_pos[k] < 0) continue;
-            load<TI, N, VEC>(x + k * P.x_stride, a[k]);
-            load<TI, N, VEC>(x + k * P.x_stride + second, b[k]);
+        for (int i = 0; i < AT; ++i) {
+            const int m = WIDE ? n : n + i * THREADS, k = WIDE ? i : over(m, P.by_items, items), item = WIDE ? n : m - k * items;
+            const int h = over(item, P.by_head, P.per_head), e = item - h * P.per_head;
+            const bool rest = e >= turned;
+            // The item's first and second values: pairs as they lie, or 2 N values of the rest.
+            at[i] = h * P.dim + (rest ? P.rot + (e - turned) * 2 * N : PAIRS ? e * 2 * N : e * N);
+            second[i] = rest || PAIRS ? N : half;
+            turn[i] = rest ? -1 : k * half + e * N;
+            row[i] = (WIDE || m < all) && s_pos[k] >= 0 && !(rest && !P.copy) ? k : -1;
+        }
+        float a[AT][N], b[AT][N];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            if (row[i] < 0) continue;
+            const TI *x = static_cast<const TI *>(P.x) + (r0 + row[i]) * P.x_stride + at[i];
+            load<TI, N, VEC>(x, a[i]);
+            load<TI, N, VEC>(x + second[i], b[i]);
         }
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            if (s_pos[k] < 0) continue;
-            if (!rest) {
-                const float2 *t = s_turn + k * half + e * N;
+        for (int i = 0; i < AT; ++i) {
+            if (row[i] < 0) continue;
+            if (turn[i] >= 0) {
+                const float2 *t = s_turn + turn[i];
                 if (PAIRS) {
                     float y[2 * N];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float u = 2 * i < N ? a[k][(2 * i) % N] : b[k][(2 * i) % N], v = 2 * i + 1 < N ? a[k][(2 * i + 1) % N] : b[k][(2 * i + 1) % N];
-                        const float2 z = t[i];
-                        y[2 * i] = u * z.x - v * z.y;
-                        y[2 * i + 1] = v * z.x + u * z.y;
+                    for (int j = 0; j < N; ++j) {
+                        const float u = 2 * j < N ? a[i][(2 * j) % N] : b[i][(2 * j) % N], v = 2 * j + 1 < N ? a[i][(2 * j + 1) % N] : b[i][(2 * j + 1) % N];
+                        const float2 z = t[j];
+                        y[2 * j] = u * z.x - v * z.y;
+                        y[2 * j + 1] = v * z.x + u * z.y;
                     }
 #pragma unroll
-                    for (int i = 0; i < N; ++i) a[k][i] = y[i], b[k][i] = y[N + i];
+                    for (int j = 0; j < N; ++j) a[i][j] = y[j], b[i][j] = y[N + j];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float2 z = t[i];
-                        const float u = a[k][i], v = b[k][i];
-                        a[k][i] = u * z.x - v * z.y;
-                        b[k][i] = v * z.x + u * z.y;
+                    for (int j = 0; j < N; ++j) {
+                        const float2 z = t[j];
+                        const float u = a[i][j], v = b[i][j];
+                        a[i][j] = u * z.x - v * z.y;
+                        b[i][j] = v * z.x + u * z.y;
                     }
                 }
             }
-            store<TO, N, VEC>(out + k * P.out_stride, a[k]);
-            store<TO, N, VEC>(out + k * P.out_stride + second, b[k]);
+            TO *out = static_cast<TO *>(P.out) + (r0 + row[i]) * P.out_stride + at[i];
+            store<TO, N, VEC>(out, a[i]);
+            store<TO, N, VEC>(out + second[i], b[i]);
         }
     }
 }
 
 template <typename TI, typename TO, int N, bool PAIRS>
-cudaError_t launch(const RopeParams &P, int nsm, cudaStream_t st) {
-    const int items = P.heads * P.per_head, most = (items + THREADS - 1) / THREADS;
-    // Four rows a CTA where that leaves some CTAs an SM, else one; and a row over as many CTAs as SMs are idle.
-    if (P.rows >= 32 * nsm / 4) {
-        rope_kernel<TI, TO, N, PAIRS, 4><<<dim3((P.rows + 3) / 4, 1), THREADS, 4 * P.rot / 2 * sizeof(float2), st>>>(P);
-    } else {
+cudaError_t launch(RopeParams &P, int nsm, cudaStream_t st) {
+    const int items = P.heads * P.per_head;
+    // Four rows a CTA where that leaves some CTAs an SM, else one, and a row over as many CTAs as SMs are idle.  Rows of few
+    // items: eight, and an item at a time.  (16000 rows of 16 heads of 64, bf16: 11 us, two or four items at a time 12 and 16 us,
+    // four rows a CTA 31 us; 4000 rows of 40 heads of 128, fp32 to bf16: 20 us, and 24 us with the items over all rows.)
+    const int half = P.rot / 2, most = (items + THREADS - 1) / THREADS;
+    auto reciprocal = [](long long n, int d) { return n * d < (1LL << 32) ? (uint32_t)((0xFFFFFFFFull + d) / d) : 0u; };     // (of 1: 0, too)
+    P.by_head = reciprocal(items, P.per_head);
+    if ((long long)P.rows < 8LL * nsm) {
         const int cols = P.rows >= nsm ? 1 : (nsm + P.rows - 1) / P.rows;
-        rope_kernel<TI, TO, N, PAIRS, 1><<<dim3(P.rows, cols < most ? cols : most), THREADS, P.rot / 2 * sizeof(float2), st>>>(P);
+        rope_kernel<TI, TO, N, PAIRS, 1, true><<<dim3(P.rows, cols < most ? cols : most), THREADS, half * sizeof(float2), st>>>(P);
+        return cudaGetLastError();
     }
+    int n = 4;
+    while (n < MAX_ROWS && n * items < 2 * THREADS && (long long)P.rows >= 8LL * nsm * n) n *= 2;
+    P.rows_cta = n;
+    P.by_items = reciprocal((long long)items * n, items);
+    const unsigned ctas = (unsigned)((P.rows + (long long)n - 1) / n);
+    if (n == 4)
+        rope_kernel<TI, TO, N, PAIRS, 4, true><<<ctas, THREADS, n * half * sizeof(float2), st>>>(P);
+    else
+        rope_kernel<TI, TO, N, PAIRS, 1, false><<<ctas, THREADS, n * half * sizeof(float2), st>>>(P);
     return cudaGetLastError();
 }
 

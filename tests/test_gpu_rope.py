@@ -68,6 +68,15 @@ def test_shapes(heads, dim, rot, src, dst, interleaved):
     check(turn, draw(1, heads, dim), [3], src, dst, inverse=True)
 
 
+@pytest.mark.parametrize("rows", [4863, 4864, 6001])
+@pytest.mark.parametrize("heads,dim,rot,interleaved", [(3, 64, 64, True), (2, 128, 32, False), (1, 6, 4, True)])
+def test_many_short_rows(rows, heads, dim, rot, interleaved):
+    # Eight rows a CTA, the last of them not whole, and rows of no position among them.
+    positions = np.random.default_rng(rows).integers(-50, 9000, rows).tolist()
+    check(tf.Rope(dim, rot, interleaved=interleaved), draw(rows, heads, dim), positions, BF16, BF16, pad=8)
+    check(tf.Rope(dim, rot, interleaved=interleaved), draw(rows, heads, dim), positions, F32, F32, pad=3, shift=1, in_place=True)
+
+
 @pytest.mark.parametrize("rows", [1, 151, 1215, 1216, 1219, 2500])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rows(rows, interleaved):
