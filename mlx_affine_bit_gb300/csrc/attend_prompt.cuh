@@ -267,16 +267,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Place in a 16-byte chunk of the fp16 tiles of eight dimensions' e-th: with 4-bit codes, the order in which a word's come
 // out in pairs (d, d + 4), the same for q and keys, and undone where outputs are stored.
 TFQ_HD constexpr int chunk_place(int f, int e) { return f == 4 ? (e & 3) * 2 + (e >> 2) : e; }
-// Eight codes of a word as fp16 (exact: 1024 + c and 64 + c, less that) times a scale plus a bias, in that order.
+// Eight codes of a word as fp16 times a scale plus a bias, in that order: codes stand as the subnormals c 2^-20, scales come
+// 2^20 larger than biases; one rounding.  (With the codes made whole numbers by a difference first: 13 instructions, now 11.)
 __device__ __forceinline__ uint4 widened(uint32_t w, __half2 scale, __half2 bias) {
-    auto value = [&](uint32_t bits, uint16_t base) {
-        const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&bits), __half2half2(__ushort_as_half(base)));
-        const __half2 y = __hfma2(c, scale, bias);
+    auto value = [&](uint32_t bits) {
+        const uint32_t code = bits & 0x00F000F0u;
+        const __half2 y = __hfma2(*reinterpret_cast<const __half2 *>(&code), scale, bias);
         return *reinterpret_cast<const uint32_t *>(&y);
     };
-    const uint32_t v = w >> 8;
-    return make_uint4(value((w & 0x000F000Fu) | 0x64006400u, 0x6400), value((w & 0x00F000F0u) | 0x54005400u, 0x5400),
-                      value((v & 0x000F000Fu) | 0x64006400u, 0x6400), value((v & 0x00F000F0u) | 0x54005400u, 0x5400));
+    return make_uint4(value(w << 4), value(w), value(w >> 4), value(w >> 8));
 }
 
 // F: bits of a code (8 or 4).
@@ -544,7 +543,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     }
                 }
             };
-            // Units of the 16 tokens of loads j0 ..: the power of two above every value; scales and biases become fp16 over it.
+            // Units of the 16 tokens of loads j0 ..: the power of two above every value; scales and biases become fp16 over it,
+            // such that widened values are a quarter of what they are over it (scales: at most 2 / 15 of it, times 2^18).
             // Returns its exponent, biased (0: only zeros).
             auto over_unit = [&](uint32_t (&a)[F == 4 ? LOADS : 1], int j0) {
                 float most = 0.f;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 const float inv = __uint_as_float((254u - unit) << 23);
 #pragma unroll
                 for (int j = j0; j < j0 + LOADS / NP; ++j)
-                    a[j] = pack_half(__uint_as_float(a[j] << 16) * inv, __uint_as_float(a[j] & 0xFFFF0000u) * inv);
+                    a[j] = pack_half(__uint_as_float(a[j] << 16) * inv * 262144.f, __uint_as_float(a[j] & 0xFFFF0000u) * inv * 0.25f);
                 return unit;
             };
             // Where this lane's 16 values of token tk go: two 16-byte chunks, 2 sub and 2 sub + 1 of the row of blocks of eight.
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     // (Keys of zeros only: scores of 0 with any unit.)
                     const uint32_t ku = lane % NP == 0 ? k_unit[0] : k_unit[NP - 1], vu = lane % NP == 0 ? v_unit[0] : v_unit[NP - 1];
                     if (k_of.scale.x >= 0.f)
-                        k_of.scale = make_float2(ku == 0 ? 1.f : __uint_as_float(ku << 23), vu == 0 ? -INFINITY : (float)((int)vu - 127));
+                        k_of.scale = make_float2(ku == 0 ? 1.f : __uint_as_float(ku << 23), vu == 0 ? -INFINITY : (float)((int)vu - 125));      // (four units: values stand as quarters)
 #pragma unroll
                     for (int j = 0; j < LOADS; ++j) v_now[j] = va[j];
                 }
@@ -825,7 +825,57 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 fq = row_factor(amax);
                 sq = P.scale < 0.f ? -fq : fq;
             };
-            if (!P.q_f32 && q16) {
+            if (F == 4 && q16) {
+                // Whole rows at a time, LR lanes a row; AT of them on their way at once.
+                constexpr int LR = D / 8, RPI = 32 / LR, AT = 4;
+#pragma unroll 1
+                for (int j0 = 0; j0 < LR; j0 += AT) {
+                    float x[AT][8];
+                    const int c = lane % LR;
+                    long long src[AT];
+#pragma unroll
+                    for (int j = 0; j < AT; ++j) src[j] = __shfl_sync(~0u, q_at, (j0 + j) * RPI + lane / LR) + 8 * c;
+                    if (P.q_f32) {
+#pragma unroll
+                        for (int j = 0; j < AT; ++j) {
+                            const float4 *at = reinterpret_cast<const float4 *>(static_cast<const float *>(P.q) + src[j]), a = at[0], b = at[1];
+                            x[j][0] = a.x, x[j][1] = a.y, x[j][2] = a.z, x[j][3] = a.w, x[j][4] = b.x, x[j][5] = b.y, x[j][6] = b.z, x[j][7] = b.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < AT; ++j) {
+                            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(P.q) + src[j]);
+                            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[j][2 * e] = __uint_as_float(u[e] << 16), x[j][2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < AT; ++j) {
+                        const int r = (j0 + j) * RPI + lane / LR;
+                        float top = 0.f, sum = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[j][e]));
+#pragma unroll
+                        for (int o = 1; o < LR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                        const float f = P.scale < 0.f ? -row_factor(top) : row_factor(top);
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            h[e] = pack_half(x[j][e] * f, x[j][e + 4] * f);
+                            sum += fabsf(x[j][e] * f) + fabsf(x[j][e + 4] * f);
+                        }
+#pragma unroll
+                        for (int o = 1; o < LR; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                        *reinterpret_cast<uint4 *>(q_s + t * TB + ((warp & 3) * 32 + r) * 128 + (c >> 3) * (KEYS * 128) + (((c & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                        // (to the thread of the row)
+                        const float row_top = __shfl_sync(~0u, top, lane % RPI * LR), row_sum = __shfl_sync(~0u, sum, lane % RPI * LR);
+                        if (lane / RPI == j0 + j) amax = row_top, sum_abs = row_sum;
+                    }
+                }
+                factors();
+            } else if (!P.q_f32 && q16) {
                 // The warp's 32 rows as they are to their places, LR lanes a row; then each thread its own row there.
                 constexpr int LR = D / 8, RPI = 32 / LR, CU = 2, QU = D == 256 ? 2 : 16;   // (measured: fewer are faster at dim 256, more at 128)
 #pragma unroll CU
@@ -897,7 +947,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             ++item;
 
             // Factor of a score in tensor memory, and the offset that comes off it first; tokens that the row sees.
-            constexpr float CODE = F == 8 ? TINY : 1.f, TOP = F == 8 ? 128.f * TINY : 1.f;   // of a key in shared memory: its unit, a bound
+            constexpr float CODE = F == 8 ? TINY : 0.25f, TOP = F == 8 ? 128.f * TINY : 0.25f;   // of a key in shared memory: its unit, a bound
             const float rowf = fabsf(P.scale) * 1.44269504088896340736f / fq * (1.f / CODE), off = F == 8 ? sum_q * (-128.f * TINY) : 0.f;
             const int first = w.s.q.end - w.s.q.n, pos = first + i_tok;
             const int see_to = P.causal ? min(w.s.q.end, pos + 1) : w.s.q.end, see_from = P.window ? pos - P.window + 1 : 0;
