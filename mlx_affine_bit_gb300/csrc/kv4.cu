@@ -7,8 +7,10 @@
 // (as two fp32 numbers) is compared with the exact border.
 //
 // Eight lanes hold a group, eight values each: 16 or 32 bytes in, one word of codes out.
-// Bound by memory on long calls (each row is read once), by latency on short ones: a
-// launch, the slot beside the row, three shuffles, the stores.
+// 4000 rows of 8 heads of 128, fp32: written 11 us, 37 MB (with every value's checks for infinities and NaN before the
+// group's instead of beside it, divisions of 64 bits for its place and an exact reciprocal: 15 us; two or four vectors a
+// thread at a time: no faster), read back 9.4 us.  A few rows take 3 us each, a chain of latencies: a launch, the slot
+// beside the row, three shuffles, the stores; lengths, pages, codes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -76,103 +78,116 @@ struct AppendParams {
     const long long *slots;
     const void *src[2];
     long long stride[2];
-    int rows, block_log2, dim_log2;
+    long long items;        // rows' keys and values: 2 rows
+    int items_cta;          // of a CTA, whose vectors of eight values go over them one after another
+    uint32_t by_row;        // 2^32 over a row's vectors, rounded up: exact for a CTA's (0: one item only)
+    int block_log2, dim_log2;
     int *status;
 };
 
-// One vector of eight values a thread, rows and keys and values one after another: an item is a row's keys or values.
-template <typename T, int AT>
+// Eight values of a group whose smallest and largest (whole numbers only) its eight lanes share: scale, bias, codes.
+// plain: no value is NaN, infinite or past 2^126, so that none lies outside of [lo, hi].
+__device__ __forceinline__ uint32_t codes_of(float (&x)[8], float lo, float hi, bool plain, float &scale, float &bias) {
+    bias = bf16_below(lo);
+    float b = bias, sc;
+    if (hi - bias < 1e-25f) {
+        // (So small numbers are scaled up first, out of the reach of subnormals; values are below 1e-17 then, or all alike.)
+        constexpr float m = 18446744073709551616.f;                  // 2^64
+        scale = hi > bias ? fmaxf(bf16_above(__fmul_rn(scale_of(bias * m, hi * m), 1.f / m)), 0x1p-133f) : 0.f;
+        b = bias * m, sc = scale * m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= m;
+    } else {
+        sc = scale = scale_of(bias, hi);
+    }
+    // x - bias over scale, rounded by a sum with 1.5 * 2^23: within 4e-6 of the true quotient (2^-24 of the difference,
+    // 2^-23 of the reciprocal and 2^-24 of their product, of up to 15).
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sc));
+    if (sc == 0.f) inv = 0.f;
+    float q[8], far = 0.f;
+    // The sums' low bits are the codes; what their high bits, 0x4B400000 each, add to the word is taken off first.
+    uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = __fmul_rn(__fsub_rn(x[i], b), inv);
+        if (!plain) q[i] = fminf(fmaxf(q[i], 0.f), 15.f);
+        const float r = __fadd_rn(q[i], 12582912.f);
+        far = fmaxf(far, fabsf(__fsub_rn(q[i], __fsub_rn(r, 12582912.f))));
+        word += __float_as_uint(r) * (1u << (4 * i));
+    }
+    if (far > 0.49999f) {
+        // Nearly the middle of two codes for some value: there the middle (exact) is compared with the exact difference.
+        word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float left;
+            const float r = rintf(q[i]), low = floorf(q[i]), d = minus(x[i], b, left), mid = __fmul_rn(low + 0.5f, sc);
+            const bool up = d > mid || (d == mid && (left > 0.f || (left == 0.f && ((int)low & 1))));
+            const int code = fabsf(q[i] - r) > 0.49999f ? (int)low + up : (int)r;
+            word |= (uint32_t)code << (4 * i);
+        }
+    }
+    return word;
+}
+
+// A vector of eight values a thread; items are a row's keys or its values.
+template <typename T>
 __global__ void __launch_bounds__(THREADS) kv4_append_kernel(const AppendParams P) {
     const tf_kv4 &kv = P.kv;
     const int H = kv.kv_heads, BL = P.block_log2, DL = P.dim_log2;
-    const int per = H << (DL - 3), lane = threadIdx.x & 31;          // vectors of a row (a multiple of 8: a group's lanes stay together)
-    const long long all = 2LL * per * P.rows, step = (long long)gridDim.x * THREADS;
-    const long long v0 = blockIdx.x * (long long)THREADS + threadIdx.x;
-    for (long long base = v0 - lane; base < all; base += AT * step) {           // (warps stay whole)
-        float x[AT][8];
-        long long slot[AT];
-        int side[AT], c[AT];
+    const int per = H << (DL - 3);               // vectors of an item (a multiple of 8: a group's lanes stay together)
+    const long long item0 = (long long)blockIdx.x * P.items_cta;
+    const int all = (int)min((long long)P.items_cta, P.items - item0) * per;
+    const int n = blockIdx.y * THREADS + threadIdx.x, in = P.by_row ? (int)__umulhi((uint32_t)n, P.by_row) : 0;
+    const long long item = item0 + in, row = item >> 1;
+    const int side = (int)(item & 1), c = n - in * per;
+    float x[8] = {};
+    long long slot = -1;
+    if (n < all) {
+        slot = P.slots[row];
+        const T *src = static_cast<const T *>(side ? P.src[1] : P.src[0]);
+        const long long stride = side ? P.stride[1] : P.stride[0];
+        const bool vec = ((reinterpret_cast<uintptr_t>(src) | (stride * sizeof(T))) & 15) == 0;
+        load8<T>(src + row * stride + 8 * c, vec, x);
+    }
+    float lo = x[0], hi = x[0], zero = 0.f;
 #pragma unroll
-        for (int k = 0; k < AT; ++k) {
-            const long long v = base + lane + k * step;
-            slot[k] = -1;
-            if (v < all) {
-                const long long item = v / per;
-                const int row = (int)(item >> 1);
-                side[k] = (int)(item & 1);
-                c[k] = (int)(v - item * per);
-                slot[k] = P.slots[row];
-                const T *src = static_cast<const T *>(side[k] ? P.src[1] : P.src[0]);
-                const long long stride = side[k] ? P.stride[1] : P.stride[0];
-                const bool vec = ((reinterpret_cast<uintptr_t>(src) | (stride * sizeof(T))) & 15) == 0;
-                load8<T>(src + row * stride + 8 * c[k], vec, x[k]);
-            } else {
-                side[k] = c[k] = 0;
+    for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        zero = fmaf(x[i], 0.f, zero);            // (NaN of an infinity or a NaN)
+    }
+    const bool plain = zero == 0.f && lo >= -MOST && hi <= MOST;
+    if (!plain) {
+        lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < AT; ++k) {
-            float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = x[k][i];
-                const bool whole = fabsf(y) < INFINITY;
-                x[k][i] = y == y ? fminf(fmaxf(y, -MOST), MOST) : 0.f;
-                lo = fminf(lo, whole ? x[k][i] : INFINITY);
-                hi = fmaxf(hi, whole ? x[k][i] : -INFINITY);
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-            }
-            if (lo == INFINITY) lo = hi = 0.f;                       // no finite value
-            const float bias = bf16_below(lo);
-            float scale, m = 1.f;
-            if (hi - bias < 1e-25f) {
-                // (So small numbers are scaled up first, out of the reach of subnormals; values are below 1e-17 then, or all alike.)
-                m = 18446744073709551616.f;                          // 2^64
-                scale = hi > bias ? fmaxf(bf16_above(__fmul_rn(scale_of(bias * m, hi * m), 1.f / m)), 0x1p-133f) : 0.f;
-            } else {
-                scale = scale_of(bias, hi);
-            }
-            // x - bias over scale, rounded by a sum with 1.5 * 2^23: within 4e-6 of the true quotient.
-            const float b = bias * m, sc = scale * m, inv = scale > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
-            uint32_t word = 0;
-            float q[8], far = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q[i] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[k][i] * m, b), inv), 0.f), 15.f);
-                const float r = __fadd_rn(q[i], 12582912.f);
-                far = fmaxf(far, fabsf(__fsub_rn(q[i], __fsub_rn(r, 12582912.f))));
-                word |= (__float_as_uint(r) & 15u) << (4 * i);
-            }
-            if (far > 0.49999f) {
-                // Nearly the middle of two codes for some value: there the middle (exact) is compared with the exact difference.
-                word = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float left;
-                    const float r = rintf(q[i]), low = floorf(q[i]), d = minus(x[k][i] * m, b, left), mid = __fmul_rn(low + 0.5f, sc);
-                    const bool up = d > mid || (d == mid && (left > 0.f || (left == 0.f && ((int)low & 1))));
-                    const int code = fabsf(q[i] - r) > 0.49999f ? (int)low + up : (int)r;
-                    word |= (uint32_t)code << (4 * i);
-                }
-            }
-            if (slot[k] < 0 || slot[k] >= (long long)kv.n_blocks << BL) {
-                if (slot[k] != -1) atomicOr(P.status, STATUS_BOUNDS);
-                continue;
-            }
-            const int h = c[k] >> (DL - 3), d = c[k] & ((1 << (DL - 3)) - 1);
-            const long long at = ((((slot[k] >> BL) * H + h) << BL) + (slot[k] & (kv.block - 1)));
-            reinterpret_cast<uint32_t *>(side[k] ? kv.v : kv.k)[(at << (DL - 3)) + d] = word;
-            if ((d & 7) == 0)
-                reinterpret_cast<uint32_t *>(side[k] ? kv.v_affine : kv.k_affine)[(at << (DL - 6)) + (d >> 3)] =
-                    (__float_as_uint(scale) >> 16) | (__float_as_uint(bias) & 0xFFFF0000u);
+        for (int i = 0; i < 8; ++i) {
+            const float y = x[i];
+            const bool whole = fabsf(y) < INFINITY;
+            x[i] = y == y ? fminf(fmaxf(y, -MOST), MOST) : 0.f;
+            lo = fminf(lo, whole ? x[i] : INFINITY);
+            hi = fmaxf(hi, whole ? x[i] : -INFINITY);
         }
     }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+    }
+    if (lo == INFINITY) lo = hi = 0.f;           // no finite value
+    float scale, bias;
+    const uint32_t word = codes_of(x, lo, hi, plain, scale, bias);
+    if (slot < 0 || slot >= (long long)kv.n_blocks << BL) {
+        if (slot != -1) atomicOr(P.status, STATUS_BOUNDS);
+        return;
+    }
+    const int h = c >> (DL - 3), d = c & ((1 << (DL - 3)) - 1);
+    const long long at = ((((slot >> BL) * H + h) << BL) + (slot & (kv.block - 1)));
+    reinterpret_cast<uint32_t *>(side ? kv.v : kv.k)[(at << (DL - 3)) + d] = word;
+    if ((d & 7) == 0)
+        reinterpret_cast<uint32_t *>(side ? kv.v_affine : kv.k_affine)[(at << (DL - 6)) + (d >> 3)] =
+            (__float_as_uint(scale) >> 16) | (__float_as_uint(bias) & 0xFFFF0000u);
 }
 
 struct ReadParams {
@@ -184,9 +199,9 @@ struct ReadParams {
     int block_log2, dim_log2;
     int *status;
 };
-constexpr int READ_ROWS = 8;
+constexpr int READ_ROWS = 4;
 
-// One CTA a (sequence, 8 of its rows, keys or values); a thread a word of codes, eight values of a row, of all those rows at once.
+// One CTA a (sequence, READ_ROWS of its rows, keys or values); a thread a word of codes, eight values of a row, of all those rows at once.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) kv4_read_kernel(const ReadParams P) {
     const tf_kv4 &kv = P.kv;
@@ -293,23 +308,18 @@ extern "C" int tf_kv4_append(const tf_kv4 *kv, const int64_t *slots, int rows, c
     int nsm = 0, *status = nullptr;
     rc = device_info(&nsm, &status);
     if (rc) return rc;
-    const AppendParams P{*kv, reinterpret_cast<const long long *>(slots), {k, v}, {k_stride, v_stride}, rows, __builtin_ctz(kv->block),
-                         __builtin_ctz(kv->dim), status};
-    const long long ctas = (2LL * rows * (width / 8) + THREADS - 1) / THREADS;
+    // A CTA has as many items as give its threads a vector each, or a part of one (blockIdx.y).
+    const int per = width / 8, items = per >= THREADS ? 1 : THREADS / per;
+    const AppendParams P{*kv, reinterpret_cast<const long long *>(slots), {k, v}, {k_stride, v_stride}, 2LL * rows, items,
+                         items == 1 ? 0u : (uint32_t)((0x100000000ull + per - 1) / per), __builtin_ctz(kv->block), __builtin_ctz(kv->dim), status};
+    const long long ctas = (2LL * rows + items - 1) / items;
+    if (ctas > 0x7FFFFFFF) return fail_message(TF_EINVAL_ROWS, "too many rows in one call");
+    const dim3 grid((unsigned)ctas, (unsigned)((per * items + THREADS - 1) / THREADS));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // Two vectors a thread at a time once every SM has a few CTAs of them.
-    if (ctas >= 16LL * nsm) {
-        const unsigned grid = (unsigned)min((ctas + 1) / 2, 0x7FFFFFFFLL);
-        if (f32)
-            kv4_append_kernel<float, 2><<<grid, THREADS, 0, st>>>(P);
-        else
-            kv4_append_kernel<__nv_bfloat16, 2><<<grid, THREADS, 0, st>>>(P);
-    } else {
-        if (f32)
-            kv4_append_kernel<float, 1><<<(unsigned)ctas, THREADS, 0, st>>>(P);
-        else
-            kv4_append_kernel<__nv_bfloat16, 1><<<(unsigned)ctas, THREADS, 0, st>>>(P);
-    }
+    if (f32)
+        kv4_append_kernel<float><<<grid, THREADS, 0, st>>>(P);
+    else
+        kv4_append_kernel<__nv_bfloat16><<<grid, THREADS, 0, st>>>(P);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TF_OK : cuda_error(e, "kv4_append launch");
 }
