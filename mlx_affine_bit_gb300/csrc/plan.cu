@@ -22,6 +22,7 @@ using namespace tfq;
 namespace {
 
 constexpr int MAX_SEQS = 4096, MAX_THREADS = 1024, ROWS_HERE = 4096;
+constexpr int AT = 4;                    // pages that a thread looks at at once, and keeps
 
 struct PlanParams {
     tf_kv_pages p;
@@ -98,16 +99,21 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const PlanParams P, b
     stands = __reduce_max_sync(~0u, stands);
     if (lane == 0) s_longest[0][warp] = longest, s_longest[1][warp] = stands;
     bad = __syncthreads_or(bad);
-    long long all[3] = {0, 0, 0};
-    for (int w = 0; w < nt / 32; ++w) {
+    // (The warps' sums, in every warp again: a loop over 32 of them takes 2 us.)
+    const bool there = lane < nt / 32;
+    longest = __reduce_max_sync(~0u, there ? s_longest[0][lane] : 0);
+    stands = __reduce_max_sync(~0u, there ? s_longest[1][lane] : 0);
+    long long all[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const long long x = s_sum[i][w];
-            if (w < warp) at[i] += x;
-            all[i] += x;
+    for (int i = 0; i < 3; ++i) {
+        const long long own = there ? s_sum[i][lane] : 0;
+        long long x = own;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
         }
-        longest = max(longest, s_longest[0][w]);
-        stands = max(stands, s_longest[1][w]);
+        all[i] = __shfl_sync(~0u, x, 31);
+        at[i] += __shfl_sync(~0u, x - own, warp);
     }
     bad = bad || all[0] > ((P.positions || P.slots) ? P.rows : INT_MAX) || n_free + all[2] > P.p.n_blocks;
     // (From here on every sum fits 32 bits: no more pages are given back than the pool has, and of pages taken no
@@ -128,36 +134,43 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const PlanParams P, b
     __syncthreads();
     auto had = [&](int s) { return (P.p.kv_len[s] + P.p.block - 1) >> BL; };
     auto has = [&](int s) { return (P.p.kv_len[s] + P.change[s] + P.p.block - 1) >> BL; };
-    // The k-th page given back: its entry of the table.
+    // The k-th page given back: its entry of the table.  It goes to the stack's place top - 1 - k, and from there, if as
+    // many are taken, to the k-th place that needs one.
     auto left = [&](int k) {
         const int s = last_at(s_gone, n, k);
         return P.p.table + s * P.p.table_stride + has(s) + (k - s_gone[s]);
     };
-    // Every number is looked at before any is changed.
+    auto page_at = [&](int k) { return k < gone ? *left(k) : P.p.free_pages[top - 1 - k]; };
+    auto move = [&](int k, int page) {
+        if (k < gone) {
+            P.p.free_pages[top - 1 - k] = page;
+            *left(k) = -1;
+        }
+        if (k < more) {
+            const int s = last_at(s_more, n, k);
+            P.p.table[s * P.p.table_stride + had(s) + (k - s_more[s])] = page;
+        }
+    };
+    // Every number is looked at before any is changed.  (No thread reads what another one changes: sequences give pages
+    // back or take some, and those that are taken from under the ones given back lie below them on the stack.)
+    const int moved = bad || few ? 0 : max(gone, more);
+    int page[AT];
     bool wrong = false;
-    if (!bad && !few) {
-        for (int k = tid; k < gone; k += nt) {
-            const int page = *left(k);
-            wrong |= page < 0 || page >= P.p.n_blocks;
-        }
-        for (int k = tid + gone; k < more; k += nt) {
-            const int page = P.p.free_pages[top - 1 - k];
-            wrong |= page < 0 || page >= P.p.n_blocks;
-        }
+#pragma unroll
+    for (int i = 0; i < AT; ++i) page[i] = tid + i * nt < moved ? page_at(tid + i * nt) : 0;
+#pragma unroll
+    for (int i = 0; i < AT; ++i) wrong |= page[i] < 0 || page[i] >= P.p.n_blocks;
+    for (int k = tid + AT * nt; k < moved; k += nt) {
+        const int x = page_at(k);
+        wrong |= x < 0 || x >= P.p.n_blocks;
     }
     bad = __syncthreads_or(wrong) || bad;
     const bool go = !bad && !few;
     if (go) {
-        for (int k = tid; k < gone; k += nt) {
-            int32_t *entry = left(k);
-            P.p.free_pages[top - 1 - k] = *entry;
-            *entry = -1;
-        }
-        if (gone) __syncthreads();
-        for (int k = tid; k < more; k += nt) {
-            const int s = last_at(s_more, n, k);
-            P.p.table[s * P.p.table_stride + had(s) + (k - s_more[s])] = P.p.free_pages[top - 1 - k];
-        }
+#pragma unroll
+        for (int i = 0; i < AT; ++i)
+            if (tid + i * nt < moved) move(tid + i * nt, page[i]);
+        for (int k = tid + AT * nt; k < moved; k += nt) move(k, page_at(k));
     }
     __syncthreads();                             // (the lengths have been read)
     int *const starts = s_gone;
