@@ -156,8 +156,13 @@ __device__ __forceinline__ float out_factor(const RowSum &a) { return a.l == 0.f
 // Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q
 // take.  48 sequences of up to 8000 tokens, 8 heads of 128: 79 us so, 81 with one tile a stage and four stages, 83
 // with three stages and two CTAs; one of 131072 tokens 52, 54 and 50.
+// 4 bits: as many CTAs as keep the step's registers: 48 x 8000 tokens of 8 heads of 128, 16 rows each: 153 us with two, 178
+// with three, whose step keeps 400 bytes in local memory; 16 x 8000 of one head of 64, 16 rows: 19 us with three, 25 with
+// four.  One row of each, 8 heads of 128: 63 us with three and three stages, 65 with four and two.
 TFQ_HD constexpr int stages(int f, int d) { return f == 4 ? (d == 256 ? 5 : d == 128 ? 3 : 4) : d == 256 ? 3 : 2; }
-TFQ_HD constexpr int ctas(int d, int nt) { return d == 64 ? (nt == 1 ? 5 : 4) : d == 128 ? 3 : 2; }
+TFQ_HD constexpr int ctas(int f, int d, int nt) {
+    return f == 4 ? (d == 64 ? 5 - nt : d == 128 ? 4 - nt : 2) : d == 64 ? (nt == 1 ? 5 : 4) : d == 128 ? 3 : 2;
+}
 TFQ_HD constexpr int tile_bytes(int f, int d) { return 4 * f * d; }     // 16 tokens of keys and of values
 TFQ_HD constexpr int affine_bytes(int f, int d) { return f == 4 ? 2 * d : 0; }   // ... and their scales and biases
 TFQ_HD constexpr int out_pitch(int d) { return d + 4; }            // floats between joined rows
@@ -568,7 +573,7 @@ struct Rows4 {
 
 // F: bits of a code (8 or 4).
 template <int F, int D, int NT>
-__global__ void __launch_bounds__(THREADS, ctas(D, NT)) rows_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __grid_constant__ Params P) {
     constexpr int R = 8 * NT;                    // rows of a tile
     constexpr int KV = D / 64;                   // vectors of a key a lane: its 16 of each 64 values
     constexpr int MT = D / 16;                   // m tiles of the transposed values
