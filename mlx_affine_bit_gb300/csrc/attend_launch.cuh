@@ -154,8 +154,14 @@ int call(Params &P, const tf_kv_batch *batch, const void *q, int64_t q_stride, i
         const int pair = 128 * p_tiles(kv->dim);
         const double pairs = (double)((max_group_rows + pair - 1) / pair), items = (double)batch->n_seqs * kv->kv_heads * pairs;
         const double ctas = std::min((double)nsm, items * MAX_SHARE);
-        const double t_rows = 12e3 + 6.5 * blocks * (double)((max_group_rows + 15) / 16) * kv->dim / 128;
-        const double t_prompt = 45e3 + 2900.0 * blocks * pairs / ctas;
+        // 4 bits: the same, over 17 to 512 rows of 1, 4 and 16 sequences of 1000, 4000 and 60000 tokens; times by the dimension.
+        // 128 rows of 16 x 4000 tokens, 8 heads of 128: 207 against 110 us; of 1 x 60000: 172 against 190; 64 rows of 16 x
+        // 4000, 2 heads of 256: 77 against 57, of 1 x 60000: 75 against 181; 128 rows of 4 x 1000, 16 heads of 64: 36 and 29.
+        const int at = kv->dim / 128;
+        constexpr double ROWS_STEP[] = {3.9, 5.8, 12.3}, TILES_CALL[] = {26e3, 30e3, 38e3}, TILES_STEP[] = {2300.0, 2900.0, 2600.0};
+        const double row_tiles = (double)((max_group_rows + 15) / 16);
+        const double t_rows = F == 4 ? 18e3 + ROWS_STEP[at] * blocks * row_tiles : 12e3 + 6.5 * blocks * row_tiles * kv->dim / 128;
+        const double t_prompt = F == 4 ? TILES_CALL[at] + TILES_STEP[at] * blocks * pairs / ctas : 45e3 + 2900.0 * blocks * pairs / ctas;
         prompt = t_prompt < t_rows;
     }
     // Rows kernel: tiles of 8 rows where no sequence has more a head (4 rows of 48 x 4000 tokens, 8 heads of 128: 71 us,

@@ -1,5 +1,5 @@
-// attend_rows.cuh -- attention of few rows (single tokens, drafts) over the
-// 8-bit paged cache.
+// attend_rows.cuh -- attention of few rows (single tokens, drafts) over the 8-bit
+// paged cache, and (from Rows4 on, where it differs) over that of 4 bits.
 //
 // For the rows r of one (sequence, key/value head) -- G query heads a token --
 // and the tokens j they see:
@@ -303,9 +303,10 @@ __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
 // or bias)), transposed in the warp, with the codes transposed by the loads (four of a token at a time); the biases' part in fp32.
 // The maxima m and d are joined over the warp's lanes only where a lane finds one passed by more than SLACK4.
 //
-// Bound by the issue of instructions and the latency between them: 48 x 8000 tokens of 8 heads of 128, 32 query heads, 71 us, 1 x 131000
-// tokens 44 us (with the rows of q as the first product's 16 rows, maxima joined at every step and the biases' sums in fp32:
-// 84 and 53 us).
+// 48 x 8000 tokens of 8 heads of 128, 32 query heads, 63 us; 1 x 131000 tokens 41 us, 5.5 TB/s of the cache while its tokens
+// run (27 us), after a beginning of 6 us and before a join of up to 8.  With the rows of q as the first product's 16 rows,
+// maxima joined at every step and the biases' sums in fp32: 84 and 53 us; with the codes by plain loads, put together by byte
+// permutes: 71 and 44.  (The next tokens' scores beside these tokens' exponentials, and shifts as products: no faster.)
 constexpr float SLACK4 = 1.f;            // in powers of two (w stays below fp16's largest: 2^18 / 15 times 2^SLACK4)
 template <int D, int NT>
 struct Rows4 {
@@ -854,31 +855,38 @@ __global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __g
                 open_chunk();
                 __syncthreads();
             }
-            for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
+            auto next_stage = [&]() {                // the codes of the tokens whose turn it is, and a fetch in place of the last ones
                 if (lane == 0) fetch(ft);
                 ft += STEP;
                 if (!mbar_try(&bar[it % NST], (it / NST) & 1)) {
                     if (!*abort) mbar_wait(&bar[it % NST], (it / NST) & 1, abort, P.status);
                     if (*abort) ft = NO_TOKEN;       // (a wait ran out: nothing more is fetched, the stages may be on their way)
                 }
-                const uint8_t *tiles = mine + (it % NST) * STAGE;
-                // Tiles t and t + 16: their pages (a tile of no page is not seen).
-                auto page_of = [&](int h) { return min(((t + 16 * h) >> BL) - pg0, npages - 1); };
-                auto there = [&](int h) { return s_page[page_of(h)] >= 0 && !(h == 1 && single && t + 16 >= c1); };
-                if constexpr (F == 4) {
-                    const bool full = t >= all_from && t + TP <= all_to && !holes;
+                return mine + (it % NST) * STAGE;
+            };
+            if constexpr (F == 4) {
+                for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
+                    const uint8_t *tiles = next_stage();
                     const uint32_t *const pairs = reinterpret_cast<const uint32_t *>(mine_affine + (it % NST) * AFFINE);
+                    const bool full = t >= all_from && t + TP <= all_to && !holes;
+                    // (a tile of no page is not seen)
+                    auto there = [&](int h) { return s_page[min(((t + 16 * h) >> BL) - pg0, npages - 1)] >= 0 && !(h == 1 && single && t + 16 >= c1); };
                     rows4.step(
                         tiles, tiles + STAGE / 2, pairs, pairs + AFFINE / 8, at4, lr, sq, lr, lc, full,
                         [&](int i) { return there(i < 16 ? 0 : 1) && t + i >= any_from && t + i < to; },
                         [&](int r, int i) { return t + i >= s_see[r].x && t + i < s_see[r].y; });
                     __syncwarp();                    // (every lane has read the stage that is filled next)
-                    continue;
                 }
+            } else for (int t = c0 + TP * warp; t < c1; t += STEP, ++it) {
+                const uint8_t *tiles = next_stage();
+                // Tiles t and t + 16: their pages (a tile of no page is not seen).
                 int pi[TILES];
                 bool on[TILES];
 #pragma unroll
-                for (int h = 0; h < TILES; ++h) pi[h] = page_of(h), on[h] = there(h);
+                for (int h = 0; h < TILES; ++h) {
+                    pi[h] = min(((t + 16 * h) >> BL) - pg0, npages - 1);
+                    on[h] = s_page[pi[h]] >= 0 && !(h == 1 && single && t + 16 >= c1);
+                }
                 const bool full = t >= all_from && t + TP <= all_to && on[0] && on[TILES - 1];
                 // Scores of the tiles' tokens: n tile 2 h + nb holds tokens t + 16 h + 8 nb + ...
                 float sc[2 * TILES][4];
