@@ -1,7 +1,7 @@
 """Generation with the library's parts together: quantized products, the 8-bit
 paged cache, attention over it and the sampling of tokens.
 
-    python -m mlx_affine_bit_gb300.decode [--seqs 8] [--prompt 500] [--tokens 64] [--layers 4]
+    python -m mlx_affine_bit_gb300.decode [--seqs 8] [--prompt 500] [--tokens 64] [--layers 4] [--serving]
 
 A small decoder of random weights (attention blocks without positions or norms, and
 a language-model head) takes a ragged batch of prompts in one step and then a token
@@ -15,6 +15,12 @@ a sequence and step.  A step of a layer is four calls:
 and ends in tf.qmm with the head and tf.sample.  Lengths, page tables and tokens stay
 on the device, so that a whole step of single tokens is one CUDA graph.  The script
 prints the first tokens and the time of a step, launched call by call and as a graph.
+
+ServingDecoder (--serving) has positions and caches of 4 bits, whose pages the device
+hands out as sequences grow: a plan at the beginning of a step, and in each layer
+
+    turn(q | k, positions)   in place, after the product
+    cache.append(k, v, slots)
 """
 from __future__ import annotations
 
@@ -61,9 +67,23 @@ class Decoder:
         self.out = [Matrix.random(width, heads * dim, bits, group, gen) for _ in range(layers)]
         self.head = Matrix.random(vocab, width, bits, group, gen)
         pages = (max_len + block - 1) // block
-        self.caches = [tf.KvCache.empty(seqs * pages, kv_heads, dim, block, seqs, torch.float32, device) for _ in range(layers)]
+        self.make_caches(layers, pages, block, device)
+
+    def make_caches(self, layers, pages, block, device):
+        self.caches = [tf.KvCache.empty(self.seqs * pages, self.kv_heads, self.dim, block, self.seqs, torch.float32, device)
+                       for _ in range(layers)]
         # Pages in any order: here those of the sequences in turn.
-        self.table = torch.arange(seqs * pages, dtype=torch.int32, device=device).view(pages, seqs).t().contiguous()
+        self.table = torch.arange(self.seqs * pages, dtype=torch.int32, device=device).view(pages, self.seqs).t().contiguous()
+
+    def begin(self, counts):
+        """New sequences of so many tokens: what step() takes for all of them, for a token each, and what makes them a
+        token longer."""
+        dev = self.embed.device
+        lengths = torch.tensor(counts, dtype=torch.int32, device=dev)
+        starts = torch.zeros(self.seqs + 1, dtype=torch.int32, device=dev)
+        starts[1:] = lengths.cumsum(0)
+        prompt = tf.KvBatch(lengths, self.table, self.max_len, row_start=starts, rows=sum(counts), max_rows=max(counts))
+        return prompt, tf.KvBatch(lengths, self.table, self.max_len), lambda: lengths.add_(1)      # (read by the device at each call)
 
     def step(self, tokens, batch, last=None):
         """Logits [seqs][vocab] after the batch's rows of tokens; last: each sequence's last row (every row if None)."""
@@ -93,24 +113,19 @@ class Decoder:
             torch.cuda.current_stream().wait_stream(side)
             result[0].record_stream(torch.cuda.current_stream())
             return result
-        dev, seqs = self.table.device, len(prompts)
+        dev, seqs = self.embed.device, len(prompts)
         gen = torch.Generator(device=dev).manual_seed(seed)
         u = torch.rand((n, seqs), generator=gen, device=dev)
         row_u = torch.empty(seqs, device=dev)
         how = dict(temperature=torch.full((seqs,), temperature, device=dev), top_p=torch.full((seqs,), top_p, device=dev),
                    top_k=torch.full((seqs,), top_k, dtype=torch.int32, device=dev))
-        lengths = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device=dev)
-        starts = torch.zeros(seqs + 1, dtype=torch.int32, device=dev)
-        starts[1:] = lengths.cumsum(0)
-        rows = sum(map(len, prompts))
-        logits = self.step(torch.tensor([t for p in prompts for t in p], device=dev),
-                           tf.KvBatch(lengths, self.table, self.max_len, row_start=starts, rows=rows, max_rows=max(map(len, prompts))),
-                           starts[1:].long() - 1)
+        counts = [len(p) for p in prompts]
+        prompt, single, grow = self.begin(counts)
+        logits = self.step(torch.tensor([t for p in prompts for t in p], device=dev), prompt, torch.tensor(counts, device=dev).cumsum(0) - 1)
         tokens, _ = tf.sample(logits, u[0], **how)
-        single = tf.KvBatch(lengths, self.table, self.max_len)
 
         def advance():
-            lengths.add_(1)                      # (read by the device at each call)
+            grow()
             tf.sample(self.step(tokens, single), row_u, tokens=tokens, **how)
 
         result, g, seconds = [tokens.clone()], None, 0.0
@@ -134,17 +149,46 @@ class Decoder:
         return torch.stack(result), seconds
 
 
+class ServingDecoder(Decoder):
+    """A Decoder with rotary positions over caches of 4 bits; pages: the KvPages of its sequences, one for all layers."""
+
+    def make_caches(self, layers, pages, block, device):
+        self.pages = tf.KvPages.empty(self.seqs, self.seqs * pages, pages, block, device)
+        self.caches = [tf.Kv4Cache.empty(self.pages.n_blocks, self.kv_heads, self.dim, block, device) for _ in range(layers)]
+        self.turn = tf.Rope(self.dim, device=device)
+
+    def begin(self, counts):
+        dev = self.embed.device
+        self.pages.plan(0).step(-self.pages.kv_len)              # (the sequences before give their pages back)
+        prompt, single = self.pages.plan(sum(counts), max(counts), self.max_len), self.pages.plan(self.seqs, 1, self.max_len)
+        prompt.step(torch.tensor(counts, dtype=torch.int32, device=dev))
+        one = torch.ones(self.seqs, dtype=torch.int32, device=dev)
+        return prompt, single, lambda: single.step(one)
+
+    def step(self, tokens, plan, last=None):
+        x = self.embed[tokens]
+        nq, nk = self.heads * self.dim, self.kv_heads * self.dim
+        for qkv, out, cache in zip(self.qkv, self.out, self.caches):
+            y = qkv(x)
+            self.turn(y[:, :nq + nk], plan.positions, out=y[:, :nq + nk])
+            cache.append(y[:, nq:nq + nk], y[:, nq + nk:], plan.slots)
+            a = cache.attend(y[:, :nq], plan.batch)
+            x = (x.float() + out(a)).to(torch.bfloat16)
+        return self.head(x if last is None else x[last])
+
+
 def main():
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     p.add_argument("--seqs", type=int, default=8)
     p.add_argument("--prompt", type=int, default=500, help="tokens of the longest prompt")
     p.add_argument("--tokens", type=int, default=64)
     p.add_argument("--layers", type=int, default=4)
+    p.add_argument("--serving", action="store_true", help="positions, caches of 4 bits, pages handed out on the device")
     a = p.parse_args()
     prompts = [[(31 * s + 7 * i) % 4096 for i in range(max(1, a.prompt - 37 * s))] for s in range(a.seqs)]
     with torch.cuda.stream(torch.cuda.Stream()):
         for graph in (False, True):
-            d = Decoder(layers=a.layers, seqs=a.seqs, max_len=a.prompt + a.tokens)
+            d = (ServingDecoder if a.serving else Decoder)(layers=a.layers, seqs=a.seqs, max_len=a.prompt + a.tokens)
             tokens, seconds = d.generate(prompts, a.tokens, graph=graph)
             print("%s: %.0f us a step of %d tokens; sequence 0: %s" %
                   ("one graph a step" if graph else "call by call", seconds * 1e6, a.seqs, tokens[:12, 0].tolist()))
