@@ -53,7 +53,7 @@ int launch_rows(Params &P, long long steps, int nsm, cudaStream_t st) {
     if (rc) return rc;
     P.part = w.part;
     P.count = w.count;
-    P.item_steps = steps > grid ? ITEM_ROWS : 0;
+    P.item_steps = steps > grid ? item_rows(D) : 0;
     rows_kernel<F, D, NT><<<(unsigned)grid, THREADS, smem_bytes(F, D, NT), st>>>(P);
     e = cudaGetLastError();
     return e == cudaSuccess ? TF_OK : cuda_error(e, "kv_attend launch");

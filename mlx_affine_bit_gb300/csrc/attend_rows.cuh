@@ -60,7 +60,8 @@ TFQ_HD constexpr int step_of(int d) { return 16 * tiles_of(d) * WARPS; }
 constexpr int CHUNK_TOKENS = 4096;       // tokens whose pages and scales a CTA keeps at a time
 constexpr int MAX_PAGES = CHUNK_TOKENS / 16;
 constexpr int MAX_PARTS = 768;           // CTAs of a launch, at most
-constexpr int ITEM_ROWS = 3;             // an item's beginning and end, in steps (4 bits)
+// An item's beginning and end, in steps (4 bits).  48 x 8000 tokens of 8 heads of 128: 63 us so, 70 with 0, 64 with 5.
+TFQ_HD constexpr int item_rows(int d) { return d == 256 ? 6 : 3; }
 constexpr int NO_TOKEN = 1 << 30;        // past every chunk
 constexpr float W_EXP = 15.f;            // exponent offset of w in fp16
 // ... by the cache's bits: of 4, w is p times the scale of a code, at most a 15th of what d stands for.
@@ -1107,20 +1108,25 @@ __global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __g
                 if (tid == 0) P.count[c_first] = 0;
                 // The row sums of all parts (in s_join) and the parts' factors, a warp a row.
                 float(*s_fac)[R] = reinterpret_cast<float(*)[R]>(ring);      // (the outputs in the ring have been read)
-                for (int r = warp; r < rows; r += WARPS) {
-                    auto sum_of = [&](int k) {
-                        const float4 x = __ldcg(sums + slot(k) * R + r);
-                        return RowSum{x.x, x.y, x.z, 0.f};
-                    };
-                    // (a lane's first parts' in one round of loads)
-                    constexpr int AT = 3;
-                    RowSum own[AT];
+                // (a lane's first parts' of all the warp's rows in one round of loads)
+                constexpr int ROWS = R / WARPS, AT = 2;
+                auto sum_of = [&](int r, int k) {
+                    const float4 x = __ldcg(sums + slot(k) * R + r);
+                    return RowSum{x.x, x.y, x.z, 0.f};
+                };
+                RowSum own[ROWS][AT];
 #pragma unroll
-                    for (int i = 0; i < AT; ++i) own[i] = sum_of(min(lane + 32 * i, parts - 1));
-                    RowSum a = own[0];
+                for (int j = 0; j < ROWS; ++j)
 #pragma unroll
-                    for (int i = 1; i < AT; ++i) join_maxima(a, own[i]);
-                    for (int k = lane + 32 * AT; k < parts; k += 32) join_maxima(a, sum_of(k));
+                    for (int i = 0; i < AT; ++i) own[j][i] = sum_of(min(warp + j * WARPS, rows - 1), min(lane + 32 * i, parts - 1));
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j) {
+                    const int r = warp + j * WARPS;
+                    if (r >= rows) break;
+                    RowSum a = own[j][0];
+#pragma unroll
+                    for (int i = 1; i < AT; ++i) join_maxima(a, own[j][i]);
+                    for (int k = lane + 32 * AT; k < parts; k += 32) join_maxima(a, sum_of(r, k));
                     for (int o = 16; o > 0; o >>= 1) {
                         const float m = __shfl_xor_sync(~0u, a.m, o), d = __shfl_xor_sync(~0u, a.d, o);
                         join_maxima(a, RowSum{m, d, 0.f, 0.f});
@@ -1132,30 +1138,39 @@ __global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __g
                     };
 #pragma unroll
                     for (int i = 0; i < AT; ++i)
-                        if (lane + 32 * i < parts) take(lane + 32 * i, own[i]);
-                    for (int k = lane + 32 * AT; k < parts; k += 32) take(k, sum_of(k));
+                        if (lane + 32 * i < parts) take(lane + 32 * i, own[j][i]);
+                    for (int k = lane + 32 * AT; k < parts; k += 32) take(k, sum_of(r, k));
                     for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(~0u, a.l, o);
                     if (lane == 0) s_join[r] = a;
                 }
                 __syncthreads();
-                // The outputs, in the parts' order, JOIN loads at a time.
-                constexpr int JOIN = F == 4 ? 16 : 8;
-                for (int v = 4 * tid; v < rows * D; v += 4 * THREADS) {
-                    const int r = v / D;
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                // The outputs, in the parts' order, JOIN parts of AT_ONCE vectors a thread at a time.
+                constexpr int JOIN = F == 4 ? 16 : 8, AT_ONCE = F == 4 && D == 256 ? 2 : 1;
+                for (int v0 = 4 * tid; v0 < rows * D; v0 += 4 * THREADS * AT_ONCE) {
+                    float4 y[AT_ONCE];
+#pragma unroll
+                    for (int i = 0; i < AT_ONCE; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int k0 = 0; k0 < parts; k0 += JOIN) {
-                        float4 x[JOIN];
+                        float4 x[AT_ONCE][JOIN];
 #pragma unroll
-                        for (int k = 0; k < JOIN; ++k)
-                            x[k] = __ldcg(reinterpret_cast<const float4 *>(P.part + (long long)slot(min(k0 + k, parts - 1)) * R * D + v));
+                        for (int i = 0; i < AT_ONCE; ++i)
 #pragma unroll
-                        for (int k = 0; k < JOIN; ++k) {
-                            const float f = k0 + k < parts ? s_fac[min(k0 + k, parts - 1)][r] : 0.f;
-                            y.x = fmaf(x[k].x, f, y.x), y.y = fmaf(x[k].y, f, y.y);
-                            y.z = fmaf(x[k].z, f, y.z), y.w = fmaf(x[k].w, f, y.w);
-                        }
+                            for (int k = 0; k < JOIN; ++k)
+                                x[i][k] = __ldcg(reinterpret_cast<const float4 *>(P.part + (long long)slot(min(k0 + k, parts - 1)) * R * D + min(v0 + 4 * THREADS * i, rows * D - 4)));
+#pragma unroll
+                        for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+                            for (int k = 0; k < JOIN; ++k) {
+                                const float f = k0 + k < parts ? s_fac[min(k0 + k, parts - 1)][min(v0 + 4 * THREADS * i, rows * D - 4) / D] : 0.f;
+                                y[i].x = fmaf(x[i][k].x, f, y[i].x), y[i].y = fmaf(x[i][k].y, f, y[i].y);
+                                y[i].z = fmaf(x[i][k].z, f, y[i].z), y[i].w = fmaf(x[i][k].w, f, y[i].w);
+                            }
                     }
-                    store4(r, v % D, y, out_factor<F>(s_join[r]));
+#pragma unroll
+                    for (int i = 0; i < AT_ONCE; ++i) {
+                        const int v = v0 + 4 * THREADS * i;
+                        if (v < rows * D) store4(v / D, v % D, y[i], out_factor<F>(s_join[v / D]));
+                    }
                 }
             }
         }
