@@ -130,6 +130,29 @@ def test_numbers_that_do_not_fit_change_nothing(bad):
     assert all(torch.equal(a, b) for a, b in zip(state, (pages.table, pages.kv_len, pages.free_pages, pages.n_free)))
 
 
+def test_more_pages_than_a_pass_looks_at():
+    # 7000 pages and more move in a step, either way and both; a bad number far down the stack stops all of it.
+    rng = np.random.default_rng(9)
+    pages, plain = make(60, 260, 16, 16000, 9, gap=1)
+    plan = pages.plan(60 * 2000, 2000)
+    for low, high in ((1800, 2001), (1900, 2001), (-2000, -1800), (-1500, 2001)):
+        change = [max(-n, int(rng.integers(low, high))) for n in plain.kv_len]
+        want = plain.step(change, plan.rows, 2000, 260 * 16)
+        assert want[3][0] == 0
+        same(plan.step(ints(change)), pages, want, plain)
+    tf.tf_device_status()
+    change = [min(2000, 260 * 16 - n) for n in plain.kv_len]
+    taken = sum(-(-(n + c) // 16) - -(-n // 16) for n, c in zip(plain.kv_len, change))
+    assert 4500 < taken <= len(plain.free)
+    pages.free_pages[pages.n_free.item() - 1 - (taken - 2)] = 16000
+    state = [t.clone() for t in (pages.table, pages.kv_len, pages.free_pages, pages.n_free)]
+    plan.step(ints(change))
+    torch.cuda.synchronize()
+    with pytest.raises(tf.TfError):
+        tf.tf_device_status()
+    assert plan.info[0].item() == 2 and all(torch.equal(a, b) for a, b in zip(state, (pages.table, pages.kv_len, pages.free_pages, pages.n_free)))
+
+
 def test_slots_past_32_bits_and_outputs_left_out():
     # Page numbers of a pool of 2^26 pages of 128 tokens (none of it is touched); positions or slots alone.
     table = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
