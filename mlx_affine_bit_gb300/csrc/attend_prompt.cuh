@@ -1,5 +1,6 @@
 // attend_prompt.cuh -- attention of many rows (prompts, chunks of prompts) over the
-// 8-bit paged cache, on the fifth-generation tensor cores.
+// 8-bit or 4-bit paged cache, on the fifth-generation tensor cores.  (Over 4 bits keys and
+// values are widened to scale c + bias, over the largest of 16 tokens: `widened`, `over_unit`.)
 //
 // For the rows r of one (sequence, key/value head) -- G query heads a token -- and
 // the tokens j they see, with q_r in fp16 times a power of two:
@@ -20,7 +21,7 @@
 // of a prompt 201 us (652 TFLOP/s), 8000 646 us (812 TFLOP/s); 16 heads of 256: 4000
 // tokens 202 us; 16 heads of 64: 88 us; three chunks of up to 509 tokens, 16 heads of
 // 256, window 4096: 91 us (scores past FAR: 4000 tokens of 32 heads 323 us, the chunks
-// 136).  A step of two tiles (256 rows, 128 tokens, dim 128) takes
+// 136; all of them before tensor memory was taken later, which is 4 to 7 us off: 4000 tokens 198).  A step of two tiles (256 rows, 128 tokens, dim 128) takes
 // 2.7 us, 1.7 us of them the products: one with N = 128 takes 94 to 107 clocks for
 // 16 of K, measured alone, which is 60 to 68 % of the peak.  An item's beginning and
 // end (the rows of q, the first scores, the outputs) cost 6 us, the launch's plan 4.
@@ -314,10 +315,6 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         B.arrived = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
 
     // The line's length and this CTA's share: first the tile pairs of all sequences, thread by thread over the
     // sequences, then their steps, thread by thread over the tile pairs.
@@ -330,11 +327,14 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
         }
         if (lane == 31) B.sums[warp] = x;
         __syncthreads();
-        long long all = 0;
-        for (int i = 0; i < P_THREADS / 32; ++i) {
-            if (i < warp) x += B.sums[i];
-            all += B.sums[i];
+        const long long own = lane < P_THREADS / 32 ? B.sums[lane] : 0;
+        long long y = own;
+        for (int o = 1; o < P_THREADS / 32; o <<= 1) {
+            const long long z = __shfl_up_sync(~0u, y, o);
+            if (lane >= o) y += z;
         }
+        const long long all = __shfl_sync(~0u, y, P_THREADS / 32 - 1);
+        x += __shfl_sync(~0u, y - own, warp);
         out[tid] = x - mine;
         __syncthreads();
         return all;
@@ -395,6 +395,12 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             at += (long long)H * n;
             ++tile;
         }
+    }
+    // (Taken as late as it can be: a CTA waits for it for some microseconds, which pass beside the plan so.  4000 tokens of 32
+    // heads of 128 over 4 bits: 204 us, and 211 with it at the beginning.)
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     fence_before();
     __syncthreads();
