@@ -363,13 +363,13 @@ struct Rows4 {
     // sees(r, i) whether row r does.
     template <typename Q, typename Seen, typename Sees>
     __device__ __forceinline__ void step(const uint8_t *tiles, const uint8_t *values, const uint32_t *k_pairs, const uint32_t *v_pairs,
-                                         const int (&at)[KV], int mine, const Q &sq, int lr, int lc, bool full, Seen seen, Sees sees) {
-        // Scores: tokens t + 8 nb + mine (mine: order(lr)) of rows 2 lc, 2 lc + 1 (+ 8).
+                                         const int (&at)[KV], const Q &sq, int lr, int lc, bool full, Seen seen, Sees sees) {
+        // Scores: tokens t + 8 nb + lr of rows 2 lc, 2 lc + 1 (+ 8).
         uint32_t pair[2 * TILES][KV];
         auto load_pairs = [&](const uint32_t *src) {
 #pragma unroll
             for (int nb = 0; nb < 2 * TILES; ++nb) {
-                const uint32_t *at = src + (8 * nb + mine) * KV;
+                const uint32_t *at = src + (8 * nb + lr) * KV;
                 if constexpr (KV == 1) pair[nb][0] = *at;
                 if constexpr (KV == 2) {
                     const uint2 x = *reinterpret_cast<const uint2 *>(at);
@@ -438,7 +438,7 @@ struct Rows4 {
         if (!full) {
 #pragma unroll
             for (int nb = 0; nb < 2 * TILES; ++nb) {
-                const int i = 8 * nb + mine;
+                const int i = 8 * nb + lr;
                 // (Where no row sees a token its values' pairs are 0: whatever stands there, infinities and NaN too, meets
                 // weights of 0.)
                 if (!seen(i))
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __g
                     // (a tile of no page is not seen)
                     auto there = [&](int h) { return s_page[min(((t + 16 * h) >> BL) - pg0, npages - 1)] >= 0 && !(h == 1 && single && t + 16 >= c1); };
                     rows4.step(
-                        tiles, tiles + STAGE / 2, pairs, pairs + AFFINE / 8, at4, lr, sq, lr, lc, full,
+                        tiles, tiles + STAGE / 2, pairs, pairs + AFFINE / 8, at4, sq, lr, lc, full,
                         [&](int i) { return there(i < 16 ? 0 : 1) && t + i >= any_from && t + i < to; },
                         [&](int r, int i) { return t + i >= s_see[r].x && t + i < s_see[r].y; });
                     __syncwarp();                    // (every lane has read the stage that is filled next)
