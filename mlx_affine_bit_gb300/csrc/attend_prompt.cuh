@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
     // (Taken as late as it can be: a CTA waits for it for some microseconds, which pass beside the plan so.  4000 tokens of 32
     // heads of 128 over 4 bits: 204 us, and 211 with it at the beginning.)
     if (warp == 0) {
+        __syncwarp();                            // (all lanes take it together, and one of them may have searched the share)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
