@@ -309,6 +309,10 @@ __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
 // maxima joined at every step and the biases' sums in fp32: 84 and 53 us; with the codes by plain loads, put together by byte
 // permutes: 71 and 44.  (The next tokens' scores beside these tokens' exponentials, and shifts as products: no faster.)
 constexpr float SLACK4 = 1.f;            // in powers of two (w stays below fp16's largest: 2^18 / 15 times 2^SLACK4)
+// d of a row that has seen a token falls no lower, so that 2^(18 - d), and a p of up to 2^SLACK4 times it, are fp32 numbers.
+// (d itself is held there, not the factor: outputs and joins count on the two being one number.  Values of 2^-126, the smallest
+// that bf16 holds in full, are then 2^-4 in fp16.)
+constexpr float LEAST4 = w_exp(4) - 126.f;
 template <int D, int NT>
 struct Rows4 {
     static constexpr int KV = D / 64, MT = D / 16, TILES = tiles_of(D), NB = KV == 4 ? 2 : 1;
@@ -487,9 +491,9 @@ struct Rows4 {
                     const float d0 = d[u][e] + (m[u][e] - base[e]);
                     fl[e] = m[u][e] == -INFINITY ? 1.f : exp2_fast(m[u][e] - mt);
                     m[u][e] = mt;
-                    d[u][e] = fmaxf(d0, dt);
+                    d[u][e] = mt == -INFINITY ? -INFINITY : fmaxf(fmaxf(d0, dt), LEAST4);
                     fac[e] = exp2_fast(d0 - base_of(d[u][e]));
-                    scale[e] = d[u][e] == -INFINITY ? 0.f : exp2_fast(fminf(w_exp(4) - d[u][e], 115.f));
+                    scale[e] = mt == -INFINITY ? 0.f : exp2_fast(w_exp(4) - d[u][e]);
                 }
                 mm[u] = two(base[0], base[1]);
                 f[u] = two(scale[0], scale[1]);

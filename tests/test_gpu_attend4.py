@@ -396,3 +396,71 @@ def test_windows_of_any_size(rows):
         assert torch.equal(q.cache.attend(x, b, window=window), want), window
     torch.cuda.synchronize()
     tf.tf_device_status()
+
+
+def run_small(q, lens, rows, heads, kernel, by=100, x=None, scale=None):
+    """run(), against the same values times 2^by: the outputs are checked relative to what they are made of alone.  (What a
+    bf16 output below 2^-126 rounds to is half of 2^-133 off at most, and a weight that fp32 holds no more is below 2^-126.)"""
+    x = queries(np.random.default_rng(0), sum(rows), heads, q.d, BF16) if x is None else x
+    got = q.cache.attend(torch.from_numpy(x.reshape(sum(rows), -1)).to(DEV).to(BF16), q.batch(lens, rows), scale=scale, kernel=kernel)
+    torch.cuda.synchronize()
+    tf.tf_device_status()
+    got = got.double().cpu().numpy().reshape(sum(rows), heads, q.d) * 2.0 ** by
+    at = 0
+    for s, (n, r) in enumerate(zip(lens, rows)):
+        k, (c, vs, vb) = q.stored(s, n)
+        up = [t.astype(np.float64) * 2.0 ** by for t in (vs, vb)]
+        want, bound = attend4(x[at:at + r], k, (c, *up), q.d ** -0.5 if scale is None else scale, True, 0, False)
+        bound += 2.0 ** (by - 134) + n * 2.0 ** -126 * max(15 * np.abs(up[0]).max(), np.abs(up[1]).max())
+        err = np.abs(got[at:at + r] - want) / bound
+        assert np.all(np.isfinite(err)) and err.max() <= 1, "sequence %d: %.3f of the bound" % (s, err.max())
+        at += r
+
+
+def shrink_values(q, lens, size):
+    """The held tokens' values times `size`, a number or one for each page of the pool; none below 0, so that what a token
+    adds is not made up for by others."""
+    held = torch.zeros(q.n_blocks * q.b, dtype=torch.bool, device=DEV)
+    held[q.slots([(0, n) for n in lens])] = True
+    size = torch.as_tensor(size, dtype=torch.float32, device=DEV).reshape(-1, 1, 1, 1, 1)
+    t = q.cache.v_affine
+    t.copy_(torch.where(held.view(-1, 1, q.b, 1, 1), (t.float().abs() * size).to(BF16), t))
+
+
+@kernels
+@pytest.mark.parametrize("size", [1e-28, 1e-30, 1e-31, 1e-33])
+@pytest.mark.parametrize("heads,kv_heads,dim,rows", [(4, 2, 64, [3, 1]), (8, 2, 128, [1, 2]), (2, 1, 256, [4, 6])])
+def test_small_values(heads, kv_heads, dim, rows, size, kernel):
+    lens = [200, 70]
+    q = filled4(lens, kv_heads, dim, 32, 41)
+    shrink_values(q, lens, size)
+    run_small(q, lens, rows, heads, kernel)
+
+
+@kernels
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_small_values_of_many_sizes(dim, kernel):
+    # Tokens of different steps, warps and parts on both sides of 2^-97, each of which counts.
+    lens = [9000]
+    q = filled4(lens, 1, dim, 64, 42)
+    shrink_values(q, lens, 2.0 ** torch.linspace(-101, -94, q.n_blocks)[torch.randperm(q.n_blocks, generator=torch.Generator().manual_seed(1))])
+    run_small(q, lens, [3], 3, kernel)
+
+
+@pytest.mark.parametrize("kernel", [ROWS], ids=["rows"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ahead", [60.0, 74.0])
+def test_the_largest_scores_belong_to_zeros(dim, ahead, kernel):
+    # All pages hold zeros but three, whose tokens' scores lie `ahead` below the largest.  So many sequences that a CTA takes
+    # several steps of one; by rows, a warp that takes token 101 takes some of the others, too.
+    lens = [333] * 160
+    q = filled4(lens, 1, dim, 16, 43)
+    x = np.abs(queries(np.random.default_rng(44), 160, 1, dim, BF16))
+    q.cache.k_affine *= 0.01
+    page = torch.from_numpy(q.table[:, 6]).to(DEV).long()
+    q.cache.k_affine[page, 0, 5, :, 0] = 0
+    q.cache.k_affine[page, 0, 5, :, 1] = torch.from_numpy(ahead / (dim ** -0.5 * x.sum((1, 2)))).to(DEV).to(BF16)[:, None]
+    size = torch.zeros(q.n_blocks)
+    size[q.table[:, [2, 7, 14]].ravel().tolist()] = 1.0
+    shrink_values(q, lens, size)
+    run_small(q, lens, [1] * 160, 1, kernel, x=x)
