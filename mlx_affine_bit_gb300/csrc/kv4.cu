@@ -91,9 +91,10 @@ __device__ __forceinline__ uint32_t codes_of(float (&x)[8], float lo, float hi, 
     bias = bf16_below(lo);
     float b = bias, sc;
     if (hi - bias < 1e-25f) {
-        // (So small numbers are scaled up first, out of the reach of subnormals; values are below 1e-17 then, or all alike.)
-        constexpr float m = 18446744073709551616.f;                  // 2^64
-        scale = hi > bias ? fmaxf(bf16_above(__fmul_rn(scale_of(bias * m, hi * m), 1.f / m)), 0x1p-133f) : 0.f;
+        // (So small numbers are scaled up first, out of the reach of subnormals: values are below 1e-17 then.  Or they are all one
+        // bf16 number of any size, which stays as it is: differences of 0, and codes of 0.)
+        const float m = hi > bias ? 18446744073709551616.f : 1.f;    // 2^64
+        scale = hi > bias ? fmaxf(bf16_above(__fmul_rn(scale_of(bias * m, hi * m), 0x1p-64f)), 0x1p-133f) : 0.f;
         b = bias * m, sc = scale * m;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= m;

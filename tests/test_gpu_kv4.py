@@ -264,3 +264,16 @@ def test_captured_append_and_read_on_another_stream():
     status_clean()
     q.check(0, 64)
     assert not math.isnan(float(out.sum()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_groups_of_one_bf16_value(dtype):
+    # Scale 0 and codes 0, at any size; beside them groups of the same size that are not constant, and constant but for an
+    # infinity or a NaN, which a scale of 0 holds as the value itself.
+    sizes = [0.0, 2.0 ** -133, 2.0 ** -126, 1.0, 1.5, 2.0 ** 63, 2.0 ** 64, 1.25 * 2.0 ** 64, 2.0 ** 70, 2.0 ** 100, 2.0 ** 126]
+    x = np.array(sizes + [-s for s in sizes[1:]], np.float32)[:, None, None] * np.ones((1, 1, 256), np.float32)
+    x[:, 0, 64 + 7] *= 2
+    x[:, 0, 128 + 9], x[:, 0, 192 + 60] = np.inf, np.nan
+    exact(x.clip(-2.0 ** 126, np.inf), dtype)
+    codes, scales, _ = held(x, dtype)
+    assert np.all(codes[:, 0, :64] == 0) and np.all(scales[:, 0, 0] == 0)
