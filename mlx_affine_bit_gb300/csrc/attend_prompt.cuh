@@ -1097,9 +1097,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     uint32_t y[16];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        // w = 2^(s - m + e), p = w 2^-e with the page's e; below 2^-45 w is 0 in fp16 whatever it is.
+                        // w = 2^(s - m + e), p = w 2^-e with the page's e; below 2^-45 w is 0 in fp16 whatever it is.  (Past 2^300 no
+                        // output is left; w itself is 2^(15 + SLACK) at most with any e.)
                         const float2 z = sc[2 * c + h];
-                        const float e0 = fminf(fmaxf(mm + z.y - nn + W_EXP, -45.f), 115.f), f = factor(z.x), k = off_s * f - mm + e0;
+                        const float e0 = fminf(fmaxf(mm + z.y - nn + W_EXP, -45.f), 300.f), f = factor(z.x), k = off_s * f - mm + e0;
                         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
                         for (int e = 16 * h; e < 16 * h + 16; e += 2) {

@@ -989,7 +989,8 @@ __global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __g
                 for (int u = 0; u < NT; ++u) {
 #pragma unroll
                     for (int h = 0; h < TILES; ++h) {
-                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf(vs[h] + (W_EXP - d[u]), 115.f));
+                        // (The largest that fp32 holds: tokens of p below 2^-112 count for less than they are.)
+                        const float f = d[u] == -INFINITY ? 0.f : exp2_fast(fminf(vs[h] + (W_EXP - d[u]), 127.f));
 #pragma unroll
                         for (int nb = 2 * h; nb < 2 * h + 2; ++nb) {
                             const float p0 = exp2_fast(sc[nb][2 * u] - mm[u]), p1 = exp2_fast(sc[nb][2 * u + 1] - mm[u]);

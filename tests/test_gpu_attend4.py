@@ -447,7 +447,7 @@ def test_small_values_of_many_sizes(dim, kernel):
     run_small(q, lens, [3], 3, kernel)
 
 
-@pytest.mark.parametrize("kernel", [ROWS], ids=["rows"])
+@kernels
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("ahead", [60.0, 74.0])
 def test_the_largest_scores_belong_to_zeros(dim, ahead, kernel):
