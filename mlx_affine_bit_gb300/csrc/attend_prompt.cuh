@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             // A part: [tile][D / 4][128 rows] of four outputs, after all parts [tile][128 rows] row sums.
             float4 *const parts4 = reinterpret_cast<float4 *>(P.part);
             float4 *const sums4 = parts4 + 2LL * gridDim.x * R * (D / 4);
-            const float f = out_factor(sum);
+            const OutFactor f = out_factor(sum);
             float4 *mine = parts4 + ((long long)slot(k_mine) * NT + t) * (D / 4) * 128 + row;
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]);
                 if (parts == 1) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = sum.l == 0.f ? 0.f : y[e] * f;
+                    for (int e = 0; e < 32; ++e) y[e] = sum.l == 0.f ? 0.f : f.of(y[e]);
                     store(d, y);
                 } else {
 #pragma unroll
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 const RowSum x = sum_of(k);
                 a.l += x.l * l_factor(x, a);
             }
-            const float fa = out_factor(a);
+            const OutFactor fa = out_factor(a);
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
                 float y[32];
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = a.l == 0.f ? 0.f : y[e] * fa;
+                for (int e = 0; e < 32; ++e) y[e] = a.l == 0.f ? 0.f : fa.of(y[e]);
                 store(d, y);
             }
         };

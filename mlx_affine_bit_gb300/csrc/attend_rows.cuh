@@ -150,9 +150,17 @@ __device__ __forceinline__ void join_maxima(RowSum &a, const RowSum &p) {
 // saw no token or only values of scale 0; NaN scores (l NaN) stay NaN.
 __device__ __forceinline__ float l_factor(const RowSum &p, const RowSum &a) { return exp2_fast(p.m - base_of(a.m)); }
 __device__ __forceinline__ float o_factor(const RowSum &p, const RowSum &a) { return exp2_fast(d_at(p, base_of(a.m)) - base_of(a.d)); }
-// Factor of the joined outputs: to the maximum of s, and by the sum.
+// Factor of the joined outputs: to the maximum of s, and by the sum.  In two, of which the second is 1 or, where d is so far
+// down that the factor could leave fp32's normal numbers and its bits, 2^-64.
+struct OutFactor {
+    float f, g;
+    __device__ __forceinline__ float of(float x) const { return x * f * g; }
+};
 template <int F = 8>
-__device__ __forceinline__ float out_factor(const RowSum &a) { return a.l == 0.f ? 0.f : exp2f(a.d - w_exp(F)) / a.l; }
+__device__ __forceinline__ OutFactor out_factor(const RowSum &a) {
+    const bool low = a.d < -64.f;
+    return {a.l == 0.f ? 0.f : exp2f((low ? a.d + 64.f : a.d) - w_exp(F)) / a.l, low ? 0x1p-64f : 1.f};
+}
 
 // Stages of a warp's ring, and CTAs an SM by the shared memory that the rings and the registers that outputs and q
 // take.  48 sequences of up to 8000 tokens, 8 heads of 128: 79 us so, 81 with one tile a stage and four stages, 83
@@ -1083,12 +1091,12 @@ __global__ void __launch_bounds__(THREADS, ctas(F, D, NT)) rows_kernel(const __g
             return y;
         };
         // Four values of an output row (aligned to 2 bytes only).
-        auto store4 = [&](int r, int d, float4 x, float f) {
+        auto store4 = [&](int r, int d, float4 x, const OutFactor &f) {
             uint16_t *dst = out_at(r) + d;
-            dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x.x * f));
-            dst[1] = __bfloat16_as_ushort(__float2bfloat16_rn(x.y * f));
-            dst[2] = __bfloat16_as_ushort(__float2bfloat16_rn(x.z * f));
-            dst[3] = __bfloat16_as_ushort(__float2bfloat16_rn(x.w * f));
+            dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(f.of(x.x)));
+            dst[1] = __bfloat16_as_ushort(__float2bfloat16_rn(f.of(x.y)));
+            dst[2] = __bfloat16_as_ushort(__float2bfloat16_rn(f.of(x.z)));
+            dst[3] = __bfloat16_as_ushort(__float2bfloat16_rn(f.of(x.w)));
         };
         // The CTAs that share the item, in order.
         const int c_first = cta_of(item_at), parts = cta_of(item_at + sw.steps - 1) - c_first + 1;

@@ -464,3 +464,12 @@ def test_the_largest_scores_belong_to_zeros(dim, ahead, kernel):
     size[q.table[:, [2, 7, 14]].ravel().tolist()] = 1.0
     shrink_values(q, lens, size)
     run_small(q, lens, [1] * 160, 1, kernel, x=x)
+
+
+@kernels
+@pytest.mark.parametrize("dim,length,size", [(64, 5000, 1e-33), (128, 5000, 1e-36), (256, 5000, 1e-36), (64, 200000, 1e-36)])
+def test_small_values_of_many_tokens_alike(dim, length, size, kernel):
+    # Outputs near bf16's smallest normal number, of a large sum of weights.
+    q = filled4([length], 1, dim, 128, 45)
+    shrink_values(q, [length], size)
+    run_small(q, [length], [2], 1, kernel, x=queries(np.random.default_rng(46), 2, 1, dim, BF16, spread=0.02))

@@ -61,3 +61,12 @@ def test_the_largest_scores_belong_to_zeros(dim, ahead, kernel):
     size[q.table[:, [2, 7, 14]].ravel().tolist()] = 1.0
     q.cache.v_scale *= size.to(DEV)
     run_small(q, lens, [1] * 160, 1, kernel, x)
+
+
+@kernels
+@pytest.mark.parametrize("dim,length,size", [(64, 5000, 1e-30), (64, 5000, 1e-33), (128, 5000, 1e-35), (256, 5000, 1e-35), (64, 200000, 1e-35)])
+def test_small_values_of_many_tokens_alike(dim, length, size, kernel):
+    # Outputs near bf16's smallest normal number, of a large sum of weights.
+    q = positive(filled([length], 1, dim, 128, 45))
+    q.cache.v_scale *= size
+    run_small(q, [length], [2], 1, kernel, queries(np.random.default_rng(46), 2, 1, dim, BF16, spread=0.02))
