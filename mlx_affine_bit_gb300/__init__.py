@@ -437,9 +437,10 @@ class KvBatch:
     kv_len [seqs] int32 (the new tokens included), table [seqs][pages] int32,
     max_len a bound of kv_len; row_start [seqs + 1] int32 with rows and
     max_rows, or max_rows (1) rows for each sequence; slots [seqs] int32, or
-    None for 0, 1, ...  The tensors are kept, and read by the device at each call."""
+    None for 0, 1, ...  block: tokens of a page, where the table was made for pages of one size (a cache of
+    another is then refused).  The tensors are kept, and read by the device at each call."""
 
-    def __init__(self, kv_len, table, max_len, row_start=None, rows=None, max_rows=1, slots=None):
+    def __init__(self, kv_len, table, max_len, row_start=None, rows=None, max_rows=1, slots=None, block=None):
         import torch
         i32 = (torch.int32,)
         n = kv_len.shape[0]
@@ -458,7 +459,7 @@ class KvBatch:
             raise ValueError("max_len exceeds the table")
         self.rows = n * max_rows if row_start is None else rows
         self._keep = (kv_len, table, row_start, slots)
-        self._pages = table.shape[1]
+        self._pages, self.block = table.shape[1], block
         self.c = TfKvBatch(n, self.rows, max_rows, max_len, _ptr(row_start), _ptr(kv_len), _ptr(table),
                            table.stride(0) if n > 1 else table.shape[1], _ptr(slots))
 
@@ -508,6 +509,8 @@ class KvCache:
                    torch.zeros((n_slots, 2, kv_heads, 2 * block), **f32))
 
     def _batch(self, batch):
+        if batch.block is not None and batch.block != self.block:
+            raise ValueError("the batch's pages hold %d tokens, the cache's %d" % (batch.block, self.block))
         if batch.c.max_len > batch._pages * self.block:
             raise ValueError("max_len exceeds the table's pages")
         if batch.device != self.device:

@@ -80,7 +80,8 @@ class KvPlan:
         if rows:
             self.positions = torch.full((rows,), -1, **i32)
             self.slots = torch.full((rows,), -1, dtype=torch.int64, device=pages.table.device)
-            self.batch = tf.KvBatch(pages.kv_len, pages.table, max_len, self.row_start, rows, min(max_rows, rows))
+            self.batch = tf.KvBatch(pages.kv_len, pages.table, max_len, self.row_start, rows, min(max_rows, rows), block=pages.block)
+            self.slots.block = pages.block       # (of the tensor itself, as Kv4Cache.append looks at it)
 
     def step(self, change, stream=None):
         """Each sequence gets change[s] tokens (int32 [n_seqs]) or gives -change[s] back; returns self."""
@@ -227,8 +228,11 @@ class Kv4Cache:
 
     def append(self, k, v, slots, stream=None) -> None:
         """Quantize rows k, v [rows][kv_heads * dim] (bf16 or fp32, row stride free) into slots [rows] int64
-        (page * block + place in the page, -1: left out), as KvPlan gives them."""
+        (page * block + place in the page, -1: left out), as KvPlan gives them.  A plan's own slots are refused where its
+        pages are of another size than the cache's; other tensors, slices of a plan's among them, are taken at their word."""
         import torch
+        if getattr(slots, "block", self.block) != self.block:
+            raise ValueError("the slots are of pages of %d tokens, the cache's hold %d" % (slots.block, self.block))
         rows, width = slots.shape[0], self.kv_heads * self.dim
         types = (torch.bfloat16, torch.float32)
         ks = _rows(k, "k", types, rows, width, self.device)

@@ -216,3 +216,23 @@ def test_frequencies(tf):
                 dict(dim=8, frequencies=[1.0] * 4, scaling=dict(type="linear", factor=2))):
         with pytest.raises(ValueError):
             tf.Rope(**bad, device="cpu")
+
+
+def test_a_plan_goes_with_caches_of_its_pages_only(tf):
+    # Pages of 16 tokens in a cache of 32 a page, and the other way round: places and lengths would be taken for others.
+    plan = tf.KvPages.empty(2, 10, 8, 16, "cpu").plan(2, 1, 64)
+    k = torch.zeros((2, 128), dtype=torch.bfloat16)
+    for block in (32, 64):
+        other = tf.Kv4Cache.empty(5, 2, 64, block, "cpu")
+        eight = tf.KvCache.empty(5, 2, 64, block, 2, device="cpu")
+        for call in (lambda: other.append(k, k, plan.slots, stream=0), lambda: other.attend(k, plan.batch, stream=0),
+                     lambda: other.read(plan.batch, stream=0), lambda: eight.attend(k, plan.batch, stream=0),
+                     lambda: eight.read(plan.batch, stream=0), lambda: eight.append(k, k, plan.batch, stream=0)):
+            with pytest.raises(ValueError, match="pages"):
+                call()
+    # Of the same size, and tensors that say nothing of pages: only that there is no GPU stands against them.
+    same = tf.Kv4Cache.empty(5, 2, 64, 16, "cpu")
+    for call in (lambda: same.append(k, k, plan.slots, stream=0), lambda: other.append(k, k, plan.slots[:], stream=0),
+                 lambda: same.attend(k, plan.batch, stream=0), lambda: same.read(plan.batch, stream=0)):
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()
