@@ -723,7 +723,12 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]);
                 if (parts == 1) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = sum.l == 0.f ? 0.f : f.of(y[e]);
+                    for (int e = 0; e < 32; e += 2) {
+                        mul2(x[e], x[e + 1], f.f);
+                        mul2(x[e], x[e + 1], f.g);
+                        y[e] = sum.l == 0.f ? 0.f : __uint_as_float(x[e]);
+                        y[e + 1] = sum.l == 0.f ? 0.f : __uint_as_float(x[e + 1]);
+                    }
                     store(d, y);
                 } else {
 #pragma unroll
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
             for (int k = AHEAD; k < parts; ++k) join_maxima(a, sum_of(k));
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
-                g[k] = o_factor(first[k], a);
+                g[k] = o_factor(first[k], a) * out_factor(a).g;
                 if (k < parts) a.l += first[k].l * l_factor(first[k], a);
             }
 #pragma unroll 1
@@ -776,7 +781,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                 const RowSum x = sum_of(k);
                 a.l += x.l * l_factor(x, a);
             }
-            const OutFactor fa = out_factor(a);
+            const float fa = out_factor(a).f;            // (its second factor is in the parts')
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
                 float y[32];
@@ -789,7 +794,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
 #pragma unroll
                         for (int e = 0; e < AHEAD; ++e) f = k == e ? g[e] : f;
                     } else {
-                        f = o_factor(sum_of(k), a);
+                        f = o_factor(sum_of(k), a) * out_factor(a).g;
                     }
                     const float4 *src = parts4 + ((long long)slot(k) * NT + t) * (D / 4) * 128 + (d / 4) * 128 + row;
                     float4 x[8];
@@ -805,7 +810,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) prompt_kernel(const __grid_const
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = a.l == 0.f ? 0.f : fa.of(y[e]);
+                for (int e = 0; e < 32; ++e) y[e] = a.l == 0.f ? 0.f : y[e] * fa;
                 store(d, y);
             }
         };
