@@ -118,7 +118,8 @@ int tf_kv_read(const tf_kv *kv, const tf_kv_batch *batch, void *k_out, int64_t k
  * scaling of its row (bf16 values keep all their bits, fp32 values are rounded
  * to 11), codes are exact there; each p times its page's value scale is rounded
  * to fp16 (11 bits) relative to the row's largest for the second product (11 bits
- * down to 2^-29 of it, nothing below 2^-40); scores, maxima, sums and accumulators
+ * down to 2^-29 of it, nothing below 2^-40, and of a token whose p is below 2^-112 of
+ * the row's largest perhaps nothing); scores, maxima, sums and accumulators
  * are fp32 (a score of 2^20 is held to 2^-3: larger ones are told apart no better
  * than fp32 does, but lose nothing else); out is rounded once to bf16.
  * A row's bits do not change from call to call with the same arguments; between

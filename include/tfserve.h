@@ -131,12 +131,14 @@ int tf_kv4_read(const tf_kv4 *kv, const tf_kv_batch *batch, void *k_out, int64_t
 /*
  * tf_kv4_attend -- attention of the batch's rows over the 4-bit cache: arguments, flags,
  * masks, workspace and streams are those of tf_kv_attend.
- * Precision: scores, maxima, sums and accumulators are fp32.  By rows, q enters the
- * tensor cores as fp16 after an exact power-of-two scaling of its row (fp32 values are
- * rounded to 11 bits), codes are exact, and each p times a value's scale is rounded to
- * fp16 (11 bits) relative to the row's largest contribution (nothing below 2^-36 of it).  By tiles (many rows) keys
- * and values themselves are rounded to fp16 too, relative to the largest of 16 tokens (11 bits, down to 2^-14 of
- * it).  out is rounded once to bf16.
+ * Precision: scores, maxima, sums and accumulators are fp32.  q enters the tensor
+ * cores as fp16 after an exact power-of-two scaling of its row (fp32 values are
+ * rounded to 11 bits).  By rows codes are exact, and each p times a value's scale is
+ * rounded to fp16.  By tiles (many rows) each p is, and keys and values themselves,
+ * relative to the largest of 16 tokens (11 bits, down to 2^-14 of it).  Fp16 stands for
+ * 11 bits down to 2^-28 of the largest p of 16 tokens times the largest value among them,
+ * whichever 16 of the row's tokens these are; what is below 2^-39 of that may be left
+ * out, and a token whose p is below 2^-112 of the row's largest.  out is rounded once to bf16.
  */
 int tf_kv4_attend(const tf_kv4 *kv, const tf_kv_batch *batch, const void *q, int64_t q_stride, int heads, void *out,
                   int64_t out_stride, float scale, int window, int flags, void *stream);

@@ -147,7 +147,7 @@ int call(Params &P, const tf_kv_batch *batch, const void *q, int64_t q_stride, i
     // against 107 us; 128 rows 197 against 107; 128 rows of 1 x 4000 tokens 32 against 42.
     // The host knows the largest number of rows and the largest length of a sequence only, and takes them for all:
     // a chunk of 500 rows beside 47 single tokens over 4000 to 4500 tokens goes to the prompt kernel as a whole and takes
-    // 334 us (by rows 272), where a call for the chunk and one for the others take 70 and 74.
+    // 328 us (by rows 270), where a call for the chunk and one for the others take 67 and 72 (4 bits: 324, 286, 67 and 58).
     bool prompt = (flags & TF_KV_BY_TILES) != 0;
     if (max_group_rows > 16 && !(flags & (TF_KV_BY_ROWS | TF_KV_BY_TILES))) {
         const double blocks = (double)batch->n_seqs * kv->kv_heads * (double)((span + 127) / 128);

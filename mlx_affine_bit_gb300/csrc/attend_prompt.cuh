@@ -17,11 +17,12 @@
 //
 // Bound by the tensor cores and, closely, by the instructions around them: per row
 // and token one exponential and about four others, per token and dimension of the
-// cache about two to widen a code.  Causal, 32 query heads of 128 over 8: 4000 tokens
-// of a prompt 201 us (652 TFLOP/s), 8000 646 us (812 TFLOP/s); 16 heads of 256: 4000
-// tokens 202 us; 16 heads of 64: 88 us; three chunks of up to 509 tokens, 16 heads of
-// 256, window 4096: 91 us (scores past FAR: 4000 tokens of 32 heads 323 us, the chunks
-// 136; all of them before tensor memory was taken later, which is 4 to 7 us off: 4000 tokens 198).  A step of two tiles (256 rows, 128 tokens, dim 128) takes
+// cache about two to widen a code.  Over 8 bits, causal, 32 query heads of 128 over 8:
+// 4000 tokens of a prompt 196 to 200 us (669 to 656 TFLOP/s), 8000 643 us (815 TFLOP/s);
+// 16 heads of 256: 4000 tokens 193 us; 16 heads of 64: 87 us; three chunks of up to 509
+// tokens, 16 heads of 256, window 4096: 86 us (scores past FAR: 4000 tokens of 32 heads
+// 318 us, the chunks 129).  Over 4 bits: 203, 657, 214 and 89 us, the chunks with fp32 q
+// 120.  A step of two tiles (256 rows, 128 tokens, dim 128) takes
 // 2.7 us, 1.7 us of them the products: one with N = 128 takes 94 to 107 clocks for
 // 16 of K, measured alone, which is 60 to 68 % of the peak.  An item's beginning and
 // end (the rows of q, the first scores, the outputs) cost 6 us, the launch's plan 4.

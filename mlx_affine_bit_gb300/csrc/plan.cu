@@ -7,7 +7,7 @@
 // sequence is the last whose rows begin at or before it.
 //
 // Bound by a chain of latencies: a launch, the lengths, two barriers of the sums,
-// the stack, the table, the rows (48 sequences of a token 4.4 us a call).  One CTA does
+// the stack, the table, the rows (48 sequences of a token 3.2 us a call in a graph).  One CTA does
 // the sums and the pages, and the rows too where they are few; more rows are filled
 // by a second kernel, a thread a row (64,000 rows of 256 sequences: 16 us in one CTA,
 // 9 in two launches; at 4096 rows both take the same).

@@ -62,7 +62,10 @@ class KvPages:
 
 class KvPlan:
     """One kind of step of a KvPages, and what it leaves on the device: row_start [n_seqs + 1], positions [rows] int32,
-    slots [rows] int64, info [4] (include/tfserve.h), and batch, the KvBatch of the step's rows."""
+    slots [rows] int64, info [4] (include/tfserve.h), and batch, the KvBatch of the step's rows.
+
+    All of it is of the plan's last step, and batch of the pages as they stand then: it reads their lengths and table, with
+    this plan's row_start.  After a step of another plan of the same pages it means other tokens; use it before."""
 
     def __init__(self, pages, rows, max_rows=1, max_len=None):
         import torch
